@@ -348,6 +348,112 @@ sparse_status_t sparse_canonicalize_static_ws(const int64_t* idx, const float* v
                                               int32_t* d_err, cudaStream_t stream);
 
 /*
+ * Operators around the table step: what a model with such a table trains and
+ * serves with next to it.  (No counterpart on the pages, which describe the
+ * optimizer alone.)  The conventions above hold: caller memory, dense row-major
+ * arrays of any alignment (16-byte aligned ones with rows of a multiple of 16
+ * bytes take the vector path), asynchronous on `stream`, the sticky error word,
+ * n = 0 is legal.  Values are fp32 or bf16 as their sparse_dtype_t says;
+ * statistics, weights, weight gradients and every sum are fp32, and a bf16
+ * output is rounded once.  Non-state outputs are undefined when *d_err is set.
+ */
+typedef enum {
+    SPARSE_F32 = 0,
+    SPARSE_BF16 = 1
+} sparse_dtype_t;
+
+/* Bytes of workspace sparse_layer_norm_grad needs for n rows of c columns. */
+size_t sparse_layer_norm_workspace_size(int64_t n, int64_t c);
+
+/*
+ * sparse_layer_norm -- layer norm of n rows: of table rows looked up by idx (the
+ * row gather and the norm in one pass), or of the first n rows of x (idx NULL).
+ *   mu = sum(x)/c, var = sum((x - mu)^2)/c, rstd = 1/sqrt(var + eps),
+ *   y = (x - mu) rstd gamma + beta
+ *   x [r, c], y [n, c]: fp32 -> fp32, fp32 -> bf16 or bf16 -> bf16
+ *   idx[n]              rows of x in any order, repeats allowed; one outside [0, r)
+ *                       sets SPARSE_ERR_INDEX_OUT_OF_RANGE and its outputs are left
+ *                       unwritten
+ *   gamma[c], beta[c]   fp32; NULL stands for ones / zeros
+ *   eps                 >= 0 and finite
+ *   mean[n], rstd[n]    out (each may be NULL): kept for the backward pass
+ * c is at most 2^31 - 1.
+ */
+sparse_status_t sparse_layer_norm(const void* x, sparse_dtype_t x_type, int64_t r, int64_t c, const int64_t* idx,
+                                  int64_t n, const float* gamma, const float* beta, double eps, void* y,
+                                  sparse_dtype_t y_type, float* mean, float* rstd, int32_t* d_err, cudaStream_t stream);
+
+/*
+ * sparse_layer_norm_grad -- the backward pass of sparse_layer_norm, from the same
+ * x, idx, gamma and the mean and rstd it wrote.  With xhat = (x - mu) rstd and
+ * h = dy gamma:
+ *   dx = rstd (h - sum(h)/c - xhat sum(h xhat)/c)
+ *   dgamma = sum over rows of dy xhat, dbeta = sum over rows of dy
+ *   dy [n, c]   of y's type;  dx [n, c]: of x's type, one row per looked-up row (with
+ *               idx it is the raw row-COO gradient of the table: rows idx, values dx)
+ *   dgamma[c], dbeta[c]  out, fp32 (each may be NULL); zeros for n = 0.  Sums are in a
+ *               fixed order: equal inputs give equal bits.
+ *   ws          sparse_layer_norm_workspace_size(n, c) bytes, 256-byte aligned (not
+ *               needed when dgamma and dbeta are both NULL)
+ */
+sparse_status_t sparse_layer_norm_grad(const void* dy, sparse_dtype_t y_type, const void* x, sparse_dtype_t x_type,
+                                       int64_t r, int64_t c, const int64_t* idx, int64_t n, const float* gamma,
+                                       const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
+                                       void* ws, size_t ws_bytes, int32_t* d_err, cudaStream_t stream);
+
+/*
+ * Tokens by expert.  n tokens name k experts each: expert[n, k] holds a slot's
+ * expert in [0, experts), or -1 for a slot that goes nowhere (a padding token's).
+ * Slot s = t*k + j.  Limits: 1 <= experts <= 1024, k >= 1, n*k < 2^31.
+ */
+/* Bytes of workspace sparse_expert_sort needs. */
+size_t sparse_expert_workspace_size(int64_t n, int64_t k, int64_t experts);
+
+/*
+ * sparse_expert_sort -- the slots sorted stably by expert.
+ *   offsets[experts+1]  out: expert e has the sorted places offsets[e] .. offsets[e+1]-1
+ *   src[n*k]            out (may be NULL): the slot at a sorted place, -1 past the last
+ *   pos[n*k]            out: the sorted place of a slot, -1 for one that goes nowhere
+ *   An expert outside [-1, experts) sets SPARSE_ERR_INDEX_OUT_OF_RANGE.
+ */
+sparse_status_t sparse_expert_sort(const int64_t* expert, int64_t n, int64_t k, int64_t experts, int64_t* offsets,
+                                   int32_t* src, int32_t* pos, void* ws, size_t ws_bytes, int32_t* d_err,
+                                   cudaStream_t stream);
+
+/*
+ * sparse_expert_dispatch -- every token's row to the sorted places of its slots:
+ * xs[pos[t*k + j]] = x[t], and zeros in the places from offsets[experts] on, so all
+ * n*k rows of xs are written.  x [n, c], xs [n*k, c] of one type, copied bit for bit;
+ * pos and offsets as sparse_expert_sort wrote them (a place outside [-1, n*k) sets
+ * SPARSE_ERR_INDEX_OUT_OF_RANGE).  Its gradient is sparse_expert_combine of the
+ * gradient of xs without weights.
+ */
+sparse_status_t sparse_expert_dispatch(const void* x, sparse_dtype_t type, int64_t n, int64_t k, int64_t c,
+                                       const int32_t* pos, const int64_t* offsets, int64_t experts, void* xs,
+                                       int32_t* d_err, cudaStream_t stream);
+
+/*
+ * sparse_expert_combine -- y[t] = sum over j of weights[t, j] ys[pos[t*k + j]], in
+ * fp32 in slot order, rounded once.  A slot that goes nowhere adds nothing, and a
+ * token with no other gets zeros; rows of ys that no slot has are not read.
+ * ys [n*k, c], y [n, c] of one type; weights[n, k] fp32 (NULL: ones).
+ */
+sparse_status_t sparse_expert_combine(const void* ys, sparse_dtype_t type, int64_t n, int64_t k, int64_t c,
+                                      const int32_t* pos, const float* weights, void* y, int32_t* d_err,
+                                      cudaStream_t stream);
+
+/*
+ * sparse_expert_combine_grad -- the backward pass of sparse_expert_combine:
+ * dys[pos[t*k + j]] = weights[t, j] dy[t] (zeros in the places from
+ * offsets[experts] on), dweights[t, j] = <dy[t], ys[pos[t*k + j]]> (0 for a slot that
+ * goes nowhere).  dweights may be NULL.
+ */
+sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, sparse_dtype_t type, int64_t n, int64_t k,
+                                           int64_t c, const int32_t* pos, const int64_t* offsets, int64_t experts,
+                                           const float* weights, void* dys, float* dweights, int32_t* d_err,
+                                           cudaStream_t stream);
+
+/*
  * Per-kernel timing (diagnostics; no counterpart on the pages).  While enabled,
  * every kernel the library enqueues is bracketed by two CUDA events on its
  * stream.  sparse_profile_read() waits for every recorded event, then reports

@@ -34,6 +34,8 @@ LAST_STEP_PER_ROW = 0
 LAST_STEP_PER_COORD = 1
 GRAD_ROW_COO = 0
 GRAD_CSR = 1
+F32 = 0            # sparse_dtype_t
+BF16 = 1
 
 
 class AdamConfig(ctypes.Structure):
@@ -82,6 +84,14 @@ def _load():
         "sparse_read_rows": (INT, [P, I64, I64, P, I64, P, P, P]),
         "sparse_check_finite": (INT, [P, I64, P, P]),
         "sparse_check_state": (INT, [P, P, I64, I64, ctypes.POINTER(Grad), P, P]),
+        "sparse_layer_norm_workspace_size": (SZ, [I64, I64]),
+        "sparse_layer_norm": (INT, [P, INT, I64, I64, P, I64, P, P, ctypes.c_double, P, INT, P, P, P, P]),
+        "sparse_layer_norm_grad": (INT, [P, INT, P, INT, I64, I64, P, I64, P, P, P, P, P, P, P, SZ, P, P]),
+        "sparse_expert_workspace_size": (SZ, [I64, I64, I64]),
+        "sparse_expert_sort": (INT, [P, I64, I64, I64, P, P, P, P, SZ, P, P]),
+        "sparse_expert_dispatch": (INT, [P, INT, I64, I64, I64, P, P, I64, P, P, P]),
+        "sparse_expert_combine": (INT, [P, INT, I64, I64, I64, P, P, P, P, P]),
+        "sparse_expert_combine_grad": (INT, [P, P, INT, I64, I64, I64, P, P, I64, P, P, P, P, P]),
         "sparse_profile_enable": (None, [INT]),
         "sparse_profile_reset": (None, []),
         "sparse_profile_read": (INT, [INT, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_int64),
@@ -99,7 +109,9 @@ EXPORTED = ("sparse_workspace_size", "sparse_status_string", "sparse_canonicaliz
             "sparse_coo_to_csr", "sparse_row_coo_to_csr", "sparse_adam_step", "sparse_adam_table_step",
             "sparse_sgd_step", "sparse_sgd_table_step", "sparse_canonicalize_static_ws", "sparse_profile_enable",
             "sparse_profile_reset", "sparse_profile_read", "sparse_read_rows", "sparse_check_finite",
-            "sparse_check_state")
+            "sparse_check_state", "sparse_layer_norm_workspace_size", "sparse_layer_norm", "sparse_layer_norm_grad",
+            "sparse_expert_workspace_size", "sparse_expert_sort", "sparse_expert_dispatch", "sparse_expert_combine",
+            "sparse_expert_combine_grad")
 STATIC_WS_BYTES = 16 * 1024 * 1024  # SPARSE_STATIC_WS_BYTES
 
 
@@ -118,6 +130,18 @@ def _ptr(t, dtype=None, name="tensor"):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _typed(t, name, like=None):
+    """(pointer, sparse_dtype_t) of an fp32 or bf16 tensor, of like's type where that is given."""
+    p = _ptr(t, like.dtype if like is not None else None, name)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
+    return p, code
 
 
 def _stream(stream):
@@ -276,6 +300,71 @@ def sparse_read_rows(table, r, c, idx, n, out, d_err, stream=None) -> int:
     return LIB.sparse_read_rows(_ptr(table, torch.float32, "table"), int(r), int(c), _ptr(idx, torch.int64, "idx"),
                                 int(n), _ptr(out, torch.float32, "out"), _ptr(d_err, torch.int32, "d_err"),
                                 _stream(stream))
+
+
+# ------------------------------------------------------------------ operators around the step
+def sparse_layer_norm_workspace_size(n: int, c: int) -> int:
+    return int(LIB.sparse_layer_norm_workspace_size(int(n), int(c)))
+
+
+def sparse_layer_norm(x, r, c, idx, n, gamma, beta, eps, y, mean, rstd, d_err, stream=None) -> int:
+    """Types are those of x and y; idx, gamma, beta, mean and rstd may be None."""
+    xp, xt = _typed(x, "x")
+    yp, yt = _typed(y, "y")
+    return LIB.sparse_layer_norm(xp, xt, int(r), int(c), _ptr(idx, torch.int64, "idx"), int(n),
+                                 _ptr(gamma, torch.float32, "gamma"), _ptr(beta, torch.float32, "beta"), float(eps),
+                                 yp, yt, _ptr(mean, torch.float32, "mean"), _ptr(rstd, torch.float32, "rstd"),
+                                 _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_layer_norm_grad(dy, x, r, c, idx, n, gamma, mean, rstd, dx, dgamma, dbeta, ws, d_err, stream=None) -> int:
+    """idx, gamma, dgamma and dbeta may be None."""
+    wp, wb = _ws(ws)
+    yp, yt = _typed(dy, "dy")
+    xp, xt = _typed(x, "x")
+    return LIB.sparse_layer_norm_grad(yp, yt, xp, xt, int(r), int(c), _ptr(idx, torch.int64, "idx"), int(n),
+                                      _ptr(gamma, torch.float32, "gamma"), _ptr(mean, torch.float32, "mean"),
+                                      _ptr(rstd, torch.float32, "rstd"), _typed(dx, "dx", x)[0],
+                                      _ptr(dgamma, torch.float32, "dgamma"), _ptr(dbeta, torch.float32, "dbeta"),
+                                      wp, wb, _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_expert_workspace_size(n: int, k: int, experts: int) -> int:
+    return int(LIB.sparse_expert_workspace_size(int(n), int(k), int(experts)))
+
+
+def sparse_expert_sort(expert, n, k, experts, offsets, src, pos, ws, d_err, stream=None) -> int:
+    wp, wb = _ws(ws)
+    return LIB.sparse_expert_sort(_ptr(expert, torch.int64, "expert"), int(n), int(k), int(experts),
+                                  _ptr(offsets, torch.int64, "offsets"), _ptr(src, torch.int32, "src"),
+                                  _ptr(pos, torch.int32, "pos"), wp, wb, _ptr(d_err, torch.int32, "d_err"),
+                                  _stream(stream))
+
+
+def sparse_expert_dispatch(x, n, k, c, pos, offsets, experts, xs, d_err, stream=None) -> int:
+    xp, xt = _typed(x, "x")
+    return LIB.sparse_expert_dispatch(xp, xt, int(n), int(k), int(c), _ptr(pos, torch.int32, "pos"),
+                                      _ptr(offsets, torch.int64, "offsets"), int(experts), _typed(xs, "xs", x)[0],
+                                      _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_expert_combine(ys, n, k, c, pos, weights, y, d_err, stream=None) -> int:
+    """weights may be None (ones: the gradient of sparse_expert_dispatch)."""
+    yp, yt = _typed(ys, "ys")
+    return LIB.sparse_expert_combine(yp, yt, int(n), int(k), int(c), _ptr(pos, torch.int32, "pos"),
+                                     _ptr(weights, torch.float32, "weights"), _typed(y, "y", ys)[0],
+                                     _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_expert_combine_grad(dy, ys, n, k, c, pos, offsets, experts, weights, dys, dweights, d_err,
+                               stream=None) -> int:
+    """weights (ones) and dweights (not wanted) may be None."""
+    yp, yt = _typed(ys, "ys")
+    return LIB.sparse_expert_combine_grad(_typed(dy, "dy", ys)[0], yp, yt, int(n), int(k), int(c),
+                                          _ptr(pos, torch.int32, "pos"), _ptr(offsets, torch.int64, "offsets"),
+                                          int(experts), _ptr(weights, torch.float32, "weights"),
+                                          _typed(dys, "dys", ys)[0], _ptr(dweights, torch.float32, "dweights"),
+                                          _ptr(d_err, torch.int32, "d_err"), _stream(stream))
 
 
 # ------------------------------------------------------------------ diagnostics

@@ -1,0 +1,143 @@
+// api_model.cu -- the extern "C" entry points of the operators around the table
+// step (declared in include/sparseopt.h): argument validation, workspace
+// carving and the choice of 16-byte accesses.  No host synchronisation.
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace {
+
+using namespace so;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool ws_ok(const void* ws, size_t have, size_t need)
+{
+    return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && have >= need;
+}
+
+bool valid_type(sparse_dtype_t t) { return t == SPARSE_F32 || t == SPARSE_BF16; }
+
+bool is_bf16(sparse_dtype_t t) { return t == SPARSE_BF16; }
+
+sparse_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? SPARSE_OK : SPARSE_ERR_CUDA; }
+
+// n rows of c values, with n * c within int64 (and far from its end).
+bool valid_rows(int64_t n, int64_t c) { return n >= 0 && c >= 1 && (n == 0 || c <= (INT64_MAX >> 4) / n); }
+
+// Layer norm's rows: x [r, c], n of them looked up, or the first n without idx.
+bool valid_norm(const void* x, sparse_dtype_t x_type, int64_t r, int64_t c, const int64_t* idx, int64_t n,
+                sparse_dtype_t y_type, const int32_t* d_err)
+{
+    return valid_type(x_type) && valid_type(y_type) && !(is_bf16(x_type) && !is_bf16(y_type)) && valid_rows(r, c) &&
+           valid_rows(n, c) && c <= INT32_MAX && (idx != nullptr || n <= r) && (n == 0 || x != nullptr) &&
+           d_err != nullptr;
+}
+
+// Values of one 16-byte access, or of the two that match it where a type is fp32 and the other bf16.
+int64_t lane_values(sparse_dtype_t x_type, sparse_dtype_t y_type)
+{
+    return is_bf16(x_type) || is_bf16(y_type) ? 8 : 4;
+}
+
+bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const int32_t* d_err)
+{
+    return valid_type(type) && n >= 0 && k >= 1 && (n == 0 || k <= INT32_MAX / n) && valid_rows(n * k, c) &&
+           d_err != nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sparse_layer_norm_workspace_size(int64_t n, int64_t c)
+{
+    if (!valid_rows(n, c)) return 0;
+    return sizeof(float) * 2 * static_cast<size_t>(c) * static_cast<size_t>(layer_norm_parts(n, c));
+}
+
+sparse_status_t sparse_layer_norm(const void* x, sparse_dtype_t x_type, int64_t r, int64_t c, const int64_t* idx,
+                                  int64_t n, const float* gamma, const float* beta, double eps, void* y,
+                                  sparse_dtype_t y_type, float* mean, float* rstd, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_norm(x, x_type, r, c, idx, n, y_type, d_err) || !(eps >= 0.0) || !std::isfinite(eps))
+        return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (y == nullptr) return SPARSE_ERR_INVALID_ARG;
+    const int vec = c % lane_values(x_type, y_type) == 0 && aligned16(x) && aligned16(y);
+    return from_cuda(layer_norm(x, is_bf16(x_type), r, c, idx, n, gamma, beta, static_cast<float>(eps), y,
+                                is_bf16(y_type), vec, mean, rstd, d_err, stream));
+}
+
+sparse_status_t sparse_layer_norm_grad(const void* dy, sparse_dtype_t y_type, const void* x, sparse_dtype_t x_type,
+                                       int64_t r, int64_t c, const int64_t* idx, int64_t n, const float* gamma,
+                                       const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
+                                       void* ws, size_t ws_bytes, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_norm(x, x_type, r, c, idx, n, y_type, d_err)) return SPARSE_ERR_INVALID_ARG;
+    if (n > 0 && (dy == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr)) return SPARSE_ERR_INVALID_ARG;
+    if ((dgamma != nullptr || dbeta != nullptr) && n > 0 &&
+        !ws_ok(ws, ws_bytes, sparse_layer_norm_workspace_size(n, c)))
+        return SPARSE_ERR_WORKSPACE;
+    const int vec = c % lane_values(x_type, y_type) == 0 && aligned16(x) && aligned16(dy) && aligned16(dx);
+    return from_cuda(layer_norm_grad(dy, is_bf16(y_type), x, is_bf16(x_type), r, c, idx, n, gamma, mean, rstd, dx,
+                                     dgamma, dbeta, static_cast<float*>(ws), vec, d_err, stream));
+}
+
+size_t sparse_expert_workspace_size(int64_t n, int64_t k, int64_t experts)
+{
+    if (n < 0 || k < 1 || (n > 0 && k > INT32_MAX / n) || experts < 1 || experts > kMaxExperts) return 0;
+    return expert_ws_bytes(n * k, experts);
+}
+
+sparse_status_t sparse_expert_sort(const int64_t* expert, int64_t n, int64_t k, int64_t experts, int64_t* offsets,
+                                   int32_t* src, int32_t* pos, void* ws, size_t ws_bytes, int32_t* d_err,
+                                   cudaStream_t stream)
+{
+    if (!valid_expert(SPARSE_F32, n, k, 1, d_err) || experts < 1 || experts > kMaxExperts || offsets == nullptr)
+        return SPARSE_ERR_INVALID_ARG;
+    if (n > 0 && (expert == nullptr || pos == nullptr)) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0)
+        return from_cuda(cudaMemsetAsync(offsets, 0, sizeof(int64_t) * static_cast<size_t>(experts + 1), stream));
+    if (!ws_ok(ws, ws_bytes, sparse_expert_workspace_size(n, k, experts))) return SPARSE_ERR_WORKSPACE;
+    return from_cuda(expert_sort(expert, n * k, experts, offsets, src, pos, ws, d_err, stream));
+}
+
+sparse_status_t sparse_expert_dispatch(const void* x, sparse_dtype_t type, int64_t n, int64_t k, int64_t c,
+                                       const int32_t* pos, const int64_t* offsets, int64_t experts, void* xs,
+                                       int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_expert(type, n, k, c, d_err) || experts < 1 || experts > kMaxExperts) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (x == nullptr || pos == nullptr || offsets == nullptr || xs == nullptr) return SPARSE_ERR_INVALID_ARG;
+    const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(x) && aligned16(xs);
+    return from_cuda(expert_dispatch(x, is_bf16(type), n, k, c, pos, offsets + experts, xs, vec, d_err, stream));
+}
+
+sparse_status_t sparse_expert_combine(const void* ys, sparse_dtype_t type, int64_t n, int64_t k, int64_t c,
+                                      const int32_t* pos, const float* weights, void* y, int32_t* d_err,
+                                      cudaStream_t stream)
+{
+    if (!valid_expert(type, n, k, c, d_err)) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (ys == nullptr || pos == nullptr || y == nullptr) return SPARSE_ERR_INVALID_ARG;
+    const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(ys) && aligned16(y);
+    return from_cuda(expert_combine(ys, is_bf16(type), n, k, c, pos, weights, y, vec, d_err, stream));
+}
+
+sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, sparse_dtype_t type, int64_t n, int64_t k,
+                                           int64_t c, const int32_t* pos, const int64_t* offsets, int64_t experts,
+                                           const float* weights, void* dys, float* dweights, int32_t* d_err,
+                                           cudaStream_t stream)
+{
+    if (!valid_expert(type, n, k, c, d_err) || experts < 1 || experts > kMaxExperts) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (dy == nullptr || ys == nullptr || pos == nullptr || offsets == nullptr || dys == nullptr)
+        return SPARSE_ERR_INVALID_ARG;
+    const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(dy) && aligned16(ys) && aligned16(dys);
+    return from_cuda(expert_combine_grad(dy, ys, is_bf16(type), n, k, c, pos, offsets + experts, weights, dys,
+                                         dweights, vec, d_err, stream));
+}
+
+}  // extern "C"

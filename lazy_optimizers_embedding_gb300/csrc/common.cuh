@@ -355,4 +355,29 @@ cudaError_t coo_to_csr(const int64_t* lin, int64_t nnz, int64_t r, int64_t c, in
 cudaError_t row_coo_to_csr(const int64_t* rows, int64_t nrows, int64_t r, int64_t c,
                            int64_t* row_off_out, int32_t* cols_out, int32_t* d_err, cudaStream_t s);
 
+
+// ------------------------------------------------- operators around the step
+// Layer norm (layer_norm.cu); vec: 16-byte accesses (see the entry points).
+int64_t layer_norm_parts(int64_t n, int64_t c);
+cudaError_t layer_norm(const void* x, int x_bf16, int64_t r, int64_t c, const int64_t* idx, int64_t n,
+                       const float* gamma, const float* beta, float eps, void* y, int y_bf16, int vec, float* mean,
+                       float* rstd, int32_t* d_err, cudaStream_t s);
+cudaError_t layer_norm_grad(const void* dy, int y_bf16, const void* x, int x_bf16, int64_t r, int64_t c,
+                            const int64_t* idx, int64_t n, const float* gamma, const float* mean, const float* rstd,
+                            void* dx, float* dgamma, float* dbeta, float* part, int vec, int32_t* d_err,
+                            cudaStream_t s);
+
+// Tokens by expert (expert.cu).
+constexpr int64_t kMaxExperts = 1024;
+size_t expert_ws_bytes(int64_t slots, int64_t experts);
+cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, int64_t* offsets, int32_t* src,
+                        int32_t* pos, void* ws, int32_t* d_err, cudaStream_t s);
+cudaError_t expert_dispatch(const void* x, int is_bf16, int64_t n, int64_t k, int64_t c, const int32_t* pos,
+                            const int64_t* end, void* xs, int vec, int32_t* d_err, cudaStream_t s);
+cudaError_t expert_combine(const void* ys, int is_bf16, int64_t n, int64_t k, int64_t c, const int32_t* pos,
+                           const float* w, void* y, int vec, int32_t* d_err, cudaStream_t s);
+cudaError_t expert_combine_grad(const void* dy, const void* ys, int is_bf16, int64_t n, int64_t k, int64_t c,
+                                const int32_t* pos, const int64_t* end, const float* w, void* dys, float* dw, int vec,
+                                int32_t* d_err, cudaStream_t s);
+
 }  // namespace so

@@ -454,6 +454,55 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
                                            cudaStream_t stream);
 
 /*
+ * Newton-Schulz orthogonalisation.  With X of min(r, c) rows (the matrix or its
+ * transpose):  X = u / (|u|_F + eps), then `steps` times A = X X^T,
+ * B = b A + c A^2, X = a X + B X.  a, b, c = 3.4445, -4.7750, 2.0315 and 5 steps
+ * bring the singular values to 1 within about 0.3; other coefficients are
+ * accepted when X, A and B stay below 3.9 from every singular value in [0, 1].
+ * products: 3 computes each matrix product to 22 bits (fp32 accuracy, for fp32
+ * results); 1 to 11 bits (about 2e-3 of the result's norm, what rounding it to
+ * bf16 costs), in about 0.4 of the time.
+ */
+typedef struct {
+    double a, b, c, eps;
+    int32_t steps;      /* 1 to 64 */
+    int32_t products;   /* 1 or 3 */
+} sparse_ns_config_t;
+
+/* One Muon step: buf = momentum*buf + g; u = g + momentum*buf (nesterov) or buf;
+ * O = Newton-Schulz of u; w = (1 - lr*weight_decay)*w - lr*scale*O. */
+typedef struct {
+    double lr, momentum, weight_decay, scale;
+    int32_t nesterov;
+    sparse_ns_config_t ns;
+} sparse_muon_config_t;
+
+/* Bytes of workspace the two entry points below need for a batch of r x c
+ * matrices.  Limits: r, c <= 2^20, batch <= 2^24, batch*r*c <= 2^40. */
+size_t sparse_muon_workspace_size(int64_t batch, int64_t r, int64_t c, int products);
+
+/*
+ * sparse_orthogonalize -- out = Newton-Schulz of every r x c matrix of u.
+ *   u, out [batch, r, c]: fp32 or bf16 each.  An element that is NaN or infinite (or a
+ *   sum of squares beyond fp32) sets SPARSE_ERR_NON_FINITE.
+ *   ws: sparse_muon_workspace_size() bytes, 256-byte aligned.
+ */
+sparse_status_t sparse_orthogonalize(const void* u, sparse_dtype_t u_type, int64_t batch, int64_t r, int64_t c,
+                                     sparse_ns_config_t cfg, void* out, sparse_dtype_t out_type, void* ws,
+                                     size_t ws_bytes, int32_t* d_err, cudaStream_t stream);
+
+/*
+ * sparse_muon_step -- the Muon step of a batch of r x c matrices (the dense
+ * matrices beside the table: an expert's, a projection's), in place.
+ *   w, buf [batch, r, c] fp32 (buf starts at 0); g [batch, r, c] fp32 or bf16.
+ *   A u that is not finite (as above) sets SPARSE_ERR_NON_FINITE, and neither w nor
+ *   buf of any matrix is written; nor are they while *d_err is set.
+ */
+sparse_status_t sparse_muon_step(float* w, float* buf, const void* g, sparse_dtype_t g_type, int64_t batch, int64_t r,
+                                 int64_t c, sparse_muon_config_t cfg, void* ws, size_t ws_bytes, int32_t* d_err,
+                                 cudaStream_t stream);
+
+/*
  * Per-kernel timing (diagnostics; no counterpart on the pages).  While enabled,
  * every kernel the library enqueues is bracketed by two CUDA events on its
  * stream.  sparse_profile_read() waits for every recorded event, then reports

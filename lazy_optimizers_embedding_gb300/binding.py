@@ -49,6 +49,18 @@ class SgdConfig(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double)]
 
 
+class NsConfig(ctypes.Structure):
+    """sparse_ns_config_t: the Newton-Schulz polynomial, its steps and its accuracy (products 1 or 3)."""
+    _fields_ = [("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double), ("eps", ctypes.c_double),
+                ("steps", ctypes.c_int32), ("products", ctypes.c_int32)]
+
+
+class MuonConfig(ctypes.Structure):
+    """sparse_muon_config_t."""
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double), ("nesterov", ctypes.c_int32), ("ns", NsConfig)]
+
+
 class Grad(ctypes.Structure):
     """sparse_grad_t: a row-COO or CSR gradient (device arrays)."""
     _fields_ = [("form", ctypes.c_int), ("n", ctypes.c_int64), ("row_idx", ctypes.c_void_p),
@@ -92,6 +104,9 @@ def _load():
         "sparse_expert_dispatch": (INT, [P, INT, I64, I64, I64, P, P, I64, P, P, P]),
         "sparse_expert_combine": (INT, [P, INT, I64, I64, I64, P, P, P, P, P]),
         "sparse_expert_combine_grad": (INT, [P, P, INT, I64, I64, I64, P, P, I64, P, P, P, P, P]),
+        "sparse_muon_workspace_size": (SZ, [I64, I64, I64, INT]),
+        "sparse_orthogonalize": (INT, [P, INT, I64, I64, I64, NsConfig, P, INT, P, SZ, P, P]),
+        "sparse_muon_step": (INT, [P, P, P, INT, I64, I64, I64, MuonConfig, P, SZ, P, P]),
         "sparse_profile_enable": (None, [INT]),
         "sparse_profile_reset": (None, []),
         "sparse_profile_read": (INT, [INT, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_int64),
@@ -111,7 +126,7 @@ EXPORTED = ("sparse_workspace_size", "sparse_status_string", "sparse_canonicaliz
             "sparse_profile_reset", "sparse_profile_read", "sparse_read_rows", "sparse_check_finite",
             "sparse_check_state", "sparse_layer_norm_workspace_size", "sparse_layer_norm", "sparse_layer_norm_grad",
             "sparse_expert_workspace_size", "sparse_expert_sort", "sparse_expert_dispatch", "sparse_expert_combine",
-            "sparse_expert_combine_grad")
+            "sparse_expert_combine_grad", "sparse_muon_workspace_size", "sparse_orthogonalize", "sparse_muon_step")
 STATIC_WS_BYTES = 16 * 1024 * 1024  # SPARSE_STATIC_WS_BYTES
 
 
@@ -365,6 +380,25 @@ def sparse_expert_combine_grad(dy, ys, n, k, c, pos, offsets, experts, weights, 
                                           int(experts), _ptr(weights, torch.float32, "weights"),
                                           _typed(dys, "dys", ys)[0], _ptr(dweights, torch.float32, "dweights"),
                                           _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_muon_workspace_size(batch: int, r: int, c: int, products: int) -> int:
+    return int(LIB.sparse_muon_workspace_size(int(batch), int(r), int(c), int(products)))
+
+
+def sparse_orthogonalize(u, batch, r, c, cfg: NsConfig, out, ws, d_err, stream=None) -> int:
+    wp, wb = _ws(ws)
+    up, ut = _typed(u, "u")
+    op, ot = _typed(out, "out")
+    return LIB.sparse_orthogonalize(up, ut, int(batch), int(r), int(c), cfg, op, ot, wp, wb,
+                                    _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_muon_step(w, buf, g, batch, r, c, cfg: MuonConfig, ws, d_err, stream=None) -> int:
+    wp, wb = _ws(ws)
+    gp, gt = _typed(g, "g")
+    return LIB.sparse_muon_step(_ptr(w, torch.float32, "w"), _ptr(buf, torch.float32, "buf"), gp, gt, int(batch),
+                                int(r), int(c), cfg, wp, wb, _ptr(d_err, torch.int32, "d_err"), _stream(stream))
 
 
 # ------------------------------------------------------------------ diagnostics

@@ -47,6 +47,51 @@ bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const in
            d_err != nullptr;
 }
 
+// Newton-Schulz keeps X, A = X X^T and B = b A + c A^2 as f16 values times 2^14: their
+// singular values, followed here over [0, 1] (all that a matrix of Frobenius norm at
+// most 1 can have), have to stay below 65504 / 2^14 with 2 % to spare.
+constexpr double kMaxNs = 3.9;
+
+bool valid_ns(const sparse_ns_config_t& c)
+{
+    if (!std::isfinite(c.a) || !std::isfinite(c.b) || !std::isfinite(c.c) || !(c.eps >= 0.0) || !std::isfinite(c.eps) ||
+        c.steps < 1 || c.steps > 64 || (c.products != 1 && c.products != 3))
+        return false;
+    constexpr int kPoints = 2048;
+    for (int i = 0; i <= kPoints; ++i) {
+        double x = static_cast<double>(i) / kPoints;
+        for (int s = 0; s < c.steps; ++s) {
+            const double l = x * x, p = c.b * l + c.c * l * l;
+            x = c.a * x + p * x;
+            if (!(std::fabs(l) <= kMaxNs && std::fabs(p) <= kMaxNs && std::fabs(x) <= kMaxNs)) return false;
+        }
+    }
+    return true;
+}
+
+// A batch of r x c matrices whose sizes the tensor copies can address.
+bool valid_batch(int64_t batch, int64_t r, int64_t c)
+{
+    return batch >= 0 && batch <= (1 << 24) && r >= 1 && c >= 1 && r <= (1 << 20) && c <= (1 << 20) &&
+           (batch == 0 || r * c <= (int64_t(1) << 40) / batch);
+}
+
+so::MuonParams muon_params(int64_t batch, int64_t r, int64_t c, const sparse_ns_config_t& ns, int32_t* d_err)
+{
+    so::MuonParams M{};
+    M.batch = batch;
+    M.r = r;
+    M.cols = c;
+    M.a = static_cast<float>(ns.a);
+    M.b = static_cast<float>(ns.b);
+    M.c = static_cast<float>(ns.c);
+    M.eps = static_cast<float>(ns.eps);
+    M.steps = ns.steps;
+    M.products = ns.products;
+    M.d_err = d_err;
+    return M;
+}
+
 }  // namespace
 
 extern "C" {
@@ -138,6 +183,52 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
     const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(dy) && aligned16(ys) && aligned16(dys);
     return from_cuda(expert_combine_grad(dy, ys, is_bf16(type), n, k, c, pos, offsets + experts, weights, dys,
                                          dweights, vec, d_err, stream));
+}
+
+size_t sparse_muon_workspace_size(int64_t batch, int64_t r, int64_t c, int products)
+{
+    if (!valid_batch(batch, r, c) || (products != 1 && products != 3)) return 0;
+    return batch > 0 ? muon_ws_bytes(batch, r, c, products) : 0;
+}
+
+sparse_status_t sparse_orthogonalize(const void* u, sparse_dtype_t u_type, int64_t batch, int64_t r, int64_t c,
+                                     sparse_ns_config_t cfg, void* out, sparse_dtype_t out_type, void* ws,
+                                     size_t ws_bytes, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_type(u_type) || !valid_type(out_type) || !valid_batch(batch, r, c) || !valid_ns(cfg) || d_err == nullptr)
+        return SPARSE_ERR_INVALID_ARG;
+    if (batch == 0) return SPARSE_OK;
+    if (u == nullptr || out == nullptr) return SPARSE_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, muon_ws_bytes(batch, r, c, cfg.products))) return SPARSE_ERR_WORKSPACE;
+    MuonParams M = muon_params(batch, r, c, cfg, d_err);
+    M.g = u;
+    M.g_bf16 = is_bf16(u_type);
+    M.out = out;
+    M.out_bf16 = is_bf16(out_type);
+    return from_cuda(muon(M, ws, stream));
+}
+
+sparse_status_t sparse_muon_step(float* w, float* buf, const void* g, sparse_dtype_t g_type, int64_t batch, int64_t r,
+                                 int64_t c, sparse_muon_config_t cfg, void* ws, size_t ws_bytes, int32_t* d_err,
+                                 cudaStream_t stream)
+{
+    if (!valid_type(g_type) || !valid_batch(batch, r, c) || !valid_ns(cfg.ns) || d_err == nullptr ||
+        !std::isfinite(cfg.lr) || !std::isfinite(cfg.scale) || !std::isfinite(cfg.momentum) || cfg.momentum < 0.0 ||
+        !std::isfinite(cfg.weight_decay) || cfg.weight_decay < 0.0)
+        return SPARSE_ERR_INVALID_ARG;
+    if (batch == 0) return SPARSE_OK;
+    if (w == nullptr || buf == nullptr || g == nullptr) return SPARSE_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, muon_ws_bytes(batch, r, c, cfg.ns.products))) return SPARSE_ERR_WORKSPACE;
+    MuonParams M = muon_params(batch, r, c, cfg.ns, d_err);
+    M.g = g;
+    M.g_bf16 = is_bf16(g_type);
+    M.buf = buf;
+    M.momentum = static_cast<float>(cfg.momentum);
+    M.nesterov = cfg.nesterov != 0;
+    M.w = w;
+    M.decay = static_cast<float>(1.0 - cfg.lr * cfg.weight_decay);
+    M.lr = static_cast<float>(cfg.lr * cfg.scale);
+    return from_cuda(muon(M, ws, stream));
 }
 
 }  // extern "C"

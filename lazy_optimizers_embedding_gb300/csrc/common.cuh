@@ -380,4 +380,23 @@ cudaError_t expert_combine_grad(const void* dy, const void* ys, int is_bf16, int
                                 const int32_t* pos, const int64_t* end, const float* w, void* dys, float* dw, int vec,
                                 int32_t* d_err, cudaStream_t s);
 
+// Newton-Schulz orthogonalisation and the Muon step (muon.cu).
+struct MuonParams {
+    const void* g;        // the update itself (buf = nullptr) or the gradient
+    int g_bf16;
+    float* buf;           // momentum buffer
+    float momentum;
+    int nesterov;
+    int64_t batch, r, cols;
+    float a, b, c, eps;
+    int steps, products;
+    void* out;            // the orthogonal update, or
+    int out_bf16;
+    float* w;             // the weights it is applied to: w = decay w - lr O
+    float decay, lr;
+    int32_t* d_err;
+};
+size_t muon_ws_bytes(int64_t batch, int64_t r, int64_t c, int products);
+cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s);
+
 }  // namespace so

@@ -35,12 +35,14 @@ namespace {
 
 constexpr float kScale = 16384.0f;              // 2^14
 constexpr float kInvScale = 1.0f / 16384.0f;
-constexpr int kBM = 128, kBK = 64;              // tile rows; K values of a stage (128 bytes)
+constexpr int kBM = 128, kBK = 64;              // rows of a block's tile; K values of a stage (128 bytes)
 constexpr int kBox = 64;                        // rows of one copied box: 64 x 128 bytes
 constexpr uint32_t kBoxBytes = kBox * kBK * 2;
+constexpr int kSub = 64;                        // columns the epilogue finishes at a time
 constexpr int kThreads = 192;                   // copy warp, product warp, 4 epilogue warps
+constexpr int kEpilogue = 128;
 constexpr int kMuonBlock = 256;
-constexpr int kNormParts = 64;                  // partial sums of squares of a matrix at most
+constexpr int64_t kNormParts = 512;             // partial sums of squares of a matrix at most
 
 // ------------------------------------------------------------------- start
 // u of one call: given, or the momentum's.
@@ -52,34 +54,60 @@ struct Update {
     int nesterov;
 };
 
-__device__ __forceinline__ float read_g(const Update& U, int64_t i)
+// Four values of u from element i on (those below `left`), and the new buffer's.
+template <bool kVec>
+__device__ __forceinline__ void read_u4(const Update& U, int64_t i, int left, float (&u)[4], float (&nb)[4])
 {
-    return U.g_bf16 ? __bfloat162float(static_cast<const bf16*>(U.g)[i]) : static_cast<const float*>(U.g)[i];
-}
-__device__ __forceinline__ float read_u(const Update& U, int64_t i, float& nb)
-{
-    const float g = read_g(U, i);
-    if (U.buf == nullptr) return g;
-    nb = fmaf(U.momentum, U.buf[i], g);
-    return U.nesterov ? fmaf(U.momentum, nb, g) : nb;
+    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (kVec) {
+        if (left > 0) {
+            if (U.g_bf16) {
+                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(U.g) + i);
+                g[0] = __uint_as_float(q.x << 16), g[1] = __uint_as_float(q.x & 0xffff0000u);
+                g[2] = __uint_as_float(q.y << 16), g[3] = __uint_as_float(q.y & 0xffff0000u);
+            } else {
+                Pack<float, 4> q;
+                q.load(static_cast<const float*>(U.g) + i);
+                q.get(g);
+            }
+            if (U.buf) {
+                Pack<float, 4> q;
+                q.load(U.buf + i);
+                q.get(b);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) {
+                g[e] = U.g_bf16 ? __bfloat162float(static_cast<const bf16*>(U.g)[i + e]) : static_cast<const float*>(U.g)[i + e];
+                if (U.buf) b[e] = U.buf[i + e];
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        nb[e] = fmaf(U.momentum, b[e], g[e]);
+        u[e] = U.buf == nullptr ? g[e] : U.nesterov ? fmaf(U.momentum, nb[e], g[e]) : nb[e];
+    }
 }
 
 // Sums of squares of one matrix's pieces; a sum that is not finite is reported
 // before anything is written.
-__global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int parts, float* __restrict__ part,
-                                                          int32_t* d_err)
+template <bool kVec>
+__global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int64_t parts,
+                                                          float* __restrict__ part, int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and the error word only
     __shared__ float tmp[2 * 32];
-    const int64_t mat = blockIdx.x / parts;
-    const int p = static_cast<int>(blockIdx.x % parts);
+    const int64_t mat = blockIdx.x / parts, p = blockIdx.x % parts;
     const int64_t base = mat * size;
-    float s[1] = {0.0f}, nb;
+    float s[1] = {0.0f};
 #pragma unroll 4
-    for (int64_t i = static_cast<int64_t>(p) * kMuonBlock + threadIdx.x; i < size;
-         i += static_cast<int64_t>(parts) * kMuonBlock) {
-        const float u = read_u(U, base + i, nb);
-        s[0] = fmaf(u, u, s[0]);
+    for (int64_t i = (p * kMuonBlock + threadIdx.x) * 4; i < size; i += parts * kMuonBlock * 4) {
+        float u[4], nb[4];
+        read_u4<kVec>(U, base + i, static_cast<int>(min(size - i, static_cast<int64_t>(4))), u, nb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[0] = fmaf(u[e], u[e], s[0]);
     }
     group_sum<1>(s, kMuonBlock, tmp, 0);
     if (threadIdx.x == 0) {
@@ -88,62 +116,95 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
     }
 }
 
-__device__ __forceinline__ void split_store(__half* hi, __half* lo, int64_t at, float v)
+// v as hi + lo f16, four at a time.
+__device__ __forceinline__ void split4(__half* hi, __half* lo, const float (&v)[4])
 {
-    const __half h = __float2half_rn(v);
-    hi[at] = h;
-    if (lo) lo[at] = __float2half_rn(v - __half2float(h));
+    __half2 h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        const float2 f = __half22float2(h[i]);
+        l[i] = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    }
+    *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<const uint2*>(h);
+    if (lo) *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(l);
 }
 
 // X = u / (|u| + eps), scaled and split, transposed where u is tall; the new momentum
-// buffer.  One 32 x 32 tile of u at a time.
+// buffer.  One 64 x 64 tile of u at a time, four values a thread.
+template <bool kVec>
 __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __restrict__ buf, int64_t r, int64_t c,
                                                            int64_t tiles_c, int64_t tiles, int64_t ntiles,
-                                                           const float* __restrict__ part, int parts, float eps,
+                                                           const float* __restrict__ part, int64_t parts, float eps,
                                                            __half* __restrict__ hi, __half* __restrict__ lo,
                                                            int64_t ldn, int tall, const int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and optimizer state only
-    __shared__ float tile[32][33];
-    __shared__ float s_scale;
+    __shared__ float tile[64][65];
+    __shared__ double sums[kMuonBlock / 32];
     if (buf != nullptr && read_error(d_err) != 0) return;   // set before this kernel: the same for every block
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t m = tall ? c : r;
     int64_t have = -1;
+    float scale = 0.0f;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
         const int64_t mat = t / tiles, q = t % tiles;
-        const int64_t r0 = q / tiles_c * 32, c0 = q % tiles_c * 32;
+        const int64_t r0 = q / tiles_c * 64, c0 = q % tiles_c * 64;
         if (mat != have) {
+            double s = 0.0;
+            for (int64_t i = threadIdx.x; i < parts; i += kMuonBlock) s += part[mat * parts + i];
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
             __syncthreads();
-            if (ty == 0) {
-                double s = 0.0;
-                for (int i = tx; i < parts; i += 32) s += part[mat * parts + i];
-                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-                if (tx == 0) s_scale = static_cast<float>(static_cast<double>(kScale) / (sqrt(s) + static_cast<double>(eps)));
-            }
+            if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
             __syncthreads();
+            s = sums[0];
+            for (int w = 1; w < kMuonBlock / 32; ++w) s += sums[w];
+            scale = static_cast<float>(static_cast<double>(kScale) / (sqrt(s) + static_cast<double>(eps)));
             have = mat;
         }
-        const float scale = s_scale;
+        float u[4][4];
 #pragma unroll
-        for (int y = ty; y < 32; y += 8) {
-            const int64_t row = r0 + y, col = c0 + tx;
-            float v = 0.0f;
-            if (row < r && col < c) {
-                const int64_t i = (mat * r + row) * c + col;
-                float nb = 0.0f;
-                v = read_u(U, i, nb) * scale;
-                if (buf) buf[i] = nb;
-                if (!tall) split_store(hi, lo, (mat * m + row) * ldn + col, v);
+        for (int y = 0; y < 4; ++y) {
+            const int64_t row = r0 + ty + 16 * y, col = c0 + 4 * tx;
+            const int64_t i = (mat * r + row) * c + col;
+            const int left = row < r ? static_cast<int>(max(min(c - col, static_cast<int64_t>(4)), static_cast<int64_t>(0))) : 0;
+            float nb[4];
+            read_u4<kVec>(U, i, left, u[y], nb);
+            if (buf) {
+                if (kVec) {
+                    if (left > 0) Pack<float, 4>::put(buf + i, nb);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) buf[i + e] = nb[e];
+                }
             }
-            if (tall) tile[y][tx] = v;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int64_t row = r0 + ty + 16 * y, col = c0 + 4 * tx;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[y][e] *= scale;
+            if (tall) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tile[ty + 16 * y][4 * tx + e] = u[y][e];
+            } else if (row < r && col < c) {   // rows of X are padded to a multiple of 8 values
+                const int64_t at = (mat * m + row) * ldn + col;
+                split4(hi + at, lo ? lo + at : nullptr, u[y]);
+            }
         }
         if (tall) {
             __syncthreads();
 #pragma unroll
-            for (int y = ty; y < 32; y += 8) {
-                const int64_t row = c0 + y, col = r0 + tx;
-                if (row < c && col < r) split_store(hi, lo, (mat * m + row) * ldn + col, tile[tx][y]);
+            for (int y = 0; y < 4; ++y) {
+                const int64_t row = c0 + ty + 16 * y, col = r0 + 4 * tx;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = tile[4 * tx + e][ty + 16 * y];
+                if (row < c && col < r) {
+                    const int64_t at = (mat * m + row) * ldn + col;
+                    split4(hi + at, lo ? lo + at : nullptr, v);
+                }
             }
             __syncthreads();
         }
@@ -153,61 +214,71 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __re
 // ---------------------------------------------------------------- products
 enum Kind { kGram, kPoly, kUpdate, kFinal };
 
+struct Maps {
+    CUtensorMap ahi, alo, bhi, blo;   // operands
+    CUtensorMap rhi, rlo;             // added term
+    CUtensorMap whi, wlo;             // result
+};
+
 struct Product {
     int64_t m, n, k;        // result m x n, inner dimension k
-    int64_t ld;             // of result and added term
     int64_t tiles;          // of one matrix
     int64_t all;            // of the batch
     int cols_of_tiles;      // tiles of a row of tiles (not the symmetric kinds)
     float add, mul;         // result = add * term + mul * product
-    const __half *rhi, *rlo;    // term (rlo may be nullptr)
-    __half *whi, *wlo;          // result (wlo may be nullptr)
+    int rlo, wlo;           // the term has, the result gets, a lo part
     // kFinal: the update applied or stored, r x c (transposed where tall)
     void* out;
     float* w;
-    int out_bf16, tall, vec;
+    int out_bf16, tall;
     float decay, lr;
     int32_t* d_err;
 };
 
-struct Maps {
-    CUtensorMap ahi, alo, bhi, blo;
-};
-
-template <int BN, int P>
+// kPair blocks (a cluster) share a tile of 128 kPair rows x BN columns.
+template <int kKind, int kPair, int BN, int P>
 struct Shape {
-    static constexpr uint32_t kA = kBM / kBox * kBoxBytes;        // one f16 part of A in a stage
-    static constexpr uint32_t kB = BN / kBox * kBoxBytes;
+    static constexpr bool kSym = kKind == kGram || kKind == kPoly;
+    static constexpr uint32_t kA = kBM / kBox * kBoxBytes;                 // one f16 part of A in a stage
+    static constexpr uint32_t kB = BN / kPair / kBox * kBoxBytes;
     static constexpr int kParts = P == 3 ? 2 : 1;
     static constexpr uint32_t kStage = kParts * (kA + kB);
-    static constexpr int kStages = (200 * 1024) / kStage;
-    static constexpr uint32_t kSmem = kStages * kStage + 1024;    // + alignment
-    static constexpr int kAccs = P == 3 ? 512 / BN : 2;           // accumulators in tensor memory
+    // Epilogue: kSub columns of the tile, hi and lo (128 x 64 each); mirror images of the symmetric
+    // kinds; the fp32 update of kFinal.
+    static constexpr uint32_t kSubBytes = kBM / kBox * kBoxBytes;
+    static constexpr int kSets = kKind == kFinal || (kSym && P == 3) ? 1 : 2;   // sets of them: one is copied while one is worked on
+    static constexpr uint32_t kSet = kSubBytes * (kKind == kFinal ? 4 : kSym ? 2 * kParts : 2);
+    static constexpr int kStages = static_cast<int>((224 * 1024 - kSets * kSet) / kStage);
+    static constexpr uint32_t kSmem = kStages * kStage + kSets * kSet + 1024;   // + alignment
+    static constexpr int kAccs = P == 3 ? 512 / BN : 2;                    // accumulators in tensor memory
     // Stages that one accumulator sums.  The unit rounds every sum towards zero: with three products
     // the 940 sums of K = 5000 were off by 6e-5 of the result, so every 24 sums (128 K values, a
     // drift below 1e-6) the epilogue adds the accumulator to its own fp32 sums, which round to nearest.
     // Against f16 operands alone (one product) the drift does not count.
     static constexpr int kChunk = P == 3 ? 2 : INT32_MAX;
+    static_assert(BN / kPair % kBox == 0 && kStages >= 2 && kAccs * BN <= 512, "shape");
 };
 
-// Tile t of a matrix.  Symmetric results need the tiles that reach the diagonal or
-// lie below it: row of tiles i has (128 i + 127) / BN + 1 of them.
-template <int BN, bool kSym>
-__device__ __forceinline__ void tile_at(const Product& Q, int64_t t, int64_t& mat, int64_t& row0, int64_t& col0)
+// Tile t of a matrix: its first row (of the pair's) and column.  Symmetric results need
+// the tiles that reach the diagonal or lie below it: row of tiles i of TM rows has
+// (TM i + TM - 1) / BN + 1 of them.
+template <int TM, int BN, bool kSym>
+__device__ __forceinline__ void tile_at(const Product& Q, int64_t t, int& mat, int& row0, int& col0)
 {
-    mat = t / Q.tiles;
-    int64_t q = t - mat * Q.tiles;
+    const int64_t z = t / Q.tiles;
+    int q = static_cast<int>(t - z * Q.tiles);
+    mat = static_cast<int>(z);
     if (kSym) {
-        int64_t i = 0;
+        int i = 0;
         for (;; ++i) {
-            const int64_t w = (i * kBM + kBM - 1) / BN + 1;
+            const int w = (i * TM + TM - 1) / BN + 1;
             if (q < w) break;
             q -= w;
         }
-        row0 = i * kBM;
+        row0 = i * TM;
         col0 = q * BN;
     } else {
-        row0 = q / Q.cols_of_tiles * kBM;
+        row0 = q / Q.cols_of_tiles * TM;
         col0 = q % Q.cols_of_tiles * BN;
     }
 }
@@ -223,111 +294,112 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8])
     }
 }
 
-// Eight consecutive results of one row.
-template <int kKind>
-__device__ __forceinline__ void finish8(const Product& Q, int64_t mat, int64_t row, int64_t col, const float* acc)
+// 32 columns of a warp's rows of the update from shared memory (`stage`: the warp's 32 rows of
+// 64 fp32 values, 16-byte pieces permuted by row) to where they belong, row by row.
+__device__ __forceinline__ void put_rows(const Product& Q, uint32_t stage, int64_t mat, int row0, int col0, int lane)
 {
-    constexpr bool kSym = kKind == kGram || kKind == kPoly;
-    if (row >= Q.m || col >= Q.n || (kSym && col > row)) return;
-    const int64_t at = (mat * Q.m + row) * Q.ld + col;   // ld and col are multiples of 8: 16-byte aligned, within the row
-    float v[8];
+    const int rows = min(32, static_cast<int>(Q.m) - row0);
+    const int64_t c = Q.n;
+    const int64_t at = (mat * Q.m + row0) * c + col0;
+    bool in[2];
+    in[0] = col0 + lane < c;
+    in[1] = col0 + 32 + lane < c;
+    for (int r0 = 0; r0 < rows; r0 += 4) {
+        float v[4][2], w[4][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = Q.mul * acc[e];
-    if (kKind != kGram) {
-        float x[8];
-        unpack8(*reinterpret_cast<const uint4*>(Q.rhi + at), x);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(Q.add, x[e], v[e]);
-        if (Q.rlo) {
-            unpack8(*reinterpret_cast<const uint4*>(Q.rlo + at), x);
+            for (int h = 0; h < 2; ++h) {
+                const int r = r0 + i, col = lane + 32 * h;
+                v[i][h] = lds32(stage + r * 256 + (((col >> 2) ^ (r & 7)) << 4) + (col & 3) * 4);
+                w[i][h] = Q.w && in[h] && r < rows ? Q.w[at + r * c + col] : 0.0f;
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(Q.add, x[e], v[e]);
-        }
-    }
-    if (kKind == kFinal) {
-        const int64_t r = Q.tall ? Q.n : Q.m, c = Q.tall ? Q.m : Q.n;
-        for (int e = 0; e < 8; ++e) {
-            if (col + e >= Q.n) break;
-            const int64_t o = mat * r * c + (Q.tall ? (col + e) * c + row : row * c + col + e);
-            const float x = v[e] * kInvScale;
-            if (Q.w)
-                Q.w[o] = fmaf(Q.decay, Q.w[o], -Q.lr * x);
-            else if (Q.out_bf16)
-                static_cast<bf16*>(Q.out)[o] = __float2bfloat16_rn(x);
-            else
-                static_cast<float*>(Q.out)[o] = x;
-        }
-        return;
-    }
-    uint4 hi, lo;
-    __half* h = reinterpret_cast<__half*>(&hi);
-    __half* l = reinterpret_cast<__half*>(&lo);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        h[e] = __float2half_rn(v[e]);
-        l[e] = __float2half_rn(v[e] - __half2float(h[e]));
-    }
-    if (!kSym) {
-        *reinterpret_cast<uint4*>(Q.whi + at) = hi;
-        if (Q.wlo) *reinterpret_cast<uint4*>(Q.wlo + at) = lo;
-        return;
-    }
-    // the element and its mirror image; across the diagonal nothing (its mirror image is written)
-    if (col + 8 <= row + 1 && col + 8 <= Q.n) {
-        *reinterpret_cast<uint4*>(Q.whi + at) = hi;
-        if (Q.wlo) *reinterpret_cast<uint4*>(Q.wlo + at) = lo;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (col + e <= row) {
-                Q.whi[at + e] = h[e];
-                if (Q.wlo) Q.wlo[at + e] = l[e];
+            for (int h = 0; h < 2; ++h) {
+                const int r = r0 + i;
+                if (!in[h] || r >= rows) continue;
+                const int64_t o = at + r * c + lane + 32 * h;
+                if (Q.w)
+                    Q.w[o] = fmaf(Q.decay, w[i][h], -Q.lr * v[i][h]);
+                else if (Q.out_bf16)
+                    static_cast<bf16*>(Q.out)[o] = __float2bfloat16_rn(v[i][h]);
+                else
+                    static_cast<float*>(Q.out)[o] = v[i][h];
             }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (col + e < row) {
-            const int64_t mt = (mat * Q.m + col + e) * Q.ld + row;
-            Q.whi[mt] = h[e];
-            if (Q.wlo) Q.wlo[mt] = l[e];
-        }
 }
 
-// One block an SM, tiles of 128 x BN in turn: warp 0 copies A and B boxes of 64 K
-// values into a ring of stages, warp 1 issues the products into one of two
-// accumulators, warps 2 to 5 finish the other.  A is K-major; B is K-major too
-// (rows of the symmetric factor) or, for B X, MN-major (X as it lies).
-template <int kKind, int BN, int P>
+// Eight columns of the transposed update: a lane's row of X is a column there, so a warp
+// writes 32 neighbours.
+__device__ __forceinline__ void put_columns(const Product& Q, int64_t mat, int row, int col, const float (&v)[8])
+{
+    if (row >= Q.m) return;
+    const int64_t at = (mat * Q.n + col) * Q.m + row;
+    const int left = static_cast<int>(min(Q.n - col, static_cast<int64_t>(8)));
+    float w[8];
+    if (Q.w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = e < left ? Q.w[at + e * Q.m] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (e >= left) continue;
+        const int64_t o = at + e * Q.m;
+        if (Q.w)
+            Q.w[o] = fmaf(Q.decay, w[e], -Q.lr * v[e]);
+        else if (Q.out_bf16)
+            static_cast<bf16*>(Q.out)[o] = __float2bfloat16_rn(v[e]);
+        else
+            static_cast<float*>(Q.out)[o] = v[e];
+    }
+}
+
+// One block an SM (or one pair of blocks on two), tiles in turn: warp 0 copies A and B
+// boxes of 64 K values into a ring of stages, warp 1 (of the pair's first block) issues
+// the products into one of the accumulators, warps 2 to 5 finish another, 64 columns at a
+// time: the added term arrives in shared memory by tensor copies, the result replaces it
+// there and leaves the same way, so every access of the matrices is whole lines.  A is
+// K-major; B is K-major too (rows of the symmetric factor) or, for B X, MN-major (X as it
+// lies).  In shared memory every box has 64 rows of 128 bytes, 16-byte pieces permuted
+// by row (the copies' 128-byte swizzle).
+template <int kKind, int kPair, int BN, int P>
 __global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_constant__ Maps maps, const Product Q)
 {
-    using S = Shape<BN, P>;
-    constexpr bool kSym = kKind == kGram || kKind == kPoly;
-    constexpr bool kBmn = !kSym;
-    constexpr int kStages = S::kStages;
+    using S = Shape<kKind, kPair, BN, P>;
+    constexpr bool kSym = S::kSym, kBmn = !S::kSym, kTerm = kKind != kGram;
+    constexpr int kStages = S::kStages, TM = kBM * kPair;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * kStages + 2 * S::kAccs + 1];
+    __shared__ uint64_t bars[2 * kStages + 2 * S::kAccs + 1 + 2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     const uint32_t data = (smem_addr(raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 8 * S::kAccs,
-                   drain = tempty + 8 * S::kAccs;
+    const uint32_t sets = data + kStages * S::kStage;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages,
+                   tempty = tfull + 8 * S::kAccs, drain = tempty + 8 * S::kAccs, term = drain + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = kPair == 2 ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t first = blockIdx.x / kPair, step = gridDim.x / kPair;
 
     if (threadIdx.x == 0) {
         dead = 0;
         for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
-        for (int s = 0; s < S::kAccs; ++s) mbar_init(tfull + 8 * s, 1), mbar_init(tempty + 8 * s, 128);
+        for (int s = 0; s < S::kAccs; ++s) mbar_init(tfull + 8 * s, 1), mbar_init(tempty + 8 * s, 4 * kPair);
         mbar_init(drain, 1);
+        for (int s = 0; s < 2; ++s) mbar_init(term + 8 * s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc(&tmem_slot, S::kAccs * BN);
+    if (warp == 1) tmem_alloc<kPair>(&tmem_slot, S::kAccs * BN);
     tc_fence_before();
-    __syncthreads();
+    if (kPair == 2)
+        cluster_sync();
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();
     if (kKind != kFinal) pdl_release();   // workspace only; after this block's allocation, so that no later block can hold what it waits for
-    fence_async_proxy();                  // the kernels before wrote with ordinary stores
+    fence_async_proxy();                  // the first kernels wrote with ordinary stores
 
     const int chunks = static_cast<int>((Q.k + kBK - 1) / kBK);
     if (warp == 0) {
@@ -335,47 +407,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_const
             tma_prefetch(&maps.ahi);
             tma_prefetch(&maps.bhi);
             uint32_t it = 0;
-            for (int64_t t = blockIdx.x; t < Q.all; t += gridDim.x) {
-                int64_t mat, row0, col0;
-                tile_at<BN, kSym>(Q, t, mat, row0, col0);
-                const int z = static_cast<int>(mat), y = static_cast<int>(row0), x = static_cast<int>(col0);
+            for (int64_t t = first; t < Q.all; t += step) {
+                int mat, row0, col0;
+                tile_at<TM, BN, kSym>(Q, t, mat, row0, col0);
+                row0 += rank * kBM;
+                col0 += rank * (BN / kPair);
                 for (int c = 0; c < chunks; ++c, ++it) {
                     const uint32_t s = it % kStages;
                     if (!mbar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, &dead)) goto copied;
-                    const uint32_t bar = full + 8 * s;
+                    const uint32_t bar = kPair == 2 ? cluster_addr(full + 8 * s, 0) : full + 8 * s;
                     uint32_t at = data + s * S::kStage;
-                    mbar_expect(bar, S::kStage);
+                    if (rank == 0) mbar_expect(full + 8 * s, kPair * S::kStage);
 #pragma unroll
                     for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
                         for (int q = 0; q < kBM / kBox; ++q, at += kBoxBytes)
-                            tma_load(at, p ? &maps.alo : &maps.ahi, bar, c * kBK, y + q * kBox, z);
+                            tma_load<kPair>(at, p ? &maps.alo : &maps.ahi, bar, c * kBK, row0 + q * kBox, mat);
 #pragma unroll
                     for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
-                        for (int q = 0; q < BN / kBox; ++q, at += kBoxBytes) {
+                        for (int q = 0; q < BN / kPair / kBox; ++q, at += kBoxBytes) {
                             if (kBmn)
-                                tma_load(at, p ? &maps.blo : &maps.bhi, bar, x + q * kBox, c * kBK, z);
+                                tma_load<kPair>(at, p ? &maps.blo : &maps.bhi, bar, col0 + q * kBox, c * kBK, mat);
                             else
-                                tma_load(at, p ? &maps.blo : &maps.bhi, bar, c * kBK, x + q * kBox, z);
+                                tma_load<kPair>(at, p ? &maps.blo : &maps.bhi, bar, c * kBK, col0 + q * kBox, mat);
                         }
                 }
             }
         copied:
-            if (dead) {   // copies in flight land before the block leaves
+            if (dead && rank == 0) {   // copies in flight land before the blocks leave
                 volatile int none = 0;
                 for (uint32_t s = 0; s < static_cast<uint32_t>(kStages) && s < it; ++s) {
                     const uint32_t last = (it - 1 - s) / kStages * kStages + s;   // the stage's last use
-                    if (last < it) mbar_wait(full + 8 * s, last / kStages & 1, &none);
+                    mbar_wait(full + 8 * s, last / kStages & 1, &none);
                 }
             }
         }
     } else if (warp == 1) {
-        if (elect_one()) {
-            constexpr uint32_t idesc = mma_desc_f16(kBM, BN, kBmn);
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = mma_desc_f16(TM, BN, kBmn);
             uint32_t it = 0, done = 0;   // stages, accumulators used
             bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < Q.all; t += gridDim.x)
+            for (int64_t t = first; ok && t < Q.all; t += step)
                 for (int c = 0; ok && c < chunks; ++done) {
                     const uint32_t acc = done % S::kAccs;
                     if (!(ok = mbar_wait(tempty + 8 * acc, (done / S::kAccs & 1) ^ 1, &dead))) break;
@@ -392,72 +465,200 @@ __global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_const
                             const uint32_t ak = k * 32, bk = kBmn ? k * 2048 : k * 32;
                             const uint32_t lead = kBmn ? kBoxBytes : 16;
                             const uint64_t ah = smem_desc(a + ak, 16, 1024), bh = smem_desc(b + bk, lead, 1024);
-                            tc_mma_f16(d, ah, bh, idesc, part + k > 0);
+                            tc_mma_f16<kPair>(d, ah, bh, idesc, part + k > 0);
                             if (P == 3) {
                                 const uint64_t al = smem_desc(a + S::kA + ak, 16, 1024);
                                 const uint64_t bl = smem_desc(b + S::kB + bk, lead, 1024);
-                                tc_mma_f16(d, ah, bl, idesc, true);
-                                tc_mma_f16(d, al, bh, idesc, true);
+                                tc_mma_f16<kPair>(d, ah, bl, idesc, true);
+                                tc_mma_f16<kPair>(d, al, bh, idesc, true);
                             }
                         }
-                        tc_commit(empty + 8 * s);
+                        tc_commit<kPair>(empty + 8 * s);
                     }
-                    if (ok) tc_commit(tfull + 8 * acc);
+                    if (ok) tc_commit<kPair>(tfull + 8 * acc);
                 }
-            if (dead) {   // products in flight finish before the block leaves
+            if (dead) {   // products in flight finish before the blocks leave
                 volatile int none = 0;
-                tc_commit(drain);
+                tc_commit<kPair>(drain);
                 mbar_wait(drain, 0, &none);
             }
         }
     } else {
-        const int quarter = warp & 3;   // the tensor memory lanes this warp can read
+        const int rowl = (warp & 3) * 32 + lane;   // the tensor memory lanes this warp can read
+        const int xr = rowl & 7;
+        const uint32_t mine = (rowl >> 6) * kBoxBytes + (rowl & 63) * 128;   // this lane's row of a 128 x 64 part
+        const bool head = warp == 2 && lane == 0;                            // issues the epilogue's copies
         const bool blocked = kKind == kFinal && Q.w != nullptr && read_error(Q.d_err) != 0;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        uint32_t done = 0;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint32_t done = 0, terms = 0;   // accumulators, sets used
+        // The term's next 64 columns into their set, once nothing leaves from there any more.
+        auto fetch = [&](uint32_t set, int col, int row0, int mat) {
+            const uint32_t at = sets + set * S::kSet, bar = term + 8 * set;
+            tma_store_read<0>();
+            mbar_expect(bar, S::kSubBytes * (Q.rlo ? 2 : 1));
+            for (int q = 0; q < kBM / kBox; ++q) {
+                tma_load<1>(at + q * kBoxBytes, &maps.rhi, bar, col, row0 + q * kBox, mat);
+                if (Q.rlo) tma_load<1>(at + S::kSubBytes + q * kBoxBytes, &maps.rlo, bar, col, row0 + q * kBox, mat);
+            }
+        };
         bool ok = true;
-        for (int64_t t = blockIdx.x; ok && t < Q.all; t += gridDim.x) {
-            int64_t mat, row0, col0;
-            tile_at<BN, kSym>(Q, t, mat, row0, col0);
-            const int64_t row = row0 + quarter * 32 + lane;
+        for (int64_t t = first; ok && t < Q.all; t += step) {
+            int mat, row0, col0;
+            tile_at<TM, BN, kSym>(Q, t, mat, row0, col0);
+            row0 += rank * kBM;
+            // 64-column pieces of this tile that are wanted: inside the matrix, not above the diagonal
+            const int cols = kSym ? min(row0 + kBM, static_cast<int>(Q.m)) : static_cast<int>(Q.n);
+            const int pieces = row0 < Q.m ? min(BN / kSub, (cols - col0 + kSub - 1) / kSub) : 0;
+            if (kTerm && head && pieces > 0) fetch(terms % S::kSets, col0, row0, mat);
             float sum[P == 3 ? BN / 32 : 1][32];
-            for (int c = 0; c < chunks; c += S::kChunk, ++done) {
-                const uint32_t acc = done % S::kAccs;
-                if (!(ok = __all_sync(kFull, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead)))) break;
+            uint32_t acc = done % S::kAccs;
+            if (P == 3) {
+                for (int c = 0; c < chunks; c += S::kChunk, ++done) {
+                    acc = done % S::kAccs;
+                    if (!(ok = all_of(1, kEpilogue, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead)))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < (P == 3 ? BN / 32 : 0); ++q) {
+                        float v[32];
+                        tmem_load32(lanes + acc * BN + q * 32, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sum[q][e] = c ? sum[q][e] + v[e] : v[e];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty + 8 * acc, 0));
+                }
+            } else {
+                ok = all_of(1, kEpilogue, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead));
                 tc_fence_after();
+                ++done;
+            }
+            if (!ok) break;
 #pragma unroll
-                for (int q = 0; q < BN / 32; ++q) {
-                    float v[32];
-                    tmem_load32(lanes + acc * BN + q * 32, v);
-                    if (P == 3) {
+            for (int j = 0; j < BN / kSub; ++j) {
+                if (j < pieces) {
+                    const uint32_t set = terms % S::kSets, at = sets + set * S::kSet;
+                    const int col = col0 + j * kSub;
+                    if (kTerm) {
+                        ok = all_of(1, kEpilogue, mbar_wait(term + 8 * set, terms / S::kSets & 1, &dead));
+                        if (!ok) break;
+                        if (S::kSets == 2 && head && j + 1 < pieces) fetch(set ^ 1, col + kSub, row0, mat);
+                    } else {
+                        if (head) tma_store_read<S::kSets - 1>();   // the set's last results have left
+                        all_of(1, kEpilogue, true);
+                    }
+                    ++terms;
+                    const bool image = kSym && col + kSub <= row0;   // wholly below the diagonal block
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) sum[q % (P == 3 ? BN / 32 : 1)][e] = c ? sum[q % (P == 3 ? BN / 32 : 1)][e] + v[e] : v[e];
-                    } else if (!blocked) {
+                    for (int h = 0; h < 2; ++h) {
+                        float v[32];
+                        if (P == 3) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) finish8<kKind>(Q, mat, row, col0 + q * 32 + e, v + e);
+                            for (int e = 0; e < 32; ++e) v[e] = sum[(2 * j + h) % (P == 3 ? BN / 32 : 1)][e];
+                        } else {
+                            tmem_load32(lanes + acc * BN + j * kSub + h * 32, v);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t piece = ((h * 4 + q) ^ xr) << 4;
+                            float x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = Q.mul * v[q * 8 + e];
+                            if (kTerm) {
+                                float r[8];
+                                unpack8(lds128(at + mine + piece), r);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.add, r[e], x[e]);
+                                if (Q.rlo) {
+                                    unpack8(lds128(at + S::kSubBytes + mine + piece), r);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.add, r[e], x[e]);
+                                }
+                            }
+                            if (kKind == kFinal) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x[e] *= kInvScale;
+                                if (Q.tall) {
+                                    if (!blocked) put_columns(Q, mat, row0 + rowl, col + h * 32 + q * 8, x);
+                                } else {
+                                    const uint32_t to = at + 2 * S::kSubBytes + rowl * 256;
+                                    const int p4 = h * 8 + q * 2;
+                                    sts128(to + ((p4 ^ xr) << 4), make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                                                             __float_as_uint(x[2]), __float_as_uint(x[3])));
+                                    sts128(to + (((p4 + 1) ^ xr) << 4), make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]),
+                                                                                   __float_as_uint(x[6]), __float_as_uint(x[7])));
+                                }
+                                continue;
+                            }
+                            uint4 hi, lo;
+                            __half2* hh = reinterpret_cast<__half2*>(&hi);
+                            __half2* ll = reinterpret_cast<__half2*>(&lo);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                hh[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+                                const float2 f = __half22float2(hh[e]);
+                                ll[e] = __floats2half2_rn(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+                            }
+                            constexpr bool kLo = P == 3 || !kSym;   // one product's symmetric results have no lo part
+                            sts128(at + mine + piece, hi);
+                            if (kLo && Q.wlo) sts128(at + S::kSubBytes + mine + piece, lo);
+                            if (image) {   // column of the image: a 128-byte row of the box with this lane's 64 rows
+                                const uint32_t im = at + (kLo ? 2 : 1) * S::kSubBytes + (rowl >> 6) * kBoxBytes;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int y = h * 32 + q * 8 + e;
+                                    const uint32_t o = y * 128 + ((((rowl & 63) >> 3) ^ (y & 7)) << 4) + (rowl & 7) * 2;
+                                    sts16(im + o, reinterpret_cast<const uint16_t*>(&hi)[e]);
+                                    if (kLo && Q.wlo) sts16(im + S::kSubBytes + o, reinterpret_cast<const uint16_t*>(&lo)[e]);
+                                }
+                            }
+                        }
+                    }
+                    if (kKind == kFinal) {
+                        __syncwarp();
+                        if (!Q.tall && !blocked && row0 + (warp & 3) * 32 < Q.m)
+                            put_rows(Q, at + 2 * S::kSubBytes + (warp & 3) * 32 * 256, mat, row0 + (warp & 3) * 32, col, lane);
+                        all_of(1, kEpilogue, true);   // every warp is done with the set
+                        if (head && j + 1 < pieces) fetch(0, col + kSub, row0, mat);
+                        continue;
+                    }
+                    fence_async_proxy();
+                    all_of(1, kEpilogue, true);
+                    if (head) {
+                        for (int q = 0; q < kBM / kBox; ++q) {
+                            tma_store(&maps.whi, at + q * kBoxBytes, col, row0 + q * kBox, mat);
+                            if (Q.wlo) tma_store(&maps.wlo, at + S::kSubBytes + q * kBoxBytes, col, row0 + q * kBox, mat);
+                        }
+                        if (image) {
+                            const uint32_t im = at + (P == 3 ? 2 : 1) * S::kSubBytes;
+                            for (int q = 0; q < kBM / kBox; ++q) {
+                                tma_store(&maps.whi, im + q * kBoxBytes, row0 + q * kBox, col, mat);
+                                if (Q.wlo) tma_store(&maps.wlo, im + S::kSubBytes + q * kBoxBytes, row0 + q * kBox, col, mat);
+                            }
+                        }
+                        tma_store_commit();
+                        if (kTerm && S::kSets == 1 && j + 1 < pieces) fetch(0, col + kSub, row0, mat);
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(tempty + 8 * acc);
-                if (P != 3) {
-                    ++done;
-                    break;   // one accumulator holds the tile
-                }
             }
-            if (P == 3 && ok && !blocked)
-#pragma unroll
-                for (int q = 0; q < BN / 32; ++q)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        finish8<kKind>(Q, mat, row, col0 + q * 32 + e, sum[q % (P == 3 ? BN / 32 : 1)] + e);
+            if (!ok) break;
+            if (P != 3) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty + 8 * acc, 0));
+            }
         }
+        if (head) tma_store_done();
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (kPair == 2)
+        cluster_sync();
+    else
+        __syncthreads();
     tc_fence_after();
     if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
-    if (warp == 1) tmem_free(tmem, S::kAccs * BN);
+    if (warp == 1) tmem_free<kPair>(tmem, S::kAccs * BN);
 }
 
 // -------------------------------------------------------------------- host
@@ -493,7 +694,7 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 struct Layout {
     int64_t m, n, ldm, ldn;
-    int parts;
+    int64_t parts;
     size_t part, x[2][2], a[2], b[2], total;   // [.][0] hi, [.][1] lo
 };
 
@@ -504,7 +705,7 @@ Layout muon_layout(int64_t batch, int64_t r, int64_t c, int products)
     L.n = std::max(r, c);
     L.ldm = up(L.m, 8);
     L.ldn = up(L.n, 8);
-    L.parts = static_cast<int>(std::min<int64_t>(kNormParts, std::max<int64_t>(1, r * c / 8192)));
+    L.parts = std::min<int64_t>(kNormParts, std::max<int64_t>(1, r * c / 8192));
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t p = at;
@@ -523,34 +724,47 @@ Layout muon_layout(int64_t batch, int64_t r, int64_t c, int products)
     return L;
 }
 
-int64_t tiles_of(int64_t m, int64_t n, int bn, bool sym)
+int64_t tiles_of(int64_t m, int64_t n, int tm, int bn, bool sym)
 {
-    if (!sym) return (m + kBM - 1) / kBM * ((n + bn - 1) / bn);
+    if (!sym) return (m + tm - 1) / tm * ((n + bn - 1) / bn);
     int64_t t = 0;
-    for (int64_t i = 0; i * kBM < m; ++i) t += (i * kBM + kBM - 1) / bn + 1;
+    for (int64_t i = 0; i * tm < m; ++i) t += (i * tm + tm - 1) / bn + 1;
     return t;
 }
 
-template <int kKind, int BN, int P>
+template <int kKind, int kPair, int BN, int P>
 cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t batch, cudaStream_t s)
 {
-    constexpr bool kSym = kKind == kGram || kKind == kPoly;
-    using S = Shape<BN, P>;
-    Q.tiles = tiles_of(Q.m, Q.n, BN, kSym);
+    using S = Shape<kKind, kPair, BN, P>;
+    auto* kernel = k_muon_product<kKind, kPair, BN, P>;
+    Q.tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym);
     Q.all = Q.tiles * batch;
     Q.cols_of_tiles = static_cast<int>((Q.n + BN - 1) / BN);
-    const cudaError_t e = cudaFuncSetAttribute(k_muon_product<kKind, BN, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(S::kSmem));
-    if (e != cudaSuccess) return e;
-    const int blocks = static_cast<int>(std::min<int64_t>(Q.all, num_sms()));
+    static const cudaError_t ready = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                          static_cast<int>(S::kSmem));
+    if (ready != cudaSuccess) return ready;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(Q.all, num_sms() / kPair) * kPair));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kPair;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     SO_PROFILE(name, s);
-    return launch_smem(k_muon_product<kKind, BN, P>, dim3(blocks), dim3(kThreads), S::kSmem, s, maps, Q);
+    return cudaLaunchKernelEx(&cfg, kernel, maps, Q);
 }
 
 template <int kKind, int P>
 cudaError_t run_kind(const char* name, const Maps& maps, const Product& Q, int64_t batch, cudaStream_t s)
 {
-    return run_product<kKind, 128, P>(name, maps, Q, batch, s);
+    return run_product<kKind, 1, 128, P>(name, maps, Q, batch, s);
 }
 
 template <int P>
@@ -565,39 +779,36 @@ cudaError_t run_steps(const Layout& L, const MuonParams& M, uint8_t* ws, cudaStr
         if (!encode(&mb[h], half(L.b[h]), L.m, L.m, L.ldm, M.batch)) return cudaErrorUnknown;
     }
     constexpr int l = P == 3 ? 1 : 0;   // without lo parts the maps of hi stand in, unread
+    if (P == 1)
+        for (int i = 0; i < 2; ++i)
+            if (!encode(&mx[i][1], half(L.x[i][1]), L.m, L.n, L.ldn, M.batch)) return cudaErrorUnknown;
     for (int step = 0; step < M.steps; ++step) {
         const int in = step & 1, out = in ^ 1;
         Product Q{};
         Q.d_err = M.d_err;
         Q.m = Q.n = L.m;
-        Q.ld = L.ldm;
         Q.k = L.n;
         Q.mul = kInvScale;
-        Q.whi = half(L.a[0]);
-        Q.wlo = P == 3 ? half(L.a[1]) : nullptr;
-        cudaError_t e = run_kind<kGram, P>("muon_gram", Maps{mx[in][0], mx[in][l], mx[in][0], mx[in][l]}, Q, M.batch, s);
+        Q.wlo = P == 3;
+        cudaError_t e = run_kind<kGram, P>("muon_gram",
+                                           Maps{mx[in][0], mx[in][l], mx[in][0], mx[in][l], ma[0], ma[l], ma[0], ma[l]},
+                                           Q, M.batch, s);
         if (e != cudaSuccess) return e;
 
         Q.k = L.m;
         Q.add = M.b;
         Q.mul = M.c * kInvScale;
-        Q.rhi = half(L.a[0]);
-        Q.rlo = P == 3 ? half(L.a[1]) : nullptr;
-        Q.whi = half(L.b[0]);
-        Q.wlo = P == 3 ? half(L.b[1]) : nullptr;
-        e = run_kind<kPoly, P>("muon_poly", Maps{ma[0], ma[l], ma[0], ma[l]}, Q, M.batch, s);
+        Q.rlo = P == 3;
+        e = run_kind<kPoly, P>("muon_poly", Maps{ma[0], ma[l], ma[0], ma[l], ma[0], ma[l], mb[0], mb[l]}, Q, M.batch, s);
         if (e != cudaSuccess) return e;
 
         const bool last = step + 1 == M.steps;
         Q.n = L.n;
-        Q.ld = L.ldn;
         Q.add = M.a;
         Q.mul = kInvScale;
-        Q.rhi = half(L.x[in][0]);
-        Q.rlo = P == 3 || !last ? half(L.x[in][1]) : nullptr;
-        Q.whi = half(L.x[out][0]);
-        Q.wlo = P == 3 || step + 2 < M.steps ? half(L.x[out][1]) : nullptr;
-        const Maps maps{mb[0], mb[l], mx[in][0], mx[in][l]};
+        Q.rlo = P == 3 || !last;
+        Q.wlo = P == 3 || step + 2 < M.steps;
+        const Maps maps{mb[0], mb[l], mx[in][0], mx[in][l], mx[in][0], mx[in][1], mx[out][0], mx[out][1]};
         if (last) {
             Q.out = M.out;
             Q.w = M.w;
@@ -627,18 +838,22 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
     const Update U{M.g, M.g_bf16, M.buf, M.momentum, M.nesterov};
     const int64_t size = M.r * M.cols;
     cudaError_t e;
+    // four values an access: rows, and so matrices, of a multiple of four, arrays aligned to match
+    const bool vec = M.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(M.g) & (M.g_bf16 ? 7u : 15u)) == 0 &&
+                     (reinterpret_cast<uintptr_t>(M.buf) & 15u) == 0;
     {
         SO_PROFILE("muon_norm", s);
-        e = launch(k_muon_norm, dim3(static_cast<unsigned>(M.batch * L.parts)), dim3(kMuonBlock), s, U, size, L.parts,
-                   part, M.d_err);
+        e = launch(vec ? k_muon_norm<true> : k_muon_norm<false>, dim3(static_cast<unsigned>(M.batch * L.parts)),
+                   dim3(kMuonBlock), s, U, size, L.parts, part, M.d_err);
     }
     if (e != cudaSuccess) return e;
     {
-        const int64_t tc = (M.cols + 31) / 32, tiles = (M.r + 31) / 32 * tc, all = tiles * M.batch;
+        const int64_t tc = (M.cols + 63) / 64, tiles = (M.r + 63) / 64 * tc, all = tiles * M.batch;
         const bool lo = M.products == 3 || M.steps > 1;
         SO_PROFILE("muon_start", s);
-        e = launch(k_muon_start, dim3(static_cast<unsigned>(std::min<int64_t>(all, 8 * num_sms()))), dim3(kMuonBlock), s,
-                   U, M.buf, M.r, M.cols, tc, tiles, all, static_cast<const float*>(part), L.parts, M.eps,
+        e = launch(vec ? k_muon_start<true> : k_muon_start<false>,
+                   dim3(static_cast<unsigned>(std::min<int64_t>(all, 8 * num_sms()))), dim3(kMuonBlock), s, U, M.buf,
+                   M.r, M.cols, tc, tiles, all, static_cast<const float*>(part), L.parts, M.eps,
                    reinterpret_cast<__half*>(base + L.x[0][0]),
                    lo ? reinterpret_cast<__half*>(base + L.x[0][1]) : static_cast<__half*>(nullptr), L.ldn,
                    M.r > M.cols ? 1 : 0, static_cast<const int32_t*>(M.d_err));

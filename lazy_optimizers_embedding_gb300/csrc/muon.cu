@@ -761,10 +761,27 @@ cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t b
     return cudaLaunchKernelEx(&cfg, kernel, maps, Q);
 }
 
+// What a shape's tiles take, in cycles of one 64-value stage times rounds over the GPU: a
+// stage needs 128 x BN x 64 x P products at 4096 a cycle and SM, and its boxes from L2 at
+// about 80 bytes a cycle and SM, whichever is longer.
+template <int kKind, int kPair, int BN, int P>
+int64_t shape_cost(const Product& Q, int64_t batch)
+{
+    using S = Shape<kKind, kPair, BN, P>;
+    const int64_t units = num_sms() / kPair;
+    const int64_t tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym) * batch;
+    return (tiles + units - 1) / units * std::max<int64_t>(2 * BN * P, S::kStage / 80);
+}
+
 template <int kKind, int P>
 cudaError_t run_kind(const char* name, const Maps& maps, const Product& Q, int64_t batch, cudaStream_t s)
 {
-    return run_product<kKind, 1, 128, P>(name, maps, Q, batch, s);
+    constexpr int kWide = P == 3 ? 128 : 256;
+    const int64_t wide = shape_cost<kKind, 2, kWide, P>(Q, batch), one = shape_cost<kKind, 1, 128, P>(Q, batch),
+                  half = shape_cost<kKind, 1, 64, P>(Q, batch);
+    if (wide <= one && wide <= half) return run_product<kKind, 2, kWide, P>(name, maps, Q, batch, s);
+    if (one <= half) return run_product<kKind, 1, 128, P>(name, maps, Q, batch, s);
+    return run_product<kKind, 1, 64, P>(name, maps, Q, batch, s);
 }
 
 template <int P>

@@ -21,76 +21,24 @@
 //                 large ones; in the last step X as rounded in both terms is the
 //                 better polynomial).  About 2e-3 of the result's norm, which is
 //                 what rounding it to bf16 costs too.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
+#include "muon.cuh"
 #include "profile.cuh"
-#include "rowio.cuh"
-#include "tensor.cuh"
 
 namespace so {
 
 namespace {
 
-constexpr float kScale = 16384.0f;              // 2^14
-constexpr float kInvScale = 1.0f / 16384.0f;
 constexpr int kBM = 128, kBK = 64;              // rows of a block's tile; K values of a stage (128 bytes)
 constexpr int kBox = 64;                        // rows of one copied box: 64 x 128 bytes
 constexpr uint32_t kBoxBytes = kBox * kBK * 2;
 constexpr int kSub = 64;                        // columns the epilogue finishes at a time
 constexpr int kThreads = 192;                   // copy warp, product warp, 4 epilogue warps
 constexpr int kEpilogue = 128;
-constexpr int kMuonBlock = 256;
 constexpr int64_t kNormParts = 512;             // partial sums of squares of a matrix at most
 
 // ------------------------------------------------------------------- start
-// u of one call: given, or the momentum's.
-struct Update {
-    const void* g;      // u itself, or the gradient
-    int g_bf16;
-    const float* buf;   // momentum buffer, nullptr: u = g
-    float momentum;
-    int nesterov;
-};
-
-// Four values of u from element i on (those below `left`), and the new buffer's.
-template <bool kVec>
-__device__ __forceinline__ void read_u4(const Update& U, int64_t i, int left, float (&u)[4], float (&nb)[4])
-{
-    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (kVec) {
-        if (left > 0) {
-            if (U.g_bf16) {
-                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(U.g) + i);
-                g[0] = __uint_as_float(q.x << 16), g[1] = __uint_as_float(q.x & 0xffff0000u);
-                g[2] = __uint_as_float(q.y << 16), g[3] = __uint_as_float(q.y & 0xffff0000u);
-            } else {
-                Pack<float, 4> q;
-                q.load(static_cast<const float*>(U.g) + i);
-                q.get(g);
-            }
-            if (U.buf) {
-                Pack<float, 4> q;
-                q.load(U.buf + i);
-                q.get(b);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < left) {
-                g[e] = U.g_bf16 ? __bfloat162float(static_cast<const bf16*>(U.g)[i + e]) : static_cast<const float*>(U.g)[i + e];
-                if (U.buf) b[e] = U.buf[i + e];
-            }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        nb[e] = fmaf(U.momentum, b[e], g[e]);
-        u[e] = U.buf == nullptr ? g[e] : U.nesterov ? fmaf(U.momentum, nb[e], g[e]) : nb[e];
-    }
-}
-
 // Sums of squares of one matrix's pieces; a sum that is not finite is reported
 // before anything is written.
 template <bool kVec>
@@ -116,20 +64,6 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
     }
 }
 
-// v as hi + lo f16, four at a time.
-__device__ __forceinline__ void split4(__half* hi, __half* lo, const float (&v)[4])
-{
-    __half2 h[2], l[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        const float2 f = __half22float2(h[i]);
-        l[i] = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
-    }
-    *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<const uint2*>(h);
-    if (lo) *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(l);
-}
-
 // X = u / (|u| + eps), scaled and split, transposed where u is tall; the new momentum
 // buffer.  One 64 x 64 tile of u at a time, four values a thread.
 template <bool kVec>
@@ -147,19 +81,13 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __re
     const int64_t m = tall ? c : r;
     int64_t have = -1;
     float scale = 0.0f;
-    for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
+    // neighbouring tiles by one block: few matrices, whose scales it has to work out
+    const int64_t t1 = ntiles * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t t = ntiles * blockIdx.x / gridDim.x; t < t1; ++t) {
         const int64_t mat = t / tiles, q = t % tiles;
         const int64_t r0 = q / tiles_c * 64, c0 = q % tiles_c * 64;
         if (mat != have) {
-            double s = 0.0;
-            for (int64_t i = threadIdx.x; i < parts; i += kMuonBlock) s += part[mat * parts + i];
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
-            __syncthreads();
-            s = sums[0];
-            for (int w = 1; w < kMuonBlock / 32; ++w) s += sums[w];
-            scale = static_cast<float>(static_cast<double>(kScale) / (sqrt(s) + static_cast<double>(eps)));
+            scale = start_scale(part + mat * parts, parts, eps, sums);
             have = mat;
         }
         float u[4][4];
@@ -280,17 +208,6 @@ __device__ __forceinline__ void tile_at(const Product& Q, int64_t t, int& mat, i
     } else {
         row0 = q / Q.cols_of_tiles * TM;
         col0 = q % Q.cols_of_tiles * BN;
-    }
-}
-
-__device__ __forceinline__ void unpack8(uint4 a, float (&x)[8])
-{
-    const __half2* h = reinterpret_cast<const __half2*>(&a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
     }
 }
 
@@ -864,6 +781,7 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
                    dim3(kMuonBlock), s, U, size, L.parts, part, M.d_err);
     }
     if (e != cudaSuccess) return e;
+    if (muon_fits_cluster(M.batch, L.m, L.n)) return muon_cluster(M, U, part, L.parts, vec, s);
     {
         const int64_t tc = (M.cols + 63) / 64, tiles = (M.r + 63) / 64 * tc, all = tiles * M.batch;
         const bool lo = M.products == 3 || M.steps > 1;

@@ -1,0 +1,385 @@
+// muon_small.cu -- Newton-Schulz for matrices of at most 128 rows (columns, where
+// tall) whose X a cluster's shared memory holds: all steps in one launch.
+//
+// A cluster of up to 8 blocks has one matrix; each block keeps a slice of up to 256
+// columns of X, hi and lo f16 (three products throughout: the time is that of the
+// phases, not of the products), and the whole of A and B.  A step is
+//   A's share of the slice     X_s X_s^T, the shares summed over the cluster through
+//                              shared memory, in block order on every block alike
+//   A A                        by every block
+//   B X_s                      by every block, in place
+// One copy of X serves both products: boxes of 64 columns, 128 rows of 128 bytes, are
+// K-major for X X^T and MN-major for B X.  Products of one hi and one lo part, 2^-11
+// of the others, have an accumulator of their own, so that the tensor unit's
+// rounding towards zero is one of K / 16 sums and not of three times as many.
+//
+// A phase is bound by latency: products of a 128 x 128 x 256 tile take 0.4 us, the
+// barriers, tensor memory reads and f16 splits around them 1 us.
+#include <algorithm>
+
+#include "muon.cuh"
+#include "profile.cuh"
+
+namespace so {
+
+namespace {
+
+constexpr int kRows = 128;                       // rows of X, A and B held, zeros past the matrix's
+constexpr int kSlice = 256;                      // columns of X a block holds at most
+constexpr uint32_t kBlockBytes = kRows * 128;    // 64 columns of 128 rows
+constexpr uint32_t kXBytes = kSlice / 64 * kBlockBytes, kSquareBytes = kRows / 64 * kBlockBytes;
+constexpr uint32_t kSmallSmem = 2 * kXBytes + 2 * kSquareBytes + 1024;
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kGramCol = 0, kCrossCol = 128, kUpdateCol = 256, kTmemCols = 512;
+
+// Byte of element (row, col) in an array of 64-column blocks, 16-byte pieces permuted by row.
+__device__ __forceinline__ uint32_t place(int row, int col)
+{
+    return (col >> 6) * kBlockBytes + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+__device__ __forceinline__ float4 lds_cluster(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Eight values as hi and lo f16 to shared memory.
+__device__ __forceinline__ void split8(uint32_t hi_at, uint32_t lo_at, const float (&x)[8])
+{
+    uint4 hi, lo;
+    __half2* hh = reinterpret_cast<__half2*>(&hi);
+    __half2* ll = reinterpret_cast<__half2*>(&lo);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        hh[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+        const float2 f = __half22float2(hh[e]);
+        ll[e] = __floats2half2_rn(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+    }
+    sts128(hi_at, hi);
+    sts128(lo_at, lo);
+}
+
+__device__ __forceinline__ uint16_t bits_of(__half h) { return __half_as_ushort(h); }
+
+__device__ __forceinline__ __half lds_half(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return __ushort_as_half(v);
+}
+
+struct Small {
+    int64_t size;        // of a matrix
+    int m, n;            // X: m x n
+    int slice;           // columns of X a block holds, a multiple of 64
+    int tall, steps;
+    float a, b, c, eps;
+    const float* part;
+    int64_t parts;
+    float* buf;
+    void* out;
+    int out_bf16;
+    float* w;
+    float decay, lr;
+    int32_t* d_err;
+};
+
+template <bool kVec>
+__global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bar_mem;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int dead;
+    __shared__ double sums[kMuonBlock / 32];
+    const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes;
+    const uint32_t bar = smem_addr(&bar_mem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t mat = blockIdx.x / blocks;
+    const int rank = static_cast<int>(blockIdx.x % blocks);
+    const int col0 = rank * Q.slice, cols = max(0, min(Q.slice, Q.n - col0));   // this block's columns of X
+    const int side = Q.m <= 64 ? 64 : 128;                                      // of A and B, in the products
+
+    if (threadIdx.x == 0) {
+        dead = 0;
+        mbar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tmem_alloc<1>(&tmem_slot, kTmemCols);
+    for (uint32_t i = threadIdx.x * 16; i < 2 * kXBytes; i += kMuonBlock * 16) sts128(xhi + i, make_uint4(0u, 0u, 0u, 0u));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();   // writes a caller output: dependents start after this grid exits
+    const bool blocked = (Q.w != nullptr) && read_error(Q.d_err) != 0;   // set before this kernel: the same for every block
+
+    // X of the slice, scaled and split; the new momentum buffer
+    const float scale = start_scale(Q.part + mat * Q.parts, Q.parts, Q.eps, sums);
+    if (!blocked) {
+        const int64_t base = mat * Q.size;
+        // along u's rows: X's rows, or its columns where u is tall
+        const int outer = Q.tall ? cols : Q.m, inner = Q.tall ? Q.m : cols, quads = (inner + 3) / 4;
+        for (int i = threadIdx.x; i < outer * quads; i += kMuonBlock) {
+            const int o = i / quads, k = i % quads * 4;
+            const int64_t at = base + (Q.tall ? static_cast<int64_t>(col0 + o) * Q.m + k : static_cast<int64_t>(o) * Q.n + col0 + k);
+            const int left = min(4, inner - k);
+            float u[4], nb[4];
+            read_u4<kVec>(U, at, left, u, nb);
+            if (Q.buf) {
+                if (kVec) {
+                    Pack<float, 4>::put(Q.buf + at, nb);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) Q.buf[at + e] = nb[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) {
+                    const float v = u[e] * scale;
+                    const __half h = __float2half_rn(v);
+                    const uint32_t p = Q.tall ? place(k + e, o) : place(o, k + e);
+                    sts16(xhi + p, bits_of(h));
+                    sts16(xlo + p, bits_of(__float2half_rn(v - __half2float(h))));
+                }
+        }
+    }
+
+    // this warp's share of an accumulator: 32 rows, half the columns
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const bool rows_used = (warp & 3) * 32 < Q.m;
+    uint32_t phase = 0;
+    auto products_done = [&] {   // of the phase's MMAs, by every thread
+        mbar_wait(bar, phase & 1, &dead);
+        ++phase;
+        __syncwarp();
+        tc_fence_after();
+    };
+    auto operands_done = [&] {   // written by every thread, for the MMAs
+        fence_async_proxy();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    // hi hi into `d`, hi lo + lo hi into `x` (the same accumulator where d == x)
+    auto issue = [&](uint32_t d, uint32_t x, uint32_t idesc, uint32_t ah, uint32_t al, uint32_t bh, uint32_t bl, uint32_t lead,
+                     bool first) {
+        const uint64_t A = smem_desc(ah, 16, 1024), AL = smem_desc(al, 16, 1024);
+        const uint64_t B = smem_desc(bh, lead, 1024), BL = smem_desc(bl, lead, 1024);
+        tc_mma_f16<1>(tmem + d, A, B, idesc, !first);
+        tc_mma_f16<1>(tmem + x, A, BL, idesc, d == x || !first);
+        tc_mma_f16<1>(tmem + x, AL, B, idesc, true);
+    };
+
+    for (int step = 0; step < Q.steps; ++step) {
+        // ---- A
+        operands_done();
+        if (warp == 0 && elect_one()) {
+            const uint32_t idesc = mma_desc_f16(kRows, side, false);
+            for (int k = 0; k < Q.slice / 16; ++k) {
+                const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32;
+                issue(kGramCol, kCrossCol, idesc, xhi + o, xlo + o, xhi + o, xlo + o, 16, k == 0);
+            }
+            tc_commit<1>(bar);
+        }
+        products_done();
+        const int per = side / 2;              // columns of A this warp has: 32 or 64
+        float av[64];
+        if (rows_used) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (q * 32 < per) {
+                    float v[32];
+                    tmem_load32(lanes + kGramCol + half * per + q * 32, v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) av[q * 32 + e] = v[e];
+                    tmem_load32(lanes + kCrossCol + half * per + q * 32, v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) av[q * 32 + e] += v[e];
+                }
+        }
+        if (blocks > 1) {
+            // the shares, fp32 rows of 512 bytes where A will be, 16-byte pieces permuted by row
+            const uint32_t at = shi + row * 512;
+            if (rows_used)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    if (q * 4 < per)
+                        sts128(at + (((half * (per / 4) + q) ^ (row & 7)) << 4),
+                               make_uint4(__float_as_uint(av[4 * q]), __float_as_uint(av[4 * q + 1]),
+                                          __float_as_uint(av[4 * q + 2]), __float_as_uint(av[4 * q + 3])));
+            cluster_sync();
+            if (rows_used) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) av[e] = 0.0f;
+                for (int r = 0; r < blocks; ++r) {
+                    const uint32_t from = cluster_addr(at, r);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (q * 4 < per) {
+                            const float4 f = lds_cluster(from + (((half * (per / 4) + q) ^ (row & 7)) << 4));
+                            av[4 * q] += f.x, av[4 * q + 1] += f.y, av[4 * q + 2] += f.z, av[4 * q + 3] += f.w;
+                        }
+                }
+            }
+            cluster_sync();   // every block has read the shares
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q * 8 < per) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = av[8 * q + e] = rows_used ? av[8 * q + e] * kInvScale : 0.0f;
+                const uint32_t p = place(row, half * per + q * 8);
+                split8(shi + p, slo + p, x);   // zeros in the rows past the matrix's
+            }
+        operands_done();
+
+        // ---- A A, and B in A's place
+        if (warp == 0 && elect_one()) {
+            const uint32_t idesc = mma_desc_f16(kRows, side, false);
+            for (int k = 0; k < side / 16; ++k) {
+                const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32;
+                issue(kGramCol, kCrossCol, idesc, shi + o, slo + o, shi + o, slo + o, 16, k == 0);
+            }
+            tc_commit<1>(bar);
+        }
+        products_done();
+        if (rows_used) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (q * 32 < per) {
+                    float v[32], y[32];
+                    tmem_load32(lanes + kGramCol + half * per + q * 32, v);
+                    tmem_load32(lanes + kCrossCol + half * per + q * 32, y);
+#pragma unroll
+                    for (int p8 = 0; p8 < 4; ++p8) {
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = p8 * 8 + e;
+                            x[e] = fmaf(Q.b, av[q * 32 + i], Q.c * kInvScale * (v[i] + y[i]));
+                        }
+                        const uint32_t p = place(row, half * per + q * 32 + p8 * 8);
+                        split8(shi + p, slo + p, x);
+                    }
+                }
+        }
+        operands_done();
+
+        // ---- B X, and the new X in its place
+        if (warp == 0 && elect_one()) {
+            const uint32_t idesc = mma_desc_f16(kRows, Q.slice, true);
+            for (int k = 0; k < side / 16; ++k) {
+                const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32, x = k * 2048;   // 16 rows of X
+                issue(kUpdateCol, kUpdateCol, idesc, shi + o, slo + o, xhi + x, xlo + x, kBlockBytes, k == 0);
+            }
+            tc_commit<1>(bar);
+        }
+        products_done();
+        if (rows_used)
+            for (int q = half; q < Q.slice / 32; q += 2) {
+                float v[32];
+                tmem_load32(lanes + kUpdateCol + q * 32, v);
+#pragma unroll
+                for (int p8 = 0; p8 < 4; ++p8) {
+                    const uint32_t p = place(row, q * 32 + p8 * 8);
+                    float x[8], l[8];
+                    unpack8(lds128(xhi + p), x);
+                    unpack8(lds128(xlo + p), l);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.a, x[e] + l[e], kInvScale * v[p8 * 8 + e]);
+                    split8(xhi + p, xlo + p, x);
+                }
+            }
+    }
+    __syncthreads();
+
+    // the update, along u's rows
+    if (!blocked) {
+        const int64_t base = mat * Q.size;
+        const int outer = Q.tall ? cols : Q.m, inner = Q.tall ? Q.m : cols;
+        for (int o = warp; o < outer; o += kMuonBlock / 32)
+            for (int k = lane; k < inner; k += 32) {
+                const uint32_t p = Q.tall ? place(k, o) : place(o, k);
+                const float x = (__half2float(lds_half(xhi + p)) + __half2float(lds_half(xlo + p))) * kInvScale;
+                const int64_t at = base + (Q.tall ? static_cast<int64_t>(col0 + o) * Q.m + k : static_cast<int64_t>(o) * Q.n + col0 + k);
+                if (Q.w)
+                    Q.w[at] = fmaf(Q.decay, Q.w[at], -Q.lr * x);
+                else if (Q.out_bf16)
+                    static_cast<bf16*>(Q.out)[at] = __float2bfloat16_rn(x);
+                else
+                    static_cast<float*>(Q.out)[at] = x;
+            }
+    }
+    if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_free<1>(tmem, kTmemCols);
+}
+
+int cluster_blocks(int64_t n)
+{
+    int b = 1;
+    while (b * kSlice < n) b *= 2;
+    return b;
+}
+
+}  // namespace
+
+bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n)
+{
+    return m <= kRows && n <= kMaxCluster * kSlice && batch * cluster_blocks(n) <= 2 * num_sms();
+}
+
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int64_t parts, bool vec, cudaStream_t s)
+{
+    Small Q{};
+    Q.size = M.r * M.cols;
+    Q.tall = M.r > M.cols;
+    Q.m = static_cast<int>(std::min(M.r, M.cols));
+    Q.n = static_cast<int>(std::max(M.r, M.cols));
+    const int blocks = cluster_blocks(Q.n);
+    Q.slice = ((Q.n + blocks - 1) / blocks + 63) / 64 * 64;
+    Q.steps = M.steps;
+    Q.a = M.a, Q.b = M.b, Q.c = M.c, Q.eps = M.eps;
+    Q.part = part;
+    Q.parts = parts;
+    Q.buf = M.buf;
+    Q.out = M.out;
+    Q.out_bf16 = M.out_bf16;
+    Q.w = M.w;
+    Q.decay = M.decay;
+    Q.lr = M.lr;
+    Q.d_err = M.d_err;
+    auto* kernel = vec ? k_muon_cluster<true> : k_muon_cluster<false>;
+    static const cudaError_t ready = [] {
+        const cudaError_t e = cudaFuncSetAttribute(k_muon_cluster<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(k_muon_cluster<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    }();
+    if (ready != cudaSuccess) return ready;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(M.batch * blocks));
+    cfg.blockDim = dim3(kMuonBlock);
+    cfg.dynamicSmemBytes = kSmallSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    SO_PROFILE("muon_cluster", s);
+    return cudaLaunchKernelEx(&cfg, kernel, U, Q, blocks);
+}
+
+}  // namespace so

@@ -52,7 +52,7 @@ __device__ __forceinline__ uint64_t now_ns()
 // Waits for a phase, two seconds at most (the longest of these kernels' phases is
 // some tens of microseconds).  False once this wait or another of the block has
 // given up: `dead` is the block's shared flag, and every role then leaves its loop.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead)
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead)
 {
     const uint64_t t0 = now_ns();
     for (;;) {

@@ -404,7 +404,8 @@ sparse_status_t sparse_layer_norm_grad(const void* dy, sparse_dtype_t y_type, co
 /*
  * Tokens by expert.  n tokens name k experts each: expert[n, k] holds a slot's
  * expert in [0, experts), or -1 for a slot that goes nowhere (a padding token's).
- * Slot s = t*k + j.  Limits: 1 <= experts <= 1024, k >= 1, n*k < 2^31.
+ * Slot s = t*k + j.  Limits: 1 <= experts <= 1024, k >= 1, n*k < 2^31,
+ * rows of c <= 2^30 columns.
  */
 /* Bytes of workspace sparse_expert_sort needs. */
 size_t sparse_expert_workspace_size(int64_t n, int64_t k, int64_t experts);

@@ -44,7 +44,7 @@ int64_t lane_values(sparse_dtype_t x_type, sparse_dtype_t y_type)
 bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const int32_t* d_err)
 {
     return valid_type(type) && n >= 0 && k >= 1 && (n == 0 || k <= INT32_MAX / n) && valid_rows(n * k, c) &&
-           d_err != nullptr;
+           c <= kMaxExpertCols && d_err != nullptr;
 }
 
 // Newton-Schulz keeps X, A = X X^T and B = b A + c A^2 as f16 values times 2^14: their

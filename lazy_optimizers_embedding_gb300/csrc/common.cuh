@@ -369,6 +369,7 @@ cudaError_t layer_norm_grad(const void* dy, int y_bf16, const void* x, int x_bf1
 
 // Tokens by expert (expert.cu).
 constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxExpertCols = int64_t(1) << 30;   // 32-bit columns, one block's stride past the last included
 size_t expert_ws_bytes(int64_t slots, int64_t experts);
 cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, int64_t* offsets, int32_t* src,
                         int32_t* pos, void* ws, int32_t* d_err, cudaStream_t s);

@@ -191,7 +191,7 @@ __device__ __forceinline__ int64_t slot_place(const int32_t* pos, int64_t s, int
 
 // Zeros in the sorted rows that no slot has, from offsets[experts] on.
 template <class T, int V>
-__device__ __forceinline__ void clear_tail(T* rows, int64_t c, int64_t slots, const int64_t* end, int G, int gl,
+__device__ __forceinline__ void clear_tail(T* rows, int c, int64_t slots, const int64_t* end, int G, int gl,
                                            int64_t first, int64_t step)
 {
     Pack<T, V> zero;
@@ -199,15 +199,16 @@ __device__ __forceinline__ void clear_tail(T* rows, int64_t c, int64_t slots, co
     float z[V];
     zero.get(z);
     const int64_t p0 = *end < 0 ? 0 : *end;
-    for (int64_t p = p0 + first; p < slots; p += step)
-        for (int64_t col = static_cast<int64_t>(gl) * V; col < c; col += static_cast<int64_t>(G) * V)
-            Pack<T, V>::put(rows + p * c + col, z);
+    for (int64_t p = p0 + first; p < slots; p += step) {
+        T* row = rows + p * c;
+        for (int col = gl * V; col < c; col += G * V) Pack<T, V>::put(row + col, z);
+    }
 }
 
 // Rows are copied as units U (16 bytes where the rows allow it): cu units a row.
 template <class U>
-__global__ void __launch_bounds__(kExBlock) k_expert_dispatch(const U* __restrict__ x, int64_t n, int64_t k,
-                                                              int64_t cu, const int32_t* __restrict__ pos,
+__global__ void __launch_bounds__(kExBlock) k_expert_dispatch(const U* __restrict__ x, int64_t n, int k, int cu,
+                                                              const int32_t* __restrict__ pos,
                                                               const int64_t* __restrict__ end, U* __restrict__ xs,
                                                               int G, int32_t* d_err)
 {
@@ -217,78 +218,102 @@ __global__ void __launch_bounds__(kExBlock) k_expert_dispatch(const U* __restric
     const int64_t group = static_cast<int64_t>(blockIdx.x) * (kExBlock / G) + threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kExBlock / G);
     const int64_t slots = n * k;
-    for (int64_t t = group; t < n; t += step)
-        for (int64_t c0 = gl; c0 < cu; c0 += static_cast<int64_t>(G) * R) {
+    for (int64_t t = group; t < n; t += step) {
+        const U* from = x + t * cu;
+        for (int c0 = gl; c0 < cu; c0 += G * R) {
             U v[R];
 #pragma unroll
             for (int q = 0; q < R; ++q)
-                if (c0 + q * G < cu) v[q] = x[t * cu + c0 + q * G];
-            for (int64_t j = 0; j < k; ++j) {
+                if (c0 + q * G < cu) v[q] = from[c0 + q * G];
+            for (int j = 0; j < k; ++j) {
                 const int64_t p = slot_place(pos, t * k + j, slots, d_err);
                 if (p < 0) continue;
+                U* to = xs + p * cu;
 #pragma unroll
                 for (int q = 0; q < R; ++q)
-                    if (c0 + q * G < cu) xs[p * cu + c0 + q * G] = v[q];
+                    if (c0 + q * G < cu) to[c0 + q * G] = v[q];
             }
         }
+    }
     const U zero{};
     const int64_t p0 = *end < 0 ? 0 : *end;
-    for (int64_t p = p0 + group; p < slots; p += step)
-        for (int64_t col = gl; col < cu; col += G) xs[p * cu + col] = zero;
+    for (int64_t p = p0 + group; p < slots; p += step) {
+        U* to = xs + p * cu;
+        for (int col = gl; col < cu; col += G) to[col] = zero;
+    }
 }
 
+// J slots' rows by their first access, nullptr where a slot has none.
+template <class T, int J>
+__device__ __forceinline__ void slot_rows(const T* (&row)[J], const T* rows, int64_t c, const int32_t* pos, int64_t t, int k,
+                                          int j0, int64_t slots, int32_t* d_err)
+{
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int64_t p = j0 + j < k ? slot_place(pos, t * k + j0 + j, slots, d_err) : -1;
+        row[j] = p >= 0 ? rows + p * c : nullptr;
+    }
+}
+
+// A lane holds R accesses of its token's sum while the slots' rows go by, J at a time.
 template <class T, int V>
-__global__ void __launch_bounds__(kExBlock) k_expert_combine(const T* __restrict__ ys, int64_t n, int64_t k, int64_t c,
+__global__ void __launch_bounds__(kExBlock) k_expert_combine(const T* __restrict__ ys, int64_t n, int k, int c,
                                                              const int32_t* __restrict__ pos,
                                                              const float* __restrict__ w, T* __restrict__ y, int G,
                                                              int32_t* d_err)
 {
     pdl_wait();   // writes a caller output
-    constexpr int J = 4;   // rows a lane requests at once
+    constexpr int J = 4, R = V == 1 ? 4 : 1;
     const int gl = threadIdx.x & (G - 1);
     const int64_t group = static_cast<int64_t>(blockIdx.x) * (kExBlock / G) + threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kExBlock / G);
     const int64_t slots = n * k;
     for (int64_t t = group; t < n; t += step)
-        for (int64_t col = static_cast<int64_t>(gl) * V; col < c; col += static_cast<int64_t>(G) * V) {
-            float a[V];
+        for (int c0 = gl * V; c0 < c; c0 += G * V * R) {
+            float a[R][V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) a[e] = 0.0f;
-            for (int64_t j0 = 0; j0 < k; j0 += J) {
-                Pack<T, V> r[J];
+            for (int q = 0; q < R; ++q)
+#pragma unroll
+                for (int e = 0; e < V; ++e) a[q][e] = 0.0f;
+            for (int j0 = 0; j0 < k; j0 += J) {
+                const T* row[J];
+                slot_rows(row, ys, c, pos, t, k, j0, slots, d_err);
+                Pack<T, V> r[J][R];
                 float wj[J];
-                bool on[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const int64_t p = j0 + j < k ? slot_place(pos, t * k + j0 + j, slots, d_err) : -1;
-                    on[j] = p >= 0;
-                    if (on[j]) {
-                        r[j].load(ys + p * c + col);
-                        wj[j] = w ? w[t * k + j0 + j] : 1.0f;
-                    }
+                    wj[j] = row[j] && w ? w[t * k + j0 + j] : 1.0f;
+#pragma unroll
+                    for (int q = 0; q < R; ++q)
+                        if (row[j] && c0 + q * G * V < c) r[j][q].load(row[j] + c0 + q * G * V);
                 }
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    if (on[j]) {
-                        float v[V];
-                        r[j].get(v);
+                    if (row[j])
 #pragma unroll
-                        for (int e = 0; e < V; ++e) a[e] = fmaf(wj[j], v[e], a[e]);
-                    }
+                        for (int q = 0; q < R; ++q) {
+                            float v[V];
+                            r[j][q].get(v);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) a[q][e] = fmaf(wj[j], v[e], a[q][e]);
+                        }
             }
-            Pack<T, V>::put(y + t * c + col, a);
+            T* to = y + t * c;
+#pragma unroll
+            for (int q = 0; q < R; ++q)
+                if (c0 + q * G * V < c) Pack<T, V>::put(to + c0 + q * G * V, a[q]);
         }
 }
 
 template <class T, int V>
 __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ dy, const T* __restrict__ ys, int64_t n,
-                                                          int64_t k, int64_t c, const int32_t* __restrict__ pos,
+                                                          int k, int c, const int32_t* __restrict__ pos,
                                                           const int64_t* __restrict__ end,
                                                           const float* __restrict__ w, T* __restrict__ dys,
                                                           float* __restrict__ dw, int G, int32_t* d_err)
 {
     pdl_wait();   // writes caller outputs
-    constexpr int J = 4;   // slots worked at once
+    constexpr int J = 4, R = V == 1 ? 4 : 1;
     __shared__ float tmp[2 * 32 * J];
     const int gl = threadIdx.x & (G - 1);
     const int groups = kExBlock / G, sub = threadIdx.x / G;
@@ -297,35 +322,44 @@ __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ 
     int half = 0;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < n; base += step) {   // block-uniform trips
         const int64_t t = base + sub;
-        for (int64_t j0 = 0; j0 < k; j0 += J) {
-            int64_t p[J];
+        const T* from = dy + t * c;
+        for (int j0 = 0; j0 < k; j0 += J) {
+            const T* row[J];
+            slot_rows(row, ys, c, pos, t < n ? t : 0, t < n ? k : 0, j0, slots, d_err);
             float wj[J], dot[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                p[j] = (t < n && j0 + j < k) ? slot_place(pos, t * k + j0 + j, slots, d_err) : -1;
-                wj[j] = (p[j] >= 0 && w) ? w[t * k + j0 + j] : 1.0f;
+                wj[j] = row[j] && w ? w[t * k + j0 + j] : 1.0f;
                 dot[j] = 0.0f;
             }
             if (t < n)
-                for (int64_t col = static_cast<int64_t>(gl) * V; col < c; col += static_cast<int64_t>(G) * V) {
-                    Pack<T, V> d, r[J];
-                    d.load(dy + t * c + col);
+                for (int c0 = gl * V; c0 < c; c0 += G * V * R) {
+                    Pack<T, V> d[R], r[J][R];
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        if (p[j] >= 0) r[j].load(ys + p[j] * c + col);
-                    float dv[V];
-                    d.get(dv);
+                    for (int q = 0; q < R; ++q)
+                        if (c0 + q * G * V < c) {
+                            d[q].load(from + c0 + q * G * V);
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        if (p[j] >= 0) {
-                            float v[V];
-                            r[j].get(v);
+                            for (int j = 0; j < J; ++j)
+                                if (row[j]) r[j][q].load(row[j] + c0 + q * G * V);
+                        }
 #pragma unroll
-                            for (int e = 0; e < V; ++e) {
-                                dot[j] = fmaf(dv[e], v[e], dot[j]);
-                                v[e] = wj[j] * dv[e];
-                            }
-                            Pack<T, V>::put(dys + p[j] * c + col, v);
+                    for (int q = 0; q < R; ++q)
+                        if (c0 + q * G * V < c) {
+                            float dv[V];
+                            d[q].get(dv);
+#pragma unroll
+                            for (int j = 0; j < J; ++j)
+                                if (row[j]) {
+                                    float v[V];
+                                    r[j][q].get(v);
+#pragma unroll
+                                    for (int e = 0; e < V; ++e) {
+                                        dot[j] = fmaf(dv[e], v[e], dot[j]);
+                                        v[e] = wj[j] * dv[e];
+                                    }
+                                    Pack<T, V>::put(dys + (row[j] - ys) + c0 + q * G * V, v);
+                                }
                         }
                 }
             if (dw == nullptr) continue;
@@ -334,7 +368,7 @@ __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ 
             if (t < n && gl == 0)
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    if (j0 + j < k) dw[t * k + j0 + j] = p[j] >= 0 ? dot[j] : 0.0f;
+                    if (j0 + j < k) dw[t * k + j0 + j] = row[j] ? dot[j] : 0.0f;
         }
     }
     clear_tail<T, V>(dys, c, slots, end, G, gl, static_cast<int64_t>(blockIdx.x) * groups + sub, step);
@@ -348,14 +382,20 @@ int lanes_for(int64_t accesses, int per)
     return G;
 }
 
+// Resident blocks of a row kernel at most.
 template <class K>
-int row_blocks(K kernel, int64_t rows, int G)
+int resident(K kernel)
 {
     int o = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kernel, kExBlock, 0);
+    return std::max(o, 1);
+}
+
+int row_blocks(int most, int64_t rows, int G)
+{
     const int64_t groups = kExBlock / G;
     return static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>((rows + groups - 1) / groups, static_cast<int64_t>(std::max(o, 1)) * num_sms())));
+        1, std::min<int64_t>((rows + groups - 1) / groups, static_cast<int64_t>(most) * num_sms())));
 }
 
 size_t place_smem(int64_t experts) { return sizeof(uint32_t) * static_cast<size_t>(2 * kExWarps * experts); }
@@ -403,9 +443,10 @@ static cudaError_t run_dispatch(const void* x, int64_t n, int64_t k, int64_t cu,
                                 const int64_t* end, void* xs, int32_t* d_err, cudaStream_t s)
 {
     const int G = lanes_for(cu, 4);
+    static const int most = resident(k_expert_dispatch<U>);
     SO_PROFILE("expert_dispatch", s);
-    return launch(k_expert_dispatch<U>, dim3(row_blocks(k_expert_dispatch<U>, n, G)), dim3(kExBlock), s,
-                  static_cast<const U*>(x), n, k, cu, pos, end, static_cast<U*>(xs), G, d_err);
+    return launch(k_expert_dispatch<U>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
+                  static_cast<const U*>(x), n, static_cast<int>(k), static_cast<int>(cu), pos, end, static_cast<U*>(xs), G, d_err);
 }
 
 cudaError_t expert_dispatch(const void* x, int is_bf16, int64_t n, int64_t k, int64_t c, const int32_t* pos,
@@ -421,10 +462,11 @@ template <class T, int V>
 static cudaError_t run_combine(const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos, const float* w,
                                void* y, int32_t* d_err, cudaStream_t s)
 {
-    const int G = lanes_for(c / V, 1);
+    const int G = lanes_for(c / V, V == 1 ? 4 : 1);
+    static const int most = resident(k_expert_combine<T, V>);
     SO_PROFILE("expert_combine", s);
-    return launch(k_expert_combine<T, V>, dim3(row_blocks(k_expert_combine<T, V>, n, G)), dim3(kExBlock), s,
-                  static_cast<const T*>(ys), n, k, c, pos, w, static_cast<T*>(y), G, d_err);
+    return launch(k_expert_combine<T, V>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
+                  static_cast<const T*>(ys), n, static_cast<int>(k), static_cast<int>(c), pos, w, static_cast<T*>(y), G, d_err);
 }
 
 cudaError_t expert_combine(const void* ys, int is_bf16, int64_t n, int64_t k, int64_t c, const int32_t* pos,
@@ -441,10 +483,11 @@ template <class T, int V>
 static cudaError_t run_grad(const void* dy, const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos,
                             const int64_t* end, const float* w, void* dys, float* dw, int32_t* d_err, cudaStream_t s)
 {
-    const int G = lanes_for(c / V, 1);
+    const int G = lanes_for(c / V, V == 1 ? 4 : 1);
+    static const int most = resident(k_expert_grad<T, V>);
     SO_PROFILE("expert_combine_grad", s);
-    return launch(k_expert_grad<T, V>, dim3(row_blocks(k_expert_grad<T, V>, n, G)), dim3(kExBlock), s,
-                  static_cast<const T*>(dy), static_cast<const T*>(ys), n, k, c, pos, end, w, static_cast<T*>(dys), dw,
+    return launch(k_expert_grad<T, V>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
+                  static_cast<const T*>(dy), static_cast<const T*>(ys), n, static_cast<int>(k), static_cast<int>(c), pos, end, w, static_cast<T*>(dys), dw,
                   G, d_err);
 }
 

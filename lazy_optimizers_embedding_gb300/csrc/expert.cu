@@ -9,14 +9,15 @@
 //                 dw[t, j] = <dy[t], ys[pos[t, j]]>
 // and dispatch's gradient is combine without weights.
 //
-// Sort: counting, in at most kSortBlocks contiguous tiles.  k_expert_count
-// counts every tile's experts, k_expert_scan turns each expert's column of tile
-// counts into a running sum, k_expert_place ranks the slots: a warp owns a
-// contiguous run of its tile and walks it 32 slots at a time; each lane ORs its
-// bit into the warp's word of its expert, so the bits below its own are the
-// slots of the same expert before it.  Up to kOneBlock slots the last kernel
-// alone does it all.  Only whole numbers are added, so the result is exact and
-// the same on every run.
+// Sort: counting.  A warp owns a contiguous run of slots and walks it 32 at a time; each
+// lane ORs its bit into the warp's word of its expert, so the bits below its own are
+// the slots of the same expert before it.  Up to kClusterSlots slots one cluster of
+// up to 8 blocks does it all in one launch (k_expert_sort: the blocks read one another's
+// counts from shared memory; 9003 slots 5 us and 131072 slots 8 us, against 15 us
+// for three launches).  More take contiguous tiles: k_expert_count counts every
+// tile's experts, k_expert_scan turns each expert's column of tile counts into a
+// running sum, k_expert_sort places.  Only whole numbers are added, so the result is
+// exact and the same on every run.
 //
 // Rows: a group of G lanes owns a token and walks the columns G * V at a time
 // (16-byte accesses where the rows allow them), so each x or dy row is read once
@@ -26,6 +27,7 @@
 
 #include "profile.cuh"
 #include "rowio.cuh"
+#include "tensor.cuh"
 
 namespace so {
 
@@ -33,21 +35,37 @@ namespace {
 
 constexpr int kExBlock = 256;
 constexpr int kExWarps = kExBlock / 32;
-constexpr int64_t kExTile = 1024;     // slots of a tile at least
-constexpr int64_t kSortBlocks = 512;  // tiles at most
-constexpr int64_t kOneBlock = 4096;   // slots that one block sorts alone
+constexpr int64_t kExTile = 1024;          // slots of a tile at least
+constexpr int64_t kSortBlocks = 512;       // tiles at most
+constexpr int64_t kClusterSlots = 16384;   // slots that one cluster sorts
+constexpr int kHeld = 4;                   // rows of 32 slots whose experts a warp keeps between its two passes
 
+// Blocks of `threads` threads (kernel k_expert_sort), each with `tile` slots; one cluster of them or
+// many with counts in the workspace.
 struct SortShape {
     int64_t tile;
-    int blocks;
+    int blocks, threads;
+    bool cluster;
 };
 
-SortShape sort_shape(int64_t slots)
+size_t sort_smem(int threads, int64_t experts) { return sizeof(uint32_t) * static_cast<size_t>((2 * (threads / 32) + 1) * experts); }
+
+SortShape sort_shape(int64_t slots, int64_t experts)
 {
-    if (slots <= kOneBlock) return {std::max<int64_t>(kExBlock, (slots + kExBlock - 1) / kExBlock * kExBlock), 1};
-    const int64_t per = (slots + kSortBlocks - 1) / kSortBlocks;
-    const int64_t tile = std::max(kExTile, (per + kExBlock - 1) / kExBlock * kExBlock);
-    return {tile, static_cast<int>((slots + tile - 1) / tile)};
+    // as many warps as have kHeld rows of 32 slots, and as their counts leave room for
+    auto threads_for = [&](int64_t tile) {
+        int t = 64;
+        while (t < 1024 && t * kHeld < tile && sort_smem(2 * t, experts) <= 160 * 1024) t *= 2;
+        return t;
+    };
+    if (slots <= kClusterSlots) {
+        int blocks = 1;
+        while (blocks < 8 && slots > 2048 * blocks) blocks *= 2;
+        const int64_t tile = (slots + blocks - 1) / blocks;
+        return {tile, blocks, threads_for(tile), true};
+    }
+    const int64_t tile = std::max(kExTile, (slots + kSortBlocks - 1) / kSortBlocks);
+    return {tile, static_cast<int>((slots + tile - 1) / tile), threads_for(tile), false};
 }
 
 // A slot's expert, or -1 where it goes nowhere; a bad one is reported.
@@ -97,52 +115,94 @@ __global__ void __launch_bounds__(kExBlock) k_expert_scan(uint32_t* __restrict__
     if (lane == 0) totals[e] = run;
 }
 
-// counts, totals: nullptr where one block has all slots.
-__global__ void __launch_bounds__(kExBlock) k_expert_place(const int64_t* __restrict__ expert, int64_t slots,
-                                                           int experts, int64_t tile,
-                                                           const uint32_t* __restrict__ counts,
-                                                           const uint32_t* __restrict__ totals,
-                                                           int64_t* __restrict__ offsets, int32_t* __restrict__ src,
-                                                           int32_t* __restrict__ pos, int32_t* d_err)
+// Exclusive scan of one value a thread over the block; *total: the block's sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* tmp, uint32_t* total)
 {
-    pdl_wait();   // writes caller outputs
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t incl = warp_incl_scan(x, lane);
+    if (lane == 31) tmp[warp] = incl;
+    __syncthreads();
+    const uint32_t w = lane < warps ? tmp[lane] : 0u;
+    const uint32_t wi = warp_incl_scan(w, lane);
+    const uint32_t before = __shfl_sync(kFull, wi - w, warp);
+    *total = __shfl_sync(kFull, wi, 31);
+    __syncthreads();
+    return before + incl - x;
+}
+
+// counts, totals: of every tile, where the tiles are not one cluster's (else nullptr).
+__global__ void __launch_bounds__(1024) k_expert_sort(const int64_t* __restrict__ expert, int64_t slots, int experts,
+                                                      int64_t tile, const uint32_t* __restrict__ counts,
+                                                      const uint32_t* __restrict__ totals,
+                                                      int64_t* __restrict__ offsets, int32_t* __restrict__ src,
+                                                      int32_t* __restrict__ pos, int32_t* d_err)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x, warps = threads >> 5;
     extern __shared__ uint32_t sh[];
-    uint32_t* cnt = sh;                              // [kExWarps][experts]: the warps' counts, then next places
-    uint32_t* bits = sh + kExWarps * experts;        // [kExWarps][experts]: lanes of the present 32 slots
-    __shared__ uint32_t scan[kExWarps + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int q = threadIdx.x; q < 2 * kExWarps * experts; q += kExBlock) sh[q] = 0;
+    uint32_t* cnt = sh;                          // [warps][experts]: the warps' counts, then next places
+    uint32_t* bits = sh + warps * experts;       // [warps][experts]: lanes of the present 32 slots
+    uint32_t* mine_all = bits + warps * experts; // [experts]: the block's counts, for its cluster
+    __shared__ uint32_t scan[32];
+    for (int q = threadIdx.x; q < 2 * warps * experts; q += threads) sh[q] = 0;
+    pdl_wait();   // writes caller outputs
     __syncthreads();
 
-    const int64_t s0 = tile * blockIdx.x, s1 = min(s0 + tile, slots);
-    const int64_t w0 = min(s0 + tile / kExWarps * warp, s1), w1 = min(w0 + tile / kExWarps, s1);
+    const int64_t s0 = min(tile * blockIdx.x, slots), s1 = min(s0 + tile, slots);
+    const int64_t run_len = ((tile + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t w0 = min(s0 + run_len * warp, s1), w1 = min(w0 + run_len, s1);
     uint32_t* mine = cnt + warp * experts;
     uint32_t* word = bits + warp * experts;
-#pragma unroll 4
-    for (int64_t s = w0 + lane; s < w1; s += 32) {
+    int held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int64_t s = w0 + 32 * i + lane;
+        held[i] = s < w1 ? slot_expert(expert, s, experts, d_err) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (held[i] >= 0) atomicAdd(&mine[held[i]], 1u);
+    for (int64_t s = w0 + 32 * kHeld + lane; s < w1; s += 32) {
         const int e = slot_expert(expert, s, experts, d_err);
         if (e >= 0) atomicAdd(&mine[e], 1u);
     }
     __syncthreads();
+    const bool cluster = counts == nullptr && gridDim.x > 1;
+    const int rank = cluster ? static_cast<int>(cluster_rank()) : 0;
+    if (counts == nullptr) {
+        for (int e = threadIdx.x; e < experts; e += threads) {
+            uint32_t v = 0;
+            for (int w = 0; w < warps; ++w) v += cnt[w * experts + e];
+            mine_all[e] = v;
+        }
+        if (cluster) cluster_sync();   // alone, a lane reads the counts that it wrote
+    }
 
     // first places: experts before this one, tiles before this one, warps before this one
     uint32_t run = 0;
-    for (int e0 = 0; e0 < experts; e0 += kExBlock) {
+    for (int e0 = 0; e0 < experts; e0 += threads) {
         const int e = e0 + threadIdx.x;
-        uint32_t all = 0;
+        uint32_t all = 0, tiles_before = 0;
         if (e < experts) {
-            if (totals != nullptr)
+            if (counts != nullptr) {
                 all = totals[e];
-            else
-                for (int w = 0; w < kExWarps; ++w) all += cnt[w * experts + e];
+                tiles_before = counts[static_cast<int64_t>(e) * gridDim.x + blockIdx.x];
+            } else if (!cluster) {
+                all = mine_all[e];
+            } else {
+                for (int r = 0; r < static_cast<int>(gridDim.x); ++r) {
+                    const uint32_t v = lds_cluster_u32(cluster_addr(smem_addr(mine_all + e), r));
+                    all += v;
+                    tiles_before += r < rank ? v : 0u;
+                }
+            }
         }
         uint32_t sum;
-        const uint32_t before = run + block_excl_scan(all, scan, &sum);
+        const uint32_t before = run + block_scan(all, scan, &sum);
         run += sum;
         if (e < experts) {
             if (blockIdx.x == 0) offsets[e] = before;
-            uint32_t at = before + (counts ? counts[static_cast<int64_t>(e) * gridDim.x + blockIdx.x] : 0u);
-            for (int w = 0; w < kExWarps; ++w) {
+            uint32_t at = before + tiles_before;
+            for (int w = 0; w < warps; ++w) {
                 const uint32_t v = cnt[w * experts + e];
                 cnt[w * experts + e] = at;
                 at += v;
@@ -150,22 +210,24 @@ __global__ void __launch_bounds__(kExBlock) k_expert_place(const int64_t* __rest
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) offsets[experts] = run;
-    __syncthreads();
+    if (cluster)
+        cluster_sync();   // every block has read the others' counts
+    else
+        __syncthreads();
 
-    for (int64_t s = w0; s < w1; s += 32) {
+    auto place = [&](int64_t s, int e) {   // 32 slots from s on, this lane's of expert e
         const bool in = s + lane < w1;
-        const int e = in ? slot_expert(expert, s + lane, experts, d_err) : -1;
         if (e >= 0) atomicOr(&word[e], 1u << lane);
         __syncwarp();
         const uint32_t same = e >= 0 ? word[e] : 0u;
         const uint32_t first = e >= 0 ? mine[e] : 0u;
         __syncwarp();
         if (e >= 0) {
-            const int rank = __popc(same & ((1u << lane) - 1u));
-            const int32_t p = static_cast<int32_t>(first) + rank;
+            const int rank_of = __popc(same & ((1u << lane) - 1u));
+            const int32_t p = static_cast<int32_t>(first) + rank_of;
             pos[s + lane] = p;
             if (src) src[p] = static_cast<int32_t>(s + lane);
-            if (rank == 0) {
+            if (rank_of == 0) {
                 word[e] = 0u;
                 mine[e] = first + __popc(same);
             }
@@ -173,10 +235,15 @@ __global__ void __launch_bounds__(kExBlock) k_expert_place(const int64_t* __rest
             pos[s + lane] = -1;
         }
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (w0 + 32 * i < w1) place(w0 + 32 * i, held[i]);
+    for (int64_t s = w0 + 32 * kHeld; s < w1; s += 32)
+        place(s, s + lane < w1 ? slot_expert(expert, s + lane, experts, d_err) : -1);
     if (src)
-        for (int64_t p = run + static_cast<int64_t>(blockIdx.x) * kExBlock + threadIdx.x; p < slots;
-             p += static_cast<int64_t>(gridDim.x) * kExBlock)
+        for (int64_t p = run + static_cast<int64_t>(blockIdx.x) * threads + threadIdx.x; p < slots;
+             p += static_cast<int64_t>(gridDim.x) * threads)
             src[p] = -1;
 }
 
@@ -263,7 +330,7 @@ __global__ void __launch_bounds__(kExBlock) k_expert_combine(const T* __restrict
                                                              int32_t* d_err)
 {
     pdl_wait();   // writes a caller output
-    constexpr int J = 4, R = V == 1 ? 4 : 1;
+    constexpr int J = 4, R = V == 1 ? 4 : 2;
     const int gl = threadIdx.x & (G - 1);
     const int64_t group = static_cast<int64_t>(blockIdx.x) * (kExBlock / G) + threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kExBlock / G);
@@ -305,81 +372,105 @@ __global__ void __launch_bounds__(kExBlock) k_expert_combine(const T* __restrict
         }
 }
 
-template <class T, int V>
+// A warp has one token: it holds 32 R accesses of dy while the rows of up to kMany slots go by, J
+// at a time, and carries those slots' dot products along.
+template <class T, int V, bool kWeights>
 __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ dy, const T* __restrict__ ys, int64_t n,
                                                           int k, int c, const int32_t* __restrict__ pos,
                                                           const int64_t* __restrict__ end,
                                                           const float* __restrict__ w, T* __restrict__ dys,
-                                                          float* __restrict__ dw, int G, int32_t* d_err)
+                                                          float* __restrict__ dw, int32_t* d_err)
 {
     pdl_wait();   // writes caller outputs
-    constexpr int J = 4, R = V == 1 ? 4 : 1;
-    __shared__ float tmp[2 * 32 * J];
-    const int gl = threadIdx.x & (G - 1);
-    const int groups = kExBlock / G, sub = threadIdx.x / G;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    constexpr int J = 2, R = V == 1 ? 8 : 4, kMany = 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kExWarps + (threadIdx.x >> 5);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kExWarps;
     const int64_t slots = n * k;
-    int half = 0;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < n; base += step) {   // block-uniform trips
-        const int64_t t = base + sub;
+    for (int64_t t = first; t < n; t += step) {
         const T* from = dy + t * c;
-        for (int j0 = 0; j0 < k; j0 += J) {
-            const T* row[J];
-            slot_rows(row, ys, c, pos, t < n ? t : 0, t < n ? k : 0, j0, slots, d_err);
-            float wj[J], dot[J];
+        for (int j0 = 0; j0 < k; j0 += kMany) {
+            int place[kMany];
+            float wj[kMany], dot[kMany];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                wj[j] = row[j] && w ? w[t * k + j0 + j] : 1.0f;
+            for (int j = 0; j < kMany; ++j) {
+                place[j] = j0 + j < k ? static_cast<int>(slot_place(pos, t * k + j0 + j, slots, d_err)) : -1;
+                wj[j] = kWeights && place[j] >= 0 ? w[t * k + j0 + j] : 1.0f;
                 dot[j] = 0.0f;
             }
-            if (t < n)
-                for (int c0 = gl * V; c0 < c; c0 += G * V * R) {
-                    Pack<T, V> d[R], r[J][R];
+            for (int c0 = 0; c0 < c; c0 += 32 * V * R) {
+                Pack<T, V> d[R];
 #pragma unroll
-                    for (int q = 0; q < R; ++q)
-                        if (c0 + q * G * V < c) {
-                            d[q].load(from + c0 + q * G * V);
+                for (int q = 0; q < R; ++q) {
+                    d[q].zero();
+                    const int col = c0 + (q * 32 + lane) * V;
+                    if (col < c) d[q].load(from + col);
+                }
 #pragma unroll
-                            for (int j = 0; j < J; ++j)
-                                if (row[j]) r[j][q].load(row[j] + c0 + q * G * V);
+                for (int j1 = 0; j1 < kMany; j1 += J) {
+                    if (j0 + j1 >= k) break;
+                    Pack<T, V> r[J][R];
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int q = 0; q < R; ++q) {
+                            const int col = c0 + (q * 32 + lane) * V;
+                            if (place[j1 + j] >= 0 && col < c) r[j][q].load(ys + static_cast<int64_t>(place[j1 + j]) * c + col);
                         }
 #pragma unroll
-                    for (int q = 0; q < R; ++q)
-                        if (c0 + q * G * V < c) {
-                            float dv[V];
-                            d[q].get(dv);
+                    for (int j = 0; j < J; ++j)
+                        if (place[j1 + j] >= 0) {
+                            T* to = dys + static_cast<int64_t>(place[j1 + j]) * c;
 #pragma unroll
-                            for (int j = 0; j < J; ++j)
-                                if (row[j]) {
-                                    float v[V];
+                            for (int q = 0; q < R; ++q) {
+                                const int col = c0 + (q * 32 + lane) * V;
+                                if (col < c) {
+                                    float dv[V], v[V];
+                                    d[q].get(dv);
                                     r[j][q].get(v);
 #pragma unroll
                                     for (int e = 0; e < V; ++e) {
-                                        dot[j] = fmaf(dv[e], v[e], dot[j]);
-                                        v[e] = wj[j] * dv[e];
+                                        dot[j1 + j] = fmaf(dv[e], v[e], dot[j1 + j]);
+                                        v[e] = wj[j1 + j] * dv[e];
                                     }
-                                    Pack<T, V>::put(dys + (row[j] - ys) + c0 + q * G * V, v);
+                                    Pack<T, V>::put(to + col, v);
                                 }
+                            }
                         }
                 }
+            }
             if (dw == nullptr) continue;
-            group_sum<J>(dot, G, tmp, half);
-            half ^= 1;
-            if (t < n && gl == 0)
+            // eight sums by butterflies that halve what a lane carries: lane 4 j ends with slot j's
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (j0 + j < k) dw[t * k + j0 + j] = row[j] ? dot[j] : 0.0f;
+            for (int h = kMany / 2, s = 16; h > 0; h >>= 1, s >>= 1) {
+                const bool up = lane & s;
+#pragma unroll
+                for (int i = 0; i < h; ++i) {
+                    const float give = up ? dot[i] : dot[i + h];
+                    dot[i] = (up ? dot[i + h] : dot[i]) + __shfl_xor_sync(kFull, give, s);
+                }
+            }
+            dot[0] += __shfl_xor_sync(kFull, dot[0], 2);
+            dot[0] += __shfl_xor_sync(kFull, dot[0], 1);
+            const int j = lane / 4;
+            if (lane % 4 == 0 && j0 + j < k) dw[t * k + j0 + j] = dot[0];   // 0 for a slot that goes nowhere
         }
     }
-    clear_tail<T, V>(dys, c, slots, end, G, gl, static_cast<int64_t>(blockIdx.x) * groups + sub, step);
+    clear_tail<T, V>(dys, c, slots, end, 32, lane, first, step);
 }
 
-// Lanes of a group: a power of two, `per` accesses of a row each where it is wide enough.
+// Lanes of a group: a power of two that walks a row of `accesses` with the fewest idle ones, `per` a
+// lane at a time; of equals the widest.
 int lanes_for(int64_t accesses, int per)
 {
-    int G = 1;
-    while (G < kExBlock && static_cast<int64_t>(G) * per < accesses) G *= 2;
-    return G;
+    int best = kExBlock;
+    int64_t least = INT64_MAX;
+    for (int G = kExBlock; G >= 8; G /= 2) {
+        const int64_t all = (accesses + static_cast<int64_t>(G) * per - 1) / (static_cast<int64_t>(G) * per) * G;
+        if (all < least) best = G, least = all;
+    }
+    while (best > 1 && best / 2 >= accesses) best /= 2;
+    return best;
 }
 
 // Resident blocks of a row kernel at most.
@@ -398,25 +489,23 @@ int row_blocks(int most, int64_t rows, int G)
         1, std::min<int64_t>((rows + groups - 1) / groups, static_cast<int64_t>(most) * num_sms())));
 }
 
-size_t place_smem(int64_t experts) { return sizeof(uint32_t) * static_cast<size_t>(2 * kExWarps * experts); }
-
 }  // namespace
 
 size_t expert_ws_bytes(int64_t slots, int64_t experts)
 {
-    const SortShape S = sort_shape(slots);
-    return sizeof(uint32_t) * static_cast<size_t>(experts) * static_cast<size_t>(S.blocks + 1);
+    const SortShape S = sort_shape(slots, experts);
+    return S.cluster ? 0 : sizeof(uint32_t) * static_cast<size_t>(experts) * static_cast<size_t>(S.blocks + 1);
 }
 
 cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, int64_t* offsets, int32_t* src,
                         int32_t* pos, void* ws, int32_t* d_err, cudaStream_t s)
 {
-    const SortShape S = sort_shape(slots);
-    uint32_t* counts = S.blocks > 1 ? static_cast<uint32_t*>(ws) : nullptr;
-    uint32_t* totals = S.blocks > 1 ? counts + experts * S.blocks : nullptr;
+    const SortShape S = sort_shape(slots, experts);
+    uint32_t* counts = S.cluster ? nullptr : static_cast<uint32_t*>(ws);
+    uint32_t* totals = S.cluster ? nullptr : counts + experts * S.blocks;
     const int E = static_cast<int>(experts);
-    cudaError_t e = cudaSuccess;
-    if (S.blocks > 1) {
+    if (!S.cluster) {
+        cudaError_t e;
         {
             SO_PROFILE("expert_count", s);
             e = launch_smem(k_expert_count, dim3(S.blocks), dim3(kExBlock), sizeof(uint32_t) * experts, s, expert,
@@ -427,15 +516,25 @@ cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, i
         e = launch(k_expert_scan, dim3((E + kExWarps - 1) / kExWarps), dim3(kExBlock), s, counts, E, S.blocks, totals);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = place_smem(experts);
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    SO_PROFILE("expert_place", s);
-    return launch_smem(k_expert_place, dim3(S.blocks), dim3(kExBlock), smem, s, expert, slots, E, S.tile,
-                       static_cast<const uint32_t*>(counts), static_cast<const uint32_t*>(totals), offsets, src, pos,
-                       d_err);
+    static const cudaError_t ready = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (ready != cudaSuccess) return ready;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S.blocks);
+    cfg.blockDim = dim3(S.threads);
+    cfg.dynamicSmemBytes = sort_smem(S.threads, experts);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S.cluster ? S.blocks : 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    SO_PROFILE("expert_sort", s);
+    return cudaLaunchKernelEx(&cfg, k_expert_sort, expert, slots, E, S.tile, static_cast<const uint32_t*>(counts),
+                              static_cast<const uint32_t*>(totals), offsets, src, pos, d_err);
 }
 
 template <class U>
@@ -462,7 +561,7 @@ template <class T, int V>
 static cudaError_t run_combine(const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos, const float* w,
                                void* y, int32_t* d_err, cudaStream_t s)
 {
-    const int G = lanes_for(c / V, V == 1 ? 4 : 1);
+    const int G = lanes_for(c / V, V == 1 ? 4 : 2);
     static const int most = resident(k_expert_combine<T, V>);
     SO_PROFILE("expert_combine", s);
     return launch(k_expert_combine<T, V>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
@@ -479,16 +578,22 @@ cudaError_t expert_combine(const void* ys, int is_bf16, int64_t n, int64_t k, in
                : run_combine<float, 1>(ys, n, k, c, pos, w, y, d_err, s);
 }
 
+template <class T, int V, bool kWeights>
+static cudaError_t run_grad_w(const void* dy, const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos,
+                              const int64_t* end, const float* w, void* dys, float* dw, int32_t* d_err, cudaStream_t s)
+{
+    static const int most = resident(k_expert_grad<T, V, kWeights>);
+    SO_PROFILE("expert_combine_grad", s);
+    return launch(k_expert_grad<T, V, kWeights>, dim3(row_blocks(most, n, 32)), dim3(kExBlock), s,
+                  static_cast<const T*>(dy), static_cast<const T*>(ys), n, static_cast<int>(k), static_cast<int>(c), pos, end, w,
+                  static_cast<T*>(dys), dw, d_err);
+}
 template <class T, int V>
 static cudaError_t run_grad(const void* dy, const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos,
                             const int64_t* end, const float* w, void* dys, float* dw, int32_t* d_err, cudaStream_t s)
 {
-    const int G = lanes_for(c / V, V == 1 ? 4 : 1);
-    static const int most = resident(k_expert_grad<T, V>);
-    SO_PROFILE("expert_combine_grad", s);
-    return launch(k_expert_grad<T, V>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
-                  static_cast<const T*>(dy), static_cast<const T*>(ys), n, static_cast<int>(k), static_cast<int>(c), pos, end, w, static_cast<T*>(dys), dw,
-                  G, d_err);
+    return w ? run_grad_w<T, V, true>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
+             : run_grad_w<T, V, false>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s);
 }
 
 cudaError_t expert_combine_grad(const void* dy, const void* ys, int is_bf16, int64_t n, int64_t k, int64_t c,

@@ -34,8 +34,7 @@ constexpr int kBM = 128, kBK = 64;              // rows of a block's tile; K val
 constexpr int kBox = 64;                        // rows of one copied box: 64 x 128 bytes
 constexpr uint32_t kBoxBytes = kBox * kBK * 2;
 constexpr int kSub = 64;                        // columns the epilogue finishes at a time
-constexpr int kThreads = 192;                   // copy warp, product warp, 4 epilogue warps
-constexpr int kEpilogue = 128;
+constexpr int kGroup = 128;                     // threads of an epilogue group
 constexpr int64_t kNormParts = 512;             // partial sums of squares of a matrix at most
 
 // ------------------------------------------------------------------- start
@@ -171,13 +170,14 @@ struct Shape {
     static constexpr uint32_t kB = BN / kPair / kBox * kBoxBytes;
     static constexpr int kParts = P == 3 ? 2 : 1;
     static constexpr uint32_t kStage = kParts * (kA + kB);
-    // Epilogue: kSub columns of the tile, hi and lo (128 x 64 each); mirror images of the symmetric
-    // kinds; the fp32 update of kFinal.
+    // Epilogue: groups of 4 warps, each with a set of its own for 64 columns of a tile: hi and lo
+    // (128 x 64 each; one product's symmetric results: hi and its mirror image).
     static constexpr uint32_t kSubBytes = kBM / kBox * kBoxBytes;
-    static constexpr int kSets = kKind == kFinal || (kSym && P == 3) ? 1 : 2;   // sets of them: one is copied while one is worked on
-    static constexpr uint32_t kSet = kSubBytes * (kKind == kFinal ? 4 : kSym ? 2 * kParts : 2);
-    static constexpr int kStages = static_cast<int>((224 * 1024 - kSets * kSet) / kStage);
-    static constexpr uint32_t kSmem = kStages * kStage + kSets * kSet + 1024;   // + alignment
+    static constexpr int kGroups = P == 3 ? 2 : 3;
+    static constexpr int kThreads = 64 + kGroups * kGroup;                 // copy warp, product warp, groups
+    static constexpr uint32_t kSet = 2 * kSubBytes;
+    static constexpr int kStages = static_cast<int>((224 * 1024 - kGroups * kSet) / kStage);
+    static constexpr uint32_t kSmem = kStages * kStage + kGroups * kSet + 1024;   // + alignment
     static constexpr int kAccs = P == 3 ? 512 / BN : 2;                    // accumulators in tensor memory
     // Stages that one accumulator sums.  The unit rounds every sum towards zero: with three products
     // the 940 sums of K = 5000 were off by 6e-5 of the result, so every 24 sums (128 K values, a
@@ -211,9 +211,17 @@ __device__ __forceinline__ void tile_at(const Product& Q, int64_t t, int& mat, i
     }
 }
 
-// 32 columns of a warp's rows of the update from shared memory (`stage`: the warp's 32 rows of
-// 64 fp32 values, 16-byte pieces permuted by row) to where they belong, row by row.
-__device__ __forceinline__ void put_rows(const Product& Q, uint32_t stage, int64_t mat, int row0, int col0, int lane)
+// Where column `col` of a row's 64 fp32 results lies in a set: the first four of each eight in the
+// hi part's 16 bytes of those columns, the others in the lo part's, as the term that they replace.
+__device__ __forceinline__ uint32_t result_at(int row, int col)
+{
+    return ((col >> 2) & 1) * (kBM / kBox * kBoxBytes) + (row >> 6) * kBoxBytes + (row & 63) * 128 +
+           (((col >> 3) ^ (row & 7)) << 4) + (col & 3) * 4;
+}
+
+// A warp's 32 rows (from `rowl` of the tile on) of 64 columns of the update from a set to where they
+// belong, row by row.
+__device__ __forceinline__ void put_rows(const Product& Q, uint32_t set, int rowl, int64_t mat, int row0, int col0, int lane)
 {
     const int rows = min(32, static_cast<int>(Q.m) - row0);
     const int64_t c = Q.n;
@@ -228,7 +236,7 @@ __device__ __forceinline__ void put_rows(const Product& Q, uint32_t stage, int64
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = r0 + i, col = lane + 32 * h;
-                v[i][h] = lds32(stage + r * 256 + (((col >> 2) ^ (r & 7)) << 4) + (col & 3) * 4);
+                v[i][h] = lds32(set + result_at(rowl + r, col));
                 w[i][h] = Q.w && in[h] && r < rows ? Q.w[at + r * c + col] : 0.0f;
             }
 #pragma unroll
@@ -272,22 +280,37 @@ __device__ __forceinline__ void put_columns(const Product& Q, int64_t mat, int r
     }
 }
 
+// Eight columns of a lane's row (piece `p` of its 64) into the mirror image's 128 x 64 part: a column
+// is a 128-byte row of the box that has this lane's 64 rows.
+__device__ __forceinline__ void put_image(uint32_t part, int rowl, int p, uint4 v)
+{
+    const uint32_t box = part + (rowl >> 6) * kBoxBytes + (rowl & 7) * 2;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int y = p * 8 + e;
+        sts16(box + y * 128 + ((((rowl & 63) >> 3) ^ (y & 7)) << 4), reinterpret_cast<const uint16_t*>(&v)[e]);
+    }
+}
+
 // One block an SM (or one pair of blocks on two), tiles in turn: warp 0 copies A and B
 // boxes of 64 K values into a ring of stages, warp 1 (of the pair's first block) issues
-// the products into one of the accumulators, warps 2 to 5 finish another, 64 columns at a
-// time: the added term arrives in shared memory by tensor copies, the result replaces it
-// there and leaves the same way, so every access of the matrices is whole lines.  A is
-// K-major; B is K-major too (rows of the symmetric factor) or, for B X, MN-major (X as it
-// lies).  In shared memory every box has 64 rows of 128 bytes, 16-byte pieces permuted
-// by row (the copies' 128-byte swizzle).
+// the products into one of the accumulators, groups of four warps finish others, each
+// 64 columns at a time: the added term arrives in the group's set in shared memory by
+// tensor copies, the result replaces it there and leaves the same way, so every access
+// of the matrices is whole lines.  The groups take the pieces in turn, so one computes
+// while the others' copies are on their way.  A is K-major; B is K-major too (rows of
+// the symmetric factor) or, for B X, MN-major (X as it lies).  In shared memory every
+// box has 64 rows of 128 bytes, 16-byte pieces permuted by row (the copies' 128-byte
+// swizzle).
 template <int kKind, int kPair, int BN, int P>
-__global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_constant__ Maps maps, const Product Q)
+__global__ void __launch_bounds__(Shape<kKind, kPair, BN, P>::kThreads, 1)
+    k_muon_product(const __grid_constant__ Maps maps, const Product Q)
 {
     using S = Shape<kKind, kPair, BN, P>;
     constexpr bool kSym = S::kSym, kBmn = !S::kSym, kTerm = kKind != kGram;
     constexpr int kStages = S::kStages, TM = kBM * kPair;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * kStages + 2 * S::kAccs + 1 + 2];
+    __shared__ uint64_t bars[2 * kStages + 2 * S::kAccs + 1 + S::kGroups];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     const uint32_t data = (smem_addr(raw) + 1023u) & ~1023u;
@@ -301,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_const
     if (threadIdx.x == 0) {
         dead = 0;
         for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
-        for (int s = 0; s < S::kAccs; ++s) mbar_init(tfull + 8 * s, 1), mbar_init(tempty + 8 * s, 4 * kPair);
+        for (int s = 0; s < S::kAccs; ++s) mbar_init(tfull + 8 * s, 1), mbar_init(tempty + 8 * s, 4 * S::kGroups * kPair);
         mbar_init(drain, 1);
-        for (int s = 0; s < 2; ++s) mbar_init(term + 8 * s, 1);
+        for (int s = 0; s < S::kGroups; ++s) mbar_init(term + 8 * s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<kPair>(&tmem_slot, S::kAccs * BN);
@@ -401,162 +424,173 @@ __global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_const
             }
         }
     } else {
+        constexpr int kGroups = S::kGroups;
+        const int group = (warp - 2) >> 2, id = 1 + group;
         const int rowl = (warp & 3) * 32 + lane;   // the tensor memory lanes this warp can read
         const int xr = rowl & 7;
         const uint32_t mine = (rowl >> 6) * kBoxBytes + (rowl & 63) * 128;   // this lane's row of a 128 x 64 part
-        const bool head = warp == 2 && lane == 0;                            // issues the epilogue's copies
+        const bool head = warp == 2 + 4 * group && lane == 0;                // issues the group's copies
         const bool blocked = kKind == kFinal && Q.w != nullptr && read_error(Q.d_err) != 0;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        uint32_t done = 0, terms = 0;   // accumulators, sets used
-        // The term's next 64 columns into their set, once nothing leaves from there any more.
-        auto fetch = [&](uint32_t set, int col, int row0, int mat) {
-            const uint32_t at = sets + set * S::kSet, bar = term + 8 * set;
+        const uint32_t at = sets + group * S::kSet, bar = term + 8 * group;
+        // A tile's 64-column pieces that are wanted: inside the matrix, not above the diagonal.  They go
+        // to the groups in turn, `before` counting the earlier tiles' (three products: piece g to group g).
+        int mat = 0, row0 = 0, col0 = 0, pieces = 0, before = 0;
+        auto plan = [&](int64_t t) {
+            before = (before + pieces) % kGroups;
+            pieces = 0;
+            if (t >= Q.all) return;
+            tile_at<TM, BN, kSym>(Q, t, mat, row0, col0);
+            row0 += rank * kBM;
+            const int cols = kSym ? min(row0 + kBM, static_cast<int>(Q.m)) : static_cast<int>(Q.n);
+            pieces = row0 < Q.m ? max(0, min(BN / kSub, (cols - col0 + kSub - 1) / kSub)) : 0;
+        };
+        auto first_piece = [&] { return P == 3 ? group : (group - before + kGroups) % kGroups; };
+        // The term of piece j into the set, once nothing leaves from there any more.
+        auto fetch = [&](int j) {
             tma_store_read<0>();
             mbar_expect(bar, S::kSubBytes * (Q.rlo ? 2 : 1));
             for (int q = 0; q < kBM / kBox; ++q) {
-                tma_load<1>(at + q * kBoxBytes, &maps.rhi, bar, col, row0 + q * kBox, mat);
-                if (Q.rlo) tma_load<1>(at + S::kSubBytes + q * kBoxBytes, &maps.rlo, bar, col, row0 + q * kBox, mat);
+                tma_load<1>(at + q * kBoxBytes, &maps.rhi, bar, col0 + j * kSub, row0 + q * kBox, mat);
+                if (Q.rlo) tma_load<1>(at + S::kSubBytes + q * kBoxBytes, &maps.rlo, bar, col0 + j * kSub, row0 + q * kBox, mat);
             }
         };
+        uint32_t done = 0, terms = 0;   // accumulators, terms used
         bool ok = true;
+        plan(first);
+        if (kTerm && head && first_piece() < pieces) fetch(first_piece());
         for (int64_t t = first; ok && t < Q.all; t += step) {
-            int mat, row0, col0;
-            tile_at<TM, BN, kSym>(Q, t, mat, row0, col0);
-            row0 += rank * kBM;
-            // 64-column pieces of this tile that are wanted: inside the matrix, not above the diagonal
-            const int cols = kSym ? min(row0 + kBM, static_cast<int>(Q.m)) : static_cast<int>(Q.n);
-            const int pieces = row0 < Q.m ? min(BN / kSub, (cols - col0 + kSub - 1) / kSub) : 0;
-            if (kTerm && head && pieces > 0) fetch(terms % S::kSets, col0, row0, mat);
-            float sum[P == 3 ? BN / 32 : 1][32];
+            float sum[P == 3 ? 2 : 1][32];
             uint32_t acc = done % S::kAccs;
             if (P == 3) {
                 for (int c = 0; c < chunks; c += S::kChunk, ++done) {
                     acc = done % S::kAccs;
-                    if (!(ok = all_of(1, kEpilogue, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead)))) break;
+                    if (!(ok = all_of(id, kGroup, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead)))) break;
                     tc_fence_after();
+                    if (group * kSub < BN) {
 #pragma unroll
-                    for (int q = 0; q < (P == 3 ? BN / 32 : 0); ++q) {
-                        float v[32];
-                        tmem_load32(lanes + acc * BN + q * 32, v);
+                        for (int q = 0; q < (P == 3 ? 2 : 0); ++q) {
+                            float v[32];
+                            tmem_load32(lanes + acc * BN + group * kSub + q * 32, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) sum[q][e] = c ? sum[q][e] + v[e] : v[e];
+                            for (int e = 0; e < 32; ++e) sum[q][e] = c ? sum[q][e] + v[e] : v[e];
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty + 8 * acc, 0));
                 }
             } else {
-                ok = all_of(1, kEpilogue, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead));
+                ok = all_of(id, kGroup, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead));
                 tc_fence_after();
                 ++done;
             }
             if (!ok) break;
-#pragma unroll
-            for (int j = 0; j < BN / kSub; ++j) {
-                if (j < pieces) {
-                    const uint32_t set = terms % S::kSets, at = sets + set * S::kSet;
-                    const int col = col0 + j * kSub;
-                    if (kTerm) {
-                        ok = all_of(1, kEpilogue, mbar_wait(term + 8 * set, terms / S::kSets & 1, &dead));
-                        if (!ok) break;
-                        if (S::kSets == 2 && head && j + 1 < pieces) fetch(set ^ 1, col + kSub, row0, mat);
-                    } else {
-                        if (head) tma_store_read<S::kSets - 1>();   // the set's last results have left
-                        all_of(1, kEpilogue, true);
-                    }
+            for (int j = first_piece(); j < pieces; j += kGroups) {
+                const int col = col0 + j * kSub;
+                const bool more = j + kGroups < pieces;
+                if (kTerm) {
+                    ok = all_of(id, kGroup, mbar_wait(bar, terms & 1, &dead));
+                    if (!ok) break;
                     ++terms;
-                    const bool image = kSym && col + kSub <= row0;   // wholly below the diagonal block
+                } else {
+                    if (head) tma_store_read<0>();   // the set's last results have left
+                    all_of(id, kGroup, true);
+                }
+                const bool image = kSym && col + kSub <= row0;   // wholly below the diagonal block
+                uint4 khi[P == 3 && kSym ? 8 : 1], klo[P == 3 && kSym ? 8 : 1];   // kept for the image
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float v[32];
-                        if (P == 3) {
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    if (P == 3) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = sum[(2 * j + h) % (P == 3 ? BN / 32 : 1)][e];
-                        } else {
-                            tmem_load32(lanes + acc * BN + j * kSub + h * 32, v);
-                        }
+                        for (int e = 0; e < 32; ++e) v[e] = sum[P == 3 ? h : 0][e];
+                    } else {
+                        tmem_load32(lanes + acc * BN + j * kSub + h * 32, v);
+                    }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t piece = ((h * 4 + q) ^ xr) << 4;
-                            float x[8];
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t piece = ((h * 4 + q) ^ xr) << 4;
+                        float x[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = Q.mul * v[q * 8 + e];
-                            if (kTerm) {
-                                float r[8];
-                                unpack8(lds128(at + mine + piece), r);
+                        for (int e = 0; e < 8; ++e) x[e] = Q.mul * v[q * 8 + e];
+                        if (kTerm) {
+                            float r[8];
+                            unpack8(lds128(at + mine + piece), r);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.add, r[e], x[e]);
+                            if (Q.rlo) {
+                                unpack8(lds128(at + S::kSubBytes + mine + piece), r);
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.add, r[e], x[e]);
-                                if (Q.rlo) {
-                                    unpack8(lds128(at + S::kSubBytes + mine + piece), r);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.add, r[e], x[e]);
-                                }
-                            }
-                            if (kKind == kFinal) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) x[e] *= kInvScale;
-                                if (Q.tall) {
-                                    if (!blocked) put_columns(Q, mat, row0 + rowl, col + h * 32 + q * 8, x);
-                                } else {
-                                    const uint32_t to = at + 2 * S::kSubBytes + rowl * 256;
-                                    const int p4 = h * 8 + q * 2;
-                                    sts128(to + ((p4 ^ xr) << 4), make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
-                                                                             __float_as_uint(x[2]), __float_as_uint(x[3])));
-                                    sts128(to + (((p4 + 1) ^ xr) << 4), make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]),
-                                                                                   __float_as_uint(x[6]), __float_as_uint(x[7])));
-                                }
-                                continue;
-                            }
-                            uint4 hi, lo;
-                            __half2* hh = reinterpret_cast<__half2*>(&hi);
-                            __half2* ll = reinterpret_cast<__half2*>(&lo);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                hh[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
-                                const float2 f = __half22float2(hh[e]);
-                                ll[e] = __floats2half2_rn(x[2 * e] - f.x, x[2 * e + 1] - f.y);
-                            }
-                            constexpr bool kLo = P == 3 || !kSym;   // one product's symmetric results have no lo part
-                            sts128(at + mine + piece, hi);
-                            if (kLo && Q.wlo) sts128(at + S::kSubBytes + mine + piece, lo);
-                            if (image) {   // column of the image: a 128-byte row of the box with this lane's 64 rows
-                                const uint32_t im = at + (kLo ? 2 : 1) * S::kSubBytes + (rowl >> 6) * kBoxBytes;
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int y = h * 32 + q * 8 + e;
-                                    const uint32_t o = y * 128 + ((((rowl & 63) >> 3) ^ (y & 7)) << 4) + (rowl & 7) * 2;
-                                    sts16(im + o, reinterpret_cast<const uint16_t*>(&hi)[e]);
-                                    if (kLo && Q.wlo) sts16(im + S::kSubBytes + o, reinterpret_cast<const uint16_t*>(&lo)[e]);
-                                }
                             }
                         }
-                    }
-                    if (kKind == kFinal) {
-                        __syncwarp();
-                        if (!Q.tall && !blocked && row0 + (warp & 3) * 32 < Q.m)
-                            put_rows(Q, at + 2 * S::kSubBytes + (warp & 3) * 32 * 256, mat, row0 + (warp & 3) * 32, col, lane);
-                        all_of(1, kEpilogue, true);   // every warp is done with the set
-                        if (head && j + 1 < pieces) fetch(0, col + kSub, row0, mat);
-                        continue;
-                    }
-                    fence_async_proxy();
-                    all_of(1, kEpilogue, true);
-                    if (head) {
-                        for (int q = 0; q < kBM / kBox; ++q) {
-                            tma_store(&maps.whi, at + q * kBoxBytes, col, row0 + q * kBox, mat);
-                            if (Q.wlo) tma_store(&maps.wlo, at + S::kSubBytes + q * kBoxBytes, col, row0 + q * kBox, mat);
-                        }
-                        if (image) {
-                            const uint32_t im = at + (P == 3 ? 2 : 1) * S::kSubBytes;
-                            for (int q = 0; q < kBM / kBox; ++q) {
-                                tma_store(&maps.whi, im + q * kBoxBytes, row0 + q * kBox, col, mat);
-                                if (Q.wlo) tma_store(&maps.wlo, im + S::kSubBytes + q * kBoxBytes, row0 + q * kBox, col, mat);
+                        if (kKind == kFinal) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] *= kInvScale;
+                            if (Q.tall) {
+                                if (!blocked) put_columns(Q, mat, row0 + rowl, col + h * 32 + q * 8, x);
+                            } else {   // see result_at
+                                sts128(at + mine + piece, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                                                     __float_as_uint(x[2]), __float_as_uint(x[3])));
+                                sts128(at + S::kSubBytes + mine + piece, make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]),
+                                                                                    __float_as_uint(x[6]), __float_as_uint(x[7])));
                             }
+                            continue;
                         }
-                        tma_store_commit();
-                        if (kTerm && S::kSets == 1 && j + 1 < pieces) fetch(0, col + kSub, row0, mat);
+                        uint4 hi, lo;
+                        __half2* hh = reinterpret_cast<__half2*>(&hi);
+                        __half2* ll = reinterpret_cast<__half2*>(&lo);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            hh[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+                            const float2 f = __half22float2(hh[e]);
+                            ll[e] = __floats2half2_rn(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+                        }
+                        sts128(at + mine + piece, hi);
+                        if ((P == 3 || !kSym) && Q.wlo) sts128(at + S::kSubBytes + mine + piece, lo);
+                        if (P == 3 && kSym) khi[h * 4 + q] = hi, klo[h * 4 + q] = lo;
+                        if (P == 1 && image) put_image(at + S::kSubBytes, rowl, h * 4 + q, hi);
                     }
                 }
+                if (kKind == kFinal) {
+                    __syncwarp();
+                    if (!Q.tall && !blocked && row0 + (warp & 3) * 32 < Q.m)
+                        put_rows(Q, at, (warp & 3) * 32, mat, row0 + (warp & 3) * 32, col, lane);
+                    fence_async_proxy();
+                    all_of(id, kGroup, true);   // every warp is done with the set
+                    if (head && more) fetch(j + kGroups);
+                    continue;
+                }
+                fence_async_proxy();
+                all_of(id, kGroup, true);
+                if (head) {
+                    for (int q = 0; q < kBM / kBox; ++q) {
+                        tma_store(&maps.whi, at + q * kBoxBytes, col, row0 + q * kBox, mat);
+                        if (Q.wlo) tma_store(&maps.wlo, at + S::kSubBytes + q * kBoxBytes, col, row0 + q * kBox, mat);
+                        if (P == 1 && image) tma_store(&maps.whi, at + S::kSubBytes + q * kBoxBytes, row0 + q * kBox, col, mat);
+                    }
+                    tma_store_commit();
+                }
+                if (P == 3 && image) {   // hi and lo fill the set: the image follows when they have left
+                    if (head) tma_store_read<0>();
+                    all_of(id, kGroup, true);
+#pragma unroll
+                    for (int p = 0; p < (P == 3 && kSym ? 8 : 0); ++p) {
+                        put_image(at, rowl, p, khi[p]);
+                        put_image(at + S::kSubBytes, rowl, p, klo[p]);
+                    }
+                    fence_async_proxy();
+                    all_of(id, kGroup, true);
+                    if (head) {
+                        for (int q = 0; q < kBM / kBox; ++q) {
+                            tma_store(&maps.whi, at + q * kBoxBytes, row0 + q * kBox, col, mat);
+                            tma_store(&maps.wlo, at + S::kSubBytes + q * kBoxBytes, row0 + q * kBox, col, mat);
+                        }
+                        tma_store_commit();
+                    }
+                }
+                if (kTerm && head && more) fetch(j + kGroups);
             }
             if (!ok) break;
             if (P != 3) {
@@ -564,6 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_muon_product(const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty + 8 * acc, 0));
             }
+            plan(t + step);
+            if (kTerm && head && first_piece() < pieces) fetch(first_piece());
         }
         if (head) tma_store_done();
     }
@@ -662,7 +698,7 @@ cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t b
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(Q.all, num_sms() / kPair) * kPair));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

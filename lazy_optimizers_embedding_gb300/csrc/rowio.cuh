@@ -22,15 +22,11 @@ struct F2 {
     __device__ __forceinline__ static F2 both(float a) { return of(a, a); }
     __device__ __forceinline__ float lo() const
     {
-        float a, b;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
-        return a;
+        return __uint_as_float(static_cast<uint32_t>(q));
     }
     __device__ __forceinline__ float hi() const
     {
-        float a, b;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
-        return b;
+        return __uint_as_float(static_cast<uint32_t>(q >> 32));
     }
     __device__ __forceinline__ float sum() const { return lo() + hi(); }
 };

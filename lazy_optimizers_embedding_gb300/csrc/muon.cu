@@ -35,31 +35,84 @@ constexpr int kBox = 64;                        // rows of one copied box: 64 x 
 constexpr uint32_t kBoxBytes = kBox * kBK * 2;
 constexpr int kSub = 64;                        // columns the epilogue finishes at a time
 constexpr int kGroup = 128;                     // threads of an epilogue group
-constexpr int64_t kNormParts = 512;             // partial sums of squares of a matrix at most
+constexpr int64_t kNormParts = 1024;            // partial sums of squares of a matrix at most
 
 // ------------------------------------------------------------------- start
 // Sums of squares of one matrix's pieces; a sum that is not finite is reported
-// before anything is written.
-template <bool kVec>
-__global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int64_t parts,
-                                                          float* __restrict__ part, int32_t* d_err)
+// before anything is written.  E: values of an access.
+template <int E>
+__global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int parts, float* __restrict__ part,
+                                                          int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and the error word only
     __shared__ float tmp[2 * 32];
-    const int64_t mat = blockIdx.x / parts, p = blockIdx.x % parts;
-    const int64_t base = mat * size;
+    const int mat = static_cast<int>(blockIdx.x) / parts, p = static_cast<int>(blockIdx.x) % parts;
+    const int64_t base = mat * size, step = static_cast<int64_t>(parts) * kMuonBlock * E;
+    constexpr int R = E == 1 ? 8 : 4;   // accesses a lane requests at once
     float s[1] = {0.0f};
-#pragma unroll 4
-    for (int64_t i = (p * kMuonBlock + threadIdx.x) * 4; i < size; i += parts * kMuonBlock * 4) {
-        float u[4], nb[4];
-        read_u4<kVec>(U, base + i, static_cast<int>(min(size - i, static_cast<int64_t>(4))), u, nb);
+    for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * E; i < size; i += R * step) {
+        float u[R][E], nb[E];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[0] = fmaf(u[e], u[e], s[0]);
+        for (int q = 0; q < R; ++q) {
+            if (i + q * step < size)
+                read_u<E>(U, base + i + q * step, u[q], nb);
+            else
+#pragma unroll
+                for (int e = 0; e < E; ++e) u[q][e] = 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[0] = fmaf(u[q][e], u[q][e], s[0]);
     }
     group_sum<1>(s, kMuonBlock, tmp, 0);
     if (threadIdx.x == 0) {
         part[blockIdx.x] = s[0];
-        if (!isfinite(s[0])) set_error(d_err, SPARSE_ERR_NON_FINITE);
+        if (!isfinite(s[0] * static_cast<float>(parts))) set_error(d_err, SPARSE_ERR_NON_FINITE);   // nor may the whole overflow
+    }
+}
+
+// X = u / (|u| + eps), scaled and split, and the new momentum buffer, where X lies as u does (wide,
+// whole 16-byte accesses): `pieces` blocks a matrix, 8 values an access.  (16 x 768 x 2048 bf16: TODO us.)
+__global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float* __restrict__ buf, int64_t size, int pieces,
+                                                                const float* __restrict__ part, int parts, float eps,
+                                                                __half* __restrict__ hi, __half* __restrict__ lo,
+                                                                int c, int64_t ldn, const int32_t* d_err)
+{
+    pdl_enter();   // writes the workspace and optimizer state only
+    __shared__ float sums[2 * 32];
+    if (buf != nullptr && read_error(d_err) != 0) return;   // set before this kernel: the same for every block
+    constexpr int R = 2;
+    const int mat = static_cast<int>(blockIdx.x) / pieces, p = static_cast<int>(blockIdx.x) % pieces;
+    const int64_t base = mat * size, step = static_cast<int64_t>(pieces) * kMuonBlock * 8;
+    const int64_t rows = size / c;
+    float scale = -1.0f;
+    for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += R * step) {
+        float u[R][8], nb[R][8];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (i + q * step < size) read_u<8>(U, base + i + q * step, u[q], nb[q]);
+        if (scale < 0.0f) scale = start_scale(part + static_cast<int64_t>(mat) * parts, parts, eps, sums);   // while those are on their way
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t at = i + q * step;
+            if (at >= size) continue;
+            if (buf) Pack<float, 8>::put(buf + base + at, nb[q]);
+            int64_t to = base + at;
+            if (ldn != c) to = (mat * rows + at / c) * ldn + at % c;
+            uint4 h, l;
+            __half2* hh = reinterpret_cast<__half2*>(&h);
+            __half2* ll = reinterpret_cast<__half2*>(&l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = u[q][2 * e] * scale, b = u[q][2 * e + 1] * scale;
+                hh[e] = __floats2half2_rn(a, b);
+                const float2 f = __half22float2(hh[e]);
+                ll[e] = __floats2half2_rn(a - f.x, b - f.y);
+            }
+            *reinterpret_cast<uint4*>(hi + to) = h;
+            if (lo) *reinterpret_cast<uint4*>(lo + to) = l;
+        }
     }
 }
 
@@ -67,25 +120,27 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
 // buffer.  One 64 x 64 tile of u at a time, four values a thread.
 template <bool kVec>
 __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __restrict__ buf, int64_t r, int64_t c,
-                                                           int64_t tiles_c, int64_t tiles, int64_t ntiles,
-                                                           const float* __restrict__ part, int64_t parts, float eps,
+                                                           int tiles_c, int tiles, int ntiles,
+                                                           const float* __restrict__ part, int parts, float eps,
                                                            __half* __restrict__ hi, __half* __restrict__ lo,
                                                            int64_t ldn, int tall, const int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and optimizer state only
     __shared__ float tile[64][65];
-    __shared__ double sums[kMuonBlock / 32];
+    __shared__ float sums[2 * 32];
     if (buf != nullptr && read_error(d_err) != 0) return;   // set before this kernel: the same for every block
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t m = tall ? c : r;
     int64_t have = -1;
     float scale = 0.0f;
     // neighbouring tiles by one block: few matrices, whose scales it has to work out
-    const int64_t t1 = ntiles * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t t = ntiles * blockIdx.x / gridDim.x; t < t1; ++t) {
-        const int64_t mat = t / tiles, q = t % tiles;
+    const int t1 = static_cast<int>(static_cast<int64_t>(ntiles) * (blockIdx.x + 1) / gridDim.x);
+    for (int t = static_cast<int>(static_cast<int64_t>(ntiles) * blockIdx.x / gridDim.x); t < t1; ++t) {
+        const int64_t mat = t / tiles;
+        const int q = t % tiles;
         const int64_t r0 = q / tiles_c * 64, c0 = q % tiles_c * 64;
         if (mat != have) {
+            if (have >= 0) __syncthreads();   // the last sums have been read
             scale = start_scale(part + mat * parts, parts, eps, sums);
             have = mat;
         }
@@ -647,7 +702,7 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 struct Layout {
     int64_t m, n, ldm, ldn;
-    int64_t parts;
+    int parts;
     size_t part, x[2][2], a[2], b[2], total;   // [.][0] hi, [.][1] lo
 };
 
@@ -656,9 +711,9 @@ Layout muon_layout(int64_t batch, int64_t r, int64_t c, int products)
     Layout L{};
     L.m = std::min(r, c);
     L.n = std::max(r, c);
-    L.ldm = up(L.m, 8);
-    L.ldn = up(L.n, 8);
-    L.parts = std::min<int64_t>(kNormParts, std::max<int64_t>(1, r * c / 8192));
+    L.ldm = up(L.m, 64);   // rows start on 128-byte lines: copies of boxes read whole ones
+    L.ldn = up(L.n, 64);
+    L.parts = static_cast<int>(std::min<int64_t>(kNormParts, std::max<int64_t>(1, r * c / 8192)));
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t p = at;
@@ -808,26 +863,34 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
     const Update U{M.g, M.g_bf16, M.buf, M.momentum, M.nesterov};
     const int64_t size = M.r * M.cols;
     cudaError_t e;
-    // four values an access: rows, and so matrices, of a multiple of four, arrays aligned to match
-    const bool vec = M.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(M.g) & (M.g_bf16 ? 7u : 15u)) == 0 &&
-                     (reinterpret_cast<uintptr_t>(M.buf) & 15u) == 0;
+    // values of an access: rows, and so matrices, of a multiple of them, arrays aligned to match
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(M.buf) | reinterpret_cast<uintptr_t>(M.g);
+    const int values = M.cols % 8 == 0 && bits % 16 == 0 ? 8 : M.cols % 4 == 0 && bits % (M.g_bf16 && !M.buf ? 8 : 16) == 0 ? 4 : 1;
     {
         SO_PROFILE("muon_norm", s);
-        e = launch(vec ? k_muon_norm<true> : k_muon_norm<false>, dim3(static_cast<unsigned>(M.batch * L.parts)),
-                   dim3(kMuonBlock), s, U, size, L.parts, part, M.d_err);
+        e = launch(values == 8 ? k_muon_norm<8> : values == 4 ? k_muon_norm<4> : k_muon_norm<1>,
+                   dim3(static_cast<unsigned>(M.batch * L.parts)), dim3(kMuonBlock), s, U, size, L.parts, part, M.d_err);
     }
     if (e != cudaSuccess) return e;
-    if (muon_fits_cluster(M.batch, L.m, L.n)) return muon_cluster(M, U, part, L.parts, vec, s);
+    if (muon_fits_cluster(M.batch, L.m, L.n)) return muon_cluster(M, U, part, L.parts, values > 1, s);
     {
-        const int64_t tc = (M.cols + 63) / 64, tiles = (M.r + 63) / 64 * tc, all = tiles * M.batch;
         const bool lo = M.products == 3 || M.steps > 1;
+        __half* xhi = reinterpret_cast<__half*>(base + L.x[0][0]);
+        __half* xlo = lo ? reinterpret_cast<__half*>(base + L.x[0][1]) : nullptr;
         SO_PROFILE("muon_start", s);
-        e = launch(vec ? k_muon_start<true> : k_muon_start<false>,
-                   dim3(static_cast<unsigned>(std::min<int64_t>(all, 8 * num_sms()))), dim3(kMuonBlock), s, U, M.buf,
-                   M.r, M.cols, tc, tiles, all, static_cast<const float*>(part), L.parts, M.eps,
-                   reinterpret_cast<__half*>(base + L.x[0][0]),
-                   lo ? reinterpret_cast<__half*>(base + L.x[0][1]) : static_cast<__half*>(nullptr), L.ldn,
-                   M.r > M.cols ? 1 : 0, static_cast<const int32_t*>(M.d_err));
+        if (values == 8 && M.r <= M.cols) {
+            const int pieces = static_cast<int>(std::max<int64_t>(1, size / (kMuonBlock * 8 * 4)));
+            e = launch(k_muon_start_flat, dim3(static_cast<unsigned>(M.batch * pieces)), dim3(kMuonBlock), s, U, M.buf, size,
+                       pieces, static_cast<const float*>(part), L.parts, M.eps, xhi, xlo, static_cast<int>(M.cols), L.ldn,
+                       static_cast<const int32_t*>(M.d_err));
+        } else {
+            const int64_t tc = (M.cols + 63) / 64, tiles = (M.r + 63) / 64 * tc, all = tiles * M.batch;
+            e = launch(values > 1 ? k_muon_start<true> : k_muon_start<false>,
+                       dim3(static_cast<unsigned>(std::min<int64_t>(all, 8 * num_sms()))), dim3(kMuonBlock), s, U, M.buf,
+                       M.r, M.cols, static_cast<int>(tc), static_cast<int>(tiles), static_cast<int>(all),
+                       static_cast<const float*>(part), L.parts, M.eps, xhi, xlo, L.ldn, M.r > M.cols ? 1 : 0,
+                       static_cast<const int32_t*>(M.d_err));
+        }
     }
     if (e != cudaSuccess) return e;
     return M.products == 3 ? run_steps<3>(L, M, base, s) : run_steps<1>(L, M, base, s);

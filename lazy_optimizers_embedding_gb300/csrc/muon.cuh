@@ -23,40 +23,56 @@ struct Update {
     int nesterov;
 };
 
-// Four values of u from element i on (those below `left`), and the new buffer's.
+// E values of u from element i on (E = 1, or 4 or 8 by 16-byte accesses, 8-byte ones of 4 bf16), and
+// the new buffer's.
+template <int E>
+__device__ __forceinline__ void read_u(const Update& U, int64_t i, float (&u)[E], float (&nb)[E])
+{
+    float g[E], b[E];
+    if (U.g_bf16) {
+        const bf16* at = static_cast<const bf16*>(U.g) + i;
+        if constexpr (E == 4) {
+            const uint2 q = *reinterpret_cast<const uint2*>(at);
+            g[0] = __uint_as_float(q.x << 16), g[1] = __uint_as_float(q.x & 0xffff0000u);
+            g[2] = __uint_as_float(q.y << 16), g[3] = __uint_as_float(q.y & 0xffff0000u);
+        } else {
+            Pack<bf16, E> q;
+            q.load(at);
+            q.get(g);
+        }
+    } else {
+        Pack<float, E> q;
+        q.load(static_cast<const float*>(U.g) + i);
+        q.get(g);
+    }
+    if (U.buf) {
+        Pack<float, E> q;
+        q.load(U.buf + i);
+        q.get(b);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        nb[e] = U.buf ? fmaf(U.momentum, b[e], g[e]) : 0.0f;
+        u[e] = U.buf == nullptr ? g[e] : U.nesterov ? fmaf(U.momentum, nb[e], g[e]) : nb[e];
+    }
+}
+
+// Four values of u from element i on, those below `left` (the others 0), and the new buffer's.
 template <bool kVec>
 __device__ __forceinline__ void read_u4(const Update& U, int64_t i, int left, float (&u)[4], float (&nb)[4])
 {
-    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = nb[e] = 0.0f;
     if (kVec) {
-        if (left > 0) {
-            if (U.g_bf16) {
-                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(U.g) + i);
-                g[0] = __uint_as_float(q.x << 16), g[1] = __uint_as_float(q.x & 0xffff0000u);
-                g[2] = __uint_as_float(q.y << 16), g[3] = __uint_as_float(q.y & 0xffff0000u);
-            } else {
-                Pack<float, 4> q;
-                q.load(static_cast<const float*>(U.g) + i);
-                q.get(g);
-            }
-            if (U.buf) {
-                Pack<float, 4> q;
-                q.load(U.buf + i);
-                q.get(b);
-            }
-        }
+        if (left > 0) read_u<4>(U, i, u, nb);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (e < left) {
-                g[e] = U.g_bf16 ? __bfloat162float(static_cast<const bf16*>(U.g)[i + e]) : static_cast<const float*>(U.g)[i + e];
-                if (U.buf) b[e] = U.buf[i + e];
+                float u1[1], b1[1];
+                read_u<1>(U, i + e, u1, b1);
+                u[e] = u1[0], nb[e] = b1[0];
             }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        nb[e] = fmaf(U.momentum, b[e], g[e]);
-        u[e] = U.buf == nullptr ? g[e] : U.nesterov ? fmaf(U.momentum, nb[e], g[e]) : nb[e];
     }
 }
 
@@ -85,24 +101,20 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8])
     }
 }
 
-// Scale of one matrix from its `parts` sums of squares, by a block of kMuonBlock threads.
-__device__ __forceinline__ float start_scale(const float* part, int64_t parts, float eps, double* sums)
+// Scale of one matrix from its `parts` sums of squares, by a block of kMuonBlock threads (`tmp`: 64
+// words).  fp32: in fp64 the root and quotient alone held a block for 4 us.
+__device__ __forceinline__ float start_scale(const float* part, int parts, float eps, float* tmp)
 {
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < parts; i += kMuonBlock) s += part[i];
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = sums[0];
-    for (int w = 1; w < kMuonBlock / 32; ++w) s += sums[w];
-    return static_cast<float>(static_cast<double>(kScale) / (sqrt(s) + static_cast<double>(eps)));
+    float s[1] = {0.0f};
+    for (int i = threadIdx.x; i < parts; i += kMuonBlock) s[0] += part[i];
+    group_sum<1>(s, kMuonBlock, tmp, 0);
+    return kScale / (sqrtf(s[0]) + eps);
 }
 
 // Whether the matrices take the cluster path, and that path, once the sums of squares are on
 // their way (`vec`: 16-byte accesses of the update).
 bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n);
-cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int64_t parts, bool vec,
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int parts, bool vec,
                          cudaStream_t s);
 
 }  // namespace so

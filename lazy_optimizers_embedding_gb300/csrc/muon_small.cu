@@ -77,7 +77,7 @@ struct Small {
     int tall, steps;
     float a, b, c, eps;
     const float* part;
-    int64_t parts;
+    int parts;
     float* buf;
     void* out;
     int out_bf16;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
     __shared__ uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
-    __shared__ double sums[kMuonBlock / 32];
+    __shared__ float sums[2 * 32];
     const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes;
     const uint32_t bar = smem_addr(&bar_mem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -338,7 +338,7 @@ bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n)
     return m <= kRows && n <= kMaxCluster * kSlice && batch * cluster_blocks(n) <= 2 * num_sms();
 }
 
-cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int64_t parts, bool vec, cudaStream_t s)
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int parts, bool vec, cudaStream_t s)
 {
     Small Q{};
     Q.size = M.r * M.cols;

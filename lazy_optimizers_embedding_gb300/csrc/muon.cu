@@ -217,8 +217,8 @@ struct Product {
     int32_t* d_err;
 };
 
-// kPair blocks (a cluster) share a tile of 128 kPair rows x BN columns.
-template <int kKind, int kPair, int BN, int P>
+// kPair blocks (a cluster) share a tile of 128 kPair rows x BN columns; P products; G epilogue groups.
+template <int kKind, int kPair, int BN, int P, int G>
 struct Shape {
     static constexpr bool kSym = kKind == kGram || kKind == kPoly;
     static constexpr uint32_t kA = kBM / kBox * kBoxBytes;                 // one f16 part of A in a stage
@@ -228,7 +228,7 @@ struct Shape {
     // Epilogue: groups of 4 warps, each with a set of its own for 64 columns of a tile: hi and lo
     // (128 x 64 each; one product's symmetric results: hi and its mirror image).
     static constexpr uint32_t kSubBytes = kBM / kBox * kBoxBytes;
-    static constexpr int kGroups = P == 3 ? 2 : 3;
+    static constexpr int kGroups = G;
     static constexpr int kThreads = 64 + kGroups * kGroup;                 // copy warp, product warp, groups
     static constexpr uint32_t kSet = 2 * kSubBytes;
     static constexpr int kStages = static_cast<int>((224 * 1024 - kGroups * kSet) / kStage);
@@ -357,11 +357,11 @@ __device__ __forceinline__ void put_image(uint32_t part, int rowl, int p, uint4 
 // the symmetric factor) or, for B X, MN-major (X as it lies).  In shared memory every
 // box has 64 rows of 128 bytes, 16-byte pieces permuted by row (the copies' 128-byte
 // swizzle).
-template <int kKind, int kPair, int BN, int P>
-__global__ void __launch_bounds__(Shape<kKind, kPair, BN, P>::kThreads, 1)
+template <int kKind, int kPair, int BN, int P, int G>
+__global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
     k_muon_product(const __grid_constant__ Maps maps, const Product Q)
 {
-    using S = Shape<kKind, kPair, BN, P>;
+    using S = Shape<kKind, kPair, BN, P, G>;
     constexpr bool kSym = S::kSym, kBmn = !S::kSym, kTerm = kKind != kGram;
     constexpr int kStages = S::kStages, TM = kBM * kPair;
     extern __shared__ uint8_t raw[];
@@ -740,11 +740,11 @@ int64_t tiles_of(int64_t m, int64_t n, int tm, int bn, bool sym)
     return t;
 }
 
-template <int kKind, int kPair, int BN, int P>
+template <int kKind, int kPair, int BN, int P, int G = 2>
 cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t batch, cudaStream_t s)
 {
-    using S = Shape<kKind, kPair, BN, P>;
-    auto* kernel = k_muon_product<kKind, kPair, BN, P>;
+    using S = Shape<kKind, kPair, BN, P, G>;
+    auto* kernel = k_muon_product<kKind, kPair, BN, P, G>;
     Q.tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym);
     Q.all = Q.tiles * batch;
     Q.cols_of_tiles = static_cast<int>((Q.n + BN - 1) / BN);
@@ -775,7 +775,7 @@ cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t b
 template <int kKind, int kPair, int BN, int P>
 int64_t shape_cost(const Product& Q, int64_t batch)
 {
-    using S = Shape<kKind, kPair, BN, P>;
+    using S = Shape<kKind, kPair, BN, P, 2>;
     const int64_t units = num_sms() / kPair;
     const int64_t tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym) * batch;
     return (tiles + units - 1) / units * std::max<int64_t>(2 * BN * P, S::kStage / 80);
@@ -784,11 +784,19 @@ int64_t shape_cost(const Product& Q, int64_t batch)
 template <int kKind, int P>
 cudaError_t run_kind(const char* name, const Maps& maps, const Product& Q, int64_t batch, cudaStream_t s)
 {
-    constexpr int kWide = P == 3 ? 128 : 256;
-    const int64_t wide = shape_cost<kKind, 2, kWide, P>(Q, batch), one = shape_cost<kKind, 1, 128, P>(Q, batch),
+    const int64_t wide = P == 1 ? shape_cost<kKind, 2, P == 1 ? 256 : 128, P>(Q, batch) : INT64_MAX;
+    const int64_t pair = shape_cost<kKind, 2, 128, P>(Q, batch), one = shape_cost<kKind, 1, 128, P>(Q, batch),
                   half = shape_cost<kKind, 1, 64, P>(Q, batch);
-    if (wide <= one && wide <= half) return run_product<kKind, 2, kWide, P>(name, maps, Q, batch, s);
-    if (one <= half) return run_product<kKind, 1, 128, P>(name, maps, Q, batch, s);
+    const int64_t least = std::min(std::min(wide, pair), std::min(one, half));
+    if (wide == least) {
+        // a short product's tile is finished in less time than two groups take over its results; a
+        // long one's fares better with a fifth stage in place of the third group's set
+        // (K = 768: 58 against 70 us; K = 4096: 118 against 108)
+        if (P == 1 && Q.k < 1024) return run_product<kKind, 2, P == 1 ? 256 : 128, P, P == 1 ? 3 : 2>(name, maps, Q, batch, s);
+        return run_product<kKind, 2, P == 1 ? 256 : 128, P>(name, maps, Q, batch, s);
+    }
+    if (pair == least) return run_product<kKind, 2, 128, P>(name, maps, Q, batch, s);
+    if (one == least) return run_product<kKind, 1, 128, P>(name, maps, Q, batch, s);
     return run_product<kKind, 1, 64, P>(name, maps, Q, batch, s);
 }
 

@@ -233,13 +233,16 @@ struct Shape {
     static constexpr uint32_t kSet = 2 * kSubBytes;
     static constexpr int kStages = static_cast<int>((224 * 1024 - kGroups * kSet) / kStage);
     static constexpr uint32_t kSmem = kStages * kStage + kGroups * kSet + 1024;   // + alignment
-    static constexpr int kAccs = P == 3 ? 512 / BN : 2;                    // accumulators in tensor memory
-    // Stages that one accumulator sums.  The unit rounds every sum towards zero: with three products
-    // the 940 sums of K = 5000 were off by 6e-5 of the result, so every 24 sums (128 K values, a
-    // drift below 1e-6) the epilogue adds the accumulator to its own fp32 sums, which round to nearest.
-    // Against f16 operands alone (one product) the drift does not count.
-    static constexpr int kChunk = P == 3 ? 2 : INT32_MAX;
-    static_assert(BN / kPair % kBox == 0 && kStages >= 2 && kAccs * BN <= 512, "shape");
+    // Accumulators in tensor memory.  The unit rounds every sum towards zero: with three products and one
+    // accumulator the 940 sums of K = 5000 were off by 6e-5 of the result.  So three products have two
+    // accumulators, hi hi and (2^-11 of it) hi lo + lo hi, and every kChunk stages, 32 sums of hi hi, a
+    // drift below 1e-6, the epilogue adds them to its own fp32 sums, which round to nearest.  (One
+    // accumulator read every 24 sums: 403 against 353 us at 2501 x 1003.)  Against f16 operands alone
+    // (one product) the drift does not count.
+    static constexpr int kAccCols = P == 3 ? 2 * BN : BN;
+    static constexpr int kAccs = 512 / kAccCols < 2 ? 1 : P == 3 ? 512 / kAccCols : 2;
+    static constexpr int kChunk = P == 3 ? 8 : INT32_MAX;
+    static_assert(BN / kPair % kBox == 0 && kStages >= 2 && kAccs * kAccCols <= 512, "shape");
 };
 
 // Tile t of a matrix: its first row (of the pair's) and column.  Symmetric results need
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
         for (int s = 0; s < S::kGroups; ++s) mbar_init(term + 8 * s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<kPair>(&tmem_slot, S::kAccs * BN);
+    if (warp == 1) tmem_alloc<kPair>(&tmem_slot, S::kAccs * S::kAccCols);
     tc_fence_before();
     if (kPair == 2)
         cluster_sync();
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                     const uint32_t acc = done % S::kAccs;
                     if (!(ok = mbar_wait(tempty + 8 * acc, (done / S::kAccs & 1) ^ 1, &dead))) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + acc * BN;
+                    const uint32_t d = tmem + acc * S::kAccCols;
                     for (int part = 0; part < S::kChunk && c < chunks; ++part, ++c, ++it) {
                         const uint32_t s = it % kStages;
                         if (!(ok = mbar_wait(full + 8 * s, it / kStages & 1, &dead))) break;
@@ -464,8 +467,8 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                             if (P == 3) {
                                 const uint64_t al = smem_desc(a + S::kA + ak, 16, 1024);
                                 const uint64_t bl = smem_desc(b + S::kB + bk, lead, 1024);
-                                tc_mma_f16<kPair>(d, ah, bl, idesc, true);
-                                tc_mma_f16<kPair>(d, al, bh, idesc, true);
+                                tc_mma_f16<kPair>(d + BN, ah, bl, idesc, part + k > 0);
+                                tc_mma_f16<kPair>(d + BN, al, bh, idesc, true);
                             }
                         }
                         tc_commit<kPair>(empty + 8 * s);
@@ -525,10 +528,11 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                     if (group * kSub < BN) {
 #pragma unroll
                         for (int q = 0; q < (P == 3 ? 2 : 0); ++q) {
-                            float v[32];
-                            tmem_load32(lanes + acc * BN + group * kSub + q * 32, v);
+                            float v[32], x[32];
+                            tmem_load32(lanes + acc * S::kAccCols + group * kSub + q * 32, v);
+                            tmem_load32(lanes + acc * S::kAccCols + BN + group * kSub + q * 32, x);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) sum[q][e] = c ? sum[q][e] + v[e] : v[e];
+                            for (int e = 0; e < 32; ++e) sum[q][e] = c ? sum[q][e] + (v[e] + x[e]) : v[e] + x[e];
                         }
                     }
                     tc_fence_before();
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = sum[P == 3 ? h : 0][e];
                     } else {
-                        tmem_load32(lanes + acc * BN + j * kSub + h * 32, v);
+                        tmem_load32(lanes + acc * S::kAccCols + j * kSub + h * 32, v);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -666,7 +670,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
         __syncthreads();
     tc_fence_after();
     if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
-    if (warp == 1) tmem_free<kPair>(tmem, S::kAccs * BN);
+    if (warp == 1) tmem_free<kPair>(tmem, S::kAccs * S::kAccCols);
 }
 
 // -------------------------------------------------------------------- host

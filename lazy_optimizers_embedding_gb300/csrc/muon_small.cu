@@ -16,6 +16,7 @@
 // A phase is bound by latency: products of a 128 x 128 x 256 tile take 0.4 us, the
 // barriers, tensor memory reads and f16 splits around them 1 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "muon.cuh"
 #include "profile.cuh"
@@ -166,26 +167,34 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
         __syncthreads();
         tc_fence_after();
     };
-    // hi hi into `d`, hi lo + lo hi into `x` (the same accumulator where d == x)
-    auto issue = [&](uint32_t d, uint32_t x, uint32_t idesc, uint32_t ah, uint32_t al, uint32_t bh, uint32_t bl, uint32_t lead,
-                     bool first) {
-        const uint64_t A = smem_desc(ah, 16, 1024), AL = smem_desc(al, 16, 1024);
-        const uint64_t B = smem_desc(bh, lead, 1024), BL = smem_desc(bl, lead, 1024);
-        tc_mma_f16<1>(tmem + d, A, B, idesc, !first);
-        tc_mma_f16<1>(tmem + x, A, BL, idesc, d == x || !first);
-        tc_mma_f16<1>(tmem + x, AL, B, idesc, true);
+    // 64-value blocks of K: hi hi into `d`, hi lo + lo hi into `x` (the same accumulator where d == x).
+    // Operands K-major, B MN-major where kMn (a K value 128 bytes on).
+    const uint64_t dxh = smem_desc(xhi, 16, 1024), dxl = smem_desc(xlo, 16, 1024);
+    const uint64_t dsh = smem_desc(shi, 16, 1024), dsl = smem_desc(slo, 16, 1024);
+    const uint64_t mxh = smem_desc(xhi, kBlockBytes, 1024), mxl = smem_desc(xlo, kBlockBytes, 1024);
+    auto issue = [&](auto mn, uint32_t d, uint32_t x, uint32_t idesc, uint64_t ah, uint64_t al, uint64_t bh, uint64_t bl,
+                     int blocks_of_k) {
+        constexpr bool kMn = decltype(mn)::value;
+        for (int k = 0; k < blocks_of_k; ++k) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint64_t a = q * 2, b = kMn ? q * 128 : q * 2;   // 16 K values, in 16-byte units
+                tc_mma_f16<1>(tmem + d, ah + a, bh + b, idesc, k + q > 0);
+                tc_mma_f16<1>(tmem + x, ah + a, bl + b, idesc, d == x || k + q > 0);
+                tc_mma_f16<1>(tmem + x, al + a, bh + b, idesc, true);
+            }
+            ah += kBlockBytes / 16, al += kBlockBytes / 16;
+            bh += kMn ? 512 : kBlockBytes / 16, bl += kMn ? 512 : kBlockBytes / 16;
+        }
+        tc_commit<1>(bar);
     };
+    const uint32_t square = mma_desc_f16(kRows, side, false), update = mma_desc_f16(kRows, Q.slice, true);
 
     for (int step = 0; step < Q.steps; ++step) {
         // ---- A
         operands_done();
         if (warp == 0 && elect_one()) {
-            const uint32_t idesc = mma_desc_f16(kRows, side, false);
-            for (int k = 0; k < Q.slice / 16; ++k) {
-                const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32;
-                issue(kGramCol, kCrossCol, idesc, xhi + o, xlo + o, xhi + o, xlo + o, 16, k == 0);
-            }
-            tc_commit<1>(bar);
+            issue(std::false_type{}, kGramCol, kCrossCol, square, dxh, dxl, dxh, dxl, Q.slice / 64);
         }
         products_done();
         const int per = side / 2;              // columns of A this warp has: 32 or 64
@@ -204,30 +213,58 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
                 }
         }
         if (blocks > 1) {
-            // the shares, fp32 rows of 512 bytes where A will be, 16-byte pieces permuted by row
-            const uint32_t at = shi + row * 512;
+            // The shares, fp32, where A will be: rows of side / 4 16-byte pieces, permuted by row.  Block r
+            // sums the r-th part of the pieces over the cluster, in block order, in place (no other block
+            // reads that part of its share), then every block fetches the others' sums, neighbouring
+            // lanes neighbouring pieces.  (Every block reading every share in its own rows' order, 16
+            // bytes of 32 rows at a time, took 130 us a step at 128 x 2048.)
+            const int quads = side / 4, mine = quads * side / blocks;
+            auto quad = [&](int q) { return shi + static_cast<uint32_t>(row * quads + ((half * (per / 4) + q) ^ (row & 7))) * 16; };
             if (rows_used)
 #pragma unroll
                 for (int q = 0; q < 16; ++q)
                     if (q * 4 < per)
-                        sts128(at + (((half * (per / 4) + q) ^ (row & 7)) << 4),
-                               make_uint4(__float_as_uint(av[4 * q]), __float_as_uint(av[4 * q + 1]),
-                                          __float_as_uint(av[4 * q + 2]), __float_as_uint(av[4 * q + 3])));
+                        sts128(quad(q), make_uint4(__float_as_uint(av[4 * q]), __float_as_uint(av[4 * q + 1]),
+                                                   __float_as_uint(av[4 * q + 2]), __float_as_uint(av[4 * q + 3])));
             cluster_sync();
-            if (rows_used) {
+            const int used = min(side, (Q.m + 31) / 32 * 32) * quads;   // pieces of rows that the warps wrote
+            for (int f = rank * mine + threadIdx.x; f < (rank + 1) * mine && f < used; f += kMuonBlock) {
+                float4 v[kMaxCluster];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) av[e] = 0.0f;
-                for (int r = 0; r < blocks; ++r) {
-                    const uint32_t from = cluster_addr(at, r);
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < blocks) v[r] = lds_cluster(cluster_addr(shi + f * 16, r));
+                float4 t = v[0];
 #pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        if (q * 4 < per) {
-                            const float4 f = lds_cluster(from + (((half * (per / 4) + q) ^ (row & 7)) << 4));
-                            av[4 * q] += f.x, av[4 * q + 1] += f.y, av[4 * q + 2] += f.z, av[4 * q + 3] += f.w;
-                        }
+                for (int r = 1; r < kMaxCluster; ++r)
+                    if (r < blocks) t.x += v[r].x, t.y += v[r].y, t.z += v[r].z, t.w += v[r].w;
+                sts128(shi + f * 16, make_uint4(__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)));
+            }
+            cluster_sync();
+            for (int f0 = threadIdx.x; f0 < used; f0 += 8 * kMuonBlock) {
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int f = f0 + i * kMuonBlock;
+                    if (f < used && f / mine != rank) v[i] = lds_cluster(cluster_addr(shi + f * 16, f / mine));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int f = f0 + i * kMuonBlock;
+                    if (f < used && f / mine != rank)
+                        sts128(shi + f * 16, make_uint4(__float_as_uint(v[i].x), __float_as_uint(v[i].y), __float_as_uint(v[i].z),
+                                                        __float_as_uint(v[i].w)));
                 }
             }
-            cluster_sync();   // every block has read the shares
+            cluster_sync();   // the block has all sums, and no block reads another's any more
+            if (rows_used)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    if (q * 4 < per) {
+                        const uint4 f = lds128(quad(q));
+                        av[4 * q] = __uint_as_float(f.x), av[4 * q + 1] = __uint_as_float(f.y);
+                        av[4 * q + 2] = __uint_as_float(f.z), av[4 * q + 3] = __uint_as_float(f.w);
+                    }
+            __syncthreads();
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -242,12 +279,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
 
         // ---- A A, and B in A's place
         if (warp == 0 && elect_one()) {
-            const uint32_t idesc = mma_desc_f16(kRows, side, false);
-            for (int k = 0; k < side / 16; ++k) {
-                const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32;
-                issue(kGramCol, kCrossCol, idesc, shi + o, slo + o, shi + o, slo + o, 16, k == 0);
-            }
-            tc_commit<1>(bar);
+            issue(std::false_type{}, kGramCol, kCrossCol, square, dsh, dsl, dsh, dsl, side / 64);
         }
         products_done();
         if (rows_used) {
@@ -274,12 +306,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
 
         // ---- B X, and the new X in its place
         if (warp == 0 && elect_one()) {
-            const uint32_t idesc = mma_desc_f16(kRows, Q.slice, true);
-            for (int k = 0; k < side / 16; ++k) {
-                const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32, x = k * 2048;   // 16 rows of X
-                issue(kUpdateCol, kUpdateCol, idesc, shi + o, slo + o, xhi + x, xlo + x, kBlockBytes, k == 0);
-            }
-            tc_commit<1>(bar);
+            issue(std::true_type{}, kUpdateCol, kUpdateCol, update, dsh, dsl, mxh, mxl, side / 64);
         }
         products_done();
         if (rows_used)

@@ -462,7 +462,7 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
  * accepted when X, A and B stay below 3.9 from every singular value in [0, 1].
  * products: 3 computes each matrix product to 22 bits (fp32 accuracy, for fp32
  * results); 1 to 11 bits (about 2e-3 of the result's norm, what rounding it to
- * bf16 costs), in about 0.4 of the time.
+ * bf16 costs), in half the time or less for large matrices.
  */
 typedef struct {
     double a, b, c, eps;
@@ -479,13 +479,13 @@ typedef struct {
 } sparse_muon_config_t;
 
 /* Bytes of workspace the two entry points below need for a batch of r x c
- * matrices.  Limits: r, c <= 2^20, batch <= 2^24, batch*r*c <= 2^40. */
+ * matrices.  Limits: r, c <= 2^20, batch <= 2^24, batch*r*c <= 2^36. */
 size_t sparse_muon_workspace_size(int64_t batch, int64_t r, int64_t c, int products);
 
 /*
  * sparse_orthogonalize -- out = Newton-Schulz of every r x c matrix of u.
- *   u, out [batch, r, c]: fp32 or bf16 each.  An element that is NaN or infinite (or a
- *   sum of squares beyond fp32) sets SPARSE_ERR_NON_FINITE.
+ *   u, out [batch, r, c]: fp32 or bf16 each.  An element that is NaN or infinite (or
+ *   values whose sum of squares fp32 cannot hold, about 1e18) sets SPARSE_ERR_NON_FINITE.
  *   ws: sparse_muon_workspace_size() bytes, 256-byte aligned.
  */
 sparse_status_t sparse_orthogonalize(const void* u, sparse_dtype_t u_type, int64_t batch, int64_t r, int64_t c,

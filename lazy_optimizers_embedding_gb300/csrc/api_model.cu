@@ -73,7 +73,7 @@ bool valid_ns(const sparse_ns_config_t& c)
 bool valid_batch(int64_t batch, int64_t r, int64_t c)
 {
     return batch >= 0 && batch <= (1 << 24) && r >= 1 && c >= 1 && r <= (1 << 20) && c <= (1 << 20) &&
-           (batch == 0 || r * c <= (int64_t(1) << 40) / batch);
+           (batch == 0 || r * c <= (int64_t(1) << 36) / batch);
 }
 
 so::MuonParams muon_params(int64_t batch, int64_t r, int64_t c, const sparse_ns_config_t& ns, int32_t* d_err)

@@ -68,6 +68,15 @@ inline cudaError_t launch_smem(void (*kernel)(P...), dim3 grid, dim3 block, size
 }
 
 
+// Lets a kernel have `bytes` of dynamic shared memory on the current device.  Said on every call that
+// needs it: another device, or the context after a reset, does not know.
+template <class K>
+inline cudaError_t allow_smem(K kernel, size_t bytes)
+{
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBlock = 256;            // threads per block of every kernel here
 #ifndef SO_PIECE_LEN

@@ -517,7 +517,7 @@ cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, i
         e = launch(k_expert_scan, dim3((E + kExWarps - 1) / kExWarps), dim3(kExBlock), s, counts, E, S.blocks, totals);
         if (e != cudaSuccess) return e;
     }
-    static const cudaError_t ready = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    const cudaError_t ready = allow_smem(k_expert_sort, sort_smem(S.threads, experts));
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S.blocks);

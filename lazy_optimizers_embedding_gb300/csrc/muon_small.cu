@@ -360,18 +360,6 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
     if (warp == 0) tmem_free<1>(tmem, kTmemCols);
 }
 
-bool cluster_ready()
-{
-    static const bool ready = [] {
-        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        return cudaFuncSetAttribute(k_muon_cluster<true, 3>, attr, kSmallSmem) == cudaSuccess &&
-               cudaFuncSetAttribute(k_muon_cluster<false, 3>, attr, kSmallSmem) == cudaSuccess &&
-               cudaFuncSetAttribute(k_muon_cluster<true, 1>, attr, kSmallSmem) == cudaSuccess &&
-               cudaFuncSetAttribute(k_muon_cluster<false, 1>, attr, kSmallSmem) == cudaSuccess;
-    }();
-    return ready;
-}
-
 // Clusters of `blocks` blocks that the GPU holds at once.
 int clusters_at_once(int blocks)
 {
@@ -389,7 +377,8 @@ int clusters_at_once(int blocks)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (!cluster_ready() || cudaOccupancyMaxActiveClusters(&n, k_muon_cluster<true, 3>, &cfg) != cudaSuccess) n = 0;
+        if (allow_smem(k_muon_cluster<true, 3>, kSmallSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_muon_cluster<true, 3>, &cfg) != cudaSuccess) n = 0;
         n = std::max(n, 1);
         known[blocks].store(n, std::memory_order_relaxed);
     }
@@ -437,7 +426,8 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.d_err = M.d_err;
     auto* kernel = M.products == 3 ? (vec ? k_muon_cluster<true, 3> : k_muon_cluster<false, 3>)
                                    : (vec ? k_muon_cluster<true, 1> : k_muon_cluster<false, 1>);
-    if (!cluster_ready()) return cudaErrorNotSupported;
+    const cudaError_t ready = allow_smem(kernel, kSmallSmem);
+    if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M.batch * blocks));
     cfg.blockDim = dim3(kMuonBlock);

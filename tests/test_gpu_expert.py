@@ -181,6 +181,33 @@ def test_a_bad_place_is_reported_and_not_followed(cuda_lib):
     assert int(case.err.item()) == so.ERR_INDEX_OUT_OF_RANGE
 
 
+def test_elements_past_32_bits(cuda_lib):
+    """2.4e9 sorted elements: rows of the first and the last expert."""
+    import torch
+    so = cuda_lib
+    n, k, e, c = 300_000, 2, 3, 4000
+    expert = torch.zeros(n, k, dtype=torch.int64, device="cuda")
+    expert[:, 1] = 2
+    x = torch.empty(n, c, dtype=torch.bfloat16, device="cuda").normal_()
+    xs = torch.empty(n * k, c, dtype=torch.bfloat16, device="cuda")
+    dxs, y = torch.empty_like(xs), torch.empty_like(x)
+    offsets = torch.empty(e + 1, dtype=torch.int64, device="cuda")
+    pos = torch.empty(n, k, dtype=torch.int32, device="cuda")
+    w = torch.full((n, k), 0.5, device="cuda")
+    ws = torch.empty(max(so.sparse_expert_workspace_size(n, k, e), 256), dtype=torch.uint8, device="cuda")
+    err = so.error_word()
+    so.check(so.sparse_expert_sort(expert, n, k, e, offsets, None, pos, ws, err))
+    so.check(so.sparse_expert_dispatch(x, n, k, c, pos, offsets, e, xs, err))
+    so.check(so.sparse_expert_combine(xs, n, k, c, pos, w, y, err))
+    so.check(so.sparse_expert_combine_grad(x, xs, n, k, c, pos, offsets, e, w, dxs, None, err))
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and offsets.tolist() == [0, n, n, 2 * n]
+    assert torch.equal(pos[:, 1], torch.arange(n, 2 * n, dtype=torch.int32, device="cuda"))
+    for at in (slice(0, 5), slice(n - 5, n)):
+        assert torch.equal(xs[at], x[at]) and torch.equal(xs[n:][at], x[at])
+        assert torch.equal(y[at], x[at]) and torch.equal(dxs[n:][at], x[at] * 0.5)
+
+
 def test_weights_gradient_against_differences(cuda_lib):
     """L = sum(dy * combine(ys, w)) is linear in w and in ys: the slope is exact up to rounding."""
     import torch

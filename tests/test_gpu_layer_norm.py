@@ -19,7 +19,7 @@ U = 2.0 ** -24
 BF = 2.0 ** -8
 TYPES = [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")]
 SHAPES = [(1, 1), (3, 1), (1, 2), (5, 7), (2, 8), (7, 31), (33, 64), (100, 129), (17, 512), (9, 1000), (4, 2048),
-          (3, 8192), (2, 8193), (3, 20001), (5000, 24), (700, 4096), (2000, 300)]
+          (3, 8192), (2, 8193), (3, 20001), (5000, 24), (700, 4096), (2000, 300), (8300, 1400), (301, 3333)]
 
 
 def _dt(torch, name):
@@ -127,9 +127,10 @@ def test_layer_norm_and_gradients(cuda_lib, n, c, xt, yt):
 
 @pytest.mark.parametrize("xt,yt", TYPES)
 @pytest.mark.parametrize("shift", [1, 3])
-def test_arrays_of_any_alignment(cuda_lib, shift, xt, yt):
+@pytest.mark.parametrize("c", [256, 1111, 2048])
+def test_arrays_of_any_alignment(cuda_lib, c, shift, xt, yt):
     import torch
-    k = Case(torch, cuda_lib, 50, 256, xt, yt, shift=shift)
+    k = Case(torch, cuda_lib, 50, c, xt, yt, shift=shift)
     k.run()
     k.compare()
 
@@ -214,6 +215,30 @@ def test_equal_inputs_give_equal_bits_on_any_stream(cuda_lib):
     k.run(stream=s)
     for a, b in zip(first, (k.y, k.dx, k.dgamma, k.dbeta, k.mean, k.rstd)):
         assert torch.equal(a, b)
+
+
+def test_elements_past_32_bits(cuda_lib):
+    """2.3e9 elements: rows at both ends against the formula, and dbeta, whose sum of equal dy is known."""
+    import torch
+    so = cuda_lib
+    n, c = 1_150_000, 2000
+    x = torch.empty(n, c, dtype=torch.bfloat16, device="cuda").normal_()
+    dy = torch.full((n, c), 0.5, dtype=torch.bfloat16, device="cuda")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    dgamma, dbeta = torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    ws = torch.empty(so.sparse_layer_norm_workspace_size(n, c), dtype=torch.uint8, device="cuda")
+    err = so.error_word()
+    so.check(so.sparse_layer_norm(x, n, c, None, n, None, None, 1e-5, y, mean, rstd, err))
+    so.check(so.sparse_layer_norm_grad(dy, x, n, c, None, n, None, mean, rstd, dx, dgamma, dbeta, ws, err))
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for rows in (slice(0, 3), slice(n - 3, n)):
+        ref = _formula(_np(x[rows]), 1.0, 0.0, 1e-5)[0]
+        assert np.abs(_np(y[rows]) - ref).max() <= BF * np.abs(ref).max()
+        assert np.abs(_np(dx[rows])).max() <= 1e-4          # equal dy: h - mean(h) and mean(h xhat) are 0
+    # 575000 is a sum of halves: exact until 2^23 of them, then partial sums of up to 2^23 / 2
+    assert np.abs(_np(dbeta) - 0.5 * n).max() <= 512 * U * 0.5 * n
 
 
 def test_gradients_against_differences_of_the_formula(cuda_lib):

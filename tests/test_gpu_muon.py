@@ -17,7 +17,7 @@ NS = (3.4445, -4.7750, 2.0315)
 TOL = {1: 5e-3, 3: 2e-5}
 SHAPES = [(1, 1, 1), (1, 1, 5), (2, 5, 1), (3, 7, 7), (1, 16, 16), (2, 64, 128), (1, 128, 64), (1, 129, 200),
           (3, 200, 129), (1, 100, 1000), (2, 1000, 100), (1, 257, 511), (2, 384, 640), (1, 24, 5000), (1, 900, 1030),
-          (40, 33, 65)]
+          (40, 33, 65), (1, 100, 600), (2, 50, 1500), (1, 2048, 120), (20, 128, 1030), (1, 1100, 1300), (400, 20, 24)]
 
 
 def _np(t):
@@ -145,6 +145,20 @@ def test_equal_inputs_give_equal_bits_alone_in_a_batch_and_on_any_stream(cuda_li
         torch.cuda.synchronize()
         assert np.array_equal(first, k.run(stream=torch.cuda.Stream()))
         assert np.array_equal(first[2:3], Case(torch, cuda_lib, u[2:3], products).run())
+
+
+def test_a_captured_call_gives_the_same_bits(cuda_lib):
+    import torch
+    for shape, products in (((1, 60, 90), 3), ((2, 300, 400), 1)):
+        k = Case(torch, cuda_lib, np.random.default_rng(8).standard_normal(shape), products)
+        first = k.run()
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            k.so.check(k.so.sparse_orthogonalize(k.u, k.b, k.r, k.c, k.cfg, k.out, k.ws, k.err, s))
+        k.out.zero_()
+        g.replay()
+        k.G.check("replay")
+        assert np.array_equal(first, _np(k.out))
 
 
 class Step:

@@ -134,6 +134,11 @@ STATIC_WS_BYTES = 16 * 1024 * 1024  # SPARSE_STATIC_WS_BYTES
 def _ptr(t, dtype=None, name="tensor"):
     if t is None:
         return None
+    try:   # what every call passes; the rest only says what is wrong
+        if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(t, int):
         return t
     if not isinstance(t, torch.Tensor):
@@ -142,9 +147,7 @@ def _ptr(t, dtype=None, name="tensor"):
         raise ValueError(f"{name}: must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
 
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -153,7 +156,7 @@ _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 def _typed(t, name, like=None):
     """(pointer, sparse_dtype_t) of an fp32 or bf16 tensor, of like's type where that is given."""
     p = _ptr(t, like.dtype if like is not None else None, name)
-    code = _DTYPES.get(t.dtype)
+    code = _DTYPES.get(t.dtype) if t is not None else F32
     if code is None:
         raise TypeError(f"{name}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
     return p, code

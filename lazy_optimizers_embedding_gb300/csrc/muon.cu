@@ -218,8 +218,9 @@ struct Product {
     int32_t* d_err;
 };
 
-// kPair blocks (a cluster) share a tile of 128 kPair rows x BN columns; P products; G epilogue groups.
-template <int kKind, int kPair, int BN, int P, int G>
+// kPair blocks (a cluster) share a tile of 128 kPair rows x BN columns, or kSplit blocks have a part of
+// the inner dimension of one tile each; P products; G epilogue groups.
+template <int kKind, int kPair, int kSplit, int BN, int P, int G>
 struct Shape {
     static constexpr bool kSym = kKind == kGram || kKind == kPoly;
     static constexpr uint32_t kA = kBM / kBox * kBoxBytes;                 // one f16 part of A in a stage
@@ -243,6 +244,10 @@ struct Shape {
     static constexpr int kAccCols = P == 3 ? 2 * BN : BN;
     static constexpr int kAccs = 512 / kAccCols < 2 ? 1 : P == 3 ? 512 / kAccCols : 2;
     static constexpr int kChunk = P == 3 ? 8 : INT32_MAX;
+    // Split tiles: a block is given one tile, and sums of 64 columns (fp32) from the kSplit - 1 others of its
+    // cluster come to where its stages were.
+    static constexpr uint32_t kSums = kBM * kSub * 4;
+    static_assert(kSplit == 1 || (kPair == 1 && BN / kSub == G && kSplit >= G && (kSplit - 1) * kSums <= kStages * kStage), "split");
     static_assert(BN / kPair % kBox == 0 && kStages >= 2 && kAccs * kAccCols <= 512, "shape");
 };
 
@@ -361,12 +366,13 @@ __device__ __forceinline__ void put_image(uint32_t part, int rowl, int p, uint4 
 // the symmetric factor) or, for B X, MN-major (X as it lies).  In shared memory every
 // box has 64 rows of 128 bytes, 16-byte pieces permuted by row (the copies' 128-byte
 // swizzle).
-template <int kKind, int kPair, int BN, int P, int G>
-__global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
+template <int kKind, int kPair, int kSplit, int BN, int P, int G>
+__global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThreads, 1)
     k_muon_product(const __grid_constant__ Maps maps, const Product Q)
 {
-    using S = Shape<kKind, kPair, BN, P, G>;
+    using S = Shape<kKind, kPair, kSplit, BN, P, G>;
     constexpr bool kSym = S::kSym, kBmn = !S::kSym, kTerm = kKind != kGram;
+    constexpr bool kSum = P == 3 || kSplit > 1;   // the epilogue sums in registers, piece g of a tile by group g
     constexpr int kStages = S::kStages, TM = kBM * kPair;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * kStages + 2 * S::kAccs + 1 + S::kGroups];
@@ -378,7 +384,8 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                    tempty = tfull + 8 * S::kAccs, drain = tempty + 8 * S::kAccs, term = drain + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = kPair == 2 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t first = blockIdx.x / kPair, step = gridDim.x / kPair;
+    const int64_t first = blockIdx.x / (kPair * kSplit), step = gridDim.x / (kPair * kSplit);
+    const int part_of_k = kSplit > 1 ? static_cast<int>(cluster_rank()) : 0;
 
     if (threadIdx.x == 0) {
         dead = 0;
@@ -400,7 +407,9 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
     if (kKind != kFinal) pdl_release();   // workspace only; after this block's allocation, so that no later block can hold what it waits for
     fence_async_proxy();                  // the first kernels wrote with ordinary stores
 
-    const int chunks = static_cast<int>((Q.k + kBK - 1) / kBK);
+    // this block's stages of the inner dimension
+    const int all_chunks = static_cast<int>((Q.k + kBK - 1) / kBK);
+    const int begin = all_chunks * part_of_k / kSplit, chunks = all_chunks * (part_of_k + 1) / kSplit;
     if (warp == 0) {
         if (elect_one()) {
             tma_prefetch(&maps.ahi);
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                 tile_at<TM, BN, kSym>(Q, t, mat, row0, col0);
                 row0 += rank * kBM;
                 col0 += rank * (BN / kPair);
-                for (int c = 0; c < chunks; ++c, ++it) {
+                for (int c = begin; c < chunks; ++c, ++it) {
                     const uint32_t s = it % kStages;
                     if (!mbar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, &dead)) goto copied;
                     const uint32_t bar = kPair == 2 ? cluster_addr(full + 8 * s, 0) : full + 8 * s;
@@ -442,13 +451,18 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                 }
             }
         }
+        if (kSplit > 1) {   // as the epilogue's
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             constexpr uint32_t idesc = mma_desc_f16(TM, BN, kBmn);
             uint32_t it = 0, done = 0;   // stages, accumulators used
             bool ok = true;
             for (int64_t t = first; ok && t < Q.all; t += step)
-                for (int c = 0; ok && c < chunks; ++done) {
+                for (int c = begin; ok && c < chunks; ++done) {
                     const uint32_t acc = done % S::kAccs;
                     if (!(ok = mbar_wait(tempty + 8 * acc, (done / S::kAccs & 1) ^ 1, &dead))) break;
                     tc_fence_after();
@@ -482,6 +496,11 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                 mbar_wait(drain, 0, &none);
             }
         }
+        if (kSplit > 1) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
         constexpr int kGroups = S::kGroups;
         const int group = (warp - 2) >> 2, id = 1 + group;
@@ -504,7 +523,10 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
             const int cols = kSym ? min(row0 + kBM, static_cast<int>(Q.m)) : static_cast<int>(Q.n);
             pieces = row0 < Q.m ? max(0, min(BN / kSub, (cols - col0 + kSub - 1) / kSub)) : 0;
         };
-        auto first_piece = [&] { return P == 3 ? group : (group - before + kGroups) % kGroups; };
+        // (split tiles: piece g is finished by block g of the cluster)
+        auto first_piece = [&] {
+            return kSum ? (kSplit == 1 || part_of_k == group ? group : BN) : (group - before + kGroups) % kGroups;
+        };
         // The term of piece j into the set, once nothing leaves from there any more.
         auto fetch = [&](int j) {
             tma_store_read<0>();
@@ -519,31 +541,64 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
         plan(first);
         if (kTerm && head && first_piece() < pieces) fetch(first_piece());
         for (int64_t t = first; ok && t < Q.all; t += step) {
-            float sum[P == 3 ? 2 : 1][32];
+            float sum[kSum ? 2 : 1][32];
             uint32_t acc = done % S::kAccs;
-            if (P == 3) {
-                for (int c = 0; c < chunks; c += S::kChunk, ++done) {
+            if (kSum) {
+#pragma unroll
+                for (int q = 0; q < 64; ++q) sum[kSum ? q / 32 : 0][q % 32] = 0.0f;
+#pragma unroll 1
+                for (int c = begin; c < chunks; c += min(S::kChunk, chunks - c), ++done) {
                     acc = done % S::kAccs;
                     if (!(ok = all_of(id, kGroup, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead)))) break;
                     tc_fence_after();
                     if (group * kSub < BN) {
 #pragma unroll
-                        for (int q = 0; q < (P == 3 ? 2 : 0); ++q) {
-                            float v[32], x[32];
-                            tmem_load32(lanes + acc * S::kAccCols + group * kSub + q * 32, v);
-                            tmem_load32(lanes + acc * S::kAccCols + BN + group * kSub + q * 32, x);
+                        for (int q = 0; q < (kSum ? 4 : 0); ++q) {
+                            const uint32_t from = lanes + acc * S::kAccCols + group * kSub + q * 16;
+                            float v[16], x[16];
+                            tmem_load16(from, P == 3 ? from + BN : from, v, x);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) sum[q][e] = c ? sum[q][e] + (v[e] + x[e]) : v[e] + x[e];
+                            for (int e = 0; e < 16; ++e) {
+                                if (P == 3) v[e] += x[e];
+                                sum[kSum ? q / 2 : 0][q % 2 * 16 + e] += v[e];
+                            }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty + 8 * acc, 0));
+                    if (lane == 0) mbar_arrive_cluster(kPair == 2 ? cluster_addr(tempty + 8 * acc, 0) : tempty + 8 * acc);
                 }
             } else {
                 ok = all_of(id, kGroup, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead));
                 tc_fence_after();
                 ++done;
+            }
+            if (kSplit > 1) {
+                // Sums go to the block that finishes their piece, four columns of 32 rows at a time, once its
+                // products have been through its stages, and are added there in block order.
+                const uint32_t to = (part_of_k < group ? part_of_k : part_of_k - 1) * S::kSums + rowl * 16;
+                __syncwarp();
+                cluster_sync();
+                if (ok && part_of_k != group) {
+                    const uint32_t there = cluster_addr(data + to, group);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        sts128_cluster(there + q * kBM * 16, make_uint4(__float_as_uint(sum[kSum ? q / 8 : 0][q % 8 * 4]),
+                                                                        __float_as_uint(sum[kSum ? q / 8 : 0][q % 8 * 4 + 1]),
+                                                                        __float_as_uint(sum[kSum ? q / 8 : 0][q % 8 * 4 + 2]),
+                                                                        __float_as_uint(sum[kSum ? q / 8 : 0][q % 8 * 4 + 3])));
+                }
+                cluster_sync();
+                if (ok && part_of_k == group)
+                    for (int r = 0; r + 1 < kSplit; ++r)
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const uint4 v = lds128(data + r * S::kSums + rowl * 16 + q * kBM * 16);
+                            sum[kSum ? q / 8 : 0][q % 8 * 4] += __uint_as_float(v.x);
+                            sum[kSum ? q / 8 : 0][q % 8 * 4 + 1] += __uint_as_float(v.y);
+                            sum[kSum ? q / 8 : 0][q % 8 * 4 + 2] += __uint_as_float(v.z);
+                            sum[kSum ? q / 8 : 0][q % 8 * 4 + 3] += __uint_as_float(v.w);
+                        }
             }
             if (!ok) break;
             for (int j = first_piece(); j < pieces; j += kGroups) {
@@ -562,9 +617,9 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[32];
-                    if (P == 3) {
+                    if (kSum) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = sum[P == 3 ? h : 0][e];
+                        for (int e = 0; e < 32; ++e) v[e] = sum[kSum ? h : 0][e];
                     } else {
                         tmem_load32(lanes + acc * S::kAccCols + j * kSub + h * 32, v);
                     }
@@ -653,10 +708,10 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, BN, P, G>::kThreads, 1)
                 if (kTerm && head && more) fetch(j + kGroups);
             }
             if (!ok) break;
-            if (P != 3) {
+            if (!kSum) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty + 8 * acc, 0));
+                if (lane == 0) mbar_arrive_cluster(kPair == 2 ? cluster_addr(tempty + 8 * acc, 0) : tempty + 8 * acc);
             }
             plan(t + step);
             if (kTerm && head && first_piece() < pieces) fetch(first_piece());
@@ -745,18 +800,19 @@ int64_t tiles_of(int64_t m, int64_t n, int tm, int bn, bool sym)
     return t;
 }
 
-template <int kKind, int kPair, int BN, int P, int G = 2>
+template <int kKind, int kPair, int kSplit, int BN, int P, int G>
 cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t batch, cudaStream_t s)
 {
-    using S = Shape<kKind, kPair, BN, P, G>;
-    auto* kernel = k_muon_product<kKind, kPair, BN, P, G>;
+    using S = Shape<kKind, kPair, kSplit, BN, P, G>;
+    auto* kernel = k_muon_product<kKind, kPair, kSplit, BN, P, G>;
+    constexpr int kCluster = kPair * kSplit;
     Q.tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym);
     Q.all = Q.tiles * batch;
     Q.cols_of_tiles = static_cast<int>((Q.n + BN - 1) / BN);
     const cudaError_t ready = allow_smem(kernel, S::kSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(Q.all, num_sms() / kPair) * kPair));
+    cfg.gridDim = dim3(static_cast<unsigned>((kSplit > 1 ? Q.all : std::min<int64_t>(Q.all, num_sms() / kPair)) * kCluster));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -764,7 +820,7 @@ cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t b
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kPair;
+    attr[1].val.clusterDim.x = kCluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -773,35 +829,42 @@ cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t b
     return cudaLaunchKernelEx(&cfg, kernel, maps, Q);
 }
 
-// What a shape's tiles take, in cycles of one 64-value stage times rounds over the GPU: a
-// stage needs 128 x BN x 64 x P products at 4096 a cycle and SM, and its boxes from L2 at
-// about 80 bytes a cycle and SM, whichever is longer.
-template <int kKind, int kPair, int BN, int P>
+// What a shape's tiles take, in cycles: rounds over the GPU times the stages of a tile.  A stage needs
+// 128 x BN x 64 x P products at 4096 a cycle and SM, and its boxes from L2 at about 80 bytes a cycle and
+// SM, whichever is longer.  Split tiles have one round, and hand their sums over in about 6000 cycles.
+template <int kKind, int kPair, int kSplit, int BN, int P>
 int64_t shape_cost(const Product& Q, int64_t batch)
 {
-    using S = Shape<kKind, kPair, BN, P, 2>;
-    const int64_t units = num_sms() / kPair;
+    using S = Shape<kKind, kPair, kSplit, BN, P, BN == 64 ? 1 : 2>;
+    const int64_t units = num_sms() / (kPair * kSplit);
     const int64_t tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym) * batch;
-    return (tiles + units - 1) / units * std::max<int64_t>(2 * BN * P, S::kStage / 80);
+    const int64_t chunks = (Q.k + kBK - 1) / kBK;
+    if (kSplit > 1 && (tiles > units || chunks < 2 * kSplit)) return INT64_MAX;
+    return (tiles + units - 1) / units * ((chunks + kSplit - 1) / kSplit) * std::max<int64_t>(2 * BN * P, S::kStage / 80) +
+           (kSplit > 1 ? 6000 : 0);
 }
 
 template <int kKind, int P>
 cudaError_t run_kind(const char* name, const Maps& maps, const Product& Q, int64_t batch, cudaStream_t s)
 {
-    const int64_t wide = P == 1 ? shape_cost<kKind, 2, P == 1 ? 256 : 128, P>(Q, batch) : INT64_MAX;
-    const int64_t pair = shape_cost<kKind, 2, 128, P>(Q, batch), one = shape_cost<kKind, 1, 128, P>(Q, batch),
-                  half = shape_cost<kKind, 1, 64, P>(Q, batch);
-    const int64_t least = std::min(std::min(wide, pair), std::min(one, half));
+    constexpr int kWide = P == 1 ? 256 : 128;
+    const int64_t wide = P == 1 ? shape_cost<kKind, 2, 1, kWide, P>(Q, batch) : INT64_MAX;
+    const int64_t pair = shape_cost<kKind, 2, 1, 128, P>(Q, batch), one = shape_cost<kKind, 1, 1, 128, P>(Q, batch),
+                  half = shape_cost<kKind, 1, 1, 64, P>(Q, batch), two = shape_cost<kKind, 1, 2, 128, P>(Q, batch),
+                  four = shape_cost<kKind, 1, 4, 128, P>(Q, batch);
+    const int64_t least = std::min(std::min(std::min(wide, pair), std::min(one, half)), std::min(two, four));
     if (wide == least) {
         // a short product's tile is finished in less time than two groups take over its results; a
         // long one's fares better with a fifth stage in place of the third group's set
         // (K = 768: 58 against 70 us; K = 4096: 118 against 108)
-        if (P == 1 && Q.k < 1024) return run_product<kKind, 2, P == 1 ? 256 : 128, P, P == 1 ? 3 : 2>(name, maps, Q, batch, s);
-        return run_product<kKind, 2, P == 1 ? 256 : 128, P>(name, maps, Q, batch, s);
+        if (P == 1 && Q.k < 1024) return run_product<kKind, 2, 1, kWide, P, P == 1 ? 3 : 2>(name, maps, Q, batch, s);
+        return run_product<kKind, 2, 1, kWide, P, 2>(name, maps, Q, batch, s);
     }
-    if (pair == least) return run_product<kKind, 2, 128, P>(name, maps, Q, batch, s);
-    if (one == least) return run_product<kKind, 1, 128, P>(name, maps, Q, batch, s);
-    return run_product<kKind, 1, 64, P>(name, maps, Q, batch, s);
+    if (pair == least) return run_product<kKind, 2, 1, 128, P, 2>(name, maps, Q, batch, s);
+    if (one == least) return run_product<kKind, 1, 1, 128, P, 2>(name, maps, Q, batch, s);
+    if (half == least) return run_product<kKind, 1, 1, 64, P, 1>(name, maps, Q, batch, s);
+    if (two == least) return run_product<kKind, 1, 2, 128, P, 2>(name, maps, Q, batch, s);
+    return run_product<kKind, 1, 4, 128, P, 2>(name, maps, Q, batch, s);
 }
 
 template <int P>

@@ -47,8 +47,8 @@ bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const in
            c <= kMaxExpertCols && d_err != nullptr;
 }
 
-// Newton-Schulz keeps X, A = X X^T and B = b A + c A^2 as f16 values times 2^14: their
-// singular values, followed here over [0, 1] (all that a matrix of Frobenius norm at
+// Newton-Schulz keeps X, A = X X^T and B = b A + c A^2, with and without a on its
+// diagonal, as f16 values times 2^14: their singular values, followed here over [0, 1] (all that a matrix of Frobenius norm at
 // most 1 can have), have to stay below 65504 / 2^14 with 2 % to spare.
 constexpr double kMaxNs = 3.9;
 
@@ -63,7 +63,7 @@ bool valid_ns(const sparse_ns_config_t& c)
         for (int s = 0; s < c.steps; ++s) {
             const double l = x * x, p = c.b * l + c.c * l * l;
             x = c.a * x + p * x;
-            if (!(std::fabs(l) <= kMaxNs && std::fabs(p) <= kMaxNs && std::fabs(x) <= kMaxNs)) return false;
+            if (!(std::fabs(l) <= kMaxNs && std::fabs(p) <= kMaxNs && std::fabs(c.a + p) <= kMaxNs && std::fabs(x) <= kMaxNs)) return false;
         }
     }
     return true;

@@ -15,12 +15,16 @@
 //   products = 3  hi hi + hi lo + lo hi: 22 bits, as accurate as fp32 products;
 //   products = 1  hi hi.  A is used as rounded in both b A and c A^2 (the
 //                 polynomial of a nearby A: its error near singular value 1 is
-//                 half that of b A exact, c A^2 rounded), and X keeps its lo in
-//                 a X in every step but the last (there the small singular
+//                 half that of b A exact, c A^2 rounded), and X's lo part is added,
+//                 times a, in every step but the last (there the small singular
 //                 values, tripled by a step, would drown in the rounding of the
-//                 large ones; in the last step X as rounded in both terms is the
-//                 better polynomial).  About 2e-3 of the result's norm, which is
-//                 what rounding it to bf16 costs too.
+//                 large ones: 2e-2 of a low-rank matrix; in the last step X as
+//                 rounded is the better polynomial).  At most 1.8e-3 of the
+//                 result's norm in a 64-bit simulation, what rounding it to bf16
+//                 costs too.
+//                 B is formed with a on its diagonal, so that B X holds a X.
+// (With three products a X is added in the epilogue: in the tensor unit's sums, which
+// round towards zero, it cost a low-rank matrix 4e-5.)
 #include <algorithm>
 
 #include "muon.cuh"
@@ -208,12 +212,14 @@ struct Product {
     int64_t tiles;          // of one matrix
     int64_t all;            // of the batch
     int cols_of_tiles;      // tiles of a row of tiles (not the symmetric kinds)
-    float add, mul;         // result = add * term + mul * product
+    float add, mul;         // result = add * term + mul * product, and
+    float diag;             // (kPoly) this on the diagonal
     int rlo, wlo;           // the term has, the result gets, a lo part
     // kFinal: the update applied or stored, r x c (transposed where tall)
     void* out;
     float* w;
     int out_bf16, tall;
+    int pairs;              // rows of an even number of values, out aligned to two of them
     float decay, lr;
     int32_t* d_err;
 };
@@ -276,7 +282,7 @@ __device__ __forceinline__ void tile_at(const Product& Q, int64_t t, int& mat, i
 }
 
 // Where column `col` of a row's 64 fp32 results lies in a set: the first four of each eight in the
-// hi part's 16 bytes of those columns, the others in the lo part's, as the term that they replace.
+// hi part's 16 bytes of those columns, the others in the lo part's.
 __device__ __forceinline__ uint32_t result_at(int row, int col)
 {
     return ((col >> 2) & 1) * (kBM / kBox * kBoxBytes) + (row >> 6) * kBoxBytes + (row & 63) * 128 +
@@ -290,6 +296,16 @@ __device__ __forceinline__ void put_rows(const Product& Q, uint32_t set, int row
     const int rows = min(32, static_cast<int>(Q.m) - row0);
     const int64_t c = Q.n;
     const int64_t at = (mat * Q.m + row0) * c + col0;
+    if (Q.w == nullptr && Q.out_bf16 && Q.pairs) {   // two neighbours a lane
+        if (col0 + 2 * lane >= c) return;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t from = set + result_at(rowl + r, 2 * lane);
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<bf16*>(Q.out) + at + r * c + 2 * lane) =
+                __floats2bfloat162_rn(lds32(from), lds32(from + 4));
+        }
+        return;
+    }
     bool in[2];
     in[0] = col0 + lane < c;
     in[1] = col0 + 32 + lane < c;
@@ -371,7 +387,8 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
     k_muon_product(const __grid_constant__ Maps maps, const Product Q)
 {
     using S = Shape<kKind, kPair, kSplit, BN, P, G>;
-    constexpr bool kSym = S::kSym, kBmn = !S::kSym, kTerm = kKind != kGram;
+    constexpr bool kSym = S::kSym, kBmn = !S::kSym,
+                   kTerm = kKind == kPoly || kKind == kUpdate || (kKind == kFinal && P == 3);
     constexpr bool kSum = P == 3 || kSplit > 1;   // the epilogue sums in registers, piece g of a tile by group g
     constexpr int kStages = S::kStages, TM = kBM * kPair;
     extern __shared__ uint8_t raw[];
@@ -608,7 +625,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
                     ok = all_of(id, kGroup, mbar_wait(bar, terms & 1, &dead));
                     if (!ok) break;
                     ++terms;
-                } else {
+                } else if (kKind != kFinal) {
                     if (head) tma_store_read<0>();   // the set's last results have left
                     all_of(id, kGroup, true);
                 }
@@ -640,6 +657,12 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
                                 for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.add, r[e], x[e]);
                             }
                         }
+                        if (kKind == kPoly && P == 1 && !image) {
+                            const int e0 = row0 + rowl - (col + h * 32 + q * 8);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (e == e0) x[e] += Q.diag;
+                        }
                         if (kKind == kFinal) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) x[e] *= kInvScale;
@@ -668,13 +691,16 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
                         if (P == 1 && image) put_image(at + S::kSubBytes, rowl, h * 4 + q, hi);
                     }
                 }
-                if (kKind == kFinal) {
+                if (kKind == kFinal) {   // a warp's rows are its own affair
                     __syncwarp();
                     if (!Q.tall && !blocked && row0 + (warp & 3) * 32 < Q.m)
                         put_rows(Q, at, (warp & 3) * 32, mat, row0 + (warp & 3) * 32, col, lane);
-                    fence_async_proxy();
-                    all_of(id, kGroup, true);   // every warp is done with the set
-                    if (head && more) fetch(j + kGroups);
+                    __syncwarp();
+                    if (kTerm) {
+                        fence_async_proxy();
+                        all_of(id, kGroup, true);   // every warp is done with the set
+                        if (head && more) fetch(j + kGroups);
+                    }
                     continue;
                 }
                 fence_async_proxy();
@@ -898,6 +924,7 @@ cudaError_t run_steps(const Layout& L, const MuonParams& M, uint8_t* ws, cudaStr
         Q.k = L.m;
         Q.add = M.b;
         Q.mul = M.c * kInvScale;
+        Q.diag = P == 1 ? M.a * kScale : 0.0f;
         Q.rlo = P == 3;
         e = run_kind<kPoly, P>("muon_poly", Maps{ma[0], ma[l], ma[0], ma[l], ma[0], ma[l], mb[0], mb[l]}, Q, M.batch, s);
         if (e != cudaSuccess) return e;
@@ -906,14 +933,17 @@ cudaError_t run_steps(const Layout& L, const MuonParams& M, uint8_t* ws, cudaStr
         Q.n = L.n;
         Q.add = M.a;
         Q.mul = kInvScale;
-        Q.rlo = P == 3 || !last;
+        Q.rlo = P == 3;
         Q.wlo = P == 3 || step + 2 < M.steps;
-        const Maps maps{mb[0], mb[l], mx[in][0], mx[in][l], mx[in][0], mx[in][1], mx[out][0], mx[out][1]};
+        // the term: X, or with one product (a lies on B's diagonal) its lo part in every step but the last
+        const CUtensorMap &term = P == 3 ? mx[in][0] : mx[in][1];
+        const Maps maps{mb[0], mb[l], mx[in][0], mx[in][l], term, mx[in][1], mx[out][0], mx[out][1]};
         if (last) {
             Q.out = M.out;
             Q.w = M.w;
             Q.out_bf16 = M.out_bf16;
             Q.tall = M.r > M.cols;
+            Q.pairs = M.cols % 2 == 0 && reinterpret_cast<uintptr_t>(M.out) % 4 == 0;
             Q.decay = M.decay;
             Q.lr = M.lr;
             e = run_kind<kFinal, P>("muon_final", maps, Q, M.batch, s);

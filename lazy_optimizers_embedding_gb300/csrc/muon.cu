@@ -659,9 +659,10 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
                         }
                         if (kKind == kPoly && P == 1 && !image) {
                             const int e0 = row0 + rowl - (col + h * 32 + q * 8);
+                            if (e0 >= 0 && e0 < 8)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (e == e0) x[e] += Q.diag;
+                                for (int e = 0; e < 8; ++e)
+                                    if (e == e0) x[e] += Q.diag;
                         }
                         if (kKind == kFinal) {
 #pragma unroll

@@ -77,8 +77,9 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
 }
 
 // X = u / (|u| + eps), scaled and split, and the new momentum buffer, where X lies as u does (wide,
-// whole 16-byte accesses): `pieces` blocks a matrix, 8 values an access.  (16 x 768 x 2048 bf16:
-// 35 us, 150 MB.)
+// whole 16-byte accesses): `pieces` blocks a matrix, 8 accesses of 8 values a thread (fewer, larger
+// blocks are busy for less time with the scale, which each works out: 16 x 768 x 2048 bf16, 150 MB, 31
+// us; 4 accesses 36 us, 32 accesses 33 us).
 __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float* __restrict__ buf, int64_t size, int pieces,
                                                                 const float* __restrict__ part, int parts, float eps,
                                                                 __half* __restrict__ hi, __half* __restrict__ lo,
@@ -87,37 +88,29 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
     pdl_enter();   // writes the workspace and optimizer state only
     __shared__ float sums[2 * 32];
     if (buf != nullptr && read_error(d_err) != 0) return;   // set before this kernel: the same for every block
-    constexpr int R = 2;
     const int mat = static_cast<int>(blockIdx.x) / pieces, p = static_cast<int>(blockIdx.x) % pieces;
     const int64_t base = mat * size, step = static_cast<int64_t>(pieces) * kMuonBlock * 8;
     const int64_t rows = size / c;
     float scale = -1.0f;
-    for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += R * step) {
-        float u[R][8], nb[R][8];
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-            if (i + q * step < size) read_u<8>(U, base + i + q * step, u[q], nb[q]);
+    for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += step) {
+        float u[8], nb[8];
+        if (i < size) read_u<8>(U, base + i, u, nb);
         if (scale < 0.0f) scale = start_scale(part + static_cast<int64_t>(mat) * parts, parts, eps, sums);   // while those are on their way
+        if (i >= size) continue;
+        if (buf) Pack<float, 8>::put(buf + base + i, nb);
+        const int64_t to = ldn == c ? base + i : (mat * rows + i / c) * ldn + i % c;
+        uint4 h, l;
+        __half2* hh = reinterpret_cast<__half2*>(&h);
+        __half2* ll = reinterpret_cast<__half2*>(&l);
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int64_t at = i + q * step;
-            if (at >= size) continue;
-            if (buf) Pack<float, 8>::put(buf + base + at, nb[q]);
-            int64_t to = base + at;
-            if (ldn != c) to = (mat * rows + at / c) * ldn + at % c;
-            uint4 h, l;
-            __half2* hh = reinterpret_cast<__half2*>(&h);
-            __half2* ll = reinterpret_cast<__half2*>(&l);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = u[q][2 * e] * scale, b = u[q][2 * e + 1] * scale;
-                hh[e] = __floats2half2_rn(a, b);
-                const float2 f = __half22float2(hh[e]);
-                ll[e] = __floats2half2_rn(a - f.x, b - f.y);
-            }
-            *reinterpret_cast<uint4*>(hi + to) = h;
-            if (lo) *reinterpret_cast<uint4*>(lo + to) = l;
+        for (int e = 0; e < 4; ++e) {
+            const float a = u[2 * e] * scale, b = u[2 * e + 1] * scale;
+            hh[e] = __floats2half2_rn(a, b);
+            const float2 f = __half22float2(hh[e]);
+            ll[e] = __floats2half2_rn(a - f.x, b - f.y);
         }
+        *reinterpret_cast<uint4*>(hi + to) = h;
+        if (lo) *reinterpret_cast<uint4*>(lo + to) = l;
     }
 }
 
@@ -404,6 +397,12 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
     const int64_t first = blockIdx.x / (kPair * kSplit), step = gridDim.x / (kPair * kSplit);
     const int part_of_k = kSplit > 1 ? static_cast<int>(cluster_rank()) : 0;
 
+    if (threadIdx.x == 32) {   // while the kernel before ends
+        tma_prefetch(&maps.ahi);
+        tma_prefetch(&maps.bhi);
+        if (kTerm) tma_prefetch(&maps.rhi);
+        if (kKind != kFinal) tma_prefetch(&maps.whi);
+    }
     if (threadIdx.x == 0) {
         dead = 0;
         for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
@@ -429,8 +428,6 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
     const int begin = all_chunks * part_of_k / kSplit, chunks = all_chunks * (part_of_k + 1) / kSplit;
     if (warp == 0) {
         if (elect_one()) {
-            tma_prefetch(&maps.ahi);
-            tma_prefetch(&maps.bhi);
             uint32_t it = 0;
             for (int64_t t = first; t < Q.all; t += step) {
                 int mat, row0, col0;
@@ -985,7 +982,7 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
         __half* xlo = lo ? reinterpret_cast<__half*>(base + L.x[0][1]) : nullptr;
         SO_PROFILE("muon_start", s);
         if (values == 8 && M.r <= M.cols) {
-            const int pieces = static_cast<int>(std::max<int64_t>(1, size / (kMuonBlock * 8 * 4)));
+            const int pieces = static_cast<int>(std::max<int64_t>(1, size / (kMuonBlock * 8 * 8)));
             e = launch(k_muon_start_flat, dim3(static_cast<unsigned>(M.batch * pieces)), dim3(kMuonBlock), s, U, M.buf, size,
                        pieces, static_cast<const float*>(part), L.parts, M.eps, xhi, xlo, static_cast<int>(M.cols), L.ldn,
                        static_cast<const int32_t*>(M.d_err));

@@ -462,7 +462,8 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
  * accepted when X, A, B and a I + B stay below 3.9 from every singular value in [0, 1].
  * products: 3 computes each matrix product to 22 bits (fp32 accuracy, for fp32
  * results); 1 to 11 bits (about 2e-3 of the result's norm, what rounding it to
- * bf16 costs), in half the time or less for large matrices.
+ * bf16 costs), in half the time or less for large matrices; matrices of at most
+ * 128 rows or columns are always computed with 3.
  */
 typedef struct {
     double a, b, c, eps;

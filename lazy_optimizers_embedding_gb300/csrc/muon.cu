@@ -19,9 +19,9 @@
 //                 times a, in every step but the last (there the small singular
 //                 values, tripled by a step, would drown in the rounding of the
 //                 large ones: 2e-2 of a low-rank matrix; in the last step X as
-//                 rounded is the better polynomial).  At most 1.8e-3 of the
-//                 result's norm in a 64-bit simulation, what rounding it to bf16
-//                 costs too.
+//                 rounded is the better polynomial).  At most 1.7e-3 of the
+//                 result's norm in a 64-bit simulation (more than 128 rows), what
+//                 rounding it to bf16 costs too.
 //                 B is formed with a on its diagonal, so that B X holds a X.
 // (With three products a X is added in the epilogue: in the tensor unit's sums, which
 // round towards zero, it cost a low-rank matrix 4e-5.)
@@ -786,14 +786,18 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 struct Layout {
     int64_t m, n, ldm, ldn;
-    int parts;
+    int parts, products;
     size_t part, x[2][2], a[2], b[2], total;   // [.][0] hi, [.][1] lo
 };
 
-Layout muon_layout(int64_t batch, int64_t r, int64_t c, int products)
+// Matrices of at most 128 rows (columns) have three products whatever was asked for: with one, the few
+// roundings that a small matrix averages over are off by up to 2.2e-3 of its norm, and its time is
+// that of the launches and phases.
+Layout muon_layout(int64_t batch, int64_t r, int64_t c, int asked)
 {
     Layout L{};
     L.m = std::min(r, c);
+    const int products = L.products = L.m <= 128 ? 3 : asked;
     L.n = std::max(r, c);
     L.ldm = up(L.m, 64);   // rows start on 128-byte lines: copies of boxes read whole ones
     L.ldn = up(L.n, 64);
@@ -977,7 +981,7 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (muon_fits_cluster(M.batch, L.m, L.n)) return muon_cluster(M, U, part, L.parts, values > 1, s);
     {
-        const bool lo = M.products == 3 || M.steps > 1;
+        const bool lo = L.products == 3 || M.steps > 1;
         __half* xhi = reinterpret_cast<__half*>(base + L.x[0][0]);
         __half* xlo = lo ? reinterpret_cast<__half*>(base + L.x[0][1]) : nullptr;
         SO_PROFILE("muon_start", s);
@@ -996,7 +1000,7 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
         }
     }
     if (e != cudaSuccess) return e;
-    return M.products == 3 ? run_steps<3>(L, M, base, s) : run_steps<1>(L, M, base, s);
+    return L.products == 3 ? run_steps<3>(L, M, base, s) : run_steps<1>(L, M, base, s);
 }
 
 }  // namespace so

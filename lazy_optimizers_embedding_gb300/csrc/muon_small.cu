@@ -2,7 +2,8 @@
 // tall) whose X a cluster's shared memory holds: all steps in one launch.
 //
 // A cluster of up to 8 blocks has one matrix; each block keeps a slice of up to 256
-// columns of X, hi and lo f16, and the whole of A and B.  A step is
+// columns of X, hi and lo f16, and the whole of A and B (three products: the time is
+// mostly that of the phases, 35 us for 64 x 128 with one or three).  A step is
 //   A's share of the slice     X_s X_s^T, the shares summed over the cluster through
 //                              shared memory, in block order on every block alike
 //   A A                        by every block
@@ -46,8 +47,7 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t addr)
     return v;
 }
 
-// Eight values as hi and (kLo) lo f16 to shared memory.
-template <bool kLo>
+// Eight values as hi and lo f16 to shared memory.
 __device__ __forceinline__ void split8(uint32_t hi_at, uint32_t lo_at, const float (&x)[8])
 {
     uint4 hi, lo;
@@ -60,7 +60,7 @@ __device__ __forceinline__ void split8(uint32_t hi_at, uint32_t lo_at, const flo
         ll[e] = __floats2half2_rn(x[2 * e] - f.x, x[2 * e + 1] - f.y);
     }
     sts128(hi_at, hi);
-    if (kLo) sts128(lo_at, lo);
+    sts128(lo_at, lo);
 }
 
 __device__ __forceinline__ uint16_t bits_of(__half h) { return __half_as_ushort(h); }
@@ -88,7 +88,7 @@ struct Small {
     int32_t* d_err;
 };
 
-template <bool kVec, int P>
+template <bool kVec>
 __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
 {
     extern __shared__ uint8_t raw[];
@@ -181,10 +181,8 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
             for (int q = 0; q < 4; ++q) {
                 const uint64_t a = q * 2, b = kMn ? q * 128 : q * 2;   // 16 K values, in 16-byte units
                 tc_mma_f16<1>(tmem + d, ah + a, bh + b, idesc, k + q > 0);
-                if (P == 3) {
-                    tc_mma_f16<1>(tmem + x, ah + a, bl + b, idesc, d == x || k + q > 0);
-                    tc_mma_f16<1>(tmem + x, al + a, bh + b, idesc, true);
-                }
+                tc_mma_f16<1>(tmem + x, ah + a, bl + b, idesc, d == x || k + q > 0);
+                tc_mma_f16<1>(tmem + x, al + a, bh + b, idesc, true);
             }
             ah += kBlockBytes / 16, al += kBlockBytes / 16;
             bh += kMn ? 512 : kBlockBytes / 16, bl += kMn ? 512 : kBlockBytes / 16;
@@ -210,11 +208,9 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
                     tmem_load32(lanes + kGramCol + half * per + q * 32, v);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) av[q * 32 + e] = v[e];
-                    if (P == 3) {
-                        tmem_load32(lanes + kCrossCol + half * per + q * 32, v);
+                    tmem_load32(lanes + kCrossCol + half * per + q * 32, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) av[q * 32 + e] += v[e];
-                    }
+                    for (int e = 0; e < 32; ++e) av[q * 32 + e] += v[e];
                 }
         }
         if (blocks > 1) {
@@ -278,10 +274,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = av[8 * q + e] = rows_used ? av[8 * q + e] * kInvScale : 0.0f;
                 const uint32_t p = place(row, half * per + q * 8);
-                split8<P == 3>(shi + p, slo + p, x);   // zeros in the rows past the matrix's
-                if (P == 1)   // A as rounded in b A too
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) av[8 * q + e] = __half2float(__float2half_rn(x[e]));
+                split8(shi + p, slo + p, x);   // zeros in the rows past the matrix's
             }
         operands_done();
 
@@ -296,17 +289,17 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
                 if (q * 32 < per) {
                     float v[32], y[32];
                     tmem_load32(lanes + kGramCol + half * per + q * 32, v);
-                    if (P == 3) tmem_load32(lanes + kCrossCol + half * per + q * 32, y);
+                    tmem_load32(lanes + kCrossCol + half * per + q * 32, y);
 #pragma unroll
                     for (int p8 = 0; p8 < 4; ++p8) {
                         float x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int i = p8 * 8 + e;
-                            x[e] = fmaf(Q.b, av[q * 32 + i], Q.c * kInvScale * (P == 3 ? v[i] + y[i] : v[i]));
+                            x[e] = fmaf(Q.b, av[q * 32 + i], Q.c * kInvScale * (v[i] + y[i]));
                         }
                         const uint32_t p = place(row, half * per + q * 32 + p8 * 8);
-                        split8<P == 3>(shi + p, slo + p, x);
+                        split8(shi + p, slo + p, x);
                     }
                 }
         }
@@ -328,9 +321,8 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
                     unpack8(lds128(xhi + p), x);
                     unpack8(lds128(xlo + p), l);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)   // one product: X as rounded in the last step
-                        x[e] = fmaf(Q.a, P == 3 || step + 1 < Q.steps ? x[e] + l[e] : x[e], kInvScale * v[p8 * 8 + e]);
-                    split8<true>(xhi + p, xlo + p, x);
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.a, x[e] + l[e], kInvScale * v[p8 * 8 + e]);
+                    split8(xhi + p, xlo + p, x);
                 }
             }
     }
@@ -377,8 +369,8 @@ int clusters_at_once(int blocks)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (allow_smem(k_muon_cluster<true, 3>, kSmallSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, k_muon_cluster<true, 3>, &cfg) != cudaSuccess) n = 0;
+        if (allow_smem(k_muon_cluster<true>, kSmallSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_muon_cluster<true>, &cfg) != cudaSuccess) n = 0;
         n = std::max(n, 1);
         known[blocks].store(n, std::memory_order_relaxed);
     }
@@ -424,8 +416,7 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.decay = M.decay;
     Q.lr = M.lr;
     Q.d_err = M.d_err;
-    auto* kernel = M.products == 3 ? (vec ? k_muon_cluster<true, 3> : k_muon_cluster<false, 3>)
-                                   : (vec ? k_muon_cluster<true, 1> : k_muon_cluster<false, 1>);
+    auto* kernel = vec ? k_muon_cluster<true> : k_muon_cluster<false>;
     const cudaError_t ready = allow_smem(kernel, kSmallSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};

@@ -459,7 +459,8 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
  * transpose):  X = u / (|u|_F + eps), then `steps` times A = X X^T,
  * B = b A + c A^2, X = a X + B X.  a, b, c = 3.4445, -4.7750, 2.0315 and 5 steps
  * bring the singular values to 1 within about 0.3; other coefficients are
- * accepted when X, A, B and a I + B stay below 3.9 from every singular value in [0, 1].
+ * accepted when the singular values of X, A, B and a I + B, bounded step by step from
+ * X's in [0, 1] on, stay below 3.9.
  * products: 3 computes each matrix product to 22 bits (fp32 accuracy, for fp32
  * results); 1 to 11 bits (about 2e-3 of the result's norm, what rounding it to
  * bf16 costs), in half the time or less for large matrices; matrices of at most

@@ -48,8 +48,11 @@ bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const in
 }
 
 // Newton-Schulz keeps X, A = X X^T and B = b A + c A^2, with and without a on its
-// diagonal, as f16 values times 2^14: their singular values, followed here over [0, 1] (all that a matrix of Frobenius norm at
-// most 1 can have), have to stay below 65504 / 2^14 with 2 % to spare.
+// diagonal, as f16 values times 2^14: their singular values have to stay below
+// 65504 / 2^14 with 2 % to spare.  Bounded step by step, X's from [0, 1] on (all that a
+// matrix of Frobenius norm at most 1 can have): with l = x^2 at most h^2, the largest
+// of |b l + c l^2|, |a + b l + c l^2| and |x (a + b l + c l^2)| is at an end of [0, h]
+// or where a derivative is 0.
 constexpr double kMaxNs = 3.9;
 
 bool valid_ns(const sparse_ns_config_t& c)
@@ -57,14 +60,31 @@ bool valid_ns(const sparse_ns_config_t& c)
     if (!std::isfinite(c.a) || !std::isfinite(c.b) || !std::isfinite(c.c) || !(c.eps >= 0.0) || !std::isfinite(c.eps) ||
         c.steps < 1 || c.steps > 64 || (c.products != 1 && c.products != 3))
         return false;
-    constexpr int kPoints = 2048;
-    for (int i = 0; i <= kPoints; ++i) {
-        double x = static_cast<double>(i) / kPoints;
-        for (int s = 0; s < c.steps; ++s) {
-            const double l = x * x, p = c.b * l + c.c * l * l;
-            x = c.a * x + p * x;
-            if (!(std::fabs(l) <= kMaxNs && std::fabs(p) <= kMaxNs && std::fabs(c.a + p) <= kMaxNs && std::fabs(x) <= kMaxNs)) return false;
+    // l of the extrema of b l + c l^2, and of x (a + b x^2 + c x^4); the ends
+    double at[5] = {0.0, 0.0, 0.0, 0.0, 0.0};   // [4]: the end 0
+    if (c.c != 0.0) {
+        at[0] = -c.b / (2.0 * c.c);
+        const double d = 9.0 * c.b * c.b - 20.0 * c.a * c.c;
+        if (d >= 0.0) {
+            at[1] = (-3.0 * c.b + std::sqrt(d)) / (10.0 * c.c);
+            at[2] = (-3.0 * c.b - std::sqrt(d)) / (10.0 * c.c);
         }
+    } else if (c.b != 0.0) {
+        at[1] = -c.a / (3.0 * c.b);
+    }
+    double h = 1.0;
+    for (int s = 0; s < c.steps; ++s) {
+        const double top = h * h;
+        double next = 0.0;
+        at[3] = top;
+        for (double l : at) {
+            if (!(l >= 0.0 && l <= top)) continue;
+            const double p = c.b * l + c.c * l * l, x = std::sqrt(l) * (c.a + p);
+            if (!(std::fabs(p) <= kMaxNs && std::fabs(c.a + p) <= kMaxNs)) return false;
+            next = std::fmax(next, std::fabs(x));
+        }
+        if (!(top <= kMaxNs && next <= kMaxNs)) return false;
+        h = next;
     }
     return true;
 }

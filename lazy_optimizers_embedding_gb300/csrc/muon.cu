@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
     for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += step) {
         float u[8], nb[8];
         if (i < size) read_u<8>(U, base + i, u, nb);
-        if (scale < 0.0f) scale = start_scale(part + static_cast<int64_t>(mat) * parts, parts, eps, sums);   // while those are on their way
+        if (scale < 0.0f) scale = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, sums);   // while those are on their way
         if (i >= size) continue;
         if (buf) Pack<float, 8>::put(buf + base + i, nb);
         const int64_t to = ldn == c ? base + i : (mat * rows + i / c) * ldn + i % c;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __re
         const int64_t r0 = q / tiles_c * 64, c0 = q % tiles_c * 64;
         if (mat != have) {
             if (have >= 0) __syncthreads();   // the last sums have been read
-            scale = start_scale(part + mat * parts, parts, eps, sums);
+            scale = start_scale<kMuonBlock>(part + mat * parts, parts, eps, sums);
             have = mat;
         }
         float u[4][4];

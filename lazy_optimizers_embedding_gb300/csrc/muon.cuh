@@ -101,13 +101,14 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8])
     }
 }
 
-// Scale of one matrix from its `parts` sums of squares, by a block of kMuonBlock threads (`tmp`: 64
+// Scale of one matrix from its `parts` sums of squares, by a block of kThreads threads (`tmp`: 64
 // words).  fp32: in fp64 the root and quotient alone held a block for 4 us.
+template <int kThreads>
 __device__ __forceinline__ float start_scale(const float* part, int parts, float eps, float* tmp)
 {
     float s[1] = {0.0f};
-    for (int i = threadIdx.x; i < parts; i += kMuonBlock) s[0] += part[i];
-    group_sum<1>(s, kMuonBlock, tmp, 0);
+    for (int i = threadIdx.x; i < parts; i += kThreads) s[0] += part[i];
+    group_sum<1>(s, kThreads, tmp, 0);
     return kScale / (sqrtf(s[0]) + eps);
 }
 

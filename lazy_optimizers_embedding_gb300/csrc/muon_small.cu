@@ -32,6 +32,7 @@ constexpr uint32_t kBlockBytes = kRows * 128;    // 64 columns of 128 rows
 constexpr uint32_t kXBytes = kSlice / 64 * kBlockBytes, kSquareBytes = kRows / 64 * kBlockBytes;
 constexpr uint32_t kSmallSmem = 2 * kXBytes + 2 * kSquareBytes + 1024;
 constexpr int kMaxCluster = 8;
+constexpr int kBlockThreads = 512, kWarps = kBlockThreads / 32;   // four warps for every 32 rows, a quarter of the columns each
 constexpr uint32_t kGramCol = 0, kCrossCol = 128, kUpdateCol = 256, kTmemCols = 512;
 
 // Byte of element (row, col) in an array of 64-column blocks, 16-byte pieces permuted by row.
@@ -82,14 +83,14 @@ struct Small {
     int parts;
     float* buf;
     void* out;
-    int out_bf16;
+    int out_bf16, vec;   // vec: rows of a multiple of four values, out (w) aligned to four of them
     float* w;
     float decay, lr;
     int32_t* d_err;
 };
 
 template <bool kVec>
-__global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
+__global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bar_mem;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc<1>(&tmem_slot, kTmemCols);
-    for (uint32_t i = threadIdx.x * 16; i < 2 * kXBytes; i += kMuonBlock * 16) sts128(xhi + i, make_uint4(0u, 0u, 0u, 0u));
+    for (uint32_t i = threadIdx.x * 16; i < 2 * kXBytes; i += kBlockThreads * 16) sts128(xhi + i, make_uint4(0u, 0u, 0u, 0u));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -119,40 +120,59 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
     const bool blocked = (Q.w != nullptr) && read_error(Q.d_err) != 0;   // set before this kernel: the same for every block
 
     // X of the slice, scaled and split; the new momentum buffer
-    const float scale = start_scale(Q.part + mat * Q.parts, Q.parts, Q.eps, sums);
-    if (!blocked) {
-        const int64_t base = mat * Q.size;
-        // along u's rows: X's rows, or its columns where u is tall
-        const int outer = Q.tall ? cols : Q.m, inner = Q.tall ? Q.m : cols, quads = (inner + 3) / 4;
-        for (int i = threadIdx.x; i < outer * quads; i += kMuonBlock) {
-            const int o = i / quads, k = i % quads * 4;
-            const int64_t at = base + (Q.tall ? static_cast<int64_t>(col0 + o) * Q.m + k : static_cast<int64_t>(o) * Q.n + col0 + k);
-            const int left = min(4, inner - k);
-            float u[4], nb[4];
-            read_u4<kVec>(U, at, left, u, nb);
-            if (Q.buf) {
-                if (kVec) {
-                    Pack<float, 4>::put(Q.buf + at, nb);
-                } else {
+    const float scale = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, sums);
+    const int64_t base = mat * Q.size;
+    // A warp takes u's rows (X's, or its columns where u is tall) kWarps apart, a lane four values at a time.
+    const int outer = Q.tall ? cols : Q.m, inner = Q.tall ? Q.m : cols;
+    auto value_at = [&](int o, int k) {
+        return base + (Q.tall ? static_cast<int64_t>(col0 + o) * Q.m + k : static_cast<int64_t>(o) * Q.n + col0 + k);
+    };
+    constexpr int kRowsAtOnce = 4;
+    if (!blocked)
+        for (int k = lane * 4; k < inner; k += 128)
+            for (int o0 = warp; o0 < outer; o0 += kWarps * kRowsAtOnce) {
+                float u[kRowsAtOnce][4], nb[kRowsAtOnce][4];
+                const int left = min(4, inner - k);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < left) Q.buf[at + e] = nb[e];
+                for (int i = 0; i < kRowsAtOnce; ++i) {
+                    const int o = o0 + i * kWarps;
+                    if (o < outer) read_u4<kVec>(U, value_at(o, k), left, u[i], nb[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kRowsAtOnce; ++i) {
+                    const int o = o0 + i * kWarps;
+                    if (o >= outer) continue;
+                    if (Q.buf) {
+                        const int64_t at = value_at(o, k);
+                        if (kVec) {
+                            Pack<float, 4>::put(Q.buf + at, nb[i]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (e < left) Q.buf[at + e] = nb[i][e];
+                        }
+                    }
+                    uint16_t h[4], l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {   // 0 past `left`
+                        const float v = u[i][e] * scale;
+                        const __half q = __float2half_rn(v);
+                        h[e] = bits_of(q), l[e] = bits_of(__float2half_rn(v - __half2float(q)));
+                    }
+                    if (Q.tall) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < left) sts16(xhi + place(k + e, o), h[e]), sts16(xlo + place(k + e, o), l[e]);
+                    } else {
+                        const uint32_t p = place(o, k);   // four columns of one 16-byte piece
+                        sts64(xhi + p, h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+                        sts64(xlo + p, l[0] | static_cast<uint32_t>(l[1]) << 16, l[2] | static_cast<uint32_t>(l[3]) << 16);
+                    }
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) {
-                    const float v = u[e] * scale;
-                    const __half h = __float2half_rn(v);
-                    const uint32_t p = Q.tall ? place(k + e, o) : place(o, k + e);
-                    sts16(xhi + p, bits_of(h));
-                    sts16(xlo + p, bits_of(__float2half_rn(v - __half2float(h))));
-                }
-        }
-    }
 
-    // this warp's share of an accumulator: 32 rows, half the columns
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    // this warp's share of an accumulator: 32 rows, a quarter of the columns
+    const int row = (warp & 3) * 32 + lane, quarter = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool rows_used = (warp & 3) * 32 < Q.m;
     uint32_t phase = 0;
@@ -198,38 +218,34 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
             issue(std::false_type{}, kGramCol, kCrossCol, square, dxh, dxl, dxh, dxl, Q.slice / 64);
         }
         products_done();
-        const int per = side / 2;              // columns of A this warp has: 32 or 64
-        float av[64];
-        if (rows_used) {
+        const int per = side / 4;              // columns of A this warp has: 16 or 32
+        float av[32];
+        if (rows_used)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                if (q * 32 < per) {
-                    float v[32];
-                    tmem_load32(lanes + kGramCol + half * per + q * 32, v);
+                if (q * 16 < per) {
+                    float v[16], x[16];
+                    tmem_load16(lanes + kGramCol + quarter * per + q * 16, lanes + kCrossCol + quarter * per + q * 16, v, x);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) av[q * 32 + e] = v[e];
-                    tmem_load32(lanes + kCrossCol + half * per + q * 32, v);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) av[q * 32 + e] += v[e];
+                    for (int e = 0; e < 16; ++e) av[q * 16 + e] = v[e] + x[e];
                 }
-        }
         if (blocks > 1) {
             // The shares, fp32, where A will be: rows of side / 4 16-byte pieces, permuted by row.  Block r
             // sums the r-th part of the pieces over the cluster, in block order, in place (no other block
             // reads that part of its share), then every block fetches the others' sums, neighbouring
             // lanes neighbouring pieces.  (Every block reading every share in its own rows' order, 16
             // bytes of 32 rows at a time, took 130 us a step at 128 x 2048.)
-            const int quads = side / 4, mine = quads * side / blocks;
-            auto quad = [&](int q) { return shi + static_cast<uint32_t>(row * quads + ((half * (per / 4) + q) ^ (row & 7))) * 16; };
+            const int quads = side / 4, mine = quads * side / blocks, shift = 31 - __clz(mine);   // powers of two
+            auto quad = [&](int q) { return shi + static_cast<uint32_t>(row * quads + ((quarter * (per / 4) + q) ^ (row & 7))) * 16; };
             if (rows_used)
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
+                for (int q = 0; q < 8; ++q)
                     if (q * 4 < per)
                         sts128(quad(q), make_uint4(__float_as_uint(av[4 * q]), __float_as_uint(av[4 * q + 1]),
                                                    __float_as_uint(av[4 * q + 2]), __float_as_uint(av[4 * q + 3])));
             cluster_sync();
             const int used = min(side, (Q.m + 31) / 32 * 32) * quads;   // pieces of rows that the warps wrote
-            for (int f = rank * mine + threadIdx.x; f < (rank + 1) * mine && f < used; f += kMuonBlock) {
+            for (int f = rank * mine + threadIdx.x; f < (rank + 1) * mine && f < used; f += kBlockThreads) {
                 float4 v[kMaxCluster];
 #pragma unroll
                 for (int r = 0; r < kMaxCluster; ++r)
@@ -241,17 +257,17 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
                 sts128(shi + f * 16, make_uint4(__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)));
             }
             cluster_sync();
-            for (int f0 = threadIdx.x; f0 < used; f0 += 8 * kMuonBlock) {
+            for (int f0 = threadIdx.x; f0 < used; f0 += 8 * kBlockThreads) {
                 float4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int f = f0 + i * kMuonBlock;
-                    if (f < used && f / mine != rank) v[i] = lds_cluster(cluster_addr(shi + f * 16, f / mine));
+                    const int f = f0 + i * kBlockThreads;
+                    if (f < used && f >> shift != rank) v[i] = lds_cluster(cluster_addr(shi + f * 16, f >> shift));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int f = f0 + i * kMuonBlock;
-                    if (f < used && f / mine != rank)
+                    const int f = f0 + i * kBlockThreads;
+                    if (f < used && f >> shift != rank)
                         sts128(shi + f * 16, make_uint4(__float_as_uint(v[i].x), __float_as_uint(v[i].y), __float_as_uint(v[i].z),
                                                         __float_as_uint(v[i].w)));
                 }
@@ -259,7 +275,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
             cluster_sync();   // the block has all sums, and no block reads another's any more
             if (rows_used)
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
+                for (int q = 0; q < 8; ++q)
                     if (q * 4 < per) {
                         const uint4 f = lds128(quad(q));
                         av[4 * q] = __uint_as_float(f.x), av[4 * q + 1] = __uint_as_float(f.y);
@@ -268,12 +284,12 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
             __syncthreads();
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 4; ++q)
             if (q * 8 < per) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = av[8 * q + e] = rows_used ? av[8 * q + e] * kInvScale : 0.0f;
-                const uint32_t p = place(row, half * per + q * 8);
+                const uint32_t p = place(row, quarter * per + q * 8);
                 split8(shi + p, slo + p, x);   // zeros in the rows past the matrix's
             }
         operands_done();
@@ -283,26 +299,24 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
             issue(std::false_type{}, kGramCol, kCrossCol, square, dsh, dsl, dsh, dsl, side / 64);
         }
         products_done();
-        if (rows_used) {
+        if (rows_used)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                if (q * 32 < per) {
-                    float v[32], y[32];
-                    tmem_load32(lanes + kGramCol + half * per + q * 32, v);
-                    tmem_load32(lanes + kCrossCol + half * per + q * 32, y);
+                if (q * 16 < per) {
+                    float v[16], y[16];
+                    tmem_load16(lanes + kGramCol + quarter * per + q * 16, lanes + kCrossCol + quarter * per + q * 16, v, y);
 #pragma unroll
-                    for (int p8 = 0; p8 < 4; ++p8) {
+                    for (int p8 = 0; p8 < 2; ++p8) {
                         float x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int i = p8 * 8 + e;
-                            x[e] = fmaf(Q.b, av[q * 32 + i], Q.c * kInvScale * (v[i] + y[i]));
+                            x[e] = fmaf(Q.b, av[q * 16 + i], Q.c * kInvScale * (v[i] + y[i]));
                         }
-                        const uint32_t p = place(row, half * per + q * 32 + p8 * 8);
+                        const uint32_t p = place(row, quarter * per + q * 16 + p8 * 8);
                         split8(shi + p, slo + p, x);
                     }
                 }
-        }
         operands_done();
 
         // ---- B X, and the new X in its place
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
         }
         products_done();
         if (rows_used)
-            for (int q = half; q < Q.slice / 32; q += 2) {
+            for (int q = quarter; q < Q.slice / 32; q += 4) {
                 float v[32];
                 tmem_load32(lanes + kUpdateCol + q * 32, v);
 #pragma unroll
@@ -328,23 +342,70 @@ __global__ void __launch_bounds__(kMuonBlock, 1) k_muon_cluster(const Update U, 
     }
     __syncthreads();
 
-    // the update, along u's rows
-    if (!blocked) {
-        const int64_t base = mat * Q.size;
-        const int outer = Q.tall ? cols : Q.m, inner = Q.tall ? Q.m : cols;
-        for (int o = warp; o < outer; o += kMuonBlock / 32)
-            for (int k = lane; k < inner; k += 32) {
-                const uint32_t p = Q.tall ? place(k, o) : place(o, k);
-                const float x = (__half2float(lds_half(xhi + p)) + __half2float(lds_half(xlo + p))) * kInvScale;
-                const int64_t at = base + (Q.tall ? static_cast<int64_t>(col0 + o) * Q.m + k : static_cast<int64_t>(o) * Q.n + col0 + k);
+    // the update, as u came
+    if (!blocked)
+        for (int k = lane * 4; k < inner; k += 128)
+            for (int o0 = warp; o0 < outer; o0 += kWarps * kRowsAtOnce) {
+                const int left = min(4, inner - k);
+                float w[kRowsAtOnce][4];
                 if (Q.w)
-                    Q.w[at] = fmaf(Q.decay, Q.w[at], -Q.lr * x);
-                else if (Q.out_bf16)
-                    static_cast<bf16*>(Q.out)[at] = __float2bfloat16_rn(x);
-                else
-                    static_cast<float*>(Q.out)[at] = x;
+#pragma unroll
+                    for (int i = 0; i < kRowsAtOnce; ++i) {
+                        const int o = o0 + i * kWarps;
+                        if (o >= outer) continue;
+                        const float* from = Q.w + value_at(o, k);
+                        if (Q.vec) {
+                            Pack<float, 4> q;
+                            q.load(from);
+                            q.get(w[i]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[i][e] = e < left ? from[e] : 0.0f;
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < kRowsAtOnce; ++i) {
+                    const int o = o0 + i * kWarps;
+                    if (o >= outer) continue;
+                    float x[4];
+                    if (Q.tall) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t p = place(k + min(e, left - 1), o);
+                            x[e] = __half2float(lds_half(xhi + p)) + __half2float(lds_half(xlo + p));
+                        }
+                    } else {
+                        const uint2 h = lds64(xhi + place(o, k)), l = lds64(xlo + place(o, k));
+                        const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x)), h1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+                        const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(&l.x)), l1 = __half22float2(*reinterpret_cast<const __half2*>(&l.y));
+                        x[0] = h0.x + l0.x, x[1] = h0.y + l0.y, x[2] = h1.x + l1.x, x[3] = h1.y + l1.y;
+                    }
+                    const int64_t at = value_at(o, k);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] *= kInvScale;
+                        if (Q.w) x[e] = fmaf(Q.decay, w[i][e], -Q.lr * x[e]);
+                    }
+                    float* to = Q.w ? Q.w : static_cast<float*>(Q.out);
+                    if (Q.out_bf16) {
+                        bf16* out = static_cast<bf16*>(Q.out) + at;
+                        if (Q.vec) {
+                            const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+                            *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (e < left) out[e] = __float2bfloat16_rn(x[e]);
+                        }
+                    } else if (Q.vec) {
+                        Pack<float, 4>::put(to + at, x);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < left) to[at + e] = x[e];
+                    }
+                }
             }
-    }
     if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
     tc_fence_before();
     __syncthreads();
@@ -360,7 +421,7 @@ int clusters_at_once(int blocks)
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(blocks);
-        cfg.blockDim = dim3(kMuonBlock);
+        cfg.blockDim = dim3(kBlockThreads);
         cfg.dynamicSmemBytes = kSmallSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -411,7 +472,8 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.parts = parts;
     Q.buf = M.buf;
     Q.out = M.out;
-    Q.out_bf16 = M.out_bf16;
+    Q.out_bf16 = M.w == nullptr && M.out_bf16;
+    Q.vec = M.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(M.w) | reinterpret_cast<uintptr_t>(M.out)) % (Q.out_bf16 ? 8 : 16) == 0;
     Q.w = M.w;
     Q.decay = M.decay;
     Q.lr = M.lr;
@@ -421,7 +483,7 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M.batch * blocks));
-    cfg.blockDim = dim3(kMuonBlock);
+    cfg.blockDim = dim3(kBlockThreads);
     cfg.dynamicSmemBytes = kSmallSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

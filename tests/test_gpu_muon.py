@@ -2,7 +2,7 @@
 
 Results are compared in the Frobenius norm.  A 64-bit simulation of the kernels' f16 splits and
 roundings over flat, decaying and low-rank spectra (64 x 128 to 1024 x 1024) is off by at most 2.0e-3 of
-the norm with one product and 3.4e-6 with three; the bounds are 2.5 times the first and 6 times the
+the norm with one product and 6.5e-6 with three; the bounds are 2.5 times the first and three times the
 second, which also holds the fp32 accumulation.  Rounding to bf16 adds at most 2^-9 of the norm.
 Weights: (1 - lr wd) w - lr s O adds the bound of O times lr s, and 2 roundings of fp32.
 """

@@ -881,14 +881,19 @@ cudaError_t run_kind(const char* name, const Maps& maps, const Product& Q, int64
                   half = shape_cost<kKind, 1, 1, 64, P>(Q, batch), two = shape_cost<kKind, 1, 2, 128, P>(Q, batch),
                   four = shape_cost<kKind, 1, 4, 128, P>(Q, batch);
     const int64_t least = std::min(std::min(std::min(wide, pair), std::min(one, half)), std::min(two, four));
-    if (wide == least) {
+    if (wide == least || pair == least) {
         // a short product's tile is finished in less time than two groups take over its results; a
         // long one's fares better with a fifth stage in place of the third group's set
-        // (K = 768: 58 against 70 us; K = 4096: 118 against 108)
-        if (P == 1 && Q.k < 1024) return run_product<kKind, 2, 1, kWide, P, P == 1 ? 3 : 2>(name, maps, Q, batch, s);
-        return run_product<kKind, 2, 1, kWide, P, 2>(name, maps, Q, batch, s);
+        // (256 wide, K = 768: 58 against 70 us, K = 4096: 118 against 108; 128 wide, 16 of K = 768:
+        // 20.9 against 22.9 us)
+        const bool brief = P == 1 && Q.k < 1024;
+        constexpr int kBrief = P == 1 ? 3 : 2;
+        if (wide == least)
+            return brief ? run_product<kKind, 2, 1, kWide, P, kBrief>(name, maps, Q, batch, s)
+                         : run_product<kKind, 2, 1, kWide, P, 2>(name, maps, Q, batch, s);
+        return brief ? run_product<kKind, 2, 1, 128, P, kBrief>(name, maps, Q, batch, s)
+                     : run_product<kKind, 2, 1, 128, P, 2>(name, maps, Q, batch, s);
     }
-    if (pair == least) return run_product<kKind, 2, 1, 128, P, 2>(name, maps, Q, batch, s);
     if (one == least) return run_product<kKind, 1, 1, 128, P, 2>(name, maps, Q, batch, s);
     if (half == least) return run_product<kKind, 1, 1, 64, P, 1>(name, maps, Q, batch, s);
     if (two == least) return run_product<kKind, 1, 2, 128, P, 2>(name, maps, Q, batch, s);

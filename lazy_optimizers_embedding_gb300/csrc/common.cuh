@@ -69,11 +69,12 @@ inline cudaError_t launch_smem(void (*kernel)(P...), dim3 grid, dim3 block, size
 
 
 // Lets a kernel have `bytes` of dynamic shared memory on the current device.  Said on every call that
-// needs it: another device, or the context after a reset, does not know.
+// needs it: another device, or the context after a reset, does not know.  (48 KB need no saying, but
+// hold the kernel's own arrays too: 8 KB at most.)
 template <class K>
 inline cudaError_t allow_smem(K kernel, size_t bytes)
 {
-    if (bytes <= 48 * 1024) return cudaSuccess;
+    if (bytes <= 40 * 1024) return cudaSuccess;
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 

@@ -492,10 +492,11 @@ int row_blocks(int most, int64_t rows, int G)
 
 }  // namespace
 
+// (A cluster uses none; a size of its own keeps a caller's pointer from being null.)
 size_t expert_ws_bytes(int64_t slots, int64_t experts)
 {
     const SortShape S = sort_shape(slots, experts);
-    return S.cluster ? 0 : sizeof(uint32_t) * static_cast<size_t>(experts) * static_cast<size_t>(S.blocks + 1);
+    return S.cluster ? 256 : sizeof(uint32_t) * static_cast<size_t>(experts) * static_cast<size_t>(S.blocks + 1);
 }
 
 cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, int64_t* offsets, int32_t* src,

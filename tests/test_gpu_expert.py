@@ -274,3 +274,14 @@ def test_refusals_and_no_tokens(cuda_lib):
     assert so.sparse_expert_combine(case.ys, 0, 2, 16, None, None, case.y, case.err) == so.OK
     torch.cuda.synchronize()
     assert (case.offsets == 0).all() and int(case.err.item()) == 0
+
+
+@pytest.mark.parametrize("n,experts", [(1000, 721), (1000, 722), (1500, 371), (1500, 372), (4096, 188), (4096, 189)])
+def test_sorts_whose_counts_are_about_48_kb(cuda_lib, n, experts):
+    """Dynamic and static shared memory together pass what a launch has without asking."""
+    import torch
+    case = Case(torch, cuda_lib, np.random.default_rng(n + experts).integers(-1, experts, (n, 1)), experts, 8, "f32")
+    case.run()
+    assert int(case.err.item()) == 0
+    case.compare()
+    assert cuda_lib.sparse_expert_workspace_size(n, 1, experts) > 0   # an array of this size has an address

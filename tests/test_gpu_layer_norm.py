@@ -293,3 +293,14 @@ def test_refusals(cuda_lib):
     torch.cuda.synchronize()
     assert int(k.err.item()) == 0
     assert so.sparse_layer_norm_workspace_size(-1, 4) == 0 and so.sparse_layer_norm_workspace_size(4, 0) == 0
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("c", [1489, 1501, 1519, 1527, 3001, 3041])
+def test_rows_whose_ring_is_about_48_kb(cuda_lib, c, xt, yt):
+    """Dynamic and static shared memory together pass what a launch has without asking."""
+    import torch
+    k = Case(torch, cuda_lib, 9, c, xt, yt)
+    k.run()
+    assert int(k.err.item()) == 0
+    k.compare()

@@ -740,7 +740,13 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
             plan(t + step);
             if (kTerm && head && first_piece() < pieces) fetch(first_piece());
         }
-        if (head) tma_store_done();
+        if (head) {
+            tma_store_done();
+            if (kTerm && dead) {   // a term that is on its way lands before the block leaves
+                volatile int none = 0;
+                mbar_wait(bar, terms & 1, &none);
+            }
+        }
     }
     __syncwarp();
     tc_fence_before();

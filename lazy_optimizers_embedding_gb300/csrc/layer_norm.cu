@@ -17,11 +17,11 @@
 // Longer and odd rows pass through a ring in shared memory (k_ln_ring,
 // k_ln_grad_ring).  The column sums are joined over the block's groups in shared
 // memory, over the blocks by k_ln_join, in fixed orders: equal inputs give equal bits.
-// Wider rows yet are walked in passes over the row (k_ln_wide, k_ln_grad_wide,
-// k_ln_cols).  All statistics and sums are fp32.
+// Wider rows yet are walked in passes over the row, held in shared memory where they fit
+// (k_ln_wide, k_ln_grad_wide, k_ln_cols).  All statistics and sums are fp32.
 //
-// Measured, 16384 x 4096 bf16: forward 48 us (268 MB, 5.6 TB/s), backward 86 us with the
-// join (403 MB, 4.7 TB/s).  262144 rows of 128 fp32 columns looked up in a 10M-row
+// Measured, 16384 x 4096 bf16: forward 48 us (268 MB, 5.6 TB/s), backward 76 us with the
+// join (403 MB, 5.3 TB/s).  262144 rows of 128 fp32 columns looked up in a 10M-row
 // table: forward 36 us, backward 66 us.
 #include <algorithm>
 #include <atomic>
@@ -198,43 +198,103 @@ __global__ void __launch_bounds__(kLnBlock, 4)
     }
 }
 
-// Rows wider than a group holds: one block a row, three passes over it (sum,
-// squares about the mean, output); the second and third find the row in L2.
-template <class X, class Y>
-__global__ void __launch_bounds__(kMaxBackGroup) k_ln_wide(const X* __restrict__ x, int64_t r, int64_t c,
-                                                       const int64_t* __restrict__ idx, int64_t n,
-                                                       const float* __restrict__ gamma, const float* __restrict__ beta,
-                                                       float eps, Y* __restrict__ y, float* __restrict__ mean,
-                                                       float* __restrict__ rstd, int32_t* d_err)
+// V values of a vector over the columns, from column j on; quad: 16-byte accesses.
+template <int V>
+__device__ __forceinline__ void ln_vector(float (&g)[V], const float* from, int64_t j, float none, bool quad)
+{
+    if constexpr (V > 1) {
+        if (from != nullptr && quad) {
+            Pack<float, V> p;
+            p.load(from + j);
+            p.get(g);
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) g[e] = from != nullptr ? from[j + e] : none;
+}
+
+// Rows wider than a group or the ring holds: R rows a block at a time, three passes over them (sum, squares
+// about the mean, output).  kHeld: the first pass leaves them in shared memory as read, every thread
+// its own accesses, so no one waits for another's; wider rows yet are read three times.  (4096 x
+// 16384 bf16: 59 us against 98.7 us with single values and three reads.)
+template <class X, class Y, int V, int R, bool kHeld>
+__global__ void __launch_bounds__(kMaxBackGroup, V == 1 && !kHeld ? 4 : 2) k_ln_wide(const X* __restrict__ x, int64_t r, int64_t c,
+                                                          const int64_t* __restrict__ idx, int64_t n,
+                                                          const float* __restrict__ gamma, const float* __restrict__ beta,
+                                                          int quad, float eps, Y* __restrict__ y, float* __restrict__ mean,
+                                                          float* __restrict__ rstd, int32_t* d_err)
 {
     pdl_wait();
-    __shared__ float tmp[2 * 32];
+    __shared__ float tmp[2 * 32 * R];
+    extern __shared__ float4 stage[];
+    X* held = reinterpret_cast<X*>(stage);
     const float inv_c = 1.0f / static_cast<float>(c);
-    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
-        const X* row = ln_row(x, r, c, idx, i, n);
-        if (row == nullptr) {   // the same for the whole block
-            if (threadIdx.x == 0) set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
-            continue;
+    const int64_t j0 = static_cast<int64_t>(threadIdx.x) * V, step = static_cast<int64_t>(kMaxBackGroup) * V;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * R; i0 < n; i0 += static_cast<int64_t>(gridDim.x) * R) {
+        const X* row[R];
+        float s[R], mu[R], rs[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {   // the same for the whole block
+            row[u] = ln_row(x, r, c, idx, i0 + u, n);
+            if (row[u] == nullptr && i0 + u < n && threadIdx.x == 0) set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
+            s[u] = 0.0f;
         }
-        float s[1] = {0.0f};
-        for (int64_t j = threadIdx.x; j < c; j += kMaxBackGroup) s[0] += static_cast<float>(row[j]);
-        group_sum<1>(s, kMaxBackGroup, tmp, 0);
-        const float mu = s[0] * inv_c;
-        s[0] = 0.0f;
-        for (int64_t j = threadIdx.x; j < c; j += kMaxBackGroup) {
-            const float d = static_cast<float>(row[j]) - mu;
-            s[0] = fmaf(d, d, s[0]);
+#pragma unroll 4
+        for (int64_t j = j0; j < c; j += step)
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                if (row[u] != nullptr) {
+                    Pack<X, V> p;
+                    float v[V];
+                    p.load(row[u] + j);
+                    if (kHeld) *reinterpret_cast<Pack<X, V>*>(held + u * c + j) = p;
+                    p.get(v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[u] += v[e];
+                }
+        group_sum<R>(s, kMaxBackGroup, tmp, 0);
+#pragma unroll
+        for (int u = 0; u < R; ++u) mu[u] = s[u] * inv_c, s[u] = 0.0f;
+#pragma unroll 4
+        for (int64_t j = j0; j < c; j += step)
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                if (row[u] != nullptr) {
+                    Pack<X, V> p;
+                    float v[V];
+                    p.load((kHeld ? held + u * c : row[u]) + j);
+                    p.get(v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[u] = fmaf(v[e] - mu[u], v[e] - mu[u], s[u]);
+                }
+        group_sum<R>(s, kMaxBackGroup, tmp, 1);
+#pragma unroll
+        for (int u = 0; u < R; ++u) rs[u] = 1.0f / sqrtf(fmaf(s[u], inv_c, eps));
+#pragma unroll 2
+        for (int64_t j = j0; j < c; j += step) {
+            float g[V], b[V];
+            ln_vector<V>(g, gamma, j, 1.0f, quad);
+            ln_vector<V>(b, beta, j, 0.0f, quad);
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                if (row[u] != nullptr) {
+                    Pack<X, V> p;
+                    float v[V];
+                    p.load((kHeld ? held + u * c : row[u]) + j);
+                    p.get(v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] = fmaf((v[e] - mu[u]) * rs[u], g[e], b[e]);
+                    Pack<Y, V>::put(y + (i0 + u) * c + j, v);
+                }
         }
-        group_sum<1>(s, kMaxBackGroup, tmp, 1);
-        const float rs = 1.0f / sqrtf(fmaf(s[0], inv_c, eps));
-        for (int64_t j = threadIdx.x; j < c; j += kMaxBackGroup) {
-            const float d = (static_cast<float>(row[j]) - mu) * rs;
-            y[i * c + j] = static_cast<Y>(fmaf(d, gamma ? gamma[j] : 1.0f, beta ? beta[j] : 0.0f));
-        }
-        if (threadIdx.x == 0) {
-            if (mean) mean[i] = mu;
-            if (rstd) rstd[i] = rs;
-        }
+        if (threadIdx.x == 0)
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                if (row[u] != nullptr) {
+                    if (mean) mean[i0 + u] = mu[u];
+                    if (rstd) rstd[i0 + u] = rs[u];
+                }
     }
 }
 
@@ -379,15 +439,13 @@ __global__ void __launch_bounds__(kMaxBackGroup, 1)
     if (groups > 1) __syncthreads();   // gamma has been read
     float* to = groups > 1 ? cols + sub * 2 * c : mine;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int col = (k * G + gl) * V + e;
-            if (col < c) {
-                to[col] = e % 2 ? sg[k][e / 2].hi() : sg[k][e / 2].lo();
-                to[c + col] = e % 2 ? sb[k][e / 2].hi() : sb[k][e / 2].lo();
-            }
+    for (int k = 0; k < NV; ++k) {
+        const int col = (k * G + gl) * V;
+        if (col < c) {
+            ln_put<float, V>(to + col, sg[k]);
+            ln_put<float, V>(to + c + col, sb[k]);
         }
+    }
     if (groups == 1) return;
     __syncthreads();
     for (int q = threadIdx.x; q < 2 * c; q += blockDim.x) {
@@ -676,6 +734,7 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
         }
         if (++stage == stages) stage = 0, parity ^= 1u;
     }
+    if (gl == 0 && S.dead) set_error(d_err, SPARSE_ERR_INTERNAL);   // its own wait ran out
 }
 
 template <class X, class Y, int V, bool kEven, int kT>
@@ -764,103 +823,165 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
         }
         if (++stage == stages) stage = 0, parity ^= 1u;
     }
+    if (gl == 0 && S.dead) set_error(d_err, SPARSE_ERR_INTERNAL);   // its own wait ran out
     if (!want) return;
     float* mine = part + static_cast<int64_t>(blockIdx.x) * 2 * c;
+    if constexpr (V > 1) {   // whole accesses (a value at a time 64 x 8192 bf16 took 22 us and not 10)
+        ring_put<float, V, false>(mine, sg, c, G, gl, used);
+        ring_put<float, V, false>(mine + c, sb, c, G, gl, used);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kRingLane; ++k) {
-        const int col = V == 1 ? k * G + gl : (k / V * G + gl) * V + k % V;
-        if (col < c) {
-            mine[col] = k % 2 ? sg[k / 2].hi() : sg[k / 2].lo();
-            mine[c + col] = k % 2 ? sb[k / 2].hi() : sb[k / 2].lo();
+        for (int k = 0; k < kRingLane; ++k) {
+            const int col = k * G + gl;
+            if (col < c) {
+                mine[col] = k % 2 ? sg[k / 2].hi() : sg[k / 2].lo();
+                mine[c + col] = k % 2 ? sb[k / 2].hi() : sb[k / 2].lo();
+            }
         }
     }
 }
 
-// Rows wider than a group holds: the row sums and dx by one block a row, the
-// column sums apart (k_ln_cols).
-template <class X, class Y>
-__global__ void __launch_bounds__(kMaxBackGroup) k_ln_grad_wide(const Y* __restrict__ dy, const X* __restrict__ x,
-                                                            int64_t r, int64_t c, const int64_t* __restrict__ idx,
-                                                            int64_t n, const float* __restrict__ gamma,
-                                                            const float* __restrict__ mean,
-                                                            const float* __restrict__ rstd, X* __restrict__ dx,
-                                                            int32_t* d_err)
+// Rows wider than a group or the ring holds: the row sums and dx by one block a row, which holds x and dy in
+// shared memory as k_ln_wide holds x; the column sums apart (k_ln_cols).  (4096 x 16384 bf16, all
+// three kernels: 149 us against 259.5 us with single values.)
+template <class X, class Y, int V, bool kHeld>
+__global__ void __launch_bounds__(kMaxBackGroup, V == 1 && !kHeld ? 4 : 2) k_ln_grad_wide(const Y* __restrict__ dy, const X* __restrict__ x,
+                                                               int64_t r, int64_t c, const int64_t* __restrict__ idx,
+                                                               int64_t n, const float* __restrict__ gamma, int quad,
+                                                               const float* __restrict__ mean,
+                                                               const float* __restrict__ rstd, X* __restrict__ dx,
+                                                               int32_t* d_err)
 {
     pdl_wait();
     __shared__ float tmp[2 * 32 * 2];
+    extern __shared__ float4 stage[];
+    X* held_x = reinterpret_cast<X*>(stage);
+    Y* held_y = reinterpret_cast<Y*>(reinterpret_cast<uint8_t*>(stage) + (c * static_cast<int64_t>(sizeof(X)) + 15) / 16 * 16);
     const float inv_c = 1.0f / static_cast<float>(c);
+    const int64_t j0 = static_cast<int64_t>(threadIdx.x) * V, step = static_cast<int64_t>(kMaxBackGroup) * V;
     int half = 0;
     for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
         const X* row = ln_row(x, r, c, idx, i, n);
-        if (row == nullptr) {
+        if (row == nullptr) {   // the same for the whole block
             if (threadIdx.x == 0) set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
             continue;
         }
+        const Y* from = dy + i * c;
         const float mu = mean[i], rs = rstd[i];
         float s[2] = {0.0f, 0.0f};
-        for (int64_t j = threadIdx.x; j < c; j += kMaxBackGroup) {
-            const float h = static_cast<float>(dy[i * c + j]) * (gamma ? gamma[j] : 1.0f);
-            s[0] += h;
-            s[1] = fmaf(h, (static_cast<float>(row[j]) - mu) * rs, s[1]);
+#pragma unroll 4
+        for (int64_t j = j0; j < c; j += step) {
+            Pack<X, V> p;
+            Pack<Y, V> q;
+            float v[V], d[V], g[V];
+            p.load(row + j);
+            q.load(from + j);
+            ln_vector<V>(g, gamma, j, 1.0f, quad);
+            if (kHeld) {
+                *reinterpret_cast<Pack<X, V>*>(held_x + j) = p;
+                *reinterpret_cast<Pack<Y, V>*>(held_y + j) = q;
+            }
+            p.get(v);
+            q.get(d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float h = d[e] * g[e];
+                s[0] += h;
+                s[1] = fmaf(h, (v[e] - mu) * rs, s[1]);
+            }
         }
         group_sum<2>(s, kMaxBackGroup, tmp, half);
         half ^= 1;
         const float a = s[0] * inv_c, b = s[1] * inv_c;
-        for (int64_t j = threadIdx.x; j < c; j += kMaxBackGroup) {
-            const float h = static_cast<float>(dy[i * c + j]) * (gamma ? gamma[j] : 1.0f);
-            dx[i * c + j] = static_cast<X>(rs * (h - a - (static_cast<float>(row[j]) - mu) * rs * b));
+#pragma unroll 2
+        for (int64_t j = j0; j < c; j += step) {
+            Pack<X, V> p;
+            Pack<Y, V> q;
+            float v[V], d[V], g[V];
+            p.load((kHeld ? held_x : row) + j);
+            q.load((kHeld ? held_y : from) + j);
+            ln_vector<V>(g, gamma, j, 1.0f, quad);
+            p.get(v);
+            q.get(d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = rs * (d[e] * g[e] - a - (v[e] - mu) * rs * b);
+            Pack<X, V>::put(dx + i * c + j, v);
         }
     }
 }
 
-// Column sums of one slab of rows (blockIdx.y) into its partial.
-template <class X, class Y>
+// Column sums of one slab of rows (blockIdx.y) into its partial, V columns a thread.
+template <class X, class Y, int V>
 __global__ void __launch_bounds__(kLnBlock) k_ln_cols(const Y* __restrict__ dy, const X* __restrict__ x, int64_t r,
                                                       int64_t c, const int64_t* __restrict__ idx, int64_t n,
                                                       const float* __restrict__ mean, const float* __restrict__ rstd,
                                                       float* __restrict__ part)
 {
     pdl_wait();
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * kLnBlock + threadIdx.x;
+    const int64_t j = (static_cast<int64_t>(blockIdx.x) * kLnBlock + threadIdx.x) * V;
     if (j >= c) return;
     const int64_t per = (n + gridDim.y - 1) / gridDim.y;
     const int64_t i0 = per * blockIdx.y, i1 = i0 + per < n ? i0 + per : n;
-    float sg = 0.0f, sb = 0.0f;
-    for (int64_t i = i0; i < i1; ++i) {
-        const X* row = ln_row(x, r, c, idx, i, n);
-        if (row == nullptr) continue;
-        const float d = static_cast<float>(dy[i * c + j]);
-        sg = fmaf(d, (static_cast<float>(row[j]) - mean[i]) * rstd[i], sg);
-        sb += d;
+    float sg[V], sb[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sg[e] = sb[e] = 0.0f;
+    constexpr int R = 4;   // rows requested at once
+    for (int64_t i = i0; i < i1; i += R) {
+        Pack<X, V> p[R];
+        Pack<Y, V> q[R];
+        float mu[R], rs[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const X* row = i + u < i1 ? ln_row(x, r, c, idx, i + u, n) : nullptr;
+            p[u].zero();
+            q[u].zero();   // a row that is not there adds nothing
+            mu[u] = rs[u] = 0.0f;
+            if (row != nullptr) {
+                p[u].load(row + j);
+                q[u].load(dy + (i + u) * c + j);
+                mu[u] = mean[i + u], rs[u] = rstd[i + u];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            float v[V], d[V];
+            p[u].get(v);
+            q[u].get(d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                sg[e] = fmaf(d[e], (v[e] - mu[u]) * rs[u], sg[e]);
+                sb[e] += d[e];
+            }
+        }
     }
-    part[(static_cast<int64_t>(blockIdx.y) * 2) * c + j] = sg;
-    part[(static_cast<int64_t>(blockIdx.y) * 2 + 1) * c + j] = sb;
+    float* to = part + static_cast<int64_t>(blockIdx.y) * 2 * c + j;
+    Pack<float, V>::put(to, sg);
+    Pack<float, V>::put(to + c, sb);
 }
 
 // dgamma[c], dbeta[c] = sums of `parts` partials [2][c], each 32 columns' by one
-// block: warp w sums partials w, w + 32, ... of its lane's column, then the warps'
-// sums are added in order.
+// block: of its W warps (a power of two up to 32), warp w sums partials w, w + W, ... of its
+// lane's column, then the warps' sums are added in order.
 __global__ void __launch_bounds__(1024) k_ln_join(const float* __restrict__ part, int64_t parts, int64_t c,
                                                   float* __restrict__ dgamma, float* __restrict__ dbeta)
 {
     pdl_wait();   // writes caller outputs
     __shared__ float t[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int64_t q = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (q < 2 * c)
-        for (int64_t p0 = warp; p0 < parts; p0 += 32 * 16) {   // 16 requests at once
+        for (int64_t p0 = warp; p0 < parts; p0 += W * 16) {   // 16 requests at once
             float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = p0 + 32 * i < parts ? part[(p0 + 32 * i) * 2 * c + q] : 0.0f;
+            for (int i = 0; i < 16; ++i) v[i] = p0 + W * i < parts ? part[(p0 + W * i) * 2 * c + q] : 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s += v[i];
         }
     t[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && q < 2 * c) {
-#pragma unroll
-        for (int w = 1; w < 32; ++w) s += t[w][lane];
+        for (int w = 1; w < W; ++w) s += t[w][lane];
         float* out = q < c ? dgamma : dbeta;
         if (out) out[q < c ? q : q - c] = s;
     }
@@ -925,8 +1046,10 @@ cudaError_t run_ln_lane(const Forward& F)
 //   30 back; 5000 x 1111: 12 against 21, 23 against 48).
 //   Packed, forward: rows that registers would spread over several warps, from 1025 columns
 //   (65536 x 2048 bf16: 84 against 95 us, 16 x 4096: 3.2 against 4.5; 65536 x 1024: 54 against 44).
-//   Packed, back: long bf16 rows, many of them (65536 x 2048: 143 against 198 us; 2000 x 2048: 21
-//   against 14; fp32, whose registers hold half as many rows, 65536 x 2048: 317 against 275).
+//   Packed, back: long bf16 rows, where there are 16 Mi values of them (16384 x 2048: 46 against 56 us,
+//   4096 x 8192: 55 against 66, 4096 x 4096: 31.5 against 32.7; 4096 x 2048: 18.7 against 17.1, 1000
+//   x 8192: 23 against 21; fp32, whose registers hold half as many rows, 65536 x 2048: 317 against 275).
+constexpr int64_t kRingBack = 16 << 20;
 struct RingShape {
     int G, stages;
     size_t smem;
@@ -936,7 +1059,7 @@ RingShape ring_shape(int64_t c, int64_t n)
 {
     RingShape s{std::max(64, lanes_of(c, kRingLane)), 0, 0};
     const bool faster = V == 1 ? c * static_cast<int64_t>(sizeof(X)) >= 1024
-                        : kBack ? sizeof(X) == 2 && c > 1024 && n >= 8192
+                        : kBack ? sizeof(X) == 2 && c > 1024 && n * c >= kRingBack
                                 : c > 1024;
     if (!faster || c > static_cast<int64_t>(kMaxBackGroup) * kRingLane) return s;
     const size_t round = ring_round<X, Y, kBack>(c);
@@ -966,6 +1089,29 @@ cudaError_t run_ln_ring(const Forward& F, const RingShape& g)
                        g.stages, F.d_err);
 }
 
+// Blocks that the GPU holds at once (few calls have rows this wide: asked every time).
+template <class K>
+int64_t wide_blocks(K kernel, size_t smem)
+{
+    int o = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kernel, kMaxBackGroup, smem);
+    return static_cast<int64_t>(std::max(o, 1)) * num_sms();
+}
+
+bool quads(const float* a, const float* b) { return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0; }
+
+template <class X, class Y, int V, int R, bool kHeld>
+cudaError_t run_ln_wide(const Forward& F, size_t smem)
+{
+    auto* kernel = k_ln_wide<X, Y, V, R, kHeld>;
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = std::min<int64_t>((F.n + R - 1) / R, wide_blocks(kernel, smem));
+    return launch_smem(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMaxBackGroup), smem, F.s, static_cast<const X*>(F.x),
+                       F.r, F.c, F.idx, F.n, F.gamma, F.beta, static_cast<int>(quads(F.gamma, F.beta)), F.eps,
+                       static_cast<Y*>(F.y), F.mean, F.rstd, F.d_err);
+}
+
 template <class X, class Y, int V>
 cudaError_t run_ln(const Forward& F)
 {
@@ -981,15 +1127,18 @@ cudaError_t run_ln(const Forward& F)
         if (V > 1 && F.c % (lanes_of(F.c, L) * V) == 0) return run_ln_lane<X, Y, V, L, (V > 1)>(F);
         return run_ln_lane<X, Y, V, L, false>(F);
     }
-    const int blocks = static_cast<int>(std::min<int64_t>(F.n, 4 * num_sms()));
-    return launch(k_ln_wide<X, Y>, dim3(blocks), dim3(kMaxBackGroup), F.s, static_cast<const X*>(F.x), F.r, F.c, F.idx, F.n,
-                  F.gamma, F.beta, F.eps, static_cast<Y*>(F.y), F.mean, F.rstd, F.d_err);
+    // two rows share gamma and beta where they leave room for two blocks an SM and the rows go round
+    const size_t row = (static_cast<size_t>(F.c) * sizeof(X) + 15) / 16 * 16;
+    const bool held = row <= kRingSmem && !(V == 1 && sizeof(X) == 2);   // (two bytes at a time they cost more than they save)
+    if (!held) return run_ln_wide<X, Y, V, 1, false>(F, 0);
+    if (2 * row <= kRingSmem / 2 && F.n >= 4 * static_cast<int64_t>(num_sms())) return run_ln_wide<X, Y, V, 2, true>(F, 2 * row);
+    return run_ln_wide<X, Y, V, 1, true>(F, row);
 }
 
 // Partial column sums that a backward pass may write, whatever its accesses.
 int64_t grad_parts(int64_t n, int64_t c)
 {
-    if (c > kMaxBackward) return std::min<int64_t>(64, std::max<int64_t>(1, n / 64));
+    if (c > kMaxBackward) return std::min<int64_t>(64, std::max<int64_t>(1, n / 16));
     const int64_t groups = c * 2 >= 1024 ? 1 : std::max(1, kLnBlock / lanes_of(c, 8));   // the fewest
     return std::min<int64_t>((n + groups - 1) / groups, kLnParts);
 }
@@ -1044,6 +1193,17 @@ cudaError_t run_grad_ring(const Backward& B, const RingShape& g, int want, int64
                        static_cast<X*>(B.dx), B.part, want, g.stages, B.d_err);
 }
 
+template <class X, class Y, int V, bool kHeld>
+cudaError_t run_grad_wide(const Backward& B, size_t smem)
+{
+    auto* kernel = k_ln_grad_wide<X, Y, V, kHeld>;
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_smem(kernel, dim3(static_cast<unsigned>(std::min<int64_t>(B.n, wide_blocks(kernel, smem)))), dim3(kMaxBackGroup), smem,
+                       B.s, static_cast<const Y*>(B.dy), static_cast<const X*>(B.x), B.r, B.c, B.idx, B.n, B.gamma,
+                       static_cast<int>(quads(B.gamma, nullptr)), B.mean, B.rstd, static_cast<X*>(B.dx), B.d_err);
+}
+
 template <class X, class Y, int V>
 cudaError_t run_ln_grad(const Backward& B)
 {
@@ -1053,13 +1213,11 @@ cudaError_t run_ln_grad(const Backward& B)
     if (B.n > 0) {
         SO_PROFILE("layer_norm_grad", B.s);
         if (B.c > kMaxBackward) {
-            const int blocks = static_cast<int>(std::min<int64_t>(B.n, 4 * num_sms()));
-            e = launch(k_ln_grad_wide<X, Y>, dim3(blocks), dim3(kMaxBackGroup), B.s, static_cast<const Y*>(B.dy),
-                       static_cast<const X*>(B.x), B.r, B.c, B.idx, B.n, B.gamma, B.mean, B.rstd, static_cast<X*>(B.dx),
-                       B.d_err);
+            const size_t smem = ((static_cast<size_t>(B.c) * sizeof(X) + 15) / 16 + (static_cast<size_t>(B.c) * sizeof(Y) + 15) / 16) * 16;
+            e = smem <= kRingSmem && !(V == 1 && sizeof(X) == 2) ? run_grad_wide<X, Y, V, true>(B, smem) : run_grad_wide<X, Y, V, false>(B, 0);
             if (e == cudaSuccess && want)
-                e = launch(k_ln_cols<X, Y>, dim3(static_cast<unsigned>((B.c + kLnBlock - 1) / kLnBlock),
-                                                 static_cast<unsigned>(parts)),
+                e = launch(k_ln_cols<X, Y, V>, dim3(static_cast<unsigned>((B.c / V + kLnBlock - 1) / kLnBlock),
+                                                    static_cast<unsigned>(parts)),
                            dim3(kLnBlock), B.s, static_cast<const Y*>(B.dy), static_cast<const X*>(B.x), B.r, B.c, B.idx,
                            B.n, B.mean, B.rstd, B.part);
         } else {
@@ -1081,7 +1239,9 @@ cudaError_t run_ln_grad(const Backward& B)
     }
     if (e != cudaSuccess || !want) return e;
     SO_PROFILE("layer_norm_grad_join", B.s);
-    return launch(k_ln_join, dim3(static_cast<unsigned>((2 * B.c + 31) / 32)), dim3(1024), B.s,
+    int threads = 64;   // of a block: about 8 partials a warp, so that more columns' blocks fit beside one another
+    while (threads < 1024 && threads / 32 * 8 < parts) threads *= 2;
+    return launch(k_ln_join, dim3(static_cast<unsigned>((2 * B.c + 31) / 32)), dim3(threads), B.s,
                   static_cast<const float*>(B.part), parts, B.c, B.dgamma, B.dbeta);
 }
 

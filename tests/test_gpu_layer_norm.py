@@ -304,3 +304,30 @@ def test_rows_whose_ring_is_about_48_kb(cuda_lib, c, xt, yt):
     k.run()
     assert int(k.err.item()) == 0
     k.compare()
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("n,c,shift", [(2, 60000, 0), (3, 60001, 0), (700, 9000, 0), (613, 8200, 1), (20, 16384, 0)])
+def test_rows_wider_than_the_groups(cuda_lib, n, c, shift, xt, yt):
+    """Rows held in shared memory, two at a time and one, and rows that shared memory does not hold."""
+    import torch
+    idx = np.random.default_rng(n).integers(0, n + 3, n)
+    idx[n // 2] = n + 3                 # bad: the odd row of a pair or the even one of another
+    k = Case(torch, cuda_lib, n, c, xt, yt, idx=np.minimum(idx, n + 2), rows=n + 3, shift=shift)
+    k.run()
+    assert int(k.err.item()) == 0
+    k.compare()
+    want = [t.clone() for t in (k.y, k.dx, k.mean, k.rstd)]
+    for t in (k.y, k.dx, k.mean, k.rstd):
+        t.zero_()
+    k.idx[n // 2] = n + 3
+    so = cuda_lib
+    assert so.sparse_layer_norm(k.x, k.r, c, k.idx, n, k.gamma, k.beta, 1e-5, k.y, k.mean, k.rstd, k.err) == so.OK
+    assert so.sparse_layer_norm_grad(k.dy, k.x, k.r, c, k.idx, n, k.gamma, want[2], want[3], k.dx, None, None, None,
+                                     k.err) == so.OK
+    k.G.check("layer norm")
+    assert int(k.err.item()) == so.ERR_INDEX_OUT_OF_RANGE
+    for got, ref in zip((k.y, k.dx, k.mean, k.rstd), want):
+        assert not got[n // 2].any()
+        got[n // 2] = ref[n // 2]
+        assert torch.equal(got, ref)

@@ -1,11 +1,14 @@
 // muon_small.cu -- Newton-Schulz for matrices of at most 128 rows (columns, where
 // tall) whose X a cluster's shared memory holds: all steps in one launch.
 //
-// A cluster of up to 8 blocks has one matrix; each block keeps a slice of up to 256
-// columns of X, hi and lo f16, and the whole of A and B (three products: the time is
-// mostly that of the phases, 35 us for 64 x 128 with one or three).  A step is
-//   A's share of the slice     X_s X_s^T, the shares summed over the cluster through
-//                              shared memory, in block order on every block alike
+// A cluster of up to 8 blocks has one matrix; each block keeps some columns of X, hi and lo f16, and
+// the whole of A and B (three products: the time is mostly that of the phases, 35 us for 64 x 128
+// with one or three).  It has room for 128 rows of 256 columns; of a matrix of at most 64 (32) rows it
+// keeps two (four) times as many, in parts that lie below one another: the products of parts with
+// themselves then add up to A's share, and B, once for every part on the diagonal, serves them
+// all.  A step is
+//   A's share of the columns   X_s X_s^T, the shares summed over the cluster (and the parts) through
+//                              shared memory, in the same order on every block
 //   A A                        by every block
 //   B X_s                      by every block, in place
 // One copy of X serves both products: boxes of 64 columns, 128 rows of 128 bytes, are
@@ -76,7 +79,8 @@ __device__ __forceinline__ __half lds_half(uint32_t a)
 struct Small {
     int64_t size;        // of a matrix
     int m, n;            // X: m x n
-    int slice;           // columns of X a block holds, a multiple of 64
+    int fold;            // parts of a block's columns that lie below one another, 128 / fold rows each
+    int slice;           // columns of a part, a multiple of 64
     int tall, steps;
     float a, b, c, eps;
     const float* part;
@@ -89,7 +93,7 @@ struct Small {
     int32_t* d_err;
 };
 
-template <bool kVec>
+template <bool kVec, bool kFold>
 __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
 {
     extern __shared__ uint8_t raw[];
@@ -99,11 +103,18 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     __shared__ float sums[2 * 32];
     const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes;
     const uint32_t bar = smem_addr(&bar_mem);
+    const int fold = kFold ? Q.fold : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t mat = blockIdx.x / blocks;
     const int rank = static_cast<int>(blockIdx.x % blocks);
-    const int col0 = rank * Q.slice, cols = max(0, min(Q.slice, Q.n - col0));   // this block's columns of X
-    const int side = Q.m <= 64 ? 64 : 128;                                      // of A and B, in the products
+    const int col0 = rank * fold * Q.slice, cols = max(0, min(fold * Q.slice, Q.n - col0));   // this block's columns of X
+    const int side = fold == 1 && Q.m <= 64 ? 64 : 128;   // of A and B, in the products
+    const int part_rows = kRows / fold;
+    auto held_at = [&](int r, int c) {   // row r, column c of the block's columns
+        int h = 0;
+        if (fold > 1) h = (c >= Q.slice) + (c >= 2 * Q.slice) + (c >= 3 * Q.slice);
+        return place(r + h * part_rows, c - h * Q.slice);
+    };
 
     if (threadIdx.x == 0) {
         dead = 0;
@@ -122,25 +133,29 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     // X of the slice, scaled and split; the new momentum buffer
     const float scale = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, sums);
     const int64_t base = mat * Q.size;
-    // A warp takes u's rows (X's, or its columns where u is tall) kWarps apart, a lane four values at a time.
+    // Groups of lanes take u's rows (X's, or its columns where u is tall), a lane four values at a time: a
+    // whole warp, or as many lanes as such a row has use for.
     const int outer = Q.tall ? cols : Q.m, inner = Q.tall ? Q.m : cols;
+    int lanes_of_row = 32;
+    while (lanes_of_row > 1 && lanes_of_row * 2 >= inner) lanes_of_row /= 2;
+    const int groups = kBlockThreads / lanes_of_row, group = threadIdx.x / lanes_of_row, k0 = threadIdx.x % lanes_of_row * 4;
     auto value_at = [&](int o, int k) {
         return base + (Q.tall ? static_cast<int64_t>(col0 + o) * Q.m + k : static_cast<int64_t>(o) * Q.n + col0 + k);
     };
     constexpr int kRowsAtOnce = 4;
     if (!blocked)
-        for (int k = lane * 4; k < inner; k += 128)
-            for (int o0 = warp; o0 < outer; o0 += kWarps * kRowsAtOnce) {
+        for (int k = k0; k < inner; k += lanes_of_row * 4)
+            for (int o0 = group; o0 < outer; o0 += groups * kRowsAtOnce) {
                 float u[kRowsAtOnce][4], nb[kRowsAtOnce][4];
                 const int left = min(4, inner - k);
 #pragma unroll
                 for (int i = 0; i < kRowsAtOnce; ++i) {
-                    const int o = o0 + i * kWarps;
+                    const int o = o0 + i * groups;
                     if (o < outer) read_u4<kVec>(U, value_at(o, k), left, u[i], nb[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kRowsAtOnce; ++i) {
-                    const int o = o0 + i * kWarps;
+                    const int o = o0 + i * groups;
                     if (o >= outer) continue;
                     if (Q.buf) {
                         const int64_t at = value_at(o, k);
@@ -162,9 +177,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                     if (Q.tall) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (e < left) sts16(xhi + place(k + e, o), h[e]), sts16(xlo + place(k + e, o), l[e]);
+                            if (e < left) sts16(xhi + held_at(k + e, o), h[e]), sts16(xlo + held_at(k + e, o), l[e]);
                     } else {
-                        const uint32_t p = place(o, k);   // four columns of one 16-byte piece
+                        const uint32_t p = held_at(o, k);   // four columns of one 16-byte piece
                         sts64(xhi + p, h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
                         sts64(xlo + p, l[0] | static_cast<uint32_t>(l[1]) << 16, l[2] | static_cast<uint32_t>(l[3]) << 16);
                     }
@@ -174,7 +189,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     // this warp's share of an accumulator: 32 rows, a quarter of the columns
     const int row = (warp & 3) * 32 + lane, quarter = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const bool rows_used = (warp & 3) * 32 < Q.m;
+    const bool rows_used = (warp & 3) * 32 % part_rows < Q.m;
+    // Of the parts' products only those of a part with itself are A's; a warp's 32 x 32 are or are not.
+    const bool own_part = fold == 1 || (warp & 3) * 32 / part_rows == quarter * 32 / part_rows;
     uint32_t phase = 0;
     auto products_done = [&] {   // of the phase's MMAs, by every thread
         mbar_wait(bar, phase & 1, &dead);
@@ -220,7 +237,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
         products_done();
         const int per = side / 4;              // columns of A this warp has: 16 or 32
         float av[32];
-        if (rows_used)
+        if (rows_used && own_part)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 if (q * 16 < per) {
@@ -229,31 +246,36 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
 #pragma unroll
                     for (int e = 0; e < 16; ++e) av[q * 16 + e] = v[e] + x[e];
                 }
-        if (blocks > 1) {
-            // The shares, fp32, where A will be: rows of side / 4 16-byte pieces, permuted by row.  Block r
-            // sums the r-th part of the pieces over the cluster, in block order, in place (no other block
-            // reads that part of its share), then every block fetches the others' sums, neighbouring
-            // lanes neighbouring pieces.  (Every block reading every share in its own rows' order, 16
-            // bytes of 32 rows at a time, took 130 us a step at 128 x 2048.)
-            const int quads = side / 4, mine = quads * side / blocks, shift = 31 - __clz(mine);   // powers of two
-            auto quad = [&](int q) { return shi + static_cast<uint32_t>(row * quads + ((quarter * (per / 4) + q) ^ (row & 7))) * 16; };
-            if (rows_used)
+        if (blocks > 1 || fold > 1) {
+            // The shares of the blocks' parts, fp32, where A will be: rows of rows_of / 4 16-byte pieces, permuted
+            // by row.  Block r sums the r-th share of the pieces over the cluster, in the order of parts
+            // and blocks, in place (no other block reads that share), then every block fetches the others'
+            // sums, neighbouring lanes neighbouring pieces.  (Every block reading every share in its own
+            // rows' order, 16 bytes of 32 rows at a time, took 130 us a step at 128 x 2048.)
+            const int rows_of = fold == 1 ? side : part_rows;
+            const int quads = rows_of / 4, all = quads * rows_of, mine = all / blocks, shift = 31 - __clz(mine);   // powers of two
+            const int r0 = fold == 1 ? row : row % part_rows, q0 = fold == 1 ? quarter * (per / 4) : quarter * 32 % part_rows / 4;
+            const uint32_t part_at = fold == 1 ? 0u : static_cast<uint32_t>(row / part_rows * all * 16);
+            auto quad = [&](int q) { return shi + static_cast<uint32_t>(r0 * quads + ((q0 + q) ^ (r0 & 7))) * 16; };
+            if (rows_used && own_part)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     if (q * 4 < per)
-                        sts128(quad(q), make_uint4(__float_as_uint(av[4 * q]), __float_as_uint(av[4 * q + 1]),
+                        sts128(quad(q) + part_at, make_uint4(__float_as_uint(av[4 * q]), __float_as_uint(av[4 * q + 1]),
                                                    __float_as_uint(av[4 * q + 2]), __float_as_uint(av[4 * q + 3])));
             cluster_sync();
-            const int used = min(side, (Q.m + 31) / 32 * 32) * quads;   // pieces of rows that the warps wrote
+            const int used = min(rows_of, (Q.m + 31) / 32 * 32) * quads;   // pieces of rows that the warps wrote
             for (int f = rank * mine + threadIdx.x; f < (rank + 1) * mine && f < used; f += kBlockThreads) {
-                float4 v[kMaxCluster];
+                float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int h = 0; h < fold; ++h) {
+                    float4 v[kMaxCluster];
 #pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r)
-                    if (r < blocks) v[r] = lds_cluster(cluster_addr(shi + f * 16, r));
-                float4 t = v[0];
+                    for (int r = 0; r < kMaxCluster; ++r)
+                        if (r < blocks) v[r] = lds_cluster(cluster_addr(shi + (h * all + f) * 16, r));
 #pragma unroll
-                for (int r = 1; r < kMaxCluster; ++r)
-                    if (r < blocks) t.x += v[r].x, t.y += v[r].y, t.z += v[r].z, t.w += v[r].w;
+                    for (int r = 0; r < kMaxCluster; ++r)
+                        if (r < blocks) t.x += v[r].x, t.y += v[r].y, t.z += v[r].z, t.w += v[r].w;
+                }
                 sts128(shi + f * 16, make_uint4(__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)));
             }
             cluster_sync();
@@ -273,7 +295,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                 }
             }
             cluster_sync();   // the block has all sums, and no block reads another's any more
-            if (rows_used)
+            if (rows_used && own_part)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     if (q * 4 < per) {
@@ -288,7 +310,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
             if (q * 8 < per) {
                 float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = av[8 * q + e] = rows_used ? av[8 * q + e] * kInvScale : 0.0f;
+                for (int e = 0; e < 8; ++e) x[e] = av[8 * q + e] = rows_used && own_part ? av[8 * q + e] * kInvScale : 0.0f;
                 const uint32_t p = place(row, quarter * per + q * 8);
                 split8(shi + p, slo + p, x);   // zeros in the rows past the matrix's
             }
@@ -344,14 +366,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
 
     // the update, as u came
     if (!blocked)
-        for (int k = lane * 4; k < inner; k += 128)
-            for (int o0 = warp; o0 < outer; o0 += kWarps * kRowsAtOnce) {
+        for (int k = k0; k < inner; k += lanes_of_row * 4)
+            for (int o0 = group; o0 < outer; o0 += groups * kRowsAtOnce) {
                 const int left = min(4, inner - k);
                 float w[kRowsAtOnce][4];
                 if (Q.w)
 #pragma unroll
                     for (int i = 0; i < kRowsAtOnce; ++i) {
-                        const int o = o0 + i * kWarps;
+                        const int o = o0 + i * groups;
                         if (o >= outer) continue;
                         const float* from = Q.w + value_at(o, k);
                         if (Q.vec) {
@@ -365,17 +387,18 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                     }
 #pragma unroll
                 for (int i = 0; i < kRowsAtOnce; ++i) {
-                    const int o = o0 + i * kWarps;
+                    const int o = o0 + i * groups;
                     if (o >= outer) continue;
                     float x[4];
                     if (Q.tall) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t p = place(k + min(e, left - 1), o);
+                            const uint32_t p = held_at(k + min(e, left - 1), o);
                             x[e] = __half2float(lds_half(xhi + p)) + __half2float(lds_half(xlo + p));
                         }
                     } else {
-                        const uint2 h = lds64(xhi + place(o, k)), l = lds64(xlo + place(o, k));
+                        const uint32_t p = held_at(o, k);
+                        const uint2 h = lds64(xhi + p), l = lds64(xlo + p);
                         const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x)), h1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
                         const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(&l.x)), l1 = __half22float2(*reinterpret_cast<const __half2*>(&l.y));
                         x[0] = h0.x + l0.x, x[1] = h0.y + l0.y, x[2] = h1.x + l1.x, x[3] = h1.y + l1.y;
@@ -430,31 +453,56 @@ int clusters_at_once(int blocks)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (allow_smem(k_muon_cluster<true>, kSmallSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, k_muon_cluster<true>, &cfg) != cudaSuccess) n = 0;
+        if (allow_smem((k_muon_cluster<true, false>), kSmallSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, (k_muon_cluster<true, false>), &cfg) != cudaSuccess) n = 0;
         n = std::max(n, 1);
         known[blocks].store(n, std::memory_order_relaxed);
     }
     return n;
 }
 
-int cluster_blocks(int64_t n)
+// How a matrix is laid out over a cluster, and what the batch then takes, in tenths of a microsecond.
+struct Fold {
+    int fold, blocks, slice;
+    int64_t cost;
+};
+
+// The cheapest layout (fold 0: none has room).  One round of clusters takes, measured at five steps:
+//   m <= 64, one part a block   26 us (64 columns), 30 (128), 40 (256); 12 more where blocks exchange sums
+//   m > 64                      38, 41 and 54 us; 24 more
+//   several parts a block       50, 57 and 74 us, sums over parts included
+// and about 2 us more for every doubling of the blocks past two.  (300 x (32 x 512): 117 us in four
+// parts of a block, 198 in two blocks; 32 x 512 alone: 57 and 50, and 37 in eight blocks.)
+Fold fold_of(int64_t batch, int64_t m, int64_t n)
 {
-    int b = 1;
-    while (b * kSlice < n) b *= 2;
-    return b;
+    Fold best{0, 0, 0, INT64_MAX};
+    for (int fold = 1; fold <= 4 && m <= kRows / fold; fold *= 2)
+        for (int blocks = 1; blocks <= kMaxCluster; blocks *= 2) {
+            const int64_t parts = static_cast<int64_t>(fold) * blocks, slice = ((n + parts - 1) / parts + 63) / 64 * 64;
+            if (slice > kSlice || parts / 2 * slice >= n) continue;   // no room, or half as many would do
+            const int64_t more = slice / 64 - 1;   // 64 columns each
+            int64_t round;
+            if (fold > 1) round = 500 + 50 * more + 10 * more * more;
+            else if (m > 64) round = 380 + 20 * more + 10 * more * more + (blocks > 1 ? 240 : 0);
+            else round = 260 + 35 * more + 4 * more * more + (blocks > 1 ? 120 : 0);
+            for (int b = 4; b <= blocks; b *= 2) round += 20;
+            const int64_t at_once = clusters_at_once(blocks), cost = (batch + at_once - 1) / at_once * round;
+            if (cost < best.cost) best = {fold, blocks, static_cast<int>(slice), cost};
+        }
+    return best;
 }
 
 }  // namespace
 
-// One round of clusters over the GPU, or two where a block has a matrix alone: 64 x 128 fp32 29 us
-// against 90 on the general path, 128 x 256 55 against 100, 8 x (128 x 2048) 90 against 172; but two
-// rounds of 8-block clusters, 16 x (64 x 2048), took as long as the general path.
+// Where the cheapest layout beats the general path, whose launches take 85 us and 1.6 us (2.9 with more than
+// 64 rows) for every 1000 columns: 64 x 128 fp32 29 us against 91, 30 x 8192 80 against 193, 11 x (64 x
+// 4000) 80 against 199, 300 x (32 x 512) 117 against 311; but 48 x (48 x 3195), four rounds, 385
+// against 336.
 bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n)
 {
-    if (m > kRows || n > kMaxCluster * kSlice) return false;
-    const int blocks = cluster_blocks(n);
-    return blocks == 1 ? batch <= 2 * num_sms() : batch <= clusters_at_once(blocks);
+    if (m > kRows || n > static_cast<int64_t>(kMaxCluster) * kSlice * 4) return false;
+    const Fold f = fold_of(batch, m, n);
+    return f.fold > 0 && f.cost < 850 + batch * n * (m > 64 ? 29 : 16) / 1000;
 }
 
 cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int parts, bool vec, cudaStream_t s)
@@ -464,8 +512,10 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.tall = M.r > M.cols;
     Q.m = static_cast<int>(std::min(M.r, M.cols));
     Q.n = static_cast<int>(std::max(M.r, M.cols));
-    const int blocks = cluster_blocks(Q.n);
-    Q.slice = ((Q.n + blocks - 1) / blocks + 63) / 64 * 64;
+    const Fold F = fold_of(M.batch, Q.m, Q.n);
+    const int blocks = F.blocks;
+    Q.fold = F.fold;
+    Q.slice = F.slice;
     Q.steps = M.steps;
     Q.a = M.a, Q.b = M.b, Q.c = M.c, Q.eps = M.eps;
     Q.part = part;
@@ -478,7 +528,8 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.decay = M.decay;
     Q.lr = M.lr;
     Q.d_err = M.d_err;
-    auto* kernel = vec ? k_muon_cluster<true> : k_muon_cluster<false>;
+    auto* kernel = F.fold > 1 ? (vec ? k_muon_cluster<true, true> : k_muon_cluster<false, true>)
+                              : (vec ? k_muon_cluster<true, false> : k_muon_cluster<false, false>);
     const cudaError_t ready = allow_smem(kernel, kSmallSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};

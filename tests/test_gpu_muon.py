@@ -254,3 +254,28 @@ def test_refusals(cuda_lib):
     assert so.sparse_muon_workspace_size(1, 8, 8, 2) == 0 and so.sparse_muon_workspace_size(1, 0, 8, 1) == 0
     torch.cuda.synchronize()
     assert int(k.err.item()) == 0 and int(s.err.item()) == 0
+
+
+FEW = [(1, 3664, 32), (1, 30, 8192), (1, 17, 831), (3, 831, 50), (59, 44, 860), (160, 32, 512), (2, 64, 4096),
+       (1, 4090, 64), (5, 8190, 3), (40, 16, 2050)]
+
+
+@pytest.mark.parametrize("kind", ["flat", "low rank", "decaying"])
+@pytest.mark.parametrize("batch,r,c", FEW)
+def test_few_long_rows(cuda_lib, batch, r, c, kind):
+    """Rows whose columns lie in parts below one another, in one block and in clusters."""
+    import torch
+    u = _spectrum(np.random.default_rng(r + c), batch, r, c, kind)
+    k = Case(torch, cuda_lib, u, 3)
+    got = k.run()
+    assert int(k.err.item()) == 0
+    assert _off(got, _formula(_np(k.u))) <= TOL[3]
+    k.out.zero_()
+    assert np.array_equal(got, k.run())
+    k = Case(torch, cuda_lib, u[:1], 1, "bf16", "bf16", shift=1)
+    assert _off(k.run(), _formula(_np(k.u))) <= TOL[3] + 2.0 ** -9
+
+
+@pytest.mark.parametrize("batch,r,c,g_type", [(70, 24, 700, "f32"), (3, 1001, 40, "bf16"), (1, 60, 4000, "bf16")])
+def test_muon_steps_of_few_long_rows(cuda_lib, batch, r, c, g_type):
+    test_muon_steps(cuda_lib, batch, r, c, g_type, 1, 3)

@@ -11,6 +11,11 @@
 //                              shared memory, in the same order on every block
 //   A A                        by every block
 //   B X_s                      by every block, in place
+// hi + lo is X to 22.6 bits, and the roundings of small singular values' directions grow with these,
+// 484 times in five steps.  Where few rows share them (at most 16) they are most of the result's
+// error (3 x 8190, singular values 1 to e^-9: 2.1e-5, fp32 products 1.4e-5), so there what hi + lo
+// leave of X is kept too, a byte of three bits and an exponent, and a X has all of it (1.6e-5; it costs a
+// sixth of the time).
 // One copy of X serves both products: boxes of 64 columns, 128 rows of 128 bytes, are
 // K-major for X X^T and MN-major for B X.  Products of one hi and one lo part, 2^-11
 // of the others, have an accumulator of their own, so that the tensor unit's
@@ -21,6 +26,8 @@
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
+
+#include <cuda_fp8.h>
 
 #include "muon.cuh"
 #include "profile.cuh"
@@ -33,7 +40,10 @@ constexpr int kRows = 128;                       // rows of X, A and B held, zer
 constexpr int kSlice = 256;                      // columns of X a block holds at most
 constexpr uint32_t kBlockBytes = kRows * 128;    // 64 columns of 128 rows
 constexpr uint32_t kXBytes = kSlice / 64 * kBlockBytes, kSquareBytes = kRows / 64 * kBlockBytes;
-constexpr uint32_t kSmallSmem = 2 * kXBytes + 2 * kSquareBytes + 1024;
+constexpr int kRestRows = 16;                     // rows up to which X has rests (below)
+constexpr uint32_t kRestBytes = kRows * kSlice;
+constexpr uint32_t kSmallSmem = 2 * kXBytes + 2 * kSquareBytes + 1024;   // and kRestBytes
+constexpr float kRestScale = 16384.0f;           // what hi + lo leave of 65504 is below 2^-8
 constexpr int kMaxCluster = 8;
 constexpr int kBlockThreads = 512, kWarps = kBlockThreads / 32;   // four warps for every 32 rows, a quarter of the columns each
 constexpr uint32_t kGramCol = 0, kCrossCol = 128, kUpdateCol = 256, kTmemCols = 512;
@@ -44,6 +54,23 @@ __device__ __forceinline__ uint32_t place(int row, int col)
     return (col >> 6) * kBlockBytes + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
 }
 
+// And in the array of what hi and lo leave, a byte each: 64-column blocks, 8-byte pieces permuted by row pair.
+__device__ __forceinline__ uint32_t rest_place(int row, int col)
+{
+    return (col >> 6) * (kRows * 64) + row * 64 + ((((col & 63) >> 3) ^ (row >> 1 & 7)) << 3) + (col & 7);
+}
+// Two values' rests as bytes, and back.
+__device__ __forceinline__ uint16_t rest_of(float a, float b)
+{
+    return __nv_cvt_float2_to_fp8x2(make_float2(a * kRestScale, b * kRestScale), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 rest_values(uint16_t q)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(q, __NV_E5M2);
+    const float2 f = __half22float2(__half2(h));
+    return make_float2(f.x * (1.0f / kRestScale), f.y * (1.0f / kRestScale));
+}
+
 __device__ __forceinline__ float4 lds_cluster(uint32_t addr)
 {
     float4 v;
@@ -51,9 +78,11 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t addr)
     return v;
 }
 
-// Eight values as hi and lo f16 to shared memory.
-__device__ __forceinline__ void split8(uint32_t hi_at, uint32_t lo_at, const float (&x)[8])
+// Eight values as hi and lo f16 to shared memory, and what these leave.
+template <bool kRest>
+__device__ __forceinline__ void split8(uint32_t hi_at, uint32_t lo_at, uint32_t rest_at, const float (&x)[8])
 {
+    uint16_t rest[4];
     uint4 hi, lo;
     __half2* hh = reinterpret_cast<__half2*>(&hi);
     __half2* ll = reinterpret_cast<__half2*>(&lo);
@@ -62,9 +91,14 @@ __device__ __forceinline__ void split8(uint32_t hi_at, uint32_t lo_at, const flo
         hh[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
         const float2 f = __half22float2(hh[e]);
         ll[e] = __floats2half2_rn(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+        if (kRest) {
+            const float2 l = __half22float2(ll[e]);
+            rest[e] = rest_of(x[2 * e] - f.x - l.x, x[2 * e + 1] - f.y - l.y);
+        }
     }
     sts128(hi_at, hi);
     sts128(lo_at, lo);
+    if (kRest) sts64(rest_at, rest[0] | static_cast<uint32_t>(rest[1]) << 16, rest[2] | static_cast<uint32_t>(rest[3]) << 16);
 }
 
 __device__ __forceinline__ uint16_t bits_of(__half h) { return __half_as_ushort(h); }
@@ -93,7 +127,9 @@ struct Small {
     int32_t* d_err;
 };
 
-template <bool kVec, bool kFold>
+// kLayout: one part, several, or (at most kRestRows rows) with rests.
+enum Layout { kOnePart, kParts, kRests };
+template <bool kVec, Layout kLayout>
 __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
 {
     extern __shared__ uint8_t raw[];
@@ -101,19 +137,20 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     __shared__ float sums[2 * 32];
-    const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes;
+    const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes, xrest = slo + kSquareBytes;
     const uint32_t bar = smem_addr(&bar_mem);
-    const int fold = kFold ? Q.fold : 1;
+    constexpr bool kRest = kLayout == kRests;
+    const int fold = kLayout == kOnePart ? 1 : Q.fold;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t mat = blockIdx.x / blocks;
     const int rank = static_cast<int>(blockIdx.x % blocks);
     const int col0 = rank * fold * Q.slice, cols = max(0, min(fold * Q.slice, Q.n - col0));   // this block's columns of X
     const int side = fold == 1 && Q.m <= 64 ? 64 : 128;   // of A and B, in the products
     const int part_rows = kRows / fold;
-    auto held_at = [&](int r, int c) {   // row r, column c of the block's columns
+    auto held = [&](int& r, int& c) {   // where row r, column c of the block's columns lies
         int h = 0;
         if (fold > 1) h = (c >= Q.slice) + (c >= 2 * Q.slice) + (c >= 3 * Q.slice);
-        return place(r + h * part_rows, c - h * Q.slice);
+        r += h * part_rows, c -= h * Q.slice;
     };
 
     if (threadIdx.x == 0) {
@@ -123,6 +160,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     }
     if (warp == 0) tmem_alloc<1>(&tmem_slot, kTmemCols);
     for (uint32_t i = threadIdx.x * 16; i < 2 * kXBytes; i += kBlockThreads * 16) sts128(xhi + i, make_uint4(0u, 0u, 0u, 0u));
+    for (uint32_t i = threadIdx.x * 16; i < (kRest ? kRestBytes : 0u); i += kBlockThreads * 16) sts128(xrest + i, make_uint4(0u, 0u, 0u, 0u));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -167,21 +205,30 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                                 if (e < left) Q.buf[at + e] = nb[i][e];
                         }
                     }
-                    uint16_t h[4], l[4];
+                    uint16_t h[4], l[4], rest[2];
+                    float left_over[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {   // 0 past `left`
                         const float v = u[i][e] * scale;
-                        const __half q = __float2half_rn(v);
-                        h[e] = bits_of(q), l[e] = bits_of(__float2half_rn(v - __half2float(q)));
+                        const __half q = __float2half_rn(v), ql = __float2half_rn(v - __half2float(q));
+                        h[e] = bits_of(q), l[e] = bits_of(ql);
+                        left_over[e] = v - __half2float(q) - __half2float(ql);
                     }
+                    if (kRest) rest[0] = rest_of(left_over[0], left_over[1]), rest[1] = rest_of(left_over[2], left_over[3]);
+                    int y = Q.tall ? k : o, x = Q.tall ? o : k;
+                    held(y, x);
                     if (Q.tall) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (e < left) sts16(xhi + held_at(k + e, o), h[e]), sts16(xlo + held_at(k + e, o), l[e]);
+                            if (e < left) {
+                                sts16(xhi + place(y + e, x), h[e]), sts16(xlo + place(y + e, x), l[e]);
+                                if (kRest) sts8(xrest + rest_place(y + e, x), rest[e / 2] >> e % 2 * 8);
+                            }
                     } else {
-                        const uint32_t p = held_at(o, k);   // four columns of one 16-byte piece
+                        const uint32_t p = place(y, x);   // four columns of one 16-byte piece
                         sts64(xhi + p, h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
                         sts64(xlo + p, l[0] | static_cast<uint32_t>(l[1]) << 16, l[2] | static_cast<uint32_t>(l[3]) << 16);
+                        if (kRest) sts32(xrest + rest_place(y, x), rest[0] | static_cast<uint32_t>(rest[1]) << 16);
                     }
                 }
             }
@@ -312,7 +359,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = av[8 * q + e] = rows_used && own_part ? av[8 * q + e] * kInvScale : 0.0f;
                 const uint32_t p = place(row, quarter * per + q * 8);
-                split8(shi + p, slo + p, x);   // zeros in the rows past the matrix's
+                split8<false>(shi + p, slo + p, 0u, x);   // zeros in the rows past the matrix's
             }
         operands_done();
 
@@ -336,7 +383,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                             x[e] = fmaf(Q.b, av[q * 16 + i], Q.c * kInvScale * (v[i] + y[i]));
                         }
                         const uint32_t p = place(row, quarter * per + q * 16 + p8 * 8);
-                        split8(shi + p, slo + p, x);
+                        split8<false>(shi + p, slo + p, 0u, x);
                     }
                 }
         operands_done();
@@ -353,12 +400,21 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
 #pragma unroll
                 for (int p8 = 0; p8 < 4; ++p8) {
                     const uint32_t p = place(row, q * 32 + p8 * 8);
+                    const uint32_t at = xrest + rest_place(row, q * 32 + p8 * 8);
                     float x[8], l[8];
                     unpack8(lds128(xhi + p), x);
                     unpack8(lds128(xlo + p), l);
+                    if (kRest) {
+                        const uint2 rest = lds64(at);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const float2 t = rest_values(static_cast<uint16_t>((e < 4 ? rest.x : rest.y) >> e % 4 * 8));
+                            l[e] += t.x, l[e + 1] += t.y;
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = fmaf(Q.a, x[e] + l[e], kInvScale * v[p8 * 8 + e]);
-                    split8(xhi + p, xlo + p, x);
+                    split8<kRest>(xhi + p, xlo + p, at, x);
                 }
             }
     }
@@ -393,11 +449,15 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                     if (Q.tall) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t p = held_at(k + min(e, left - 1), o);
+                            int y = k + min(e, left - 1), c = o;
+                            held(y, c);
+                            const uint32_t p = place(y, c);
                             x[e] = __half2float(lds_half(xhi + p)) + __half2float(lds_half(xlo + p));
                         }
                     } else {
-                        const uint32_t p = held_at(o, k);
+                        int y = o, c = k;
+                        held(y, c);
+                        const uint32_t p = place(y, c);
                         const uint2 h = lds64(xhi + p), l = lds64(xlo + p);
                         const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x)), h1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
                         const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(&l.x)), l1 = __half22float2(*reinterpret_cast<const __half2*>(&l.y));
@@ -453,8 +513,8 @@ int clusters_at_once(int blocks)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (allow_smem((k_muon_cluster<true, false>), kSmallSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, (k_muon_cluster<true, false>), &cfg) != cudaSuccess) n = 0;
+        if (allow_smem((k_muon_cluster<true, kOnePart>), kSmallSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, (k_muon_cluster<true, kOnePart>), &cfg) != cudaSuccess) n = 0;
         n = std::max(n, 1);
         known[blocks].store(n, std::memory_order_relaxed);
     }
@@ -528,14 +588,16 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.decay = M.decay;
     Q.lr = M.lr;
     Q.d_err = M.d_err;
-    auto* kernel = F.fold > 1 ? (vec ? k_muon_cluster<true, true> : k_muon_cluster<false, true>)
-                              : (vec ? k_muon_cluster<true, false> : k_muon_cluster<false, false>);
-    const cudaError_t ready = allow_smem(kernel, kSmallSmem);
+    auto* kernel = Q.m <= kRestRows ? (vec ? k_muon_cluster<true, kRests> : k_muon_cluster<false, kRests>)
+                   : F.fold > 1     ? (vec ? k_muon_cluster<true, kParts> : k_muon_cluster<false, kParts>)
+                                    : (vec ? k_muon_cluster<true, kOnePart> : k_muon_cluster<false, kOnePart>);
+    const uint32_t smem = kSmallSmem + (Q.m <= kRestRows ? kRestBytes : 0);   // (what is not asked for is cache)
+    const cudaError_t ready = allow_smem(kernel, smem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M.batch * blocks));
     cfg.blockDim = dim3(kBlockThreads);
-    cfg.dynamicSmemBytes = kSmallSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

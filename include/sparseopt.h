@@ -352,7 +352,8 @@ sparse_status_t sparse_canonicalize_static_ws(const int64_t* idx, const float* v
  * serves with next to it.  (No counterpart on the pages, which describe the
  * optimizer alone.)  The conventions above hold: caller memory, dense row-major
  * arrays of any alignment (16-byte aligned ones with rows of a multiple of 16
- * bytes take the vector path), asynchronous on `stream`, the sticky error word,
+ * bytes take the vector path, rows of aligned pairs the next best), asynchronous
+ * on `stream`, the sticky error word,
  * n = 0 is legal.  Values are fp32 or bf16 as their sparse_dtype_t says;
  * statistics, weights, weight gradients and every sum are fp32, and a bf16
  * output is rounded once.  Non-state outputs are undefined when *d_err is set.

@@ -1,6 +1,7 @@
 // api_model.cu -- the extern "C" entry points of the operators around the table
 // step (declared in include/sparseopt.h): argument validation, workspace
 // carving and the choice of 16-byte accesses.  No host synchronisation.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -9,8 +10,6 @@
 namespace {
 
 using namespace so;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool ws_ok(const void* ws, size_t have, size_t need)
 {
@@ -35,10 +34,16 @@ bool valid_norm(const void* x, sparse_dtype_t x_type, int64_t r, int64_t c, cons
            d_err != nullptr;
 }
 
-// Values of one 16-byte access, or of the two that match it where a type is fp32 and the other bf16.
-int64_t lane_values(sparse_dtype_t x_type, sparse_dtype_t y_type)
+// Values of an access to rows of c values in all these arrays: those of 16 bytes (of two accesses to an fp32
+// array beside a bf16 one), two, or 0 for single ones.
+int access(int64_t c, bool any_bf16, const void* a, bool a_bf16, const void* b, bool b_bf16, const void* d, bool d_bf16)
 {
-    return is_bf16(x_type) || is_bf16(y_type) ? 8 : 4;
+    auto fits = [&](const void* p, bool bf16, int64_t v) {
+        return reinterpret_cast<uintptr_t>(p) % std::min<uintptr_t>(16, static_cast<uintptr_t>(v * (bf16 ? 2 : 4))) == 0;
+    };
+    for (int v : {any_bf16 ? 8 : 4, 2})
+        if (c % v == 0 && fits(a, a_bf16, v) && fits(b, b_bf16, v) && fits(d, d_bf16, v)) return v;
+    return 0;
 }
 
 bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const int32_t* d_err)
@@ -130,7 +135,8 @@ sparse_status_t sparse_layer_norm(const void* x, sparse_dtype_t x_type, int64_t 
         return SPARSE_ERR_INVALID_ARG;
     if (n == 0) return SPARSE_OK;
     if (y == nullptr) return SPARSE_ERR_INVALID_ARG;
-    const int vec = c % lane_values(x_type, y_type) == 0 && aligned16(x) && aligned16(y);
+    const bool xb = is_bf16(x_type), yb = is_bf16(y_type);
+    const int vec = access(c, xb || yb, x, xb, y, yb, y, yb);
     return from_cuda(layer_norm(x, is_bf16(x_type), r, c, idx, n, gamma, beta, static_cast<float>(eps), y,
                                 is_bf16(y_type), vec, mean, rstd, d_err, stream));
 }
@@ -145,7 +151,8 @@ sparse_status_t sparse_layer_norm_grad(const void* dy, sparse_dtype_t y_type, co
     if ((dgamma != nullptr || dbeta != nullptr) && n > 0 &&
         !ws_ok(ws, ws_bytes, sparse_layer_norm_workspace_size(n, c)))
         return SPARSE_ERR_WORKSPACE;
-    const int vec = c % lane_values(x_type, y_type) == 0 && aligned16(x) && aligned16(dy) && aligned16(dx);
+    const bool xb = is_bf16(x_type), yb = is_bf16(y_type);
+    const int vec = access(c, xb || yb, x, xb, dy, yb, dx, xb);
     return from_cuda(layer_norm_grad(dy, is_bf16(y_type), x, is_bf16(x_type), r, c, idx, n, gamma, mean, rstd, dx,
                                      dgamma, dbeta, static_cast<float*>(ws), vec, d_err, stream));
 }
@@ -176,7 +183,8 @@ sparse_status_t sparse_expert_dispatch(const void* x, sparse_dtype_t type, int64
     if (!valid_expert(type, n, k, c, d_err) || experts < 1 || experts > kMaxExperts) return SPARSE_ERR_INVALID_ARG;
     if (n == 0) return SPARSE_OK;
     if (x == nullptr || pos == nullptr || offsets == nullptr || xs == nullptr) return SPARSE_ERR_INVALID_ARG;
-    const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(x) && aligned16(xs);
+    const bool b = is_bf16(type);
+    const int vec = access(c, b, x, b, xs, b, xs, b);
     return from_cuda(expert_dispatch(x, is_bf16(type), n, k, c, pos, offsets + experts, xs, vec, d_err, stream));
 }
 
@@ -187,7 +195,8 @@ sparse_status_t sparse_expert_combine(const void* ys, sparse_dtype_t type, int64
     if (!valid_expert(type, n, k, c, d_err)) return SPARSE_ERR_INVALID_ARG;
     if (n == 0) return SPARSE_OK;
     if (ys == nullptr || pos == nullptr || y == nullptr) return SPARSE_ERR_INVALID_ARG;
-    const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(ys) && aligned16(y);
+    const bool b = is_bf16(type);
+    const int vec = access(c, b, ys, b, y, b, y, b);
     return from_cuda(expert_combine(ys, is_bf16(type), n, k, c, pos, weights, y, vec, d_err, stream));
 }
 
@@ -200,7 +209,8 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
     if (n == 0) return SPARSE_OK;
     if (dy == nullptr || ys == nullptr || pos == nullptr || offsets == nullptr || dys == nullptr)
         return SPARSE_ERR_INVALID_ARG;
-    const int vec = c * (is_bf16(type) ? 2 : 4) % 16 == 0 && aligned16(dy) && aligned16(ys) && aligned16(dys);
+    const bool b = is_bf16(type);
+    const int vec = access(c, b, dy, b, ys, b, dys, b);
     return from_cuda(expert_combine_grad(dy, ys, is_bf16(type), n, k, c, pos, offsets + experts, weights, dys,
                                          dweights, vec, d_err, stream));
 }

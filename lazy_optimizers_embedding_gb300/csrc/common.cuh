@@ -367,7 +367,7 @@ cudaError_t row_coo_to_csr(const int64_t* rows, int64_t nrows, int64_t r, int64_
 
 
 // ------------------------------------------------- operators around the step
-// Layer norm (layer_norm.cu); vec: 16-byte accesses (see the entry points).
+// Layer norm (layer_norm.cu); vec: values of an access, 8 or 4, 2, or 0 for single ones (see the entry points).
 int64_t layer_norm_parts(int64_t n, int64_t c);
 cudaError_t layer_norm(const void* x, int x_bf16, int64_t r, int64_t c, const int64_t* idx, int64_t n,
                        const float* gamma, const float* beta, float eps, void* y, int y_bf16, int vec, float* mean,

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kExBlock) k_expert_combine(const T* __restrict
                                                              int32_t* d_err)
 {
     pdl_wait();   // writes a caller output
-    constexpr int J = 4, R = V == 1 ? 4 : 2;
+    constexpr int J = 4, R = V < 4 ? 4 : 2;
     const int gl = threadIdx.x & (G - 1);
     const int64_t group = static_cast<int64_t>(blockIdx.x) * (kExBlock / G) + threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kExBlock / G);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ 
                                                           float* __restrict__ dw, int32_t* d_err)
 {
     pdl_wait();   // writes caller outputs
-    constexpr int J = 2, R = V == 1 ? 8 : 4, kMany = 8;
+    constexpr int J = 2, R = V < 4 ? 8 : 4, kMany = 8;
     const int lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kExWarps + (threadIdx.x >> 5);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kExWarps;
@@ -554,7 +554,9 @@ cudaError_t expert_dispatch(const void* x, int is_bf16, int64_t n, int64_t k, in
                             const int64_t* end, void* xs, int vec, int32_t* d_err, cudaStream_t s)
 {
     const int64_t bytes = c * (is_bf16 ? 2 : 4);
-    if (vec) return run_dispatch<uint4>(x, n, k, bytes / 16, pos, end, xs, d_err, s);
+    if (vec > 2) return run_dispatch<uint4>(x, n, k, bytes / 16, pos, end, xs, d_err, s);
+    if (vec && !is_bf16) return run_dispatch<uint2>(x, n, k, bytes / 8, pos, end, xs, d_err, s);
+    if (vec) return run_dispatch<uint32_t>(x, n, k, bytes / 4, pos, end, xs, d_err, s);
     if (!is_bf16) return run_dispatch<uint32_t>(x, n, k, c, pos, end, xs, d_err, s);
     return run_dispatch<uint16_t>(x, n, k, c, pos, end, xs, d_err, s);
 }
@@ -563,7 +565,7 @@ template <class T, int V>
 static cudaError_t run_combine(const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos, const float* w,
                                void* y, int32_t* d_err, cudaStream_t s)
 {
-    const int G = lanes_for(c / V, V == 1 ? 4 : 2);
+    const int G = lanes_for(c / V, V < 4 ? 4 : 2);
     static const int most = resident(k_expert_combine<T, V>);
     SO_PROFILE("expert_combine", s);
     return launch(k_expert_combine<T, V>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
@@ -574,10 +576,12 @@ cudaError_t expert_combine(const void* ys, int is_bf16, int64_t n, int64_t k, in
                            const float* w, void* y, int vec, int32_t* d_err, cudaStream_t s)
 {
     if (is_bf16)
-        return vec ? run_combine<bf16, 8>(ys, n, k, c, pos, w, y, d_err, s)
-                   : run_combine<bf16, 1>(ys, n, k, c, pos, w, y, d_err, s);
-    return vec ? run_combine<float, 4>(ys, n, k, c, pos, w, y, d_err, s)
-               : run_combine<float, 1>(ys, n, k, c, pos, w, y, d_err, s);
+        return vec > 2 ? run_combine<bf16, 8>(ys, n, k, c, pos, w, y, d_err, s)
+               : vec   ? run_combine<bf16, 2>(ys, n, k, c, pos, w, y, d_err, s)
+                       : run_combine<bf16, 1>(ys, n, k, c, pos, w, y, d_err, s);
+    return vec > 2 ? run_combine<float, 4>(ys, n, k, c, pos, w, y, d_err, s)
+           : vec   ? run_combine<float, 2>(ys, n, k, c, pos, w, y, d_err, s)
+                   : run_combine<float, 1>(ys, n, k, c, pos, w, y, d_err, s);
 }
 
 template <class T, int V, bool kWeights>
@@ -603,10 +607,12 @@ cudaError_t expert_combine_grad(const void* dy, const void* ys, int is_bf16, int
                                 int32_t* d_err, cudaStream_t s)
 {
     if (is_bf16)
-        return vec ? run_grad<bf16, 8>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
-                   : run_grad<bf16, 1>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s);
-    return vec ? run_grad<float, 4>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
-               : run_grad<float, 1>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s);
+        return vec > 2 ? run_grad<bf16, 8>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
+               : vec   ? run_grad<bf16, 2>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
+                       : run_grad<bf16, 1>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s);
+    return vec > 2 ? run_grad<float, 4>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
+           : vec   ? run_grad<float, 2>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s)
+                   : run_grad<float, 1>(dy, ys, n, k, c, pos, end, w, dys, dw, d_err, s);
 }
 
 }  // namespace so

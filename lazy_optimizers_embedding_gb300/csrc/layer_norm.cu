@@ -90,12 +90,12 @@ __device__ __forceinline__ void ln_put(T* to, const F2 (&v)[kPairs<V>])
     Pack<T, V>::put(to, x);
 }
 
-// A vector over the columns in shared memory as its lanes read it: 16-byte pieces of
+// A vector over the columns in shared memory as its lanes read it: 16-byte pieces (or 8, 4) of
 // an access lie G apart, so neighbouring lanes read neighbouring pieces.
 template <int V>
 __device__ __forceinline__ int ln_slot(int k, int e, int G, int gl)
 {
-    constexpr int W = V < 4 ? 1 : 4;
+    constexpr int W = V < 4 ? V : 4;
     return ((k * (V / W) + e / W) * G + gl) * W + e % W;
 }
 template <int V>
@@ -110,6 +110,9 @@ __device__ __forceinline__ void ln_staged(F2 (&g)[kPairs<V>], const float* from,
 {
     if constexpr (V == 1) {
         g[0] = F2::of(from[ln_slot<V>(k, 0, G, gl)], 0.0f);
+    } else if constexpr (V == 2) {
+        const float2 q = *reinterpret_cast<const float2*>(from + ln_slot<V>(k, 0, G, gl));
+        g[0] = F2::of(q.x, q.y);
     } else {
 #pragma unroll
         for (int e = 0; e < V; e += 4) {
@@ -219,7 +222,7 @@ __device__ __forceinline__ void ln_vector(float (&g)[V], const float* from, int6
 // its own accesses, so no one waits for another's; wider rows yet are read three times.  (4096 x
 // 16384 bf16: 59 us against 98.7 us with single values and three reads.)
 template <class X, class Y, int V, int R, bool kHeld>
-__global__ void __launch_bounds__(kMaxBackGroup, V == 1 && !kHeld ? 4 : 2) k_ln_wide(const X* __restrict__ x, int64_t r, int64_t c,
+__global__ void __launch_bounds__(kMaxBackGroup, V < 4 && !kHeld ? 4 : 2) k_ln_wide(const X* __restrict__ x, int64_t r, int64_t c,
                                                           const int64_t* __restrict__ idx, int64_t n,
                                                           const float* __restrict__ gamma, const float* __restrict__ beta,
                                                           int quad, float eps, Y* __restrict__ y, float* __restrict__ mean,
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
 #pragma unroll
         for (int u = 0; u < R; ++u) {
             found[u] = S.found[stage][u] != 0;
-            const int skew = V == 1 && found[u] ? S.found[stage][u] - 1 : 0;
+            const int skew = V < 4 && found[u] ? S.found[stage][u] - 1 : 0;
             ring_get<X, V, kEven>(v[u], at + u * bytes + skew, c, G, gl, used);
             F2 t = v[u][0];
 #pragma unroll
@@ -790,8 +793,8 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
             found[u] = S.found[stage][u] != 0;
             s[2 * u] = s[2 * u + 1] = 0.0f;
             if (!found[u]) continue;   // the same for the whole block
-            const int xs = V == 1 ? S.found[stage][u] - 1 : 0;
-            const int ys = V == 1 ? static_cast<int>(reinterpret_cast<uintptr_t>(dy + (i0 + u) * c) & 15u) : 0;
+            const int xs = V < 4 ? S.found[stage][u] - 1 : 0;
+            const int ys = V < 4 ? static_cast<int>(reinterpret_cast<uintptr_t>(dy + (i0 + u) * c) & 15u) : 0;
             ring_get<X, V, kEven>(xh[u], at + u * (xb + yb) + xs, c, G, gl, used);
             ring_get<Y, V, kEven>(h[u], at + u * (xb + yb) + xb + ys, c, G, gl, used);
             const F2 rs2 = F2::both(rs[u]), off2 = F2::both(off[u]);
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
 // shared memory as k_ln_wide holds x; the column sums apart (k_ln_cols).  (4096 x 16384 bf16, all
 // three kernels: 149 us against 259.5 us with single values.)
 template <class X, class Y, int V, bool kHeld>
-__global__ void __launch_bounds__(kMaxBackGroup, V == 1 && !kHeld ? 4 : 2) k_ln_grad_wide(const Y* __restrict__ dy, const X* __restrict__ x,
+__global__ void __launch_bounds__(kMaxBackGroup, V < 4 && !kHeld ? 4 : 2) k_ln_grad_wide(const Y* __restrict__ dy, const X* __restrict__ x,
                                                                int64_t r, int64_t c, const int64_t* __restrict__ idx,
                                                                int64_t n, const float* __restrict__ gamma, int quad,
                                                                const float* __restrict__ mean,
@@ -1058,7 +1061,7 @@ template <class X, class Y, int V, bool kBack>
 RingShape ring_shape(int64_t c, int64_t n)
 {
     RingShape s{std::max(64, lanes_of(c, kRingLane)), 0, 0};
-    const bool faster = V == 1 ? c * static_cast<int64_t>(sizeof(X)) >= 1024
+    const bool faster = V < 4 ? c * static_cast<int64_t>(sizeof(X)) >= 1024
                         : kBack ? sizeof(X) == 2 && c > 1024 && n * c >= kRingBack
                                 : c > 1024;
     if (!faster || c > static_cast<int64_t>(kMaxBackGroup) * kRingLane) return s;
@@ -1129,7 +1132,7 @@ cudaError_t run_ln(const Forward& F)
     }
     // two rows share gamma and beta where they leave room for two blocks an SM and the rows go round
     const size_t row = (static_cast<size_t>(F.c) * sizeof(X) + 15) / 16 * 16;
-    const bool held = row <= kRingSmem && !(V == 1 && sizeof(X) == 2);   // (two bytes at a time they cost more than they save)
+    const bool held = row <= kRingSmem && !(V * sizeof(X) == 2);   // (two bytes at a time they cost more than they save)
     if (!held) return run_ln_wide<X, Y, V, 1, false>(F, 0);
     if (2 * row <= kRingSmem / 2 && F.n >= 4 * static_cast<int64_t>(num_sms())) return run_ln_wide<X, Y, V, 2, true>(F, 2 * row);
     return run_ln_wide<X, Y, V, 1, true>(F, row);
@@ -1214,23 +1217,24 @@ cudaError_t run_ln_grad(const Backward& B)
         SO_PROFILE("layer_norm_grad", B.s);
         if (B.c > kMaxBackward) {
             const size_t smem = ((static_cast<size_t>(B.c) * sizeof(X) + 15) / 16 + (static_cast<size_t>(B.c) * sizeof(Y) + 15) / 16) * 16;
-            e = smem <= kRingSmem && !(V == 1 && sizeof(X) == 2) ? run_grad_wide<X, Y, V, true>(B, smem) : run_grad_wide<X, Y, V, false>(B, 0);
+            e = smem <= kRingSmem && !(V * sizeof(X) == 2) ? run_grad_wide<X, Y, V, true>(B, smem) : run_grad_wide<X, Y, V, false>(B, 0);
             if (e == cudaSuccess && want)
                 e = launch(k_ln_cols<X, Y, V>, dim3(static_cast<unsigned>((B.c / V + kLnBlock - 1) / kLnBlock),
                                                     static_cast<unsigned>(parts)),
                            dim3(kLnBlock), B.s, static_cast<const Y*>(B.dy), static_cast<const X*>(B.x), B.r, B.c, B.idx,
                            B.n, B.mean, B.rstd, B.part);
         } else {
-            // two rows at a time where a lane's shares of both leave it the registers
-            constexpr int R = V > 1 && sizeof(X) == 2 ? 2 : 1;
+            // two rows at a time where a lane's shares of both leave it the registers (single values, 123154
+            // x 236 fp32: one row 107 us, two, which spilled, 200)
+            constexpr int R = V > 2 && sizeof(X) == 2 ? 2 : 1;
             const RingShape g = ring_shape<X, Y, V, true>(B.c, B.n);
             const bool even = V > 1 && B.c % (g.G * V) == 0;
             if (g.stages && g.G <= 256)
                 e = even ? run_grad_ring<X, Y, V, (V > 1), 256>(B, g, want, parts) : run_grad_ring<X, Y, V, false, 256>(B, g, want, parts);
             else if (g.stages)
                 e = even ? run_grad_ring<X, Y, V, (V > 1), 512>(B, g, want, parts) : run_grad_ring<X, Y, V, false, 512>(B, g, want, parts);
-            else if (V == 1 && B.c <= static_cast<int64_t>(kMaxBackGroup) * 8)
-                e = run_grad_lane<X, Y, V, 8, 2, false>(B, want, parts);
+            else if (V < 4 && B.c <= static_cast<int64_t>(kMaxBackGroup) * 8)
+                e = run_grad_lane<X, Y, V, 8, 1, false>(B, want, parts);
             else if (V > 1 && B.c % (lanes_of(B.c, 16) * V) == 0)
                 e = run_grad_lane<X, Y, V, 16, R, (V > 1)>(B, want, parts);
             else
@@ -1254,9 +1258,9 @@ cudaError_t layer_norm(const void* x, int x_bf16, int64_t r, int64_t c, const in
                        float* rstd, int32_t* d_err, cudaStream_t s)
 {
     const Forward F{x, r, c, idx, n, gamma, beta, eps, y, mean, rstd, d_err, s};
-    if (!x_bf16 && !y_bf16) return vec ? run_ln<float, float, 4>(F) : run_ln<float, float, 1>(F);
-    if (!x_bf16) return vec ? run_ln<float, bf16, 8>(F) : run_ln<float, bf16, 1>(F);
-    return vec ? run_ln<bf16, bf16, 8>(F) : run_ln<bf16, bf16, 1>(F);
+    if (!x_bf16 && !y_bf16) return vec > 2 ? run_ln<float, float, 4>(F) : vec ? run_ln<float, float, 2>(F) : run_ln<float, float, 1>(F);
+    if (!x_bf16) return vec > 2 ? run_ln<float, bf16, 8>(F) : vec ? run_ln<float, bf16, 2>(F) : run_ln<float, bf16, 1>(F);
+    return vec > 2 ? run_ln<bf16, bf16, 8>(F) : vec ? run_ln<bf16, bf16, 2>(F) : run_ln<bf16, bf16, 1>(F);
 }
 
 cudaError_t layer_norm_grad(const void* dy, int y_bf16, const void* x, int x_bf16, int64_t r, int64_t c,
@@ -1265,9 +1269,9 @@ cudaError_t layer_norm_grad(const void* dy, int y_bf16, const void* x, int x_bf1
                             cudaStream_t s)
 {
     const Backward B{dy, x, r, c, idx, n, gamma, mean, rstd, dx, dgamma, dbeta, part, d_err, s};
-    if (!x_bf16 && !y_bf16) return vec ? run_ln_grad<float, float, 4>(B) : run_ln_grad<float, float, 1>(B);
-    if (!x_bf16) return vec ? run_ln_grad<float, bf16, 8>(B) : run_ln_grad<float, bf16, 1>(B);
-    return vec ? run_ln_grad<bf16, bf16, 8>(B) : run_ln_grad<bf16, bf16, 1>(B);
+    if (!x_bf16 && !y_bf16) return vec > 2 ? run_ln_grad<float, float, 4>(B) : vec ? run_ln_grad<float, float, 2>(B) : run_ln_grad<float, float, 1>(B);
+    if (!x_bf16) return vec > 2 ? run_ln_grad<float, bf16, 8>(B) : vec ? run_ln_grad<float, bf16, 2>(B) : run_ln_grad<float, bf16, 1>(B);
+    return vec > 2 ? run_ln_grad<bf16, bf16, 8>(B) : vec ? run_ln_grad<bf16, bf16, 2>(B) : run_ln_grad<bf16, bf16, 1>(B);
 }
 
 }  // namespace so

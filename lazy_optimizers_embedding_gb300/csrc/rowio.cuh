@@ -60,6 +60,13 @@ template <> struct Pack<float, 1> {
     __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = a; }
     __device__ __forceinline__ static void put(float* p, const float (&x)[1]) { *p = x[0]; }
 };
+template <> struct Pack<float, 2> {
+    float2 a;
+    __device__ __forceinline__ void load(const float* p) { a = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void zero() { a = make_float2(0.0f, 0.0f); }
+    __device__ __forceinline__ void get(float (&x)[2]) const { x[0] = a.x, x[1] = a.y; }
+    __device__ __forceinline__ static void put(float* p, const float (&x)[2]) { *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]); }
+};
 template <> struct Pack<float, 4> {
     float4 a;
     __device__ __forceinline__ void load(const float* p) { a = *reinterpret_cast<const float4*>(p); }
@@ -91,6 +98,13 @@ template <> struct Pack<bf16, 1> {
     __device__ __forceinline__ void zero() { a = __float2bfloat16_rn(0.0f); }
     __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = __bfloat162float(a); }
     __device__ __forceinline__ static void put(bf16* p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
+};
+template <> struct Pack<bf16, 2> {
+    uint32_t a;
+    __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void zero() { a = 0u; }
+    __device__ __forceinline__ void get(float (&x)[2]) const { x[0] = __uint_as_float(a << 16), x[1] = __uint_as_float(a & 0xffff0000u); }
+    __device__ __forceinline__ static void put(bf16* p, const float (&x)[2]) { *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x[0], x[1]); }
 };
 template <> struct Pack<bf16, 8> {
     uint4 a;

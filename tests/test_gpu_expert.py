@@ -285,3 +285,14 @@ def test_sorts_whose_counts_are_about_48_kb(cuda_lib, n, experts):
     assert int(case.err.item()) == 0
     case.compare()
     assert cuda_lib.sparse_expert_workspace_size(n, 1, experts) > 0   # an array of this size has an address
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("c,shift", [(2, 0), (6, 0), (30, 0), (262, 0), (1030, 0), (64, 2), (1024, 2)])
+def test_rows_of_pairs(cuda_lib, c, shift, kind):
+    """Rows of an even number of values, or arrays aligned to two of them: accesses of two."""
+    import torch
+    case = Case(torch, cuda_lib, np.random.default_rng(c).integers(-1, 7, (210, 3)), 7, c, kind, shift=shift)
+    case.run()
+    assert int(case.err.item()) == 0
+    case.compare()

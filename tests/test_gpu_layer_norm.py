@@ -331,3 +331,16 @@ def test_rows_wider_than_the_groups(cuda_lib, n, c, shift, xt, yt):
         assert not got[n // 2].any()
         got[n // 2] = ref[n // 2]
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("n,c,shift", [(40, 22, 0), (300, 94, 0), (33, 236, 0), (40, 602, 0), (700, 1110, 0),
+                                       (20, 4098, 0), (9, 9002, 0), (50, 64, 2), (50, 256, 2), (50, 2048, 2),
+                                       (9, 8200, 2)])
+def test_rows_of_pairs(cuda_lib, n, c, shift, xt, yt):
+    """Rows of an even number of values, or arrays aligned to two of them: accesses of two."""
+    import torch
+    k = Case(torch, cuda_lib, n, c, xt, yt, shift=shift)
+    k.run()
+    assert int(k.err.item()) == 0
+    k.compare()

@@ -101,6 +101,15 @@ __device__ __forceinline__ int ln_slot(int k, int e, int G, int gl)
 template <int V>
 __device__ __forceinline__ void ln_stage(float* to, const float* v, float none, int c, int G, int threads)
 {
+    if ((G & (G - 1)) != 0) {   // the one group of its block
+        for (int k = 0; k * G * V < c; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int col = (k * G + static_cast<int>(threadIdx.x)) * V + e;
+                to[ln_slot<V>(k, e, G, threadIdx.x)] = v != nullptr && col < c ? v[col] : none;
+            }
+        return;
+    }
     const int step = 31 - __clz(G * V), gmask = G - 1;
     for (int q = threadIdx.x; q < ((c + G * V - 1) >> step << step); q += threads)
         to[ln_slot<V>(q >> step, q % V, G, q / V & gmask)] = v != nullptr && q < c ? v[q] : none;
@@ -301,12 +310,12 @@ __global__ void __launch_bounds__(kMaxBackGroup, V < 4 && !kHeld ? 4 : 2) k_ln_w
     }
 }
 
-// Sums of N values (1, 2 or 4) over a group of W warps (a power of two up to 16): the
+// Sums of N values (1, 2 or 4) over a group of W warps (up to 16, from warp `first` on): the
 // first butterfly steps halve the values a lane carries instead of carrying all of
 // them through, then N lanes' sums of every warp meet in `tmp` (32 N words).
 // The group's block meets at named barrier 1, `threads` of it (other warps of the block do not).
 template <int N>
-__device__ __forceinline__ void warps_sum(float (&x)[N], int W, float* tmp, int threads)
+__device__ __forceinline__ void warps_sum(float (&x)[N], int W, int first, float* tmp, int threads)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kPer = 32 / N;   // lanes that end with one value's sum
@@ -327,7 +336,7 @@ __device__ __forceinline__ void warps_sum(float (&x)[N], int W, float* tmp, int 
     const int mine = lane / kPer, at = lane % kPer;   // the value this lane has now
     if (at == 0) tmp[mine * 32 + warp] = v[0];
     asm volatile("barrier.cta.sync 1, %0;" ::"r"(threads) : "memory");
-    const float* t = tmp + mine * 32 + (warp & ~(W - 1));
+    const float* t = tmp + mine * 32 + first;
     v[0] = at < W ? t[at] : 0.0f;
     if (kPer < 16 && at + kPer < W) v[0] += t[at + kPer];
 #pragma unroll
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kMaxBackGroup, 1)
     __shared__ float tmp[2][2 * R * 32];
     extern __shared__ float4 stage[];   // gamma; then [groups][2][c], the groups' column sums
     float* sgamma = reinterpret_cast<float*>(stage);
-    const int gl = threadIdx.x & (G - 1), sub = threadIdx.x / G, groups = blockDim.x / G;
+    const int groups = blockDim.x / G, sub = groups == 1 ? 0 : threadIdx.x / G, gl = threadIdx.x - sub * G;
     const int used = (c + G * V - 1) / (G * V);
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     const float inv_c = 1.0f / static_cast<float>(c);
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(kMaxBackGroup, 1)
 #pragma unroll
         for (int u = 0; u < R; ++u) s[2 * u] = s0[u].sum(), s[2 * u + 1] = s1[u].sum();
         if (G > 32) {
-            warps_sum<2 * R>(s, G >> 5, tmp[half], blockDim.x);
+            warps_sum<2 * R>(s, G >> 5, sub * (G >> 5), tmp[half], blockDim.x);
             half ^= 1;
         } else {
             group_sum<2 * R>(s, G, nullptr, 0);
@@ -703,7 +712,7 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
         }
         __syncwarp();
         if ((gl & 31) == 0) mbar_arrive(smem_addr(&S.empty[stage]));   // the warp has read the stage
-        warps_sum<R>(s, G >> 5, S.tmp[0], G);
+        warps_sum<R>(s, G >> 5, 0, S.tmp[0], G);
         float mu[R];
 #pragma unroll
         for (int u = 0; u < R; ++u) {
@@ -721,7 +730,7 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
             }
             s[u] = t.sum();
         }
-        warps_sum<R>(s, G >> 5, S.tmp[1], G);
+        warps_sum<R>(s, G >> 5, 0, S.tmp[1], G);
 #pragma unroll
         for (int u = 0; u < R; ++u) {
             if (!found[u]) continue;
@@ -813,7 +822,7 @@ __global__ void __launch_bounds__(kT + 32, kT <= 256 ? 2 : 1)
         }
         __syncwarp();
         if ((gl & 31) == 0) mbar_arrive(smem_addr(&S.empty[stage]));   // the warp has read the stage
-        warps_sum<2 * R>(s, G >> 5, S.tmp[it & 1], G);
+        warps_sum<2 * R>(s, G >> 5, 0, S.tmp[it & 1], G);
 #pragma unroll
         for (int u = 0; u < R; ++u) {
             if (!found[u]) continue;
@@ -997,13 +1006,22 @@ int lanes_of(int64_t c, int lane)
     while (static_cast<int64_t>(G) * lane < c) G *= 2;
     return G;
 }
+// The same for a group that may be a block of its own: whole warps then (4744 fp32 columns by 297 lanes, 320
+// of them and not 512).
+int lanes_of_block(int64_t c, int lane, int least)
+{
+    const int G = lanes_of(c, lane);
+    return G < least ? G : std::max<int>(least, static_cast<int>((c + lane - 1) / lane + 31) / 32 * 32);
+}
 // Resident blocks of a kernel that groups of G lanes share (G sets its threads and, at most, its
 // shared memory).
+constexpr int kGroupKinds = 5 + kMaxBackGroup / 32 + 1;
 template <class K>
-int resident(std::atomic<int> (&known)[11], K kernel, int G, int threads, size_t smem)
+int resident(std::atomic<int> (&known)[kGroupKinds], K kernel, int G, int threads, size_t smem)
 {
-    int i = 0;
-    while ((1 << i) < G) ++i;
+    int i = 0;   // of G: powers of two to 32, multiples of 32 past it
+    while (i < 5 && (1 << i) < G) ++i;
+    i += (G - 1) / 32;
     int o = known[i].load(std::memory_order_relaxed);
     if (o == 0) {
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kernel, threads, smem);
@@ -1034,7 +1052,7 @@ cudaError_t run_ln_lane(const Forward& F)
     const int64_t row = (F.c + G * V - 1) / (G * V) * (G * V);
     cudaError_t e = allow_smem(kernel, sizeof(float) * 2 * row);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> known[11];
+    static std::atomic<int> known[kGroupKinds];
     const int blocks = static_cast<int>(std::min<int64_t>(
         (F.n + groups - 1) / groups,
         static_cast<int64_t>(resident(known, kernel, G, kLnBlock, sizeof(float) * 2 * L * G)) * num_sms()));
@@ -1060,7 +1078,7 @@ struct RingShape {
 template <class X, class Y, int V, bool kBack>
 RingShape ring_shape(int64_t c, int64_t n)
 {
-    RingShape s{std::max(64, lanes_of(c, kRingLane)), 0, 0};
+    RingShape s{lanes_of_block(std::max<int64_t>(c, 64 * kRingLane), kRingLane, 64), 0, 0};
     const bool faster = V < 4 ? c * static_cast<int64_t>(sizeof(X)) >= 1024
                         : kBack ? sizeof(X) == 2 && c > 1024 && n * c >= kRingBack
                                 : c > 1024;
@@ -1073,7 +1091,7 @@ RingShape ring_shape(int64_t c, int64_t n)
 }
 // Blocks of a ring kernel that an SM holds: its registers' limit, and the shared memory's.
 template <class K>
-int ring_blocks(std::atomic<int> (&known)[11], K kernel, const RingShape& s)
+int ring_blocks(std::atomic<int> (&known)[kGroupKinds], K kernel, const RingShape& s)
 {
     return static_cast<int>(std::max<size_t>(1, std::min<size_t>(resident(known, kernel, s.G, s.G + 32, 0), 227 * 1024 / (s.smem + sizeof(Ring) + 1024))));
 }
@@ -1084,7 +1102,7 @@ cudaError_t run_ln_ring(const Forward& F, const RingShape& g)
     auto* kernel = k_ln_ring<X, Y, V, kEven, kT>;
     cudaError_t e = allow_smem(kernel, g.smem);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> known[11];
+    static std::atomic<int> known[kGroupKinds];
     const int64_t blocks = std::min<int64_t>((F.n + kRingRows - 1) / kRingRows,
                                              static_cast<int64_t>(ring_blocks(known, kernel, g)) * num_sms());
     return launch_smem(kernel, dim3(static_cast<unsigned>(blocks)), dim3(g.G + 32), g.smem, F.s, static_cast<const X*>(F.x), F.r,
@@ -1170,11 +1188,11 @@ template <class X, class Y, int V, int L, int R, bool kEven>
 cudaError_t run_grad_lane(const Backward& B, int want, int64_t& parts)
 {
     auto* kernel = k_ln_grad<X, Y, V, L, R, kEven>;
-    const int G = lanes_of(B.c, L), threads = std::max(kLnBlock, G), groups = threads / G;
+    const int G = lanes_of_block(B.c, L, kLnBlock), threads = std::max(kLnBlock, G), groups = threads / G;
     const size_t smem = sizeof(float) * L * (groups > 1 ? 2 * threads : G);   // column sums, or gamma
     cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> known[11];
+    static std::atomic<int> known[kGroupKinds];
     parts = std::min<int64_t>(std::min<int64_t>(parts, back_blocks(B.n, groups)),
                               static_cast<int64_t>(resident(known, kernel, G, threads, smem)) * num_sms());
     return launch_smem(kernel, dim3(static_cast<unsigned>(parts)), dim3(threads), smem, B.s, static_cast<const Y*>(B.dy),
@@ -1188,7 +1206,7 @@ cudaError_t run_grad_ring(const Backward& B, const RingShape& g, int want, int64
     auto* kernel = k_ln_grad_ring<X, Y, V, kEven, kT>;
     cudaError_t e = allow_smem(kernel, g.smem);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> known[11];
+    static std::atomic<int> known[kGroupKinds];
     parts = std::min<int64_t>(std::min<int64_t>(parts, back_blocks(B.n, kBackRows)),
                               static_cast<int64_t>(ring_blocks(known, kernel, g)) * num_sms());
     return launch_smem(kernel, dim3(static_cast<unsigned>(parts)), dim3(g.G + 32), g.smem, B.s, static_cast<const Y*>(B.dy),
@@ -1235,7 +1253,7 @@ cudaError_t run_ln_grad(const Backward& B)
                 e = even ? run_grad_ring<X, Y, V, (V > 1), 512>(B, g, want, parts) : run_grad_ring<X, Y, V, false, 512>(B, g, want, parts);
             else if (V < 4 && B.c <= static_cast<int64_t>(kMaxBackGroup) * 8)
                 e = run_grad_lane<X, Y, V, 8, 1, false>(B, want, parts);
-            else if (V > 1 && B.c % (lanes_of(B.c, 16) * V) == 0)
+            else if (V > 1 && B.c % (lanes_of_block(B.c, 16, kLnBlock) * V) == 0)
                 e = run_grad_lane<X, Y, V, 16, R, (V > 1)>(B, want, parts);
             else
                 e = run_grad_lane<X, Y, V, 16, R, false>(B, want, parts);

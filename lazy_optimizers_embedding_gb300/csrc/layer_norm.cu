@@ -1067,9 +1067,12 @@ cudaError_t run_ln_lane(const Forward& F)
 //   30 back; 5000 x 1111: 12 against 21, 23 against 48).
 //   Packed, forward: rows that registers would spread over several warps, from 1025 columns
 //   (65536 x 2048 bf16: 84 against 95 us, 16 x 4096: 3.2 against 4.5; 65536 x 1024: 54 against 44).
-//   Packed, back: long bf16 rows, where there are 16 Mi values of them (16384 x 2048: 46 against 56 us,
-//   4096 x 8192: 55 against 66, 4096 x 4096: 31.5 against 32.7; 4096 x 2048: 18.7 against 17.1, 1000
-//   x 8192: 23 against 21; fp32, whose registers hold half as many rows, 65536 x 2048: 317 against 275).
+//   Packed, back: long rows with a bf16 side, where there are 16 Mi values of them (bf16 16384 x 2048: 46
+//   against 56 us, 4096 x 8192: 55 against 66, 4096 x 4096: 31.5 against 32.7, but 4096 x 2048: 18.7
+//   against 17.1, 1000 x 8192: 23 against 21; fp32 and bf16 16384 x 2560: 73 against 114); of fp32
+//   alone, whose registers hold half as many rows, those past 4096 columns (8192 x 5120: 98 against 134)
+//   or that leave over a quarter of the registers' lanes idle (24480 x 1208: 80 against 94; but
+//   20000 x 1536: 83 against 82, 8192 x 4096: 121 against 79).
 constexpr int64_t kRingBack = 16 << 20;
 struct RingShape {
     int G, stages;
@@ -1080,7 +1083,8 @@ RingShape ring_shape(int64_t c, int64_t n)
 {
     RingShape s{lanes_of_block(std::max<int64_t>(c, 64 * kRingLane), kRingLane, 64), 0, 0};
     const bool faster = V < 4 ? c * static_cast<int64_t>(sizeof(X)) >= 1024
-                        : kBack ? sizeof(X) == 2 && c > 1024 && n * c >= kRingBack
+                        : kBack ? c > 1024 && n * c >= kRingBack &&
+                                      (sizeof(X) == 2 || sizeof(Y) == 2 || c > 4096 || c < 12 * lanes_of(c, 16))
                                 : c > 1024;
     if (!faster || c > static_cast<int64_t>(kMaxBackGroup) * kRingLane) return s;
     const size_t round = ring_round<X, Y, kBack>(c);

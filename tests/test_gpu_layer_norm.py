@@ -344,3 +344,14 @@ def test_rows_of_pairs(cuda_lib, n, c, shift, xt, yt):
     k.run()
     assert int(k.err.item()) == 0
     k.compare()
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("n,c", [(16700, 1048), (6600, 2560), (4100, 4104), (3300, 5120)])
+def test_many_long_rows(cuda_lib, n, c, xt, yt):
+    """Enough long rows for the ring backward, groups of 72 to 320 lanes."""
+    import torch
+    k = Case(torch, cuda_lib, n, c, xt, yt)
+    k.run()
+    assert int(k.err.item()) == 0
+    k.compare()

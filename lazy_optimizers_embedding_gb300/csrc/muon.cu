@@ -711,20 +711,25 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
                     }
                     tma_store_commit();
                 }
-                if (P == 3 && image) {   // hi and lo fill the set: the image follows when they have left
-                    if (head) tma_store_read<0>();
-                    all_of(id, kGroup, true);
+                if (P == 3 && image) {
+                    // hi and lo fill the set: the image follows when they have left, or (a split tile, the
+                    // block's only one) goes by way of the stages, whose sums every warp has read
+                    const uint32_t by = kSplit > 1 ? data : at;
+                    if (kSplit == 1) {
+                        if (head) tma_store_read<0>();
+                        all_of(id, kGroup, true);
+                    }
 #pragma unroll
                     for (int p = 0; p < (P == 3 && kSym ? 8 : 0); ++p) {
-                        put_image(at, rowl, p, khi[p]);
-                        put_image(at + S::kSubBytes, rowl, p, klo[p]);
+                        put_image(by, rowl, p, khi[p]);
+                        put_image(by + S::kSubBytes, rowl, p, klo[p]);
                     }
                     fence_async_proxy();
                     all_of(id, kGroup, true);
                     if (head) {
                         for (int q = 0; q < kBM / kBox; ++q) {
-                            tma_store(&maps.whi, at + q * kBoxBytes, row0 + q * kBox, col, mat);
-                            tma_store(&maps.wlo, at + S::kSubBytes + q * kBoxBytes, row0 + q * kBox, col, mat);
+                            tma_store(&maps.whi, by + q * kBoxBytes, row0 + q * kBox, col, mat);
+                            tma_store(&maps.wlo, by + S::kSubBytes + q * kBoxBytes, row0 + q * kBox, col, mat);
                         }
                         tma_store_commit();
                     }

@@ -1,10 +1,13 @@
-"""Thin ctypes binding of libsparseopt (include/sparseopt.h).
+"""Thin binding of libsparseopt (include/sparseopt.h).
 
 Argument marshalling only: every function passes tensor data pointers, sizes and
 the current CUDA stream to the C entry point of the same name and returns its
-status code.  All work runs in the library's kernels; PyTorch only supplies the
-device memory and the stream.  There is no fallback: if the library is not
-built, importing this module raises.
+status code: by ctypes or, for the operators around the table step, whose smallest
+calls take less time on the GPU than ctypes does, by the compiled module _pycall
+(ctypes takes what that leaves: other streams, pointers as integers, arguments that
+are refused).  All work runs in the library's kernels; PyTorch only supplies the
+device memory and the stream.  There is no fallback: if the library or the module is
+not built, importing this module raises.
 """
 from __future__ import annotations
 
@@ -78,6 +81,8 @@ def _load():
     path = _build.LIB
     if not os.path.exists(path):
         raise ImportError(f"libsparseopt.so is not built ({path}); run __graft_entry__.build()")
+    if not os.path.exists(_build.PYCALL):
+        raise ImportError(f"_pycall.so is not built ({_build.PYCALL}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I64, INT, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     sig = {
@@ -120,6 +125,9 @@ def _load():
 
 
 LIB = _load()
+from . import _pycall  # noqa: E402  (needs the library)
+
+_pycall.configs(NsConfig, MuonConfig)
 EXPORTED = ("sparse_workspace_size", "sparse_status_string", "sparse_canonicalize", "sparse_csr_to_coo",
             "sparse_coo_to_csr", "sparse_row_coo_to_csr", "sparse_adam_step", "sparse_adam_table_step",
             "sparse_sgd_step", "sparse_sgd_table_step", "sparse_canonicalize_static_ws", "sparse_profile_enable",
@@ -327,6 +335,9 @@ def sparse_layer_norm_workspace_size(n: int, c: int) -> int:
 
 def sparse_layer_norm(x, r, c, idx, n, gamma, beta, eps, y, mean, rstd, d_err, stream=None) -> int:
     """Types are those of x and y; idx, gamma, beta, mean and rstd may be None."""
+    code = _pycall.layer_norm(x, r, c, idx, n, gamma, beta, eps, y, mean, rstd, d_err, stream)
+    if code is not None:
+        return code
     xp, xt = _typed(x, "x")
     yp, yt = _typed(y, "y")
     return LIB.sparse_layer_norm(xp, xt, int(r), int(c), _ptr(idx, torch.int64, "idx"), int(n),
@@ -337,6 +348,9 @@ def sparse_layer_norm(x, r, c, idx, n, gamma, beta, eps, y, mean, rstd, d_err, s
 
 def sparse_layer_norm_grad(dy, x, r, c, idx, n, gamma, mean, rstd, dx, dgamma, dbeta, ws, d_err, stream=None) -> int:
     """idx, gamma, dgamma and dbeta may be None."""
+    code = _pycall.layer_norm_grad(dy, x, r, c, idx, n, gamma, mean, rstd, dx, dgamma, dbeta, ws, d_err, stream)
+    if code is not None:
+        return code
     wp, wb = _ws(ws)
     yp, yt = _typed(dy, "dy")
     xp, xt = _typed(x, "x")
@@ -352,6 +366,9 @@ def sparse_expert_workspace_size(n: int, k: int, experts: int) -> int:
 
 
 def sparse_expert_sort(expert, n, k, experts, offsets, src, pos, ws, d_err, stream=None) -> int:
+    code = _pycall.expert_sort(expert, n, k, experts, offsets, src, pos, ws, d_err, stream)
+    if code is not None:
+        return code
     wp, wb = _ws(ws)
     return LIB.sparse_expert_sort(_ptr(expert, torch.int64, "expert"), int(n), int(k), int(experts),
                                   _ptr(offsets, torch.int64, "offsets"), _ptr(src, torch.int32, "src"),
@@ -360,6 +377,9 @@ def sparse_expert_sort(expert, n, k, experts, offsets, src, pos, ws, d_err, stre
 
 
 def sparse_expert_dispatch(x, n, k, c, pos, offsets, experts, xs, d_err, stream=None) -> int:
+    code = _pycall.expert_dispatch(x, n, k, c, pos, offsets, experts, xs, d_err, stream)
+    if code is not None:
+        return code
     xp, xt = _typed(x, "x")
     return LIB.sparse_expert_dispatch(xp, xt, int(n), int(k), int(c), _ptr(pos, torch.int32, "pos"),
                                       _ptr(offsets, torch.int64, "offsets"), int(experts), _typed(xs, "xs", x)[0],
@@ -368,6 +388,9 @@ def sparse_expert_dispatch(x, n, k, c, pos, offsets, experts, xs, d_err, stream=
 
 def sparse_expert_combine(ys, n, k, c, pos, weights, y, d_err, stream=None) -> int:
     """weights may be None (ones: the gradient of sparse_expert_dispatch)."""
+    code = _pycall.expert_combine(ys, n, k, c, pos, weights, y, d_err, stream)
+    if code is not None:
+        return code
     yp, yt = _typed(ys, "ys")
     return LIB.sparse_expert_combine(yp, yt, int(n), int(k), int(c), _ptr(pos, torch.int32, "pos"),
                                      _ptr(weights, torch.float32, "weights"), _typed(y, "y", ys)[0],
@@ -377,6 +400,9 @@ def sparse_expert_combine(ys, n, k, c, pos, weights, y, d_err, stream=None) -> i
 def sparse_expert_combine_grad(dy, ys, n, k, c, pos, offsets, experts, weights, dys, dweights, d_err,
                                stream=None) -> int:
     """weights (ones) and dweights (not wanted) may be None."""
+    code = _pycall.expert_combine_grad(dy, ys, n, k, c, pos, offsets, experts, weights, dys, dweights, d_err, stream)
+    if code is not None:
+        return code
     yp, yt = _typed(ys, "ys")
     return LIB.sparse_expert_combine_grad(_typed(dy, "dy", ys)[0], yp, yt, int(n), int(k), int(c),
                                           _ptr(pos, torch.int32, "pos"), _ptr(offsets, torch.int64, "offsets"),
@@ -390,6 +416,9 @@ def sparse_muon_workspace_size(batch: int, r: int, c: int, products: int) -> int
 
 
 def sparse_orthogonalize(u, batch, r, c, cfg: NsConfig, out, ws, d_err, stream=None) -> int:
+    code = _pycall.orthogonalize(u, batch, r, c, cfg, out, ws, d_err, stream)
+    if code is not None:
+        return code
     wp, wb = _ws(ws)
     up, ut = _typed(u, "u")
     op, ot = _typed(out, "out")
@@ -398,6 +427,9 @@ def sparse_orthogonalize(u, batch, r, c, cfg: NsConfig, out, ws, d_err, stream=N
 
 
 def sparse_muon_step(w, buf, g, batch, r, c, cfg: MuonConfig, ws, d_err, stream=None) -> int:
+    code = _pycall.muon_step(w, buf, g, batch, r, c, cfg, ws, d_err, stream)
+    if code is not None:
+        return code
     wp, wb = _ws(ws)
     gp, gt = _typed(g, "g")
     return LIB.sparse_muon_step(_ptr(w, torch.float32, "w"), _ptr(buf, torch.float32, "buf"), gp, gt, int(batch),

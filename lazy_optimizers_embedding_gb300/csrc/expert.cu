@@ -323,14 +323,14 @@ __device__ __forceinline__ void slot_rows(const T* (&row)[J], const T* rows, int
 }
 
 // A lane holds R accesses of its token's sum while the slots' rows go by, J at a time.
-template <class T, int V>
+template <class T, int V, int J>
 __global__ void __launch_bounds__(kExBlock) k_expert_combine(const T* __restrict__ ys, int64_t n, int k, int c,
                                                              const int32_t* __restrict__ pos,
                                                              const float* __restrict__ w, T* __restrict__ y, int G,
                                                              int32_t* d_err)
 {
     pdl_wait();   // writes a caller output
-    constexpr int J = 4, R = V < 4 ? 4 : 2;
+    constexpr int R = V < 4 ? 4 : 2;
     const int gl = threadIdx.x & (G - 1);
     const int64_t group = static_cast<int64_t>(blockIdx.x) * (kExBlock / G) + threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kExBlock / G);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ 
                                                           float* __restrict__ dw, int32_t* d_err)
 {
     pdl_wait();   // writes caller outputs
-    constexpr int J = 2, R = V < 4 ? 8 : 4, kMany = 8;
+    constexpr int J = 2, R = V < 4 ? 6 : 4, kMany = 8;   // (8 narrow accesses, one block an SM less: 105 against 92 us at 26775 x 8 x 393 bf16)
     const int lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kExWarps + (threadIdx.x >> 5);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kExWarps;
@@ -561,15 +561,24 @@ cudaError_t expert_dispatch(const void* x, int is_bf16, int64_t n, int64_t k, in
     return run_dispatch<uint16_t>(x, n, k, c, pos, end, xs, d_err, s);
 }
 
+template <class T, int V, int J>
+static cudaError_t run_combine_j(const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos, const float* w,
+                                 void* y, int32_t* d_err, cudaStream_t s)
+{
+    const int G = lanes_for(c / V, V < 4 ? 4 : 2);
+    static const int most = resident(k_expert_combine<T, V, J>);
+    SO_PROFILE("expert_combine", s);
+    return launch(k_expert_combine<T, V, J>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
+                  static_cast<const T*>(ys), n, static_cast<int>(k), static_cast<int>(c), pos, w, static_cast<T*>(y), G, d_err);
+}
+// As many slots' rows at a time as tokens have, up to four (25986 x 1 x 269 bf16: 13.7 us, by four 23.6; 32768 x 2 x 4096 bf16 121, by four 139).
 template <class T, int V>
 static cudaError_t run_combine(const void* ys, int64_t n, int64_t k, int64_t c, const int32_t* pos, const float* w,
                                void* y, int32_t* d_err, cudaStream_t s)
 {
-    const int G = lanes_for(c / V, V < 4 ? 4 : 2);
-    static const int most = resident(k_expert_combine<T, V>);
-    SO_PROFILE("expert_combine", s);
-    return launch(k_expert_combine<T, V>, dim3(row_blocks(most, n, G)), dim3(kExBlock), s,
-                  static_cast<const T*>(ys), n, static_cast<int>(k), static_cast<int>(c), pos, w, static_cast<T*>(y), G, d_err);
+    if (k == 1) return run_combine_j<T, V, 1>(ys, n, k, c, pos, w, y, d_err, s);
+    if (k == 2) return run_combine_j<T, V, 2>(ys, n, k, c, pos, w, y, d_err, s);
+    return run_combine_j<T, V, 4>(ys, n, k, c, pos, w, y, d_err, s);
 }
 
 cudaError_t expert_combine(const void* ys, int is_bf16, int64_t n, int64_t k, int64_t c, const int32_t* pos,

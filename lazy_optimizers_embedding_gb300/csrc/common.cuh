@@ -68,14 +68,16 @@ inline cudaError_t launch_smem(void (*kernel)(P...), dim3 grid, dim3 block, size
 }
 
 
-// Lets a kernel have `bytes` of dynamic shared memory on the current device.  Said on every call that
-// needs it: another device, or the context after a reset, does not know.  (48 KB need no saying, but
-// hold the kernel's own arrays too: 8 KB at most.)
+// Lets a kernel have `most` bytes of dynamic shared memory on the current device: the most that any of its
+// launches has.  The limit belongs to the kernel, so one that followed a call's own size would be lowered
+// under another host thread's launch, which is then refused.  Said on every call that needs it (`bytes`): another
+// device, or the context after a reset, does not know.  (48 KB need no saying, but hold the kernel's
+// own arrays too: 8 KB at most.)
 template <class K>
-inline cudaError_t allow_smem(K kernel, size_t bytes)
+inline cudaError_t allow_smem(K kernel, size_t bytes, size_t most)
 {
     if (bytes <= 40 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
 }
 
 constexpr unsigned kFull = 0xffffffffu;

@@ -38,6 +38,7 @@ constexpr int kExWarps = kExBlock / 32;
 constexpr int64_t kExTile = 1024;          // slots of a tile at least
 constexpr int64_t kSortBlocks = 512;       // tiles at most
 constexpr int64_t kClusterSlots = 16384;   // slots that one cluster sorts
+constexpr size_t kSortSmem = 160 * 1024;   // dynamic shared memory of k_expert_sort at most
 constexpr int kHeld = 4;                   // rows of 32 slots whose experts a warp keeps between its two passes
 
 // Blocks of `threads` threads (kernel k_expert_sort), each with `tile` slots; one cluster of them or
@@ -55,7 +56,7 @@ SortShape sort_shape(int64_t slots, int64_t experts)
     // as many warps as have kHeld rows of 32 slots, and as their counts leave room for
     auto threads_for = [&](int64_t tile) {
         int t = 64;
-        while (t < 1024 && t * kHeld < tile && sort_smem(2 * t, experts) <= 160 * 1024) t *= 2;
+        while (t < 1024 && t * kHeld < tile && sort_smem(2 * t, experts) <= kSortSmem) t *= 2;
         return t;
     };
     if (slots <= kClusterSlots) {
@@ -518,7 +519,7 @@ cudaError_t expert_sort(const int64_t* expert, int64_t slots, int64_t experts, i
         e = launch(k_expert_scan, dim3((E + kExWarps - 1) / kExWarps), dim3(kExBlock), s, counts, E, S.blocks, totals);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t ready = allow_smem(k_expert_sort, sort_smem(S.threads, experts));
+    const cudaError_t ready = allow_smem(k_expert_sort, sort_smem(S.threads, experts), kSortSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S.blocks);

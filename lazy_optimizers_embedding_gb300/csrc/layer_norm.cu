@@ -34,7 +34,7 @@ namespace so {
 
 namespace {
 
-constexpr size_t kRingSmem = 200 * 1024;
+constexpr size_t kRingSmem = 200 * 1024;   // dynamic shared memory that a launch has at most
 constexpr int kLnBlock = 256;           // threads of a block (of the groups that are no wider)
 constexpr int kMaxBackGroup = 512;      // backward: lanes of a group at most
 constexpr int64_t kLnParts = 1024;      // blocks of the backward kernel at most, hence partial column sums
@@ -1050,7 +1050,7 @@ cudaError_t run_ln_lane(const Forward& F)
     auto* kernel = k_ln<X, Y, V, L, kEven>;
     const int G = lanes_of(F.c, L), groups = kLnBlock / G;
     const int64_t row = (F.c + G * V - 1) / (G * V) * (G * V);
-    cudaError_t e = allow_smem(kernel, sizeof(float) * 2 * row);
+    cudaError_t e = allow_smem(kernel, sizeof(float) * 2 * row, sizeof(float) * 2 * kLnBlock * L);
     if (e != cudaSuccess) return e;
     static std::atomic<int> known[kGroupKinds];
     const int blocks = static_cast<int>(std::min<int64_t>(
@@ -1104,7 +1104,7 @@ template <class X, class Y, int V, bool kEven, int kT>
 cudaError_t run_ln_ring(const Forward& F, const RingShape& g)
 {
     auto* kernel = k_ln_ring<X, Y, V, kEven, kT>;
-    cudaError_t e = allow_smem(kernel, g.smem);
+    cudaError_t e = allow_smem(kernel, g.smem, kRingSmem);
     if (e != cudaSuccess) return e;
     static std::atomic<int> known[kGroupKinds];
     const int64_t blocks = std::min<int64_t>((F.n + kRingRows - 1) / kRingRows,
@@ -1129,7 +1129,7 @@ template <class X, class Y, int V, int R, bool kHeld>
 cudaError_t run_ln_wide(const Forward& F, size_t smem)
 {
     auto* kernel = k_ln_wide<X, Y, V, R, kHeld>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    const cudaError_t e = allow_smem(kernel, smem, kRingSmem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = std::min<int64_t>((F.n + R - 1) / R, wide_blocks(kernel, smem));
     return launch_smem(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMaxBackGroup), smem, F.s, static_cast<const X*>(F.x),
@@ -1194,7 +1194,7 @@ cudaError_t run_grad_lane(const Backward& B, int want, int64_t& parts)
     auto* kernel = k_ln_grad<X, Y, V, L, R, kEven>;
     const int G = lanes_of_block(B.c, L, kLnBlock), threads = std::max(kLnBlock, G), groups = threads / G;
     const size_t smem = sizeof(float) * L * (groups > 1 ? 2 * threads : G);   // column sums, or gamma
-    cudaError_t e = allow_smem(kernel, smem);
+    cudaError_t e = allow_smem(kernel, smem, sizeof(float) * L * kMaxBackGroup);
     if (e != cudaSuccess) return e;
     static std::atomic<int> known[kGroupKinds];
     parts = std::min<int64_t>(std::min<int64_t>(parts, back_blocks(B.n, groups)),
@@ -1208,7 +1208,7 @@ template <class X, class Y, int V, bool kEven, int kT>
 cudaError_t run_grad_ring(const Backward& B, const RingShape& g, int want, int64_t& parts)
 {
     auto* kernel = k_ln_grad_ring<X, Y, V, kEven, kT>;
-    cudaError_t e = allow_smem(kernel, g.smem);
+    cudaError_t e = allow_smem(kernel, g.smem, kRingSmem);
     if (e != cudaSuccess) return e;
     static std::atomic<int> known[kGroupKinds];
     parts = std::min<int64_t>(std::min<int64_t>(parts, back_blocks(B.n, kBackRows)),
@@ -1222,7 +1222,7 @@ template <class X, class Y, int V, bool kHeld>
 cudaError_t run_grad_wide(const Backward& B, size_t smem)
 {
     auto* kernel = k_ln_grad_wide<X, Y, V, kHeld>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    const cudaError_t e = allow_smem(kernel, smem, kRingSmem);
     if (e != cudaSuccess) return e;
     return launch_smem(kernel, dim3(static_cast<unsigned>(std::min<int64_t>(B.n, wide_blocks(kernel, smem)))), dim3(kMaxBackGroup), smem,
                        B.s, static_cast<const Y*>(B.dy), static_cast<const X*>(B.x), B.r, B.c, B.idx, B.n, B.gamma,

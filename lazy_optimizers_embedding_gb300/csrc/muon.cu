@@ -848,7 +848,7 @@ cudaError_t run_product(const char* name, const Maps& maps, Product Q, int64_t b
     Q.tiles = tiles_of(Q.m, Q.n, kBM * kPair, BN, S::kSym);
     Q.all = Q.tiles * batch;
     Q.cols_of_tiles = static_cast<int>((Q.n + BN - 1) / BN);
-    const cudaError_t ready = allow_smem(kernel, S::kSmem);
+    const cudaError_t ready = allow_smem(kernel, S::kSmem, S::kSmem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((kSplit > 1 ? Q.all : std::min<int64_t>(Q.all, num_sms() / kPair)) * kCluster));

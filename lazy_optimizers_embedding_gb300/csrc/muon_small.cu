@@ -513,7 +513,7 @@ int clusters_at_once(int blocks)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (allow_smem((k_muon_cluster<true, kOnePart>), kSmallSmem) != cudaSuccess ||
+        if (allow_smem((k_muon_cluster<true, kOnePart>), kSmallSmem, kSmallSmem) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, (k_muon_cluster<true, kOnePart>), &cfg) != cudaSuccess) n = 0;
         n = std::max(n, 1);
         known[blocks].store(n, std::memory_order_relaxed);
@@ -592,7 +592,7 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
                    : F.fold > 1     ? (vec ? k_muon_cluster<true, kParts> : k_muon_cluster<false, kParts>)
                                     : (vec ? k_muon_cluster<true, kOnePart> : k_muon_cluster<false, kOnePart>);
     const uint32_t smem = kSmallSmem + (Q.m <= kRestRows ? kRestBytes : 0);   // (what is not asked for is cache)
-    const cudaError_t ready = allow_smem(kernel, smem);
+    const cudaError_t ready = allow_smem(kernel, smem, smem);
     if (ready != cudaSuccess) return ready;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M.batch * blocks));

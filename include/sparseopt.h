@@ -487,8 +487,10 @@ size_t sparse_muon_workspace_size(int64_t batch, int64_t r, int64_t c, int produ
 
 /*
  * sparse_orthogonalize -- out = Newton-Schulz of every r x c matrix of u.
- *   u, out [batch, r, c]: fp32 or bf16 each.  An element that is NaN or infinite (or
- *   values whose sum of squares fp32 cannot hold, about 1e18) sets SPARSE_ERR_NON_FINITE.
+ *   u, out [batch, r, c]: fp32 or bf16 each.  An element that is NaN or infinite sets
+ *   SPARSE_ERR_NON_FINITE, and so may values whose sum of squares nears what fp32 holds
+ *   (norms from about 5e17 on).  Small norms are taken at any scale, and a matrix of
+ *   zeros gives zeros, with eps = 0 too.
  *   ws: sparse_muon_workspace_size() bytes, 256-byte aligned.
  */
 sparse_status_t sparse_orthogonalize(const void* u, sparse_dtype_t u_type, int64_t batch, int64_t r, int64_t c,

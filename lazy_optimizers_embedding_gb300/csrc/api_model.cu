@@ -2,6 +2,7 @@
 // step (declared in include/sparseopt.h): argument validation, workspace
 // carving and the choice of 16-byte accesses.  No host synchronisation.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -110,7 +111,9 @@ so::MuonParams muon_params(int64_t batch, int64_t r, int64_t c, const sparse_ns_
     M.a = static_cast<float>(ns.a);
     M.b = static_cast<float>(ns.b);
     M.c = static_cast<float>(ns.c);
-    M.eps = static_cast<float>(ns.eps);
+    auto narrow = [](double x) { return static_cast<float>(std::min(x, static_cast<double>(FLT_MAX))); };
+    M.eps = narrow(ns.eps);
+    M.eps_raised = narrow(ns.eps * 0x1p100);
     M.steps = ns.steps;
     M.products = ns.products;
     M.d_err = d_err;

@@ -401,7 +401,7 @@ struct MuonParams {
     float momentum;
     int nesterov;
     int64_t batch, r, cols;
-    float a, b, c, eps;
+    float a, b, c, eps, eps_raised;   // eps times 2^100 too (muon.cuh)
     int steps, products;
     void* out;            // the orthogonal update, or
     int out_bf16;

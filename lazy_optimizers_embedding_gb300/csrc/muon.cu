@@ -42,19 +42,21 @@ constexpr int kGroup = 128;                     // threads of an epilogue group
 constexpr int64_t kNormParts = 1024;            // partial sums of squares of a matrix at most
 
 // ------------------------------------------------------------------- start
-// Sums of squares of one matrix's pieces; a sum that is not finite is reported
-// before anything is written.  E: values of an access.
+// Sums of squares of one matrix's pieces, where they are small (a matrix of zeros among them) also of the
+// values times kRaise; a sum that is not finite is reported before anything is written.  E: values
+// of an access.
 template <int E>
-__global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int parts, float* __restrict__ part,
+__global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int parts, float2* __restrict__ part,
                                                           int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and the error word only
     __shared__ float tmp[2 * 32];
     const int mat = static_cast<int>(blockIdx.x) / parts, p = static_cast<int>(blockIdx.x) % parts;
     const int64_t base = mat * size, step = static_cast<int64_t>(parts) * kMuonBlock * E;
+    const int64_t first = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * E;
     constexpr int R = E == 1 ? 8 : 4;   // accesses a lane requests at once
-    float s[1] = {0.0f};
-    for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * E; i < size; i += R * step) {
+    float s[1] = {0.0f}, raised[1] = {0.0f};
+    for (int64_t i = first; i < size; i += R * step) {
         float u[R][E], nb[E];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
@@ -70,8 +72,18 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
             for (int e = 0; e < E; ++e) s[0] = fmaf(u[q][e], u[q][e], s[0]);
     }
     group_sum<1>(s, kMuonBlock, tmp, 0);
+    if (s[0] < kSmallSquares) {   // the same for the whole block
+#pragma unroll 1
+        for (int64_t i = first; i < size; i += step) {
+            float u[E], nb[E];
+            read_u<E>(U, base + i, u, nb);
+#pragma unroll
+            for (int e = 0; e < E; ++e) raised[0] = fmaf(u[e] * kRaise, u[e] * kRaise, raised[0]);
+        }
+        group_sum<1>(raised, kMuonBlock, tmp, 1);
+    }
     if (threadIdx.x == 0) {
-        part[blockIdx.x] = s[0];
+        part[blockIdx.x] = make_float2(s[0], raised[0]);
         if (!isfinite(s[0] * static_cast<float>(parts))) set_error(d_err, SPARSE_ERR_NON_FINITE);   // nor may the whole overflow
     }
 }
@@ -81,7 +93,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
 // blocks are busy for less time with the scale, which each works out: 16 x 768 x 2048 bf16, 150 MB, 31
 // us; 4 accesses 36 us, 32 accesses 33 us).
 __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float* __restrict__ buf, int64_t size, int pieces,
-                                                                const float* __restrict__ part, int parts, float eps,
+                                                                const float2* __restrict__ part, int parts, float eps, float eps_raised,
                                                                 __half* __restrict__ hi, __half* __restrict__ lo,
                                                                 int c, int64_t ldn, const int32_t* d_err)
 {
@@ -91,11 +103,11 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
     const int mat = static_cast<int>(blockIdx.x) / pieces, p = static_cast<int>(blockIdx.x) % pieces;
     const int64_t base = mat * size, step = static_cast<int64_t>(pieces) * kMuonBlock * 8;
     const int64_t rows = size / c;
-    float scale = -1.0f;
+    Start st{0.0f, 0.0f};   // not worked out yet
     for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += step) {
         float u[8], nb[8];
         if (i < size) read_u<8>(U, base + i, u, nb);
-        if (scale < 0.0f) scale = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, sums);   // while those are on their way
+        if (st.raise == 0.0f) st = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, eps_raised, sums);   // while those are on their way
         if (i >= size) continue;
         if (buf) Pack<float, 8>::put(buf + base + i, nb);
         const int64_t to = ldn == c ? base + i : (mat * rows + i / c) * ldn + i % c;
@@ -104,7 +116,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
         __half2* ll = reinterpret_cast<__half2*>(&l);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float a = u[2 * e] * scale, b = u[2 * e + 1] * scale;
+            const float a = u[2 * e] * st.raise * st.scale, b = u[2 * e + 1] * st.raise * st.scale;
             hh[e] = __floats2half2_rn(a, b);
             const float2 f = __half22float2(hh[e]);
             ll[e] = __floats2half2_rn(a - f.x, b - f.y);
@@ -115,11 +127,12 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
 }
 
 // X = u / (|u| + eps), scaled and split, transposed where u is tall; the new momentum
-// buffer.  One 64 x 64 tile of u at a time, four values a thread.
+// buffer.  One 64 x 64 tile of u at a time, four values a thread.  (Five blocks an SM: with four the 640 tiles of
+// 2501 x 1003 go round twice, 12 us and not 10.)
 template <bool kVec>
-__global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __restrict__ buf, int64_t r, int64_t c,
+__global__ void __launch_bounds__(kMuonBlock, 5) k_muon_start(Update U, float* __restrict__ buf, int64_t r, int64_t c,
                                                            int tiles_c, int tiles, int ntiles,
-                                                           const float* __restrict__ part, int parts, float eps,
+                                                           const float2* __restrict__ part, int parts, float eps, float eps_raised,
                                                            __half* __restrict__ hi, __half* __restrict__ lo,
                                                            int64_t ldn, int tall, const int32_t* d_err)
 {
@@ -130,7 +143,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __re
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t m = tall ? c : r;
     int64_t have = -1;
-    float scale = 0.0f;
+    Start st{0.0f, 0.0f};
     // neighbouring tiles by one block: few matrices, whose scales it has to work out
     const int t1 = static_cast<int>(static_cast<int64_t>(ntiles) * (blockIdx.x + 1) / gridDim.x);
     for (int t = static_cast<int>(static_cast<int64_t>(ntiles) * blockIdx.x / gridDim.x); t < t1; ++t) {
@@ -139,7 +152,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __re
         const int64_t r0 = q / tiles_c * 64, c0 = q % tiles_c * 64;
         if (mat != have) {
             if (have >= 0) __syncthreads();   // the last sums have been read
-            scale = start_scale<kMuonBlock>(part + mat * parts, parts, eps, sums);
+            st = start_scale<kMuonBlock>(part + mat * parts, parts, eps, eps_raised, sums);
             have = mat;
         }
         float u[4][4];
@@ -164,7 +177,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start(Update U, float* __re
         for (int y = 0; y < 4; ++y) {
             const int64_t row = r0 + ty + 16 * y, col = c0 + 4 * tx;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[y][e] *= scale;
+            for (int e = 0; e < 4; ++e) u[y][e] = u[y][e] * st.raise * st.scale;
             if (tall) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) tile[ty + 16 * y][4 * tx + e] = u[y][e];
@@ -819,7 +832,7 @@ Layout muon_layout(int64_t batch, int64_t r, int64_t c, int asked)
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    L.part = take(sizeof(float) * static_cast<size_t>(batch * L.parts));
+    L.part = take(sizeof(float2) * static_cast<size_t>(batch * L.parts));
     for (int i = 0; i < 2; ++i)
         for (int h = 0; h < 2; ++h) L.x[i][h] = take(2 * static_cast<size_t>(batch * L.m * L.ldn));
     for (int h = 0; h < 2; ++h) {
@@ -982,7 +995,7 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
     if (encoder() == nullptr) return cudaErrorNotSupported;
     const Layout L = muon_layout(M.batch, M.r, M.cols, M.products);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    float* part = reinterpret_cast<float*>(base + L.part);
+    float2* part = reinterpret_cast<float2*>(base + L.part);
     const Update U{M.g, M.g_bf16, M.buf, M.momentum, M.nesterov};
     const int64_t size = M.r * M.cols;
     cudaError_t e;
@@ -1004,14 +1017,14 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
         if (values == 8 && M.r <= M.cols) {
             const int pieces = static_cast<int>(std::max<int64_t>(1, size / (kMuonBlock * 8 * 8)));
             e = launch(k_muon_start_flat, dim3(static_cast<unsigned>(M.batch * pieces)), dim3(kMuonBlock), s, U, M.buf, size,
-                       pieces, static_cast<const float*>(part), L.parts, M.eps, xhi, xlo, static_cast<int>(M.cols), L.ldn,
+                       pieces, static_cast<const float2*>(part), L.parts, M.eps, M.eps_raised, xhi, xlo, static_cast<int>(M.cols), L.ldn,
                        static_cast<const int32_t*>(M.d_err));
         } else {
             const int64_t tc = (M.cols + 63) / 64, tiles = (M.r + 63) / 64 * tc, all = tiles * M.batch;
             e = launch(values > 1 ? k_muon_start<true> : k_muon_start<false>,
                        dim3(static_cast<unsigned>(std::min<int64_t>(all, 8 * num_sms()))), dim3(kMuonBlock), s, U, M.buf,
                        M.r, M.cols, static_cast<int>(tc), static_cast<int>(tiles), static_cast<int>(all),
-                       static_cast<const float*>(part), L.parts, M.eps, xhi, xlo, L.ldn, M.r > M.cols ? 1 : 0,
+                       static_cast<const float2*>(part), L.parts, M.eps, M.eps_raised, xhi, xlo, L.ldn, M.r > M.cols ? 1 : 0,
                        static_cast<const int32_t*>(M.d_err));
         }
     }

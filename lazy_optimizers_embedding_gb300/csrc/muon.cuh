@@ -101,21 +101,37 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8])
     }
 }
 
-// Scale of one matrix from its `parts` sums of squares, by a block of kThreads threads (`tmp`: 64
-// words).  fp32: in fp64 the root and quotient alone held a block for 4 us.
+// Squares leave fp32 below about 1e-38, so a matrix whose squares sum to less than kSmallSquares (a norm
+// below 2^-40) is summed again with its values times kRaise, which the smallest fp32 value's
+// square survives too.
+constexpr float kSmallSquares = 0x1p-80f;
+constexpr float kRaise = 0x1p100f;
+
+// X = u raise scale: scale is 2^14 / (|u| raise + eps raise).  A matrix of zeros has scale 0, whatever eps.
+struct Start {
+    float raise, scale;
+};
+
+// The start of one matrix from its `parts` sums of squares (x, and raised y where x is small), by a block of
+// kThreads threads (`tmp`: 64 words).  fp32: in fp64 the root and quotient alone held a block for 4 us.
 template <int kThreads>
-__device__ __forceinline__ float start_scale(const float* part, int parts, float eps, float* tmp)
+__device__ __forceinline__ Start start_scale(const float2* part, int parts, float eps, float eps_raised, float* tmp)
 {
-    float s[1] = {0.0f};
-    for (int i = threadIdx.x; i < parts; i += kThreads) s[0] += part[i];
-    group_sum<1>(s, kThreads, tmp, 0);
-    return kScale / (sqrtf(s[0]) + eps);
+    float s[2] = {0.0f, 0.0f};
+    for (int i = threadIdx.x; i < parts; i += kThreads) {
+        const float2 q = part[i];
+        s[0] += q.x, s[1] += q.y;
+    }
+    group_sum<2>(s, kThreads, tmp, 0);
+    const bool small = s[0] < kSmallSquares;   // both sums at once: a branch between two kept a block 2 us longer
+    const float sum = small ? s[1] : s[0];
+    return {small ? kRaise : 1.0f, sum != 0.0f ? kScale / (sqrtf(sum) + (small ? eps_raised : eps)) : 0.0f};
 }
 
 // Whether the matrices take the cluster path, and that path, once the sums of squares are on
 // their way (`vec`: 16-byte accesses of the update).
 bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n);
-cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int parts, bool vec,
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* part, int parts, bool vec,
                          cudaStream_t s);
 
 }  // namespace so

@@ -116,8 +116,8 @@ struct Small {
     int fold;            // parts of a block's columns that lie below one another, 128 / fold rows each
     int slice;           // columns of a part, a multiple of 64
     int tall, steps;
-    float a, b, c, eps;
-    const float* part;
+    float a, b, c, eps, eps_raised;
+    const float2* part;
     int parts;
     float* buf;
     void* out;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     const bool blocked = (Q.w != nullptr) && read_error(Q.d_err) != 0;   // set before this kernel: the same for every block
 
     // X of the slice, scaled and split; the new momentum buffer
-    const float scale = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, sums);
+    const Start st = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, Q.eps_raised, sums);
     const int64_t base = mat * Q.size;
     // Groups of lanes take u's rows (X's, or its columns where u is tall), a lane four values at a time: a
     // whole warp, or as many lanes as such a row has use for.
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                     float left_over[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {   // 0 past `left`
-                        const float v = u[i][e] * scale;
+                        const float v = u[i][e] * st.raise * st.scale;
                         const __half q = __float2half_rn(v), ql = __float2half_rn(v - __half2float(q));
                         h[e] = bits_of(q), l[e] = bits_of(ql);
                         left_over[e] = v - __half2float(q) - __half2float(ql);
@@ -565,7 +565,7 @@ bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n)
     return f.fold > 0 && f.cost < 850 + batch * n * (m > 64 ? 29 : 16) / 1000;
 }
 
-cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part, int parts, bool vec, cudaStream_t s)
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* part, int parts, bool vec, cudaStream_t s)
 {
     Small Q{};
     Q.size = M.r * M.cols;
@@ -577,7 +577,7 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float* part
     Q.fold = F.fold;
     Q.slice = F.slice;
     Q.steps = M.steps;
-    Q.a = M.a, Q.b = M.b, Q.c = M.c, Q.eps = M.eps;
+    Q.a = M.a, Q.b = M.b, Q.c = M.c, Q.eps = M.eps, Q.eps_raised = M.eps_raised;
     Q.part = part;
     Q.parts = parts;
     Q.buf = M.buf;

@@ -1,0 +1,136 @@
+"""Newton-Schulz and the Muon step where they can go wrong: matrices without a norm or with a tiny one,
+values that are not finite and set error words on the path of matrices that no cluster holds, blocks that
+work on several tiles, long sums, arrays past 2^31 elements.
+
+Bounds, in the Frobenius norm relative to the result's.  A 64-bit simulation of the kernels' splits
+and roundings is off by at most 2.6e-3 with one product and 3.6e-5 with three over flat, decaying,
+low-rank and rank-one spectra, the largest of both for rank one (fp32 products: 1e-4); over the flat
+ones used here, 1.5e-3 and 5e-7.  Asserted: 5e-3 and 2e-5, as fp32 accumulation adds to both.  The unit
+rounds every one of K / 16 sums towards zero, by at most 2^-23 of it: with one product A is smaller by
+up to K 2^-27 of itself.  The result moves by at most twice that (x (a + b x^2 + c x^4) by
+|b x^3 + 2 c x^5| <= 1.3 for x up to 1.13, and later steps do not enlarge it about their fixed points).
+Rounding to bf16 adds 2^-9."""
+import pytest
+
+from gpu_harness import Guarded
+
+pytestmark = pytest.mark.gpu
+
+NS = (3.4445, -4.7750, 2.0315)
+TOL = {1: 5e-3, 3: 2e-5}
+DTYPES = {"f32": "float32", "bf16": "bfloat16"}
+
+
+def _formula(torch, u, eps=1e-7, steps=5):
+    """In 64 bits, on the device, by plain products."""
+    a, b, c = NS
+    u = u.double()
+    tall = u.shape[1] > u.shape[2]
+    x = u.transpose(1, 2) if tall else u
+    norm = (x * x).sum((1, 2), keepdim=True).sqrt() + eps
+    x = torch.where(norm > 0, x / norm, torch.zeros_like(x))
+    for _ in range(steps):
+        g = x @ x.transpose(1, 2)
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.transpose(1, 2) if tall else x
+
+
+def _off(got, ref):
+    d = (got.double() - ref).square().sum((1, 2)).sqrt()
+    return float((d / ref.square().sum((1, 2)).sqrt().clamp_min(1e-30)).max())
+
+
+class Case:
+    def __init__(self, torch, so, u, products, out_type="f32", eps=1e-7, shift=0, guarded=True):
+        self.torch, self.so, self.shape = torch, so, tuple(u.shape)
+        self.u = u
+        self.G = G = Guarded(seed=u.shape[1])
+        dt = getattr(torch, DTYPES[out_type])
+        self.out = G.zeros(u.numel() + shift, dt)[shift:].view(u.shape) if guarded else torch.zeros(u.shape, dtype=dt, device="cuda")
+        size = so.sparse_muon_workspace_size(*self.shape, products)
+        self.ws = G.empty(size, torch.uint8) if guarded else torch.empty(size, dtype=torch.uint8, device="cuda")
+        self.ws.fill_(255)
+        self.err = G.error_word()
+        self.cfg = so.NsConfig(a=NS[0], b=NS[1], c=NS[2], eps=eps, steps=5, products=products)
+
+    def run(self):
+        self.so.check(self.so.sparse_orthogonalize(self.u, *self.shape, self.cfg, self.out, self.ws, self.err))
+        self.G.check("orthogonalize")
+        return self.out
+
+
+class Step:
+    def __init__(self, torch, so, shape, g_type="f32", products=3, eps=1e-7, seed=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.torch, self.so, self.shape = torch, so, shape
+        self.G = G = Guarded(seed=shape[1])
+        rand = lambda: torch.randn(*shape, device="cuda", generator=gen)  # noqa: E731
+        self.w, self.buf = G.zeros(shape), G.zeros(shape)
+        self.w.copy_(0.1 * rand())
+        self.buf.copy_(rand())
+        self.g = G.zeros(shape, getattr(torch, DTYPES[g_type]))
+        self.g.copy_(rand())
+        self.ws = G.empty(so.sparse_muon_workspace_size(*shape, products), torch.uint8)
+        self.err = G.error_word()
+        self.cfg = so.MuonConfig(lr=0.02, momentum=0.95, weight_decay=0.1, scale=1.5, nesterov=1,
+                                 ns=so.NsConfig(a=NS[0], b=NS[1], c=NS[2], eps=eps, steps=5, products=products))
+
+    def run(self, err=None, stream=None):
+        self.so.check(self.so.sparse_muon_step(self.w, self.buf, self.g, *self.shape, self.cfg, self.ws,
+                                               self.err if err is None else err, stream))
+
+
+def _randn(torch, shape, seed=0, dtype="f32"):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, device="cuda", generator=g).to(getattr(torch, DTYPES[dtype]))
+
+
+# of a cluster; of the general path: wide, tall, wide with odd rows, tall with odd rows
+PATHS = [(3, 20, 30), (3, 300, 400), (3, 400, 300), (3, 201, 333), (3, 333, 201)]
+
+
+@pytest.mark.parametrize("products", [1, 3])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-60, 1e-7])
+@pytest.mark.parametrize("shape", PATHS)
+def test_a_matrix_of_zeros_gives_zeros(cuda_lib, shape, eps, products):
+    import torch
+    u = _randn(torch, shape)
+    u[1] = 0.0
+    k = Case(torch, cuda_lib, u, products, eps=eps)
+    got = k.run()
+    assert int(k.err.item()) == 0 and (got[1] == 0).all()
+    assert _off(got, _formula(torch, u, eps)) <= TOL[products]
+
+
+@pytest.mark.parametrize("products", [1, 3])
+@pytest.mark.parametrize("shape", PATHS)
+def test_a_norm_whose_square_fp32_cannot_hold(cuda_lib, shape, products):
+    """Down to values below the normal range; norms on both sides of 2^-40, where the sums change over."""
+    import torch
+    for scale, eps in ((1e-24, 0.0), (1e-24, 1e-30), (1e-24, 1e-23), (1e-30, 1e-40), (1e-36, 0.0), (1e-20, 0.0), (3e-15, 0.0),
+                       (1e-14, 1e-14), (1e-12, 0.0)):
+        u = _randn(torch, shape) * scale
+        k = Case(torch, cuda_lib, u, products, eps=eps)
+        got = k.run()
+        assert int(k.err.item()) == 0
+        assert _off(got, _formula(torch, u, eps)) <= TOL[products], (scale, eps)
+
+
+@pytest.mark.parametrize("products", [1, 3])
+@pytest.mark.parametrize("shape", PATHS)
+def test_a_step_without_gradient_only_decays(cuda_lib, shape, products):
+    import torch
+    k = Step(torch, cuda_lib, shape, products=products, eps=0.0)
+    k.g.zero_()
+    k.buf[1] = 0.0
+    k.g[2].copy_(_randn(torch, shape)[2] * 1e-24)
+    k.buf[2] = 0.0
+    w = k.w.double()
+    k.run()
+    k.G.check("muon step")
+    assert int(k.err.item()) == 0 and (k.buf[1] == 0).all()
+    keep = 1 - 0.02 * 0.1
+    assert float((k.w[1].double() - keep * w[1]).abs().max()) <= 2.0 ** -23 * float(w[1].abs().max())
+    o = _formula(torch, k.g.double() + 0.95 * k.buf.double(), 0.0)[2]
+    off = (k.w[2].double() - (keep * w[2] - 0.03 * o)).norm()
+    assert float(off) <= 0.03 * TOL[products] * float(o.norm()) + 2.0 ** -22 * float(w[2].norm() + 0.03 * o.norm())

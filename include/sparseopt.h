@@ -502,7 +502,9 @@ sparse_status_t sparse_orthogonalize(const void* u, sparse_dtype_t u_type, int64
  * matrices beside the table: an expert's, a projection's), in place.
  *   w, buf [batch, r, c] fp32 (buf starts at 0); g [batch, r, c] fp32 or bf16.
  *   A u that is not finite (as above) sets SPARSE_ERR_NON_FINITE, and neither w nor
- *   buf of any matrix is written; nor are they while *d_err is set.
+ *   buf of any matrix is written; nor are they while *d_err is set.  Whether it is, is
+ *   settled once for the whole step: a word that is set while the step runs (by a stream
+ *   that shares it) stops all of it or nothing.  SPARSE_ERR_INTERNAL leaves both undefined.
  */
 sparse_status_t sparse_muon_step(float* w, float* buf, const void* g, sparse_dtype_t g_type, int64_t batch, int64_t r,
                                  int64_t c, sparse_muon_config_t cfg, void* ws, size_t ws_bytes, int32_t* d_err,

@@ -47,9 +47,10 @@ constexpr int64_t kNormParts = 1024;            // partial sums of squares of a 
 // of an access.
 template <int E>
 __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size, int parts, float2* __restrict__ part,
-                                                          int32_t* d_err)
+                                                          uint32_t* verdict, int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and the error word only
+    if (blockIdx.x == 0 && threadIdx.x == 0) *verdict = kUndecided;
     __shared__ float tmp[2 * 32];
     const int mat = static_cast<int>(blockIdx.x) / parts, p = static_cast<int>(blockIdx.x) % parts;
     const int64_t base = mat * size, step = static_cast<int64_t>(parts) * kMuonBlock * E;
@@ -95,11 +96,12 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
 __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float* __restrict__ buf, int64_t size, int pieces,
                                                                 const float2* __restrict__ part, int parts, float eps, float eps_raised,
                                                                 __half* __restrict__ hi, __half* __restrict__ lo,
-                                                                int c, int64_t ldn, const int32_t* d_err)
+                                                                int c, int64_t ldn, uint32_t* verdict, const int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and optimizer state only
     __shared__ float sums[2 * 32];
-    if (buf != nullptr && read_error(d_err) != 0) return;   // set before this kernel: the same for every block
+    __shared__ bool goes;
+    if (threadIdx.x == 0) goes = buf == nullptr || step_goes(verdict, d_err);
     const int mat = static_cast<int>(blockIdx.x) / pieces, p = static_cast<int>(blockIdx.x) % pieces;
     const int64_t base = mat * size, step = static_cast<int64_t>(pieces) * kMuonBlock * 8;
     const int64_t rows = size / c;
@@ -107,7 +109,10 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
     for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += step) {
         float u[8], nb[8];
         if (i < size) read_u<8>(U, base + i, u, nb);
-        if (st.raise == 0.0f) st = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, eps_raised, sums);   // while those are on their way
+        if (st.raise == 0.0f) {   // while those are on their way
+            st = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, eps_raised, sums);
+            if (!goes) return;   // (start_scale's barrier lies between)
+        }
         if (i >= size) continue;
         if (buf) Pack<float, 8>::put(buf + base + i, nb);
         const int64_t to = ldn == c ? base + i : (mat * rows + i / c) * ldn + i % c;
@@ -134,12 +139,13 @@ __global__ void __launch_bounds__(kMuonBlock, 5) k_muon_start(Update U, float* _
                                                            int tiles_c, int tiles, int ntiles,
                                                            const float2* __restrict__ part, int parts, float eps, float eps_raised,
                                                            __half* __restrict__ hi, __half* __restrict__ lo,
-                                                           int64_t ldn, int tall, const int32_t* d_err)
+                                                           int64_t ldn, int tall, uint32_t* verdict, const int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and optimizer state only
     __shared__ float tile[64][65];
     __shared__ float sums[2 * 32];
-    if (buf != nullptr && read_error(d_err) != 0) return;   // set before this kernel: the same for every block
+    __shared__ bool goes;
+    if (threadIdx.x == 0) goes = buf == nullptr || step_goes(verdict, d_err);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t m = tall ? c : r;
     int64_t have = -1;
@@ -154,6 +160,7 @@ __global__ void __launch_bounds__(kMuonBlock, 5) k_muon_start(Update U, float* _
             if (have >= 0) __syncthreads();   // the last sums have been read
             st = start_scale<kMuonBlock>(part + mat * parts, parts, eps, eps_raised, sums);
             have = mat;
+            if (!goes) return;   // (start_scale's barrier lies between)
         }
         float u[4][4];
 #pragma unroll
@@ -227,6 +234,7 @@ struct Product {
     int out_bf16, tall;
     int pairs;              // rows of an even number of values, out aligned to two of them
     float decay, lr;
+    uint32_t* verdict;      // of a Muon step, else nullptr
     int32_t* d_err;
 };
 
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
         const int xr = rowl & 7;
         const uint32_t mine = (rowl >> 6) * kBoxBytes + (rowl & 63) * 128;   // this lane's row of a 128 x 64 part
         const bool head = warp == 2 + 4 * group && lane == 0;                // issues the group's copies
-        const bool blocked = kKind == kFinal && Q.w != nullptr && read_error(Q.d_err) != 0;
+        const bool blocked = kKind == kFinal && Q.w != nullptr && ld_volatile(Q.verdict) != kGo;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t at = sets + group * S::kSet, bar = term + 8 * group;
         // A tile's 64-column pieces that are wanted: inside the matrix, not above the diagonal.  They go
@@ -773,7 +781,10 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
     else
         __syncthreads();
     tc_fence_after();
-    if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
+    if (dead && threadIdx.x == 0) {
+        if (Q.verdict != nullptr) *Q.verdict = kStop;   // no weights from what this product has not finished
+        set_error(Q.d_err, SPARSE_ERR_INTERNAL);
+    }
     if (warp == 1) tmem_free<kPair>(tmem, S::kAccs * S::kAccCols);
 }
 
@@ -811,7 +822,7 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 struct Layout {
     int64_t m, n, ldm, ldn;
     int parts, products;
-    size_t part, x[2][2], a[2], b[2], total;   // [.][0] hi, [.][1] lo
+    size_t part, verdict, x[2][2], a[2], b[2], total;   // [.][0] hi, [.][1] lo
 };
 
 // Matrices of at most 128 rows (columns) have three products whatever was asked for: with one, the few
@@ -833,6 +844,7 @@ Layout muon_layout(int64_t batch, int64_t r, int64_t c, int asked)
         return p;
     };
     L.part = take(sizeof(float2) * static_cast<size_t>(batch * L.parts));
+    L.verdict = take(sizeof(uint32_t));
     for (int i = 0; i < 2; ++i)
         for (int h = 0; h < 2; ++h) L.x[i][h] = take(2 * static_cast<size_t>(batch * L.m * L.ldn));
     for (int h = 0; h < 2; ++h) {
@@ -942,6 +954,7 @@ cudaError_t run_steps(const Layout& L, const MuonParams& M, uint8_t* ws, cudaStr
     for (int step = 0; step < M.steps; ++step) {
         const int in = step & 1, out = in ^ 1;
         Product Q{};
+        Q.verdict = M.w != nullptr ? reinterpret_cast<uint32_t*>(ws + L.verdict) : nullptr;
         Q.d_err = M.d_err;
         Q.m = Q.n = L.m;
         Q.k = L.n;
@@ -996,6 +1009,7 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
     const Layout L = muon_layout(M.batch, M.r, M.cols, M.products);
     uint8_t* base = static_cast<uint8_t*>(ws);
     float2* part = reinterpret_cast<float2*>(base + L.part);
+    uint32_t* verdict = reinterpret_cast<uint32_t*>(base + L.verdict);
     const Update U{M.g, M.g_bf16, M.buf, M.momentum, M.nesterov};
     const int64_t size = M.r * M.cols;
     cudaError_t e;
@@ -1005,10 +1019,10 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
     {
         SO_PROFILE("muon_norm", s);
         e = launch(values == 8 ? k_muon_norm<8> : values == 4 ? k_muon_norm<4> : k_muon_norm<1>,
-                   dim3(static_cast<unsigned>(M.batch * L.parts)), dim3(kMuonBlock), s, U, size, L.parts, part, M.d_err);
+                   dim3(static_cast<unsigned>(M.batch * L.parts)), dim3(kMuonBlock), s, U, size, L.parts, part, verdict, M.d_err);
     }
     if (e != cudaSuccess) return e;
-    if (muon_fits_cluster(M.batch, L.m, L.n)) return muon_cluster(M, U, part, L.parts, values > 1, s);
+    if (muon_fits_cluster(M.batch, L.m, L.n)) return muon_cluster(M, U, part, L.parts, verdict, values > 1, s);
     {
         const bool lo = L.products == 3 || M.steps > 1;
         __half* xhi = reinterpret_cast<__half*>(base + L.x[0][0]);
@@ -1017,14 +1031,14 @@ cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
         if (values == 8 && M.r <= M.cols) {
             const int pieces = static_cast<int>(std::max<int64_t>(1, size / (kMuonBlock * 8 * 8)));
             e = launch(k_muon_start_flat, dim3(static_cast<unsigned>(M.batch * pieces)), dim3(kMuonBlock), s, U, M.buf, size,
-                       pieces, static_cast<const float2*>(part), L.parts, M.eps, M.eps_raised, xhi, xlo, static_cast<int>(M.cols), L.ldn,
+                       pieces, static_cast<const float2*>(part), L.parts, M.eps, M.eps_raised, xhi, xlo, static_cast<int>(M.cols), L.ldn, verdict,
                        static_cast<const int32_t*>(M.d_err));
         } else {
             const int64_t tc = (M.cols + 63) / 64, tiles = (M.r + 63) / 64 * tc, all = tiles * M.batch;
             e = launch(values > 1 ? k_muon_start<true> : k_muon_start<false>,
                        dim3(static_cast<unsigned>(std::min<int64_t>(all, 8 * num_sms()))), dim3(kMuonBlock), s, U, M.buf,
                        M.r, M.cols, static_cast<int>(tc), static_cast<int>(tiles), static_cast<int>(all),
-                       static_cast<const float2*>(part), L.parts, M.eps, M.eps_raised, xhi, xlo, L.ldn, M.r > M.cols ? 1 : 0,
+                       static_cast<const float2*>(part), L.parts, M.eps, M.eps_raised, xhi, xlo, L.ldn, M.r > M.cols ? 1 : 0, verdict,
                        static_cast<const int32_t*>(M.d_err));
         }
     }

@@ -14,6 +14,21 @@ constexpr float kScale = 16384.0f;              // 2^14: X, A and B are held tim
 constexpr float kInvScale = 1.0f / 16384.0f;
 constexpr int kMuonBlock = 256;
 
+// Whether a Muon step takes place, a word of the workspace that one block settles for all (k_muon_norm
+// clears it): the caller's error word may be set at any moment, by another stream that shares it, and a
+// step that part of its blocks had left out would have moved the buffer without the weights, or
+// half of either.
+constexpr uint32_t kUndecided = 0, kGo = 1, kStop = 2;
+
+// By one thread of a block.
+__device__ __forceinline__ bool step_goes(uint32_t* verdict, const int32_t* d_err)
+{
+    const uint32_t mine = read_error(d_err) != 0 ? kStop : kGo;
+    uint32_t v = ld_volatile(verdict);
+    if (v == kUndecided) v = atomicCAS(verdict, kUndecided, mine);
+    return (v == kUndecided ? mine : v) == kGo;
+}
+
 // u of one call: given, or the momentum's.
 struct Update {
     const void* g;      // u itself, or the gradient
@@ -131,7 +146,7 @@ __device__ __forceinline__ Start start_scale(const float2* part, int parts, floa
 // Whether the matrices take the cluster path, and that path, once the sums of squares are on
 // their way (`vec`: 16-byte accesses of the update).
 bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n);
-cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* part, int parts, bool vec,
-                         cudaStream_t s);
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* part, int parts, uint32_t* verdict,
+                         bool vec, cudaStream_t s);
 
 }  // namespace so

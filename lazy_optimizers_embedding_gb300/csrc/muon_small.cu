@@ -124,6 +124,7 @@ struct Small {
     int out_bf16, vec;   // vec: rows of a multiple of four values, out (w) aligned to four of them
     float* w;
     float decay, lr;
+    uint32_t* verdict;   // of a Muon step
     int32_t* d_err;
 };
 
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     __shared__ uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
+    __shared__ bool goes;
     __shared__ float sums[2 * 32];
     const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes, xrest = slo + kSquareBytes;
     const uint32_t bar = smem_addr(&bar_mem);
@@ -166,10 +168,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();   // writes a caller output: dependents start after this grid exits
-    const bool blocked = (Q.w != nullptr) && read_error(Q.d_err) != 0;   // set before this kernel: the same for every block
+    if (threadIdx.x == 0) goes = Q.w == nullptr || step_goes(Q.verdict, Q.d_err);
 
     // X of the slice, scaled and split; the new momentum buffer
     const Start st = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, Q.eps_raised, sums);
+    const bool blocked = !goes;   // (start_scale's barrier lies between)
     const int64_t base = mat * Q.size;
     // Groups of lanes take u's rows (X's, or its columns where u is tall), a lane four values at a time: a
     // whole warp, or as many lanes as such a row has use for.
@@ -565,7 +568,8 @@ bool muon_fits_cluster(int64_t batch, int64_t m, int64_t n)
     return f.fold > 0 && f.cost < 850 + batch * n * (m > 64 ? 29 : 16) / 1000;
 }
 
-cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* part, int parts, bool vec, cudaStream_t s)
+cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* part, int parts, uint32_t* verdict, bool vec,
+                         cudaStream_t s)
 {
     Small Q{};
     Q.size = M.r * M.cols;
@@ -587,6 +591,7 @@ cudaError_t muon_cluster(const MuonParams& M, const Update& U, const float2* par
     Q.w = M.w;
     Q.decay = M.decay;
     Q.lr = M.lr;
+    Q.verdict = verdict;
     Q.d_err = M.d_err;
     auto* kernel = Q.m <= kRestRows ? (vec ? k_muon_cluster<true, kRests> : k_muon_cluster<false, kRests>)
                    : F.fold > 1     ? (vec ? k_muon_cluster<true, kParts> : k_muon_cluster<false, kParts>)

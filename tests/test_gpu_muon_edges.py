@@ -134,3 +134,62 @@ def test_a_step_without_gradient_only_decays(cuda_lib, shape, products):
     o = _formula(torch, k.g.double() + 0.95 * k.buf.double(), 0.0)[2]
     off = (k.w[2].double() - (keep * w[2] - 0.03 * o)).norm()
     assert float(off) <= 0.03 * TOL[products] * float(o.norm()) + 2.0 ** -22 * float(w[2].norm() + 0.03 * o.norm())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("products", [1, 3])
+@pytest.mark.parametrize("shape", PATHS)
+def test_a_bad_value_or_a_set_word_leaves_the_weights(cuda_lib, shape, products, bad):
+    import torch
+    so = cuda_lib
+    k = Case(torch, so, _randn(torch, shape), products)
+    k.u[2, -1, -1] = bad
+    k.run()
+    assert int(k.err.item()) == so.ERR_NON_FINITE
+    for g_type in ("f32", "bf16"):
+        for what in ("value", "word"):
+            k = Step(torch, so, shape, g_type, products)
+            w, buf = k.w.clone(), k.buf.clone()
+            if what == "value":
+                k.g[0, 1, 2] = bad
+            else:
+                k.err.fill_(so.ERR_STEP_ORDER)
+            k.run()
+            k.G.check("muon step")
+            assert torch.equal(w, k.w) and torch.equal(buf, k.buf)
+            assert int(k.err.item()) == (so.ERR_NON_FINITE if what == "value" else so.ERR_STEP_ORDER)
+
+
+@pytest.mark.parametrize("shape,products", [((2000, 64, 128), 3), ((1, 1500, 1500), 3), ((6, 1000, 1100), 1), ((1, 1600, 700), 1)])
+def test_a_word_set_while_a_step_runs_stops_all_of_it_or_nothing(cuda_lib, shape, products):
+    """Another stream copies an error into the word at some moment: the step is whole or has not been."""
+    import torch
+    so = cuda_lib
+    k = Step(torch, so, shape, products=products)
+    w0, buf0 = k.w.clone(), k.buf.clone()
+    k.run()
+    torch.cuda.synchronize()
+    t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    k.w.copy_(w0), k.buf.copy_(buf0)
+    t0.record()
+    k.run()
+    t1.record()
+    torch.cuda.synchronize()
+    w1, buf1 = k.w.clone(), k.buf.clone()
+    cycles = int(t0.elapsed_time(t1) * 1.9e6 * 1.2)
+    word = torch.full((1,), so.ERR_STEP_ORDER, dtype=torch.int32).pin_memory()
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    seen = set()
+    for i in range(60):
+        k.w.copy_(w0), k.buf.copy_(buf0), k.err.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(max(1, cycles * i // 60))
+            k.err.copy_(word, non_blocking=True)
+        k.run(stream=main)
+        torch.cuda.synchronize()
+        whole = torch.equal(k.w, w1) and torch.equal(k.buf, buf1)
+        assert whole or (torch.equal(k.w, w0) and torch.equal(k.buf, buf0)), i
+        seen.add(whole)
+    k.G.check("muon step")
+    assert True in seen

@@ -1,0 +1,65 @@
+"""Layer norm where each of its kernels can go wrong: looked-up rows that are not there, values that are
+not finite, means far above the spread, widths on both sides of where another kernel takes over.
+
+Bounds as in the tests of the ordinary cases: u = 2^-24, a row sum's error is below K u sum|terms|
+with K = c / 512 + 64, a column sum adds at most 512 terms in a row."""
+import numpy as np
+import pytest
+
+from test_gpu_layer_norm import Case, _np
+
+pytestmark = pytest.mark.gpu
+
+# rows, columns, types: of registers, of the ring forward (packed, pairs, single values), of the ring
+# backward too, of wide rows
+KERNELS = [(33, 512, "f32", "f32"), (33, 1000, "bf16", "bf16"), (33, 2048, "bf16", "bf16"), (33, 2050, "f32", "bf16"),
+           (33, 1111, "f32", "f32"), (33, 1111, "bf16", "bf16"), (33, 1111, "f32", "bf16"), (2100, 8192, "f32", "f32"),
+           (2100, 8192, "bf16", "bf16"), (6600, 2560, "f32", "bf16"), (33, 9000, "bf16", "bf16")]
+
+
+@pytest.mark.parametrize("n,c,xt,yt", KERNELS)
+def test_rows_that_are_not_there(cuda_lib, n, c, xt, yt):
+    import torch
+    so = cuda_lib
+    rng = np.random.default_rng(n + c)
+    idx = rng.integers(0, 40, n)
+    k = Case(torch, so, n, c, xt, yt, idx=idx, rows=40)
+    k.run()
+    assert int(k.err.item()) == 0
+    want = [t.clone() for t in (k.y, k.dx, k.mean, k.rstd)]
+    bad = [0, n // 2, n // 2 + 1, n - 1]
+    idx[bad] = [40, -1, 1 << 40, -(1 << 62)]
+    k.idx.copy_(torch.from_numpy(idx))
+    for t in (k.y, k.dx, k.mean, k.rstd):
+        t.fill_(7.0)
+    so.check(so.sparse_layer_norm(k.x, 40, c, k.idx, n, k.gamma, k.beta, 1e-5, k.y, k.mean, k.rstd, k.err))
+    assert int(k.err.item()) == so.ERR_INDEX_OUT_OF_RANGE
+    k.err.zero_()
+    so.check(so.sparse_layer_norm_grad(k.dy, k.x, 40, c, k.idx, n, k.gamma, k.mean, k.rstd, k.dx, k.dgamma, k.dbeta,
+                                       k.ws, k.err))
+    assert int(k.err.item()) == so.ERR_INDEX_OUT_OF_RANGE
+    k.G.check("layer norm")
+    for got, ref in zip((k.y, k.dx, k.mean, k.rstd), want):
+        assert (got[bad] == 7.0).all()
+        got[bad] = ref[bad]
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("n,c,xt,yt", KERNELS)
+def test_nan_and_infinity_stay_in_their_rows(cuda_lib, n, c, xt, yt):
+    import torch
+    k = Case(torch, cuda_lib, n, c, xt, yt)
+    rows = {1: (0, float("nan")), n // 2: (c - 1, float("inf")), n - 2: (c // 2, -float("inf"))}
+    for i, (j, v) in rows.items():
+        k.x[i, j] = v
+    k.run()
+    bad = list(rows)
+    keep = np.array([i not in rows for i in range(n)])
+    assert torch.isnan(k.y[bad]).all() and torch.isnan(k.dx[bad]).all()
+    assert np.isfinite(_np(k.y)[keep]).all() and np.isfinite(_np(k.dx)[keep]).all()
+    k = Case(torch, cuda_lib, n, c, xt, yt)
+    k.dy[1, c - 1] = float("nan")
+    k.run()
+    assert torch.isnan(k.dx[1]).all() and torch.isnan(k.dbeta[c - 1]) and torch.isnan(k.dgamma[c - 1])
+    k.dx[1] = 0.0
+    assert torch.isfinite(k.dx).all() and torch.isfinite(k.dgamma[:c - 1]).all() and torch.isfinite(k.dbeta[:c - 1]).all()

@@ -6,7 +6,7 @@ with K = c / 512 + 64, a column sum adds at most 512 terms in a row."""
 import numpy as np
 import pytest
 
-from test_gpu_layer_norm import Case, _np
+from test_gpu_layer_norm import U, Case, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,32 @@ def test_nan_and_infinity_stay_in_their_rows(cuda_lib, n, c, xt, yt):
     assert torch.isnan(k.dx[1]).all() and torch.isnan(k.dbeta[c - 1]) and torch.isnan(k.dgamma[c - 1])
     k.dx[1] = 0.0
     assert torch.isfinite(k.dx).all() and torch.isfinite(k.dgamma[:c - 1]).all() and torch.isfinite(k.dbeta[:c - 1]).all()
+
+
+@pytest.mark.parametrize("n,c,yt", [(40, 64, "f32"), (40, 200, "bf16"), (40, 1024, "f32"), (40, 3000, "f32"), (2100, 8192, "f32"),
+                                    (6600, 2560, "bf16"), (40, 333, "f32"), (40, 1111, "f32"), (40, 1111, "bf16"), (40, 2050, "f32"),
+                                    (40, 9000, "f32")])
+def test_a_mean_far_above_the_spread(cuda_lib, n, c, yt):
+    """x - mean is exact here, so xhat is off by the roundings of the difference times rstd alone, 3 u of
+    itself, and not by a rounding of mean times rstd."""
+    import torch
+    so = cuda_lib
+    k = Case(torch, so, n, c, "f32", yt)
+    rng = np.random.default_rng(c)
+    d = rng.integers(-8, 9, (n, c)).astype(np.float64)
+    mean = 2.0 ** 20 + rng.integers(-1000, 1000, (n, 1))
+    rstd = np.float32(1.0 / np.sqrt((d * d).mean(1, keepdims=True))).astype(np.float64)
+    k.x.copy_(torch.from_numpy((mean + d).astype(np.float32)))
+    k.mean.copy_(torch.from_numpy(mean[:, 0].astype(np.float32)))
+    k.rstd.copy_(torch.from_numpy(rstd[:, 0].astype(np.float32)))
+    so.check(so.sparse_layer_norm_grad(k.dy, k.x, n, c, None, n, k.gamma, k.mean, k.rstd, k.dx, k.dgamma, k.dbeta,
+                                       k.ws, k.err))
+    k.G.check("layer norm")
+    dy, gamma, xhat = _np(k.dy), _np(k.gamma), d * rstd
+    h = dy * gamma
+    a, b = h.mean(1, keepdims=True), (h * xhat).mean(1, keepdims=True)
+    K = c / 512 + 64
+    size = np.abs(h) + np.abs(h).mean(1, keepdims=True) + np.abs(xhat) * np.abs(h * xhat).mean(1, keepdims=True)
+    assert (np.abs(_np(k.dx) - rstd * (h - a - xhat * b)) <= 2 * K * U * rstd * size).all()
+    assert (np.abs(_np(k.dgamma) - (dy * xhat).sum(0)) <= (512 + 4) * U * np.abs(dy * xhat).sum(0)).all()
+    assert (np.abs(_np(k.dbeta) - dy.sum(0)) <= 512 * U * np.abs(dy).sum(0)).all()

@@ -660,11 +660,20 @@ __device__ __forceinline__ void ring_requests(Ring& S, uint8_t* data, int stages
     if ((threadIdx.x & 31) != 0) return;
     int stage = 0;
     uint32_t parity = 1;
-    for (int64_t it = 0; (it * gridDim.x + blockIdx.x) * ring_rows(kBack) < n; ++it) {
+    int64_t it = 0;
+    for (; (it * gridDim.x + blockIdx.x) * ring_rows(kBack) < n; ++it) {
         if (!mbar_wait(smem_addr(&S.empty[stage]), parity, &S.dead)) break;
         ring_fill<X, Y, kBack>(S, data, it, stage, x, r, c, idx, n, dy, d_err);
+        if (it == 0)
+            for (int s = 1; s < kRingStages; ++s) S.found[s][0] = S.found[s][kRingRows - 1] = 0;   // what a wait that runs out, two seconds on, finds
         if (++stage == stages) stage = 0, parity ^= 1u;
     }
+    // The copies land before this warp, and so the block, leaves, also where a wait ran out (two seconds at most).
+    const uint64_t t0 = now_ns();
+    for (int s = 0; s < stages; ++s)
+        if (s < stage || it >= stages)
+            while (!mbar_try(smem_addr(&S.full[s]), s < stage ? parity ^ 1u : parity) && now_ns() - t0 < 2000000000ull) {
+            }
     if (S.dead) set_error(d_err, SPARSE_ERR_INTERNAL);
 }
 __device__ __forceinline__ void ring_init(Ring& S, int G)

@@ -134,13 +134,13 @@ template <bool kVec, Layout kLayout>
 __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update U, const Small Q, int blocks)
 {
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bar_mem;
+    __shared__ uint64_t bar_mem[2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     __shared__ bool goes;
     __shared__ float sums[2 * 32];
     const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes, xrest = slo + kSquareBytes;
-    const uint32_t bar = smem_addr(&bar_mem);
+    const uint32_t bar = smem_addr(bar_mem), drain = bar + 8;
     constexpr bool kRest = kLayout == kRests;
     const int fold = kLayout == kOnePart ? 1 : Q.fold;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
 
     if (threadIdx.x == 0) {
         dead = 0;
-        mbar_init(bar, 1);
+        mbar_init(bar, 1), mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc<1>(&tmem_slot, kTmemCols);
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     __syncthreads();
 
     // the update, as u came
-    if (!blocked)
+    if (!blocked && !dead)
         for (int k = k0; k < inner; k += lanes_of_row * 4)
             for (int o0 = group; o0 < outer; o0 += groups * kRowsAtOnce) {
                 const int left = min(4, inner - k);
@@ -493,6 +493,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                 }
             }
     if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
+    if (warp == 0 && dead && elect_one()) {   // products in flight finish before their memory is given back
+        volatile int none = 0;
+        tc_commit<1>(drain);
+        mbar_wait(drain, 0, &none);
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

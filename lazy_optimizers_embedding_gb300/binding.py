@@ -5,14 +5,17 @@ the current CUDA stream to the C entry point of the same name and returns its
 status code: by ctypes or, for the operators around the table step, whose smallest
 calls take less time on the GPU than ctypes does, by the compiled module _pycall
 (ctypes takes what that leaves: other streams, pointers as integers, arguments that
-are refused).  All work runs in the library's kernels; PyTorch only supplies the
-device memory and the stream.  There is no fallback: if the library or the module is
-not built, importing this module raises.
+are refused; and everything, with a warning, where there is no module for this
+Python and PyTorch).  All work runs in the library's kernels; PyTorch only supplies
+the device memory and the stream.  There is no fallback: if the library is not
+built, importing this module raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -81,8 +84,6 @@ def _load():
     path = _build.LIB
     if not os.path.exists(path):
         raise ImportError(f"libsparseopt.so is not built ({path}); run __graft_entry__.build()")
-    if not os.path.exists(_build.PYCALL):
-        raise ImportError(f"_pycall.so is not built ({_build.PYCALL}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
     P, I64, INT, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     sig = {
@@ -125,8 +126,32 @@ def _load():
 
 
 LIB = _load()
-from . import _pycall  # noqa: E402  (needs the library)
 
+
+class _NoModule:
+    """Stands in for the compiled module: leaves every call to ctypes."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_pycall():
+    """The compiled module, where it is there and was built for this Python and PyTorch."""
+    why = f"not built for {_build.pycall_key()}"
+    if _build.pycall_usable():
+        try:
+            spec = importlib.util.spec_from_file_location(__package__ + "._pycall", _build.PYCALL)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            return module
+        except ImportError as e:
+            why = str(e)
+    warnings.warn(f"{_build.PYCALL}: {why}; ctypes takes the operators' calls (slower by some microseconds each) until "
+                  "__graft_entry__.build()", stacklevel=3)
+    return _NoModule()
+
+
+_pycall = _load_pycall()
 _pycall.configs(NsConfig, MuonConfig)
 EXPORTED = ("sparse_workspace_size", "sparse_status_string", "sparse_canonicalize", "sparse_csr_to_coo",
             "sparse_coo_to_csr", "sparse_row_coo_to_csr", "sparse_adam_step", "sparse_adam_table_step",

@@ -4,12 +4,15 @@ Each translation unit under ``csrc/`` is compiled in parallel, then linked into
 ``lazy_optimizers_embedding_gb300/libsparseopt.so``; ``csrc/pycall.cpp`` becomes the
 module ``_pycall.so`` (the binding's calls with tensors), against the library and the
 installed PyTorch.  Objects go to ``_build/`` (git-ignored).  Rebuilds only when a
-source or header is newer than the library.
+source or header is newer than the library, and the module also for another Python or
+PyTorch.  Where the module cannot be built (no C++ compiler, no headers) the library is
+built all the same, and ctypes takes the module's calls.
 """
 from __future__ import annotations
 
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -43,24 +46,51 @@ def sources():
 
 
 STAMP = os.path.join(BUILD, "defines.txt")   # the extra defines the current library was built with
+PYCALL_STAMP = os.path.join(BUILD, "pycall.txt")   # the Python and PyTorch the module was built for
+
+
+def pycall_key() -> str:
+    """The Python and PyTorch that a module built now would be for."""
+    import torch
+    return f"{platform.machine()} {sys.implementation.cache_tag} torch {torch.__version__}"
+
+
+def _read(path) -> str | None:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def pycall_usable() -> bool:
+    """Whether the module is there and was built for this Python and PyTorch."""
+    return os.path.exists(PYCALL) and _read(PYCALL_STAMP) == pycall_key()
+
+
+def _older(path, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PYCALL):
-        return True
-    try:
-        with open(STAMP) as f:
-            if f.read() != " ".join(EXTRA_DEFS):
-                return True
-    except OSError:
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
-    deps = [PYCALL_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return (_read(STAMP) != " ".join(EXTRA_DEFS) or
+            _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers()))
+
+
+def _pycall_stale() -> bool:
+    deps = [PYCALL_SRC] + _headers()
+    if _read(PYCALL_STAMP) == "none for " + pycall_key():   # it could not be built, and nothing has changed
+        return _older(PYCALL_STAMP, deps)
+    return not pycall_usable() or _older(PYCALL, deps)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not _stale():
+    library, module = force or _stale(), force or _pycall_stale()
+    if not library and not module:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -96,24 +126,30 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 os.path.join(at, "lib"),
                 "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
-    srcs = sources()
+    def link(cmd, to):
+        tmp = to + f".{os.getpid()}.tmp"
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, to)
+
+    srcs = sources() if library else []
     with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        pycall = ex.submit(compile_pycall)
+        pycall = ex.submit(compile_pycall) if module else None
         objs = list(ex.map(compile_one, srcs))
-        link_pycall = pycall.result()
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = PYCALL + f".{os.getpid()}.tmp"
-    r = subprocess.run([*link_pycall, "-o", tmp], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, PYCALL)
-    with open(STAMP, "w") as f:
-        f.write(" ".join(EXTRA_DEFS))
+    if library:
+        link([cc, *ARCH, "-shared", *objs], LIB)
+        with open(STAMP, "w") as f:
+            f.write(" ".join(EXTRA_DEFS))
+    if module:
+        key = pycall_key()
+        try:
+            link(pycall.result(), PYCALL)
+        except (RuntimeError, OSError) as e:   # the library is whole without it
+            sys.stderr.write(f"no compiled calls (ctypes takes the operators' calls): {e}\n")
+            key = "none for " + key
+        with open(PYCALL_STAMP, "w") as f:
+            f.write(key)
     return LIB
 
 

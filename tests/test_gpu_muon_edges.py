@@ -193,3 +193,105 @@ def test_a_word_set_while_a_step_runs_stops_all_of_it_or_nothing(cuda_lib, shape
         seen.add(whole)
     k.G.check("muon step")
     assert True in seen
+
+
+def _shape(kind, m, n, k, batch, sms):
+    """Blocks to a tile, parts of its inner dimension, columns; tiles; blocks or pairs that share them: the
+    cheapest by the kernels' rule, for one product."""
+    sym = kind != "update"
+    best = None
+    chunks = -(-k // 64)
+    for pair, split, bn in ((2, 1, 256), (2, 1, 128), (1, 1, 128), (1, 1, 64), (1, 2, 128), (1, 4, 128)):
+        units, tm = sms // (pair * split), 128 * pair
+        tiles = batch * (sum((i * tm + tm - 1) // bn + 1 for i in range(-(-m // tm))) if sym else -(-m // tm) * -(-n // bn))
+        if split > 1 and (tiles > units or chunks < 2 * split):
+            continue
+        stage = 8192 * (2 + bn // pair // 64)
+        cost = -(-tiles // units) * -(-chunks // split) * max(2 * bn, stage // 80) + (6000 if split > 1 else 0)
+        if best is None or cost < best[0]:
+            best = cost, (pair, split, bn), tiles, units
+    return best[1:]
+
+
+# one product: tiles of 256 columns and of 128, by pairs and alone, three epilogue groups (inner
+# dimension below 1024) and two, several tiles a block, remainders in rows and columns, tall ones
+TILES = [(16, 760, 2040), (1, 3001, 4090), (1, 4090, 4100), (1, 4100, 3001), (20, 1000, 1001), (6, 1000, 1100), (1, 1500, 2300),
+         (2, 3000, 1400), (8, 520, 1500), (40, 300, 1100), (12, 700, 500), (2, 200, 20000), (30, 129, 4000)]
+
+
+def test_the_shapes_reach_every_kind_of_tile(cuda_lib):
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    reached = set()
+    for batch, r, c in TILES:
+        m, n = min(r, c), max(r, c)
+        for kind, cols, inner in (("gram", m, n), ("poly", m, m), ("update", n, m)):
+            shape, tiles, units = _shape(kind, m, cols, inner, batch, sms)
+            reached.add((kind, shape, inner < 1024 and shape[0] == 2, tiles > units))
+    assert {("gram", (2, 1, 256), False, True), ("gram", (1, 1, 128), False, True), ("gram", (2, 1, 128), False, True),
+            ("poly", (2, 1, 256), False, True), ("poly", (2, 1, 256), True, True), ("poly", (2, 1, 128), True, True),
+            ("update", (2, 1, 256), False, True), ("update", (2, 1, 256), True, True),
+            ("update", (2, 1, 128), True, True)} <= reached
+
+
+@pytest.mark.parametrize("in_type,out_type", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("shape", TILES)
+def test_blocks_with_several_tiles(cuda_lib, shape, in_type, out_type):
+    import torch
+    u = _randn(torch, shape, dtype=in_type)
+    k = Case(torch, cuda_lib, u, 1, out_type)
+    got = k.run().clone()
+    assert int(k.err.item()) == 0
+    assert _off(got, _formula(torch, u)) <= TOL[1] + (2.0 ** -9 if out_type == "bf16" else 0.0)
+    k.out.zero_()
+    assert torch.equal(got, k.run())
+
+
+@pytest.mark.parametrize("shape", [(16, 760, 2040), (1, 4100, 3001), (20, 1000, 1001)])
+@pytest.mark.parametrize("g_type,products", [("bf16", 1), ("f32", 3)])
+def test_steps_of_blocks_with_several_tiles(cuda_lib, shape, g_type, products):
+    import torch
+    k = Step(torch, cuda_lib, shape, g_type, products)
+    w, buf = k.w.double(), k.buf.double()
+    k.run()
+    k.G.check("muon step")
+    assert int(k.err.item()) == 0
+    g = k.g.double()
+    new = 0.95 * buf + g
+    assert ((k.buf.double() - new).abs() <= 2.0 ** -23 * (0.95 * buf.abs() + g.abs())).all()
+    o = _formula(torch, g + 0.95 * k.buf.double())
+    norm = lambda t: t.square().sum((1, 2)).sqrt()  # noqa: E731
+    off = norm(k.w.double() - ((1 - 0.02 * 0.1) * w - 0.03 * o))
+    assert (off <= 0.03 * TOL[products] * norm(o) + 2.0 ** -22 * (norm(w) + 0.03 * norm(o))).all()
+
+
+@pytest.mark.parametrize("shift", [1, 2])
+@pytest.mark.parametrize("shape", [(2, 300, 402), (2, 402, 300), (2, 302, 400), (2, 130, 1001)])
+def test_arrays_of_any_alignment_past_a_cluster(cuda_lib, shape, shift):
+    import torch
+    for products, t in ((1, "bf16"), (3, "f32")):
+        base = _randn(torch, (shape[0] * shape[1] * shape[2] + shift,), dtype=t)
+        u = base[shift:].view(shape)
+        k = Case(torch, cuda_lib, u, products, t, shift=shift)
+        got = k.run()
+        assert _off(got, _formula(torch, u)) <= TOL[products] + (2.0 ** -9 if t == "bf16" else 0.0)
+
+
+@pytest.mark.parametrize("shape,products", [((33000, 256, 256), 1), ((265000, 64, 128), 3)])
+def test_elements_past_2_31(cuda_lib, shape, products):
+    import torch
+    free, _ = torch.cuda.mem_get_info()
+    if free < 100 << 30:
+        pytest.skip("needs 100 GB")
+    u = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    assert u.numel() > 1 << 31
+    for i in range(0, shape[0], 8192):
+        u[i:i + 8192] = _randn(torch, u[i:i + 8192].shape, seed=i, dtype="bf16")
+    k = Case(torch, cuda_lib, u, products, "bf16", guarded=False)
+    got = k.run()
+    assert int(k.err.item()) == 0
+    last = shape[0]
+    for i in (0, last // 2, last - 3):
+        assert _off(got[i:i + 3], _formula(torch, u[i:i + 3])) <= TOL[products] + 2.0 ** -9
+    del k, got, u
+    torch.cuda.empty_cache()

@@ -463,9 +463,11 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
  * accepted when the singular values of X, A, B and a I + B, bounded step by step from
  * X's in [0, 1] on, stay below 3.9.
  * products: 3 computes each matrix product to 22 bits (fp32 accuracy, for fp32
- * results); 1 to 11 bits (about 2e-3 of the result's norm, what rounding it to
- * bf16 costs), in half the time or less for large matrices; matrices of at most
- * 128 rows or columns are always computed with 3.
+ * results); 1 to 11 bits (1.3e-3 to 2.5e-3 of the result's norm, the most where one singular
+ * value is all there is: what rounding it to bf16 costs), in half the time or less for
+ * large matrices.  Its sums over rows of n values drift by another n 2^-28 (5e-4 of the norm
+ * at 131072 values, 4e-3 at 2^20, where 3 should be asked for).  Matrices of at
+ * most 128 rows or columns are always computed with 3.
  */
 typedef struct {
     double a, b, c, eps;

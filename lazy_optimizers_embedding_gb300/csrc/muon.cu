@@ -19,12 +19,13 @@
 //                 times a, in every step but the last (there the small singular
 //                 values, tripled by a step, would drown in the rounding of the
 //                 large ones: 2e-2 of a low-rank matrix; in the last step X as
-//                 rounded is the better polynomial).  At most 1.7e-3 of the
-//                 result's norm in a 64-bit simulation (more than 128 rows), what
-//                 rounding it to bf16 costs too.
+//                 rounded is the better polynomial).  In a 64-bit simulation (more than 128 rows)
+//                 1.1e-3 to 1.5e-3 of the result's norm over flat, decaying and low-rank spectra,
+//                 2.5e-3 for rank one, about what rounding it to bf16 costs.
 //                 B is formed with a on its diagonal, so that B X holds a X.
 // (With three products a X is added in the epilogue: in the tensor unit's sums, which
-// round towards zero, it cost a low-rank matrix 4e-5.)
+// round towards zero, it cost a low-rank matrix 4e-5.  Simulated as above: 4e-7 flat, 5e-6 low rank, 3.6e-5 for
+// rank one, where fp32 products give 1e-4.)
 #include <algorithm>
 
 #include "muon.cuh"
@@ -259,8 +260,9 @@ struct Shape {
     // accumulator the 940 sums of K = 5000 were off by 6e-5 of the result.  So three products have two
     // accumulators, hi hi and (2^-11 of it) hi lo + lo hi, and every kChunk stages, 32 sums of hi hi, a
     // drift below 1e-6, the epilogue adds them to its own fp32 sums, which round to nearest.  (One
-    // accumulator read every 24 sums: 403 against 353 us at 2501 x 1003.)  Against f16 operands alone
-    // (one product) the drift does not count.
+    // accumulator read every 24 sums: 403 against 353 us at 2501 x 1003.)  With one product f16's own roundings are
+    // 1e-3 and more, and the drift is K 2^-28: nothing at 128000 columns (200 x 131072 off by 1.0e-3 with and
+    // without it), as much again and more at 2^20 (140 rows: 4.0e-3).
     static constexpr int kAccCols = P == 3 ? 2 * BN : BN;
     static constexpr int kAccs = 512 / kAccCols < 2 ? 1 : P == 3 ? 512 / kAccCols : 2;
     static constexpr int kChunk = P == 3 ? 8 : INT32_MAX;

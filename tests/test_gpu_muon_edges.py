@@ -265,6 +265,17 @@ def test_steps_of_blocks_with_several_tiles(cuda_lib, shape, g_type, products):
     assert (off <= 0.03 * TOL[products] * norm(o) + 2.0 ** -22 * (norm(w) + 0.03 * norm(o))).all()
 
 
+@pytest.mark.parametrize("shape", [(1, 200, 131072), (1, 1 << 18, 130), (1, 140, 1 << 20)])
+def test_one_product_over_long_rows(cuda_lib, shape):
+    """The drift of sums that are rounded towards zero, K 2^-27 of A and at most twice that of the result."""
+    import torch
+    u = _randn(torch, shape)
+    k = Case(torch, cuda_lib, u, 1)
+    got = k.run()
+    assert int(k.err.item()) == 0
+    assert _off(got, _formula(torch, u)) <= TOL[1] + 2 * max(shape) * 2.0 ** -27
+
+
 @pytest.mark.parametrize("shift", [1, 2])
 @pytest.mark.parametrize("shape", [(2, 300, 402), (2, 402, 300), (2, 302, 400), (2, 130, 1001)])
 def test_arrays_of_any_alignment_past_a_cluster(cuda_lib, shape, shift):

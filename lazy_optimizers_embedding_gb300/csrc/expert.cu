@@ -13,8 +13,8 @@
 // lane ORs its bit into the warp's word of its expert, so the bits below its own are
 // the slots of the same expert before it.  Up to kClusterSlots slots one cluster of
 // up to 8 blocks does it all in one launch (k_expert_sort: the blocks read one another's
-// counts from shared memory; 9003 slots 5 us and 131072 slots 8 us, against 15 us
-// for three launches).  More take contiguous tiles: k_expert_count counts every
+// counts from shared memory; 16384 slots of 64 experts 4.6 us, and 8 more, which take
+// three launches, 6.4).  More take contiguous tiles: k_expert_count counts every
 // tile's experts, k_expert_scan turns each expert's column of tile counts into a
 // running sum, k_expert_sort places.  Only whole numbers are added, so the result is
 // exact and the same on every run.
@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(kExBlock) k_expert_grad(const T* __restrict__ 
                                                           float* __restrict__ dw, int32_t* d_err)
 {
     pdl_wait();   // writes caller outputs
-    constexpr int J = 2, R = V < 4 ? 6 : 4, kMany = 8;   // (8 narrow accesses, one block an SM less: 105 against 92 us at 26775 x 8 x 393 bf16)
+    // Six narrow accesses were the fastest of 4, 6 and 8 in 17 of 20 shapes (26775 x 8 x 393 bf16: 106, 92 and 106 us;
+    // 5000 x 4 x 1333 fp32: 52, 44 and 51); 8, a block an SM less, where a few tokens more than the GPU has warps
+    // make another round of six (4167 x 6 x 1081 fp32: 50 and 46 us, 2000 x 8 x 5001: 133 and 122).
+    constexpr int J = 2, R = V < 4 ? 6 : 4, kMany = 8;
     const int lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kExWarps + (threadIdx.x >> 5);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kExWarps;

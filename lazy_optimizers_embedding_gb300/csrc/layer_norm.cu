@@ -10,9 +10,9 @@
 // what a row costs once (addresses, butterflies, a root and a quotient) is spread
 // over many values a lane.
 //
-// Forward, a group of G lanes holds a row of up to 1024 packed columns (or an odd one
-// of less than 1 KB) in registers, 32 values a lane, with its whole share of the row
-// in flight at once; gamma and beta lie in shared memory.  Backward the lanes also
+// Forward, a group of G lanes, a warp at most, holds a row of up to 1024 packed columns (or
+// an odd one of less than 1 KB) in registers, 32 values a lane, with its whole share of the
+// row in flight at once; gamma and beta lie in shared memory.  Backward the lanes also
 // carry the column sums, so a lane has 8 or 16 columns and a row up to 512 lanes.
 // Longer and odd rows pass through a ring in shared memory (k_ln_ring,
 // k_ln_grad_ring).  The column sums are joined over the block's groups in shared
@@ -139,7 +139,6 @@ __global__ void __launch_bounds__(kLnBlock, 4)
 {
     pdl_wait();   // writes caller outputs: dependents start after this grid exits
     constexpr int NV = L / V, NP = kPairs<V>;
-    __shared__ float tmp[2 * 32];
     extern __shared__ float4 stage[];
     const int gl = threadIdx.x & (G - 1), sub = threadIdx.x / G, groups = blockDim.x / G;
     const int used = (c + G * V - 1) / (G * V);
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(kLnBlock, 4)
             }
         }
         float s[1] = {s2.sum()};
-        group_sum<1>(s, G, tmp, 0);
+        lanes_sum<1>(s, G);
         const float mu = s[0] * inv_c;
         s2 = F2::both(0.0f);
         const F2 off = V == 1 ? F2::of(-mu, 0.0f) : F2::both(-mu), none = F2::both(0.0f);
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kLnBlock, 4)
             }
         }
         s[0] = s2.sum();
-        group_sum<1>(s, G, tmp, 1);
+        lanes_sum<1>(s, G);
         const float rs = rsqrtf(fmaf(s[0], inv_c, eps));   // within 2 ulp
         if (row != nullptr) {
             Y* to = y + i * c;
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(kMaxBackGroup, V < 4 && !kHeld ? 4 : 2) k_ln_w
 #pragma unroll
                     for (int e = 0; e < V; ++e) s[u] += v[e];
                 }
-        group_sum<R>(s, kMaxBackGroup, tmp, 0);
+        block_sum<R>(s, kMaxBackGroup, tmp, 0);
 #pragma unroll
         for (int u = 0; u < R; ++u) mu[u] = s[u] * inv_c, s[u] = 0.0f;
 #pragma unroll 4
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kMaxBackGroup, V < 4 && !kHeld ? 4 : 2) k_ln_w
 #pragma unroll
                     for (int e = 0; e < V; ++e) s[u] = fmaf(v[e] - mu[u], v[e] - mu[u], s[u]);
                 }
-        group_sum<R>(s, kMaxBackGroup, tmp, 1);
+        block_sum<R>(s, kMaxBackGroup, tmp, 1);
 #pragma unroll
         for (int u = 0; u < R; ++u) rs[u] = 1.0f / sqrtf(fmaf(s[u], inv_c, eps));
 #pragma unroll 2
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(kMaxBackGroup, 1)
             warps_sum<2 * R>(s, G >> 5, sub * (G >> 5), tmp[half], blockDim.x);
             half ^= 1;
         } else {
-            group_sum<2 * R>(s, G, nullptr, 0);
+            lanes_sum<2 * R>(s, G);
         }
 #pragma unroll
         for (int u = 0; u < R; ++u) {
@@ -920,7 +919,7 @@ __global__ void __launch_bounds__(kMaxBackGroup, V < 4 && !kHeld ? 4 : 2) k_ln_g
                 s[1] = fmaf(h, (v[e] - mu) * rs, s[1]);
             }
         }
-        group_sum<2>(s, kMaxBackGroup, tmp, half);
+        block_sum<2>(s, kMaxBackGroup, tmp, half);
         half ^= 1;
         const float a = s[0] * inv_c, b = s[1] * inv_c;
 #pragma unroll 2
@@ -1068,8 +1067,6 @@ cudaError_t run_ln_lane(const Forward& F)
     auto* kernel = k_ln<X, Y, V, L, kEven>;
     const int G = lanes_of(F.c, L), groups = kLnBlock / G;
     const int64_t row = (F.c + G * V - 1) / (G * V) * (G * V);
-    cudaError_t e = allow_smem(kernel, sizeof(float) * 2 * row, sizeof(float) * 2 * kLnBlock * L);
-    if (e != cudaSuccess) return e;
     static std::atomic<int> known[kGroupKinds];
     const int blocks = static_cast<int>(std::min<int64_t>(
         (F.n + groups - 1) / groups,
@@ -1158,18 +1155,20 @@ cudaError_t run_ln_wide(const Forward& F, size_t smem)
 template <class X, class Y, int V>
 cudaError_t run_ln(const Forward& F)
 {
-    SO_PROFILE("layer_norm", F.s);
     const RingShape g = ring_shape<X, Y, V, false>(F.c, F.n);
     if (g.stages) {
+        SO_PROFILE("layer_norm_ring", F.s);
         const bool even = V > 1 && F.c % (g.G * V) == 0;
         if (g.G <= 256) return even ? run_ln_ring<X, Y, V, (V > 1), 256>(F, g) : run_ln_ring<X, Y, V, false, 256>(F, g);
         return even ? run_ln_ring<X, Y, V, (V > 1), 512>(F, g) : run_ln_ring<X, Y, V, false, 512>(F, g);
     }
     constexpr int L = V == 1 ? 16 : 32;   // values a lane holds (single ones take two registers each)
-    if (F.c <= static_cast<int64_t>(kLnBlock) * L) {
+    if (F.c <= 32 * L) {   // what the ring leaves of the rows that it could hold: a warp has a row at most
+        SO_PROFILE("layer_norm", F.s);
         if (V > 1 && F.c % (lanes_of(F.c, L) * V) == 0) return run_ln_lane<X, Y, V, L, (V > 1)>(F);
         return run_ln_lane<X, Y, V, L, false>(F);
     }
+    SO_PROFILE("layer_norm_wide", F.s);
     // two rows share gamma and beta where they leave room for two blocks an SM and the rows go round
     const size_t row = (static_cast<size_t>(F.c) * sizeof(X) + 15) / 16 * 16;
     const bool held = row <= kRingSmem && !(V * sizeof(X) == 2);   // (two bytes at a time they cost more than they save)
@@ -1212,8 +1211,6 @@ cudaError_t run_grad_lane(const Backward& B, int want, int64_t& parts)
     auto* kernel = k_ln_grad<X, Y, V, L, R, kEven>;
     const int G = lanes_of_block(B.c, L, kLnBlock), threads = std::max(kLnBlock, G), groups = threads / G;
     const size_t smem = sizeof(float) * L * (groups > 1 ? 2 * threads : G);   // column sums, or gamma
-    cudaError_t e = allow_smem(kernel, smem, sizeof(float) * L * kMaxBackGroup);
-    if (e != cudaSuccess) return e;
     static std::atomic<int> known[kGroupKinds];
     parts = std::min<int64_t>(std::min<int64_t>(parts, back_blocks(B.n, groups)),
                               static_cast<int64_t>(resident(known, kernel, G, threads, smem)) * num_sms());
@@ -1254,8 +1251,8 @@ cudaError_t run_ln_grad(const Backward& B)
     int64_t parts = B.n > 0 ? grad_parts(B.n, B.c) : 0;
     cudaError_t e = cudaSuccess;
     if (B.n > 0) {
-        SO_PROFILE("layer_norm_grad", B.s);
         if (B.c > kMaxBackward) {
+            SO_PROFILE("layer_norm_grad_wide", B.s);
             const size_t smem = ((static_cast<size_t>(B.c) * sizeof(X) + 15) / 16 + (static_cast<size_t>(B.c) * sizeof(Y) + 15) / 16) * 16;
             e = smem <= kRingSmem && !(V * sizeof(X) == 2) ? run_grad_wide<X, Y, V, true>(B, smem) : run_grad_wide<X, Y, V, false>(B, 0);
             if (e == cudaSuccess && want)
@@ -1263,22 +1260,23 @@ cudaError_t run_ln_grad(const Backward& B)
                                                     static_cast<unsigned>(parts)),
                            dim3(kLnBlock), B.s, static_cast<const Y*>(B.dy), static_cast<const X*>(B.x), B.r, B.c, B.idx,
                            B.n, B.mean, B.rstd, B.part);
-        } else {
-            // two rows at a time where a lane's shares of both leave it the registers (single values, 123154
-            // x 236 fp32: one row 107 us, two, which spilled, 200)
-            constexpr int R = V > 2 && sizeof(X) == 2 ? 2 : 1;
-            const RingShape g = ring_shape<X, Y, V, true>(B.c, B.n);
+        } else if (const RingShape g = ring_shape<X, Y, V, true>(B.c, B.n); g.stages) {
+            SO_PROFILE("layer_norm_grad_ring", B.s);
             const bool even = V > 1 && B.c % (g.G * V) == 0;
-            if (g.stages && g.G <= 256)
+            if (g.G <= 256)
                 e = even ? run_grad_ring<X, Y, V, (V > 1), 256>(B, g, want, parts) : run_grad_ring<X, Y, V, false, 256>(B, g, want, parts);
-            else if (g.stages)
-                e = even ? run_grad_ring<X, Y, V, (V > 1), 512>(B, g, want, parts) : run_grad_ring<X, Y, V, false, 512>(B, g, want, parts);
-            else if (V < 4 && B.c <= static_cast<int64_t>(kMaxBackGroup) * 8)
-                e = run_grad_lane<X, Y, V, 8, 1, false>(B, want, parts);
-            else if (V > 1 && B.c % (lanes_of_block(B.c, 16, kLnBlock) * V) == 0)
-                e = run_grad_lane<X, Y, V, 16, R, (V > 1)>(B, want, parts);
             else
-                e = run_grad_lane<X, Y, V, 16, R, false>(B, want, parts);
+                e = even ? run_grad_ring<X, Y, V, (V > 1), 512>(B, g, want, parts) : run_grad_ring<X, Y, V, false, 512>(B, g, want, parts);
+        } else {
+            SO_PROFILE("layer_norm_grad", B.s);
+            if constexpr (V < 4) {   // rows of less than 1 KB
+                e = run_grad_lane<X, Y, V, 8, 1, false>(B, want, parts);
+            } else {
+                // two rows at a time where a lane's shares of both leave it the registers
+                constexpr int R = sizeof(X) == 2 ? 2 : 1;
+                e = B.c % (lanes_of_block(B.c, 16, kLnBlock) * V) == 0 ? run_grad_lane<X, Y, V, 16, R, true>(B, want, parts)
+                                                                       : run_grad_lane<X, Y, V, 16, R, false>(B, want, parts);
+            }
         }
     }
     if (e != cudaSuccess || !want) return e;

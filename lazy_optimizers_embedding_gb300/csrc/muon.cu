@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
 #pragma unroll
             for (int e = 0; e < E; ++e) s[0] = fmaf(u[q][e], u[q][e], s[0]);
     }
-    group_sum<1>(s, kMuonBlock, tmp, 0);
+    block_sum<1>(s, kMuonBlock, tmp, 0);
     if (s[0] < kSmallSquares) {   // the same for the whole block
 #pragma unroll 1
         for (int64_t i = first; i < size; i += step) {
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_norm(Update U, int64_t size
 #pragma unroll
             for (int e = 0; e < E; ++e) raised[0] = fmaf(u[e] * kRaise, u[e] * kRaise, raised[0]);
         }
-        group_sum<1>(raised, kMuonBlock, tmp, 1);
+        block_sum<1>(raised, kMuonBlock, tmp, 1);
     }
     if (threadIdx.x == 0) {
         part[blockIdx.x] = make_float2(s[0], raised[0]);

@@ -137,7 +137,7 @@ __device__ __forceinline__ Start start_scale(const float2* part, int parts, floa
         const float2 q = part[i];
         s[0] += q.x, s[1] += q.y;
     }
-    group_sum<2>(s, kThreads, tmp, 0);
+    block_sum<2>(s, kThreads, tmp, 0);
     const bool small = s[0] < kSmallSquares;   // both sums at once: a branch between two kept a block 2 us longer
     const float sum = small ? s[1] : s[0];
     return {small ? kRaise : 1.0f, sum != 0.0f ? kScale / (sqrtf(sum) + (small ? eps_raised : eps)) : 0.0f};

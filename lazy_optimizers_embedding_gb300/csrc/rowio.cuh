@@ -1,5 +1,5 @@
 // rowio.cuh -- a lane's share of a row of fp32 or bf16 values, held as read
-// (packed) until it is used, and the group sums of the row operators.
+// (packed) until it is used, and the sums over lanes and blocks.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -132,16 +132,11 @@ template <> struct Pack<bf16, 8> {
     }
 };
 
-// Sums of N values over a group of G lanes (a power of two, 1 to the block
-// size; groups start at multiples of G).  By butterflies: within a warp, then,
-// where a group is wider, over its warps' sums in `tmp` (2 * 32 * N words, the half
-// `half` used by turns: the barrier of the next call is what frees it), so every
-// lane holds the same bits.  (The warps' sums one after the other took 0.2 us more
-// for 8 warps.)  Every thread of the block calls it together when G > 32.
+// Sums of N values over a group of G lanes (a power of two, 1 to 32), by butterflies.
 template <int N>
-__device__ __forceinline__ void group_sum(float (&x)[N], int G, float* tmp, int half)
+__device__ __forceinline__ void lanes_sum(float (&x)[N], int G)
 {
-    if (G >= 32) {
+    if (G == 32) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
@@ -151,16 +146,27 @@ __device__ __forceinline__ void group_sum(float (&x)[N], int G, float* tmp, int 
 #pragma unroll
             for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(kFull, x[i], d);
     }
-    if (G <= 32) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = G >> 5;
+}
+
+// Sums of N values over a block of `threads` threads (a power of two).  By butterflies: within a warp,
+// then over the warps' sums in `tmp` (2 * 32 * N words, the half `half` used by turns: the
+// barrier of the next call is what frees it), so every lane holds the same bits.  (The
+// warps' sums one after the other took 0.2 us more for 8 warps.)
+template <int N>
+__device__ __forceinline__ void block_sum(float (&x)[N], int threads, float* tmp, int half)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(kFull, x[i], d);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = threads >> 5;
     float* t = tmp + half * 32 * N;
     if (lane == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i) t[i * 32 + warp] = x[i];
     __syncthreads();
-    const int w = (warp & ~(warps - 1)) + (lane & (warps - 1));
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = t[i * 32 + w];
+    for (int i = 0; i < N; ++i) x[i] = t[i * 32 + (lane & (warps - 1))];
     for (int d = warps >> 1; d > 0; d >>= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(kFull, x[i], d);

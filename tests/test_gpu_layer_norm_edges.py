@@ -92,3 +92,30 @@ def test_a_mean_far_above_the_spread(cuda_lib, n, c, yt):
     assert (np.abs(_np(k.dx) - rstd * (h - a - xhat * b)) <= 2 * K * U * rstd * size).all()
     assert (np.abs(_np(k.dgamma) - (dy * xhat).sum(0)) <= (512 + 4) * U * np.abs(dy * xhat).sum(0)).all()
     assert (np.abs(_np(k.dbeta) - dy.sum(0)) <= 512 * U * np.abs(dy).sum(0)).all()
+
+
+# columns on both sides of where another kernel takes over: (fp32 or bf16 x), (single values, pairs, packed)
+TAKEN = [(255, "f32", 9, "", ""), (256, "f32", 9, "", ""), (257, "f32", 9, "ring", "ring"), (254, "f32", 9, "", ""),
+         (258, "f32", 9, "ring", "ring"), (511, "bf16", 9, "", ""), (513, "bf16", 9, "ring", "ring"), (510, "bf16", 9, "", ""),
+         (514, "bf16", 9, "ring", "ring"), (1024, "f32", 9, "", ""), (1028, "f32", 9, "ring", ""), (1024, "bf16", 9, "", ""),
+         (1032, "bf16", 9, "ring", ""), (8192, "bf16", 2047, "ring", ""), (8192, "bf16", 2048, "ring", "ring"),
+         (4096, "f32", 4096, "ring", ""), (4100, "f32", 4096, "ring", "ring"), (8191, "f32", 9, "ring", "ring"),
+         (8192, "f32", 9, "ring", ""), (8193, "f32", 9, "wide", "wide"), (8196, "f32", 9, "wide", "wide"),
+         (8200, "bf16", 9, "wide", "wide")]
+
+
+@pytest.mark.parametrize("c,kind,n,forward,back", TAKEN)
+def test_which_kernel_takes_a_row(cuda_lib, c, kind, n, forward, back):
+    import torch
+    so = cuda_lib
+    k = Case(torch, so, n, c, kind, kind)
+    so.sparse_profile_enable()
+    so.sparse_profile_reset()
+    try:
+        k.run()
+        names = set(so.sparse_profile_read())
+    finally:
+        so.sparse_profile_enable(False)
+    name = lambda base, which: base + ("_" + which if which else "")  # noqa: E731
+    assert names == {name("layer_norm", forward), name("layer_norm_grad", back), "layer_norm_grad_join"}
+    k.compare()

@@ -188,6 +188,8 @@ _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 def _typed(t, name, like=None):
     """(pointer, sparse_dtype_t) of an fp32 or bf16 tensor, of like's type where that is given."""
+    if not (t is None or isinstance(t, torch.Tensor)):
+        raise TypeError(f"{name}: must be a tensor, whose type the call takes, got {type(t).__name__}")
     p = _ptr(t, like.dtype if like is not None else None, name)
     code = _DTYPES.get(t.dtype) if t is not None else F32
     if code is None:

@@ -1,5 +1,5 @@
-"""The package where the compiled module of the operators' calls is missing, was built for another PyTorch or
-cannot be built: the library is usable, and ctypes takes every call."""
+"""The binding where the compiled module of the operators' calls is missing, was built for another PyTorch or
+cannot be built (the library is usable, and ctypes takes every call), and what it refuses."""
 import os
 import shutil
 import subprocess
@@ -81,3 +81,15 @@ def test_another_pytorch_makes_the_module_stale(monkeypatch):
     assert not build._pycall_stale()
     monkeypatch.setattr(build, "pycall_key", lambda: "another")
     assert build._pycall_stale() and not build.pycall_usable()
+
+
+def test_a_pointer_where_a_tensor_says_the_type():
+    """An array whose type the call takes from it cannot come as an integer."""
+    import torch
+
+    from lazy_optimizers_embedding_gb300 import binding as so
+    e = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(TypeError, match="x: must be a tensor"):
+        so.sparse_layer_norm(256, 4, 8, None, 4, None, None, 1e-5, 256, None, None, e)
+    with pytest.raises(TypeError, match="u: must be a tensor"):
+        so.sparse_orthogonalize(256, 1, 4, 8, so.NsConfig(), 256, None, e)

@@ -21,6 +21,12 @@ bool valid_type(sparse_dtype_t t) { return t == SPARSE_F32 || t == SPARSE_BF16; 
 
 bool is_bf16(sparse_dtype_t t) { return t == SPARSE_BF16; }
 
+// An eps as fp32: one above 0 stays there (a row without spread has xhat = 0 with any but 0), a large one finite.
+float small_eps(double eps)
+{
+    return eps > 0.0 ? static_cast<float>(std::clamp(eps, static_cast<double>(FLT_TRUE_MIN), static_cast<double>(FLT_MAX))) : 0.0f;
+}
+
 sparse_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? SPARSE_OK : SPARSE_ERR_CUDA; }
 
 // n rows of c values, with n * c within int64 (and far from its end).
@@ -111,9 +117,8 @@ so::MuonParams muon_params(int64_t batch, int64_t r, int64_t c, const sparse_ns_
     M.a = static_cast<float>(ns.a);
     M.b = static_cast<float>(ns.b);
     M.c = static_cast<float>(ns.c);
-    auto narrow = [](double x) { return static_cast<float>(std::min(x, static_cast<double>(FLT_MAX))); };
-    M.eps = narrow(ns.eps);
-    M.eps_raised = narrow(ns.eps * 0x1p100);
+    M.eps = small_eps(ns.eps);
+    M.eps_raised = small_eps(ns.eps * 0x1p100);
     M.steps = ns.steps;
     M.products = ns.products;
     M.d_err = d_err;
@@ -140,7 +145,7 @@ sparse_status_t sparse_layer_norm(const void* x, sparse_dtype_t x_type, int64_t 
     if (y == nullptr) return SPARSE_ERR_INVALID_ARG;
     const bool xb = is_bf16(x_type), yb = is_bf16(y_type);
     const int vec = access(c, xb || yb, x, xb, y, yb, y, yb);
-    return from_cuda(layer_norm(x, is_bf16(x_type), r, c, idx, n, gamma, beta, static_cast<float>(eps), y,
+    return from_cuda(layer_norm(x, is_bf16(x_type), r, c, idx, n, gamma, beta, small_eps(eps), y,
                                 is_bf16(y_type), vec, mean, rstd, d_err, stream));
 }
 

@@ -119,3 +119,16 @@ def test_which_kernel_takes_a_row(cuda_lib, c, kind, n, forward, back):
     name = lambda base, which: base + ("_" + which if which else "")  # noqa: E731
     assert names == {name("layer_norm", forward), name("layer_norm_grad", back), "layer_norm_grad_join"}
     k.compare()
+
+
+@pytest.mark.parametrize("c", [64, 1111, 2048, 9000])
+def test_rows_of_zeros_with_any_eps_above_zero(cuda_lib, c):
+    """x - mean is 0, so y is beta, also where eps is below what fp32 holds or past it."""
+    import torch
+    for eps in (1e-5, 1e-38, 1e-44, 1e-60, 1e60):
+        k = Case(torch, cuda_lib, 5, c, "f32", "f32")
+        k.x.zero_()
+        so = cuda_lib
+        so.check(so.sparse_layer_norm(k.x, 5, c, None, 5, k.gamma, k.beta, eps, k.y, k.mean, k.rstd, k.err))
+        k.G.check("layer norm")
+        assert (k.y == k.beta).all() and (k.mean == 0).all() and torch.isfinite(k.rstd).all(), eps

@@ -19,13 +19,13 @@
 //                 times a, in every step but the last (there the small singular
 //                 values, tripled by a step, would drown in the rounding of the
 //                 large ones: 2e-2 of a low-rank matrix; in the last step X as
-//                 rounded is the better polynomial).  In a 64-bit simulation (more than 128 rows)
-//                 1.1e-3 to 1.5e-3 of the result's norm over flat, decaying and low-rank spectra,
-//                 2.5e-3 for rank one, about what rounding it to bf16 costs.
+//                 rounded is the better polynomial).  In a 64-bit simulation (more than 128 rows) at
+//                 most 1.7e-3 of the result's norm over flat, decaying and low-rank spectra and 2.5e-3
+//                 for rank one, about what rounding it to bf16 costs.
 //                 B is formed with a on its diagonal, so that B X holds a X.
 // (With three products a X is added in the epilogue: in the tensor unit's sums, which
-// round towards zero, it cost a low-rank matrix 4e-5.  Simulated as above: 4e-7 flat, 5e-6 low rank, 3.6e-5 for
-// rank one, where fp32 products give 1e-4.)
+// round towards zero, it cost a low-rank matrix 4e-5.  Simulated as above: 5e-7 flat, 6.5e-6 low rank, 3.6e-5
+// for rank one, where fp32 products give 1e-4.)
 #include <algorithm>
 
 #include "muon.cuh"

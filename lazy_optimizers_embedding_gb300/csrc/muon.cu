@@ -102,16 +102,18 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
     pdl_enter();   // writes the workspace and optimizer state only
     __shared__ float sums[2 * 32];
     __shared__ bool goes;
-    if (threadIdx.x == 0) goes = buf == nullptr || step_goes(verdict, d_err);
+    if (threadIdx.x == kMuonBlock - 1) goes = buf == nullptr || step_goes(verdict, d_err);
     const int mat = static_cast<int>(blockIdx.x) / pieces, p = static_cast<int>(blockIdx.x) % pieces;
     const int64_t base = mat * size, step = static_cast<int64_t>(pieces) * kMuonBlock * 8;
     const int64_t rows = size / c;
-    Start st{0.0f, 0.0f};   // not worked out yet
+    float scale = 0.0f;
+    bool scaled = false;
     for (int64_t i = (static_cast<int64_t>(p) * kMuonBlock + threadIdx.x) * 8; i - threadIdx.x * 8 < size; i += step) {
         float u[8], nb[8];
         if (i < size) read_u<8>(U, base + i, u, nb);
-        if (st.raise == 0.0f) {   // while those are on their way
-            st = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, eps_raised, sums);
+        if (!scaled) {   // while those are on their way
+            scaled = true;
+            scale = start_scale<kMuonBlock>(part + static_cast<int64_t>(mat) * parts, parts, eps, eps_raised, sums);
             if (!goes) return;   // (start_scale's barrier lies between)
         }
         if (i >= size) continue;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kMuonBlock) k_muon_start_flat(Update U, float*
         __half2* ll = reinterpret_cast<__half2*>(&l);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float a = u[2 * e] * st.raise * st.scale, b = u[2 * e + 1] * st.raise * st.scale;
+            const float a = x_of(u[2 * e], scale), b = x_of(u[2 * e + 1], scale);
             hh[e] = __floats2half2_rn(a, b);
             const float2 f = __half22float2(hh[e]);
             ll[e] = __floats2half2_rn(a - f.x, b - f.y);
@@ -146,11 +148,11 @@ __global__ void __launch_bounds__(kMuonBlock, 5) k_muon_start(Update U, float* _
     __shared__ float tile[64][65];
     __shared__ float sums[2 * 32];
     __shared__ bool goes;
-    if (threadIdx.x == 0) goes = buf == nullptr || step_goes(verdict, d_err);
+    if (threadIdx.x == kMuonBlock - 1) goes = buf == nullptr || step_goes(verdict, d_err);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t m = tall ? c : r;
     int64_t have = -1;
-    Start st{0.0f, 0.0f};
+    float scale = 0.0f;
     // neighbouring tiles by one block: few matrices, whose scales it has to work out
     const int t1 = static_cast<int>(static_cast<int64_t>(ntiles) * (blockIdx.x + 1) / gridDim.x);
     for (int t = static_cast<int>(static_cast<int64_t>(ntiles) * blockIdx.x / gridDim.x); t < t1; ++t) {
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kMuonBlock, 5) k_muon_start(Update U, float* _
         const int64_t r0 = q / tiles_c * 64, c0 = q % tiles_c * 64;
         if (mat != have) {
             if (have >= 0) __syncthreads();   // the last sums have been read
-            st = start_scale<kMuonBlock>(part + mat * parts, parts, eps, eps_raised, sums);
+            scale = start_scale<kMuonBlock>(part + mat * parts, parts, eps, eps_raised, sums);
             have = mat;
             if (!goes) return;   // (start_scale's barrier lies between)
         }
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kMuonBlock, 5) k_muon_start(Update U, float* _
         for (int y = 0; y < 4; ++y) {
             const int64_t row = r0 + ty + 16 * y, col = c0 + 4 * tx;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[y][e] = u[y][e] * st.raise * st.scale;
+            for (int e = 0; e < 4; ++e) u[y][e] = x_of(u[y][e], scale);
             if (tall) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) tile[ty + 16 * y][4 * tx + e] = u[y][e];

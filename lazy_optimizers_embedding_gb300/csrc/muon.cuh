@@ -122,15 +122,11 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8])
 constexpr float kSmallSquares = 0x1p-80f;
 constexpr float kRaise = 0x1p100f;
 
-// X = u raise scale: scale is 2^14 / (|u| raise + eps raise).  A matrix of zeros has scale 0, whatever eps.
-struct Start {
-    float raise, scale;
-};
-
-// The start of one matrix from its `parts` sums of squares (x, and raised y where x is small), by a block of
-// kThreads threads (`tmp`: 64 words).  fp32: in fp64 the root and quotient alone held a block for 4 us.
+// The scale of one matrix from its `parts` sums of squares (x, and raised y where x is small), by a block of
+// kThreads threads (`tmp`: 64 words).  Negative: of raised values, 2^14 / (|u| kRaise + eps kRaise), for x_of; a
+// matrix of zeros has scale 0, whatever eps.  fp32: in fp64 the root and quotient alone held a block for 4 us.
 template <int kThreads>
-__device__ __forceinline__ Start start_scale(const float2* part, int parts, float eps, float eps_raised, float* tmp)
+__device__ __forceinline__ float start_scale(const float2* part, int parts, float eps, float eps_raised, float* tmp)
 {
     float s[2] = {0.0f, 0.0f};
     for (int i = threadIdx.x; i < parts; i += kThreads) {
@@ -140,8 +136,10 @@ __device__ __forceinline__ Start start_scale(const float2* part, int parts, floa
     block_sum<2>(s, kThreads, tmp, 0);
     const bool small = s[0] < kSmallSquares;   // both sums at once: a branch between two kept a block 2 us longer
     const float sum = small ? s[1] : s[0];
-    return {small ? kRaise : 1.0f, sum != 0.0f ? kScale / (sqrtf(sum) + (small ? eps_raised : eps)) : 0.0f};
+    return sum != 0.0f ? (small ? -kScale : kScale) / (sqrtf(sum) + (small ? eps_raised : eps)) : 0.0f;
 }
+// X's value of u.
+__device__ __forceinline__ float x_of(float u, float scale) { return (scale < 0.0f ? u * -kRaise : u) * scale; }
 
 // Whether the matrices take the cluster path, and that path, once the sums of squares are on
 // their way (`vec`: 16-byte accesses of the update).

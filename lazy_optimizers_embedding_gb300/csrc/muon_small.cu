@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     __shared__ bool goes;
     __shared__ float sums[2 * 32];
     const uint32_t xhi = (smem_addr(raw) + 1023u) & ~1023u, xlo = xhi + kXBytes, shi = xlo + kXBytes, slo = shi + kSquareBytes, xrest = slo + kSquareBytes;
-    const uint32_t bar = smem_addr(bar_mem), drain = bar + 8;
+    const uint32_t bar = smem_addr(bar_mem);
     constexpr bool kRest = kLayout == kRests;
     const int fold = kLayout == kOnePart ? 1 : Q.fold;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
 
     if (threadIdx.x == 0) {
         dead = 0;
-        mbar_init(bar, 1), mbar_init(drain, 1);
+        mbar_init(bar, 1), mbar_init(bar + 8, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc<1>(&tmem_slot, kTmemCols);
@@ -168,10 +168,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();   // writes a caller output: dependents start after this grid exits
-    if (threadIdx.x == 0) goes = Q.w == nullptr || step_goes(Q.verdict, Q.d_err);
+    if (threadIdx.x == kBlockThreads - 1) goes = Q.w == nullptr || step_goes(Q.verdict, Q.d_err);   // (one that reads no sums)
 
     // X of the slice, scaled and split; the new momentum buffer
-    const Start st = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, Q.eps_raised, sums);
+    const float scale = start_scale<kBlockThreads>(Q.part + mat * Q.parts, Q.parts, Q.eps, Q.eps_raised, sums);
     const bool blocked = !goes;   // (start_scale's barrier lies between)
     const int64_t base = mat * Q.size;
     // Groups of lanes take u's rows (X's, or its columns where u is tall), a lane four values at a time: a
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
                     float left_over[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {   // 0 past `left`
-                        const float v = u[i][e] * st.raise * st.scale;
+                        const float v = x_of(u[i][e], scale);
                         const __half q = __float2half_rn(v), ql = __float2half_rn(v - __half2float(q));
                         h[e] = bits_of(q), l[e] = bits_of(ql);
                         left_over[e] = v - __half2float(q) - __half2float(ql);
@@ -494,9 +494,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1) k_muon_cluster(const Update 
             }
     if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
     if (warp == 0 && dead && elect_one()) {   // products in flight finish before their memory is given back
-        volatile int none = 0;
+        const uint32_t drain = smem_addr(bar_mem + 1);   // (by mbar_wait here the kernel's registers spilled)
         tc_commit<1>(drain);
-        mbar_wait(drain, 0, &none);
+        for (const uint64_t t0 = now_ns(); !mbar_try(drain, 0) && now_ns() - t0 < 2000000000ull;) {
+        }
     }
     __syncwarp();
     tc_fence_before();

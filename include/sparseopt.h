@@ -456,6 +456,102 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
                                            cudaStream_t stream);
 
 /*
+ * sparse_expert_route -- the experts of n tokens from their scores: the k largest of
+ * each row of logits [n, experts], largest first, of equal scores the lower index first,
+ * and their softmax weights: over the k that were picked (renormalize not 0) or over
+ * all experts (0).
+ *   logits              fp32 or bf16; -inf closes an expert to a token.  A NaN or +inf sets
+ *                       SPARSE_ERR_NON_FINITE
+ *   expert[n, k]        out: as sparse_expert_sort reads it; -1 where no score above -inf is left
+ *   weights[n, k]       out, fp32: as sparse_expert_combine reads them; 0 beside a -1
+ * 1 <= k <= experts <= 1024, k <= 32.
+ */
+sparse_status_t sparse_expert_route(const void* logits, sparse_dtype_t type, int64_t n, int64_t experts, int64_t k,
+                                    int renormalize, int64_t* expert, float* weights, int32_t* d_err, cudaStream_t stream);
+
+/*
+ * sparse_expert_route_grad -- the backward pass of sparse_expert_route, from the expert
+ * and weights that it wrote (a row's experts are different ones).  With s = sum of
+ * weights dweights over a token's picks:
+ *   renormalize: dlogits = weights (dweights - s) at the picks, 0 elsewhere (logits are not
+ *   read and may be NULL);  else, p the softmax over all experts: -p s, and
+ *   weights (dweights - s) at the picks
+ *   dweights[n, k] fp32 (beside a -1 not looked at); dlogits [n, experts] of logits' type.
+ * An expert outside [-1, experts) sets SPARSE_ERR_INDEX_OUT_OF_RANGE.
+ */
+sparse_status_t sparse_expert_route_grad(const float* dweights, const void* logits, sparse_dtype_t type, int64_t n,
+                                         int64_t experts, int64_t k, int renormalize, const int64_t* expert,
+                                         const float* weights, void* dlogits, int32_t* d_err, cudaStream_t stream);
+
+/* Bytes of workspace that sparse_expert_matmul (either way round) and
+ * sparse_expert_matmul_grad need for n rows and `experts` a x b matrices.  aligned: not 0
+ * says that every array given is on a 16-byte boundary; then bf16 arrays with rows of a
+ * multiple of 8 values are read where they lie. */
+size_t sparse_expert_matmul_workspace_size(sparse_dtype_t type, int64_t n, int64_t a, int64_t b, int64_t experts,
+                                           int aligned);
+
+/*
+ * sparse_expert_matmul -- every expert's rows by its matrix: the sorted places
+ * offsets[e] .. offsets[e+1]-1 (as sparse_expert_sort writes offsets) of x times w[e], and
+ * zeros in the places from offsets[experts] on, whatever lies there in x.
+ *   w [experts, a, b];  transpose 0: x [n, a], y [n, b] = x w[e];  not 0: x [n, b],
+ *   y [n, a] = x w[e]^T (the gradient of x, from that of y)
+ * x, w and y of one type.  bf16: products of bf16 values, fp32 sums, rounded once.  fp32:
+ * each value as three bf16 parts, the six products of parts above 2^-24 (22 bits and more);
+ * an infinite value gives NaN where fp32 arithmetic would give an infinity.  A row that is not
+ * finite spoils its own results only, a matrix its own expert's.
+ * Offsets that do not ascend from 0 to at most n set SPARSE_ERR_INDEX_OUT_OF_RANGE.
+ * Limits: experts <= 1024, n < 2^31, a, b <= 2^20, n max(a, b) and experts a b <= 2^37.
+ *   ws          sparse_expert_matmul_workspace_size() bytes, 256-byte aligned
+ */
+sparse_status_t sparse_expert_matmul(const void* x, const void* w, sparse_dtype_t type, int64_t n, int64_t a, int64_t b,
+                                     int transpose, const int64_t* offsets, int64_t experts, void* y, void* ws,
+                                     size_t ws_bytes, int32_t* d_err, cudaStream_t stream);
+
+/*
+ * sparse_expert_matmul_grad -- the matrices' gradient: dw[e] = x_e^T dy_e over expert
+ * e's places, zeros for an expert without any.
+ *   x [n, a], dy [n, b] of one type; dw [experts, a, b]: fp32, or bf16 beside bf16.
+ * Sums are fp32 in a fixed order.  Places from offsets[experts] on are not looked at.
+ */
+sparse_status_t sparse_expert_matmul_grad(const void* x, const void* dy, sparse_dtype_t type, int64_t n, int64_t a,
+                                          int64_t b, const int64_t* offsets, int64_t experts, void* dw,
+                                          sparse_dtype_t dw_type, void* ws, size_t ws_bytes, int32_t* d_err,
+                                          cudaStream_t stream);
+
+/* Bytes of workspace that sparse_vocab_loss (grad 0) or both sparse_vocab_loss and
+ * sparse_vocab_loss_grad (grad not 0) need; aligned as above. */
+size_t sparse_vocab_loss_workspace_size(sparse_dtype_t type, int64_t n, int64_t c, int64_t v, int grad, int aligned);
+
+/*
+ * sparse_vocab_loss -- softmax cross entropy of n tokens against all v rows of a table
+ * (an output layer, or the embedding table itself), without the n x v scores in memory:
+ *   z = x w^T, lse = log(sum over the rows of exp(z)), loss = lse - z[target]
+ *   x [n, c], w [v, c]  of one type, fp32 or bf16 (fp32 as in sparse_expert_matmul); scores and sums fp32
+ *   target[n]           a row of w, or -1 for a token that does not count: its loss is 0.
+ *                       Others set SPARSE_ERR_INDEX_OUT_OF_RANGE
+ *   loss[n], lse[n]     out, fp32; lse is kept for the backward pass
+ * Limits: n, v <= 2^30, c <= 2^20, n c and v c <= 2^37.
+ */
+sparse_status_t sparse_vocab_loss(const void* x, const void* w, sparse_dtype_t type, int64_t n, int64_t c, int64_t v,
+                                  const int64_t* target, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                  int32_t* d_err, cudaStream_t stream);
+
+/*
+ * sparse_vocab_loss_grad -- the backward pass of sparse_vocab_loss, from the lse it wrote:
+ *   G = dloss (exp(z - lse) - [target]) (0 for a token that does not count),
+ *   dx = G w, dw = G^T x
+ *   dloss[n]            fp32 (NULL: ones); dx [n, c], dw [v, c]: of x's type (each may be NULL);
+ *                       dw is the whole table's gradient, zeros where v has none
+ * With bf16, G is rounded to bf16 (an operand of the two products: 2^-9 of each of its values).
+ * A token that does not count has part in the products all the same, times zero: its x must be finite.
+ * Sums are in a fixed order: equal inputs give equal bits.
+ */
+sparse_status_t sparse_vocab_loss_grad(const float* dloss, const void* x, const void* w, sparse_dtype_t type, int64_t n,
+                                       int64_t c, int64_t v, const int64_t* target, const float* lse, void* dx, void* dw,
+                                       void* ws, size_t ws_bytes, int32_t* d_err, cudaStream_t stream);
+
+/*
  * Newton-Schulz orthogonalisation.  With X of min(r, c) rows (the matrix or its
  * transpose):  X = u / (|u|_F + eps), then `steps` times A = X X^T,
  * B = b A + c A^2, X = a X + B X.  a, b, c = 3.4445, -4.7750, 2.0315 and 5 steps

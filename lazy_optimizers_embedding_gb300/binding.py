@@ -110,6 +110,14 @@ def _load():
         "sparse_expert_dispatch": (INT, [P, INT, I64, I64, I64, P, P, I64, P, P, P]),
         "sparse_expert_combine": (INT, [P, INT, I64, I64, I64, P, P, P, P, P]),
         "sparse_expert_combine_grad": (INT, [P, P, INT, I64, I64, I64, P, P, I64, P, P, P, P, P]),
+        "sparse_expert_route": (INT, [P, INT, I64, I64, I64, INT, P, P, P, P]),
+        "sparse_expert_route_grad": (INT, [P, P, INT, I64, I64, I64, INT, P, P, P, P, P]),
+        "sparse_expert_matmul_workspace_size": (SZ, [INT, I64, I64, I64, I64, INT]),
+        "sparse_expert_matmul": (INT, [P, P, INT, I64, I64, I64, INT, P, I64, P, P, SZ, P, P]),
+        "sparse_expert_matmul_grad": (INT, [P, P, INT, I64, I64, I64, P, I64, P, INT, P, SZ, P, P]),
+        "sparse_vocab_loss_workspace_size": (SZ, [INT, I64, I64, I64, INT, INT]),
+        "sparse_vocab_loss": (INT, [P, P, INT, I64, I64, I64, P, P, P, P, SZ, P, P]),
+        "sparse_vocab_loss_grad": (INT, [P, P, P, INT, I64, I64, I64, P, P, P, P, P, SZ, P, P]),
         "sparse_muon_workspace_size": (SZ, [I64, I64, I64, INT]),
         "sparse_orthogonalize": (INT, [P, INT, I64, I64, I64, NsConfig, P, INT, P, SZ, P, P]),
         "sparse_muon_step": (INT, [P, P, P, INT, I64, I64, I64, MuonConfig, P, SZ, P, P]),
@@ -159,7 +167,10 @@ EXPORTED = ("sparse_workspace_size", "sparse_status_string", "sparse_canonicaliz
             "sparse_profile_reset", "sparse_profile_read", "sparse_read_rows", "sparse_check_finite",
             "sparse_check_state", "sparse_layer_norm_workspace_size", "sparse_layer_norm", "sparse_layer_norm_grad",
             "sparse_expert_workspace_size", "sparse_expert_sort", "sparse_expert_dispatch", "sparse_expert_combine",
-            "sparse_expert_combine_grad", "sparse_muon_workspace_size", "sparse_orthogonalize", "sparse_muon_step")
+            "sparse_expert_combine_grad", "sparse_expert_route", "sparse_expert_route_grad",
+            "sparse_expert_matmul_workspace_size", "sparse_expert_matmul", "sparse_expert_matmul_grad",
+            "sparse_vocab_loss_workspace_size", "sparse_vocab_loss", "sparse_vocab_loss_grad",
+            "sparse_muon_workspace_size", "sparse_orthogonalize", "sparse_muon_step")
 STATIC_WS_BYTES = 16 * 1024 * 1024  # SPARSE_STATIC_WS_BYTES
 
 
@@ -436,6 +447,93 @@ def sparse_expert_combine_grad(dy, ys, n, k, c, pos, offsets, experts, weights, 
                                           int(experts), _ptr(weights, torch.float32, "weights"),
                                           _typed(dys, "dys", ys)[0], _ptr(dweights, torch.float32, "dweights"),
                                           _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_expert_route(logits, n, experts, k, renormalize, expert, weights, d_err, stream=None) -> int:
+    """The type is that of logits."""
+    code = _pycall.expert_route(logits, n, experts, k, renormalize, expert, weights, d_err, stream)
+    if code is not None:
+        return code
+    lp, lt = _typed(logits, "logits")
+    return LIB.sparse_expert_route(lp, lt, int(n), int(experts), int(k), int(renormalize),
+                                   _ptr(expert, torch.int64, "expert"), _ptr(weights, torch.float32, "weights"),
+                                   _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_expert_route_grad(dweights, logits, n, experts, k, renormalize, expert, weights, dlogits, d_err,
+                             stream=None) -> int:
+    """The type is that of dlogits; logits may be None where the weights are renormalized."""
+    code = _pycall.expert_route_grad(dweights, logits, n, experts, k, renormalize, expert, weights, dlogits, d_err, stream)
+    if code is not None:
+        return code
+    dp, dt = _typed(dlogits, "dlogits")
+    return LIB.sparse_expert_route_grad(_ptr(dweights, torch.float32, "dweights"),
+                                        None if logits is None else _typed(logits, "logits", dlogits)[0], dt, int(n),
+                                        int(experts), int(k), int(renormalize), _ptr(expert, torch.int64, "expert"),
+                                        _ptr(weights, torch.float32, "weights"), dp, _ptr(d_err, torch.int32, "d_err"),
+                                        _stream(stream))
+
+
+def sparse_expert_matmul_workspace_size(dtype, n: int, a: int, b: int, experts: int, aligned: bool = True) -> int:
+    """dtype: torch.float32 or torch.bfloat16; aligned: every array lies on a 16-byte boundary, as torch's own
+    allocations do."""
+    return int(LIB.sparse_expert_matmul_workspace_size(_DTYPES[dtype], int(n), int(a), int(b), int(experts),
+                                                       int(bool(aligned))))
+
+
+def sparse_expert_matmul(x, w, n, a, b, transpose, offsets, experts, y, ws, d_err, stream=None) -> int:
+    code = _pycall.expert_matmul(x, w, n, a, b, transpose, offsets, experts, y, ws, d_err, stream)
+    if code is not None:
+        return code
+    wp, wb = _ws(ws)
+    xp, xt = _typed(x, "x")
+    return LIB.sparse_expert_matmul(xp, _typed(w, "w", x)[0], xt, int(n), int(a), int(b), int(transpose),
+                                    _ptr(offsets, torch.int64, "offsets"), int(experts), _typed(y, "y", x)[0], wp, wb,
+                                    _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_expert_matmul_grad(x, dy, n, a, b, offsets, experts, dw, ws, d_err, stream=None) -> int:
+    """dw may be fp32 beside bf16 rows."""
+    code = _pycall.expert_matmul_grad(x, dy, n, a, b, offsets, experts, dw, ws, d_err, stream)
+    if code is not None:
+        return code
+    wp, wb = _ws(ws)
+    xp, xt = _typed(x, "x")
+    dp, dt = _typed(dw, "dw")
+    return LIB.sparse_expert_matmul_grad(xp, _typed(dy, "dy", x)[0], xt, int(n), int(a), int(b),
+                                         _ptr(offsets, torch.int64, "offsets"), int(experts), dp, dt, wp, wb,
+                                         _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_vocab_loss_workspace_size(dtype, n: int, c: int, v: int, grad: bool, aligned: bool = True) -> int:
+    """dtype and aligned as in sparse_expert_matmul_workspace_size; grad: for the backward pass too."""
+    return int(LIB.sparse_vocab_loss_workspace_size(_DTYPES[dtype], int(n), int(c), int(v), int(bool(grad)),
+                                                    int(bool(aligned))))
+
+
+def sparse_vocab_loss(x, w, n, c, v, target, loss, lse, ws, d_err, stream=None) -> int:
+    code = _pycall.vocab_loss(x, w, n, c, v, target, loss, lse, ws, d_err, stream)
+    if code is not None:
+        return code
+    wp, wb = _ws(ws)
+    xp, xt = _typed(x, "x")
+    return LIB.sparse_vocab_loss(xp, _typed(w, "w", x)[0], xt, int(n), int(c), int(v), _ptr(target, torch.int64, "target"),
+                                 _ptr(loss, torch.float32, "loss"), _ptr(lse, torch.float32, "lse"), wp, wb,
+                                 _ptr(d_err, torch.int32, "d_err"), _stream(stream))
+
+
+def sparse_vocab_loss_grad(dloss, x, w, n, c, v, target, lse, dx, dw, ws, d_err, stream=None) -> int:
+    """dloss (ones), dx and dw (not wanted) may be None."""
+    code = _pycall.vocab_loss_grad(dloss, x, w, n, c, v, target, lse, dx, dw, ws, d_err, stream)
+    if code is not None:
+        return code
+    wp, wb = _ws(ws)
+    xp, xt = _typed(x, "x")
+    return LIB.sparse_vocab_loss_grad(_ptr(dloss, torch.float32, "dloss"), xp, _typed(w, "w", x)[0], xt, int(n), int(c),
+                                      int(v), _ptr(target, torch.int64, "target"), _ptr(lse, torch.float32, "lse"),
+                                      None if dx is None else _typed(dx, "dx", x)[0],
+                                      None if dw is None else _typed(dw, "dw", x)[0], wp, wb,
+                                      _ptr(d_err, torch.int32, "d_err"), _stream(stream))
 
 
 def sparse_muon_workspace_size(batch: int, r: int, c: int, products: int) -> int:

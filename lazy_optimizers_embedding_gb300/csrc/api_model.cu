@@ -59,6 +59,27 @@ bool valid_expert(sparse_dtype_t type, int64_t n, int64_t k, int64_t c, const in
            c <= kMaxExpertCols && d_err != nullptr;
 }
 
+bool valid_route(sparse_dtype_t type, int64_t n, int64_t experts, int64_t k, const int32_t* d_err)
+{
+    return valid_type(type) && n >= 0 && experts >= 1 && experts <= kMaxExperts && k >= 1 && k <= experts && k <= 32 &&
+           valid_rows(n, experts) && d_err != nullptr;
+}
+
+// Sizes that the tensor copies can address.
+constexpr int64_t kMaxCols = int64_t(1) << 20, kMaxValues = int64_t(1) << 37;
+
+bool valid_matmul(sparse_dtype_t type, int64_t n, int64_t a, int64_t b, int64_t experts)
+{
+    return valid_type(type) && n >= 0 && n <= INT32_MAX && a >= 1 && a <= kMaxCols && b >= 1 && b <= kMaxCols &&
+           experts >= 1 && experts <= kMaxExperts && n <= kMaxValues / std::max(a, b) && experts * a <= kMaxValues / b;
+}
+
+bool valid_loss(sparse_dtype_t type, int64_t n, int64_t c, int64_t v)
+{
+    return valid_type(type) && n >= 0 && n <= (1 << 30) && c >= 1 && c <= kMaxCols && v >= 1 && v <= (1 << 30) &&
+           n <= kMaxValues / c && v <= kMaxValues / c;
+}
+
 // Newton-Schulz keeps X, A = X X^T and B = b A + c A^2, with and without a on its
 // diagonal, as f16 values times 2^14: their singular values have to stay below
 // 65504 / 2^14 with 2 % to spare.  Bounded step by step, X's from [0, 1] on (all that a
@@ -221,6 +242,142 @@ sparse_status_t sparse_expert_combine_grad(const void* dy, const void* ys, spars
     const int vec = access(c, b, dy, b, ys, b, dys, b);
     return from_cuda(expert_combine_grad(dy, ys, is_bf16(type), n, k, c, pos, offsets + experts, weights, dys,
                                          dweights, vec, d_err, stream));
+}
+
+sparse_status_t sparse_expert_route(const void* logits, sparse_dtype_t type, int64_t n, int64_t experts, int64_t k,
+                                    int renormalize, int64_t* expert, float* weights, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_route(type, n, experts, k, d_err)) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (logits == nullptr || expert == nullptr || weights == nullptr) return SPARSE_ERR_INVALID_ARG;
+    return from_cuda(expert_route(logits, is_bf16(type), n, experts, static_cast<int>(k), renormalize != 0, expert, weights,
+                                  d_err, stream));
+}
+
+sparse_status_t sparse_expert_route_grad(const float* dweights, const void* logits, sparse_dtype_t type, int64_t n,
+                                         int64_t experts, int64_t k, int renormalize, const int64_t* expert,
+                                         const float* weights, void* dlogits, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_route(type, n, experts, k, d_err)) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (dweights == nullptr || (logits == nullptr && renormalize == 0) || expert == nullptr || weights == nullptr ||
+        dlogits == nullptr)
+        return SPARSE_ERR_INVALID_ARG;
+    return from_cuda(expert_route_grad(dweights, logits, is_bf16(type), n, experts, static_cast<int>(k), renormalize != 0,
+                                       expert, weights, dlogits, d_err, stream));
+}
+
+size_t sparse_expert_matmul_workspace_size(sparse_dtype_t type, int64_t n, int64_t a, int64_t b, int64_t experts, int aligned)
+{
+    if (!valid_matmul(type, n, a, b, experts)) return 0;
+    return n > 0 ? expert_matmul_ws_bytes(!is_bf16(type), n, a, b, experts, aligned != 0) : 256;
+}
+
+sparse_status_t sparse_expert_matmul(const void* x, const void* w, sparse_dtype_t type, int64_t n, int64_t a, int64_t b,
+                                     int transpose, const int64_t* offsets, int64_t experts, void* y, void* ws,
+                                     size_t ws_bytes, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_matmul(type, n, a, b, experts) || d_err == nullptr) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (x == nullptr || w == nullptr || offsets == nullptr || y == nullptr) return SPARSE_ERR_INVALID_ARG;
+    ExpertMatmul M{};
+    M.x = x;
+    M.w = w;
+    M.f32 = !is_bf16(type);
+    M.transpose = transpose != 0;
+    M.n = n;
+    M.a = a;
+    M.b = b;
+    M.experts = experts;
+    M.offsets = offsets;
+    M.out = y;
+    M.d_err = d_err;
+    if (!ws_ok(ws, ws_bytes, expert_matmul_ws_bytes(M))) return SPARSE_ERR_WORKSPACE;
+    return from_cuda(expert_matmul(M, ws, stream));
+}
+
+sparse_status_t sparse_expert_matmul_grad(const void* x, const void* dy, sparse_dtype_t type, int64_t n, int64_t a,
+                                          int64_t b, const int64_t* offsets, int64_t experts, void* dw,
+                                          sparse_dtype_t dw_type, void* ws, size_t ws_bytes, int32_t* d_err,
+                                          cudaStream_t stream)
+{
+    if (!valid_matmul(type, n, a, b, experts) || !valid_type(dw_type) || (is_bf16(dw_type) && !is_bf16(type)) ||
+        dw == nullptr || d_err == nullptr)
+        return SPARSE_ERR_INVALID_ARG;
+    if (n == 0)
+        return from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(experts * a * b) * (is_bf16(dw_type) ? 2 : 4), stream));
+    if (x == nullptr || dy == nullptr || offsets == nullptr) return SPARSE_ERR_INVALID_ARG;
+    ExpertMatmul M{};
+    M.x = x;
+    M.dy = dy;
+    M.f32 = !is_bf16(type);
+    M.out_bf16 = is_bf16(dw_type);
+    M.n = n;
+    M.a = a;
+    M.b = b;
+    M.experts = experts;
+    M.offsets = offsets;
+    M.out = dw;
+    M.d_err = d_err;
+    if (!ws_ok(ws, ws_bytes, expert_matmul_ws_bytes(M))) return SPARSE_ERR_WORKSPACE;
+    return from_cuda(expert_matmul_grad(M, ws, stream));
+}
+
+size_t sparse_vocab_loss_workspace_size(sparse_dtype_t type, int64_t n, int64_t c, int64_t v, int grad, int aligned)
+{
+    if (!valid_loss(type, n, c, v)) return 0;
+    if (n == 0) return 256;
+    const size_t forward = vocab_loss_ws_bytes(!is_bf16(type), n, c, v, 0, aligned != 0);
+    return grad ? std::max(forward, vocab_loss_ws_bytes(!is_bf16(type), n, c, v, 1, aligned != 0)) : forward;
+}
+
+sparse_status_t sparse_vocab_loss(const void* x, const void* w, sparse_dtype_t type, int64_t n, int64_t c, int64_t v,
+                                  const int64_t* target, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                  int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_loss(type, n, c, v) || d_err == nullptr) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0) return SPARSE_OK;
+    if (x == nullptr || w == nullptr || target == nullptr || loss == nullptr || lse == nullptr) return SPARSE_ERR_INVALID_ARG;
+    VocabLoss V{};
+    V.x = x;
+    V.w = w;
+    V.f32 = !is_bf16(type);
+    V.n = n;
+    V.c = c;
+    V.v = v;
+    V.target = target;
+    V.loss = loss;
+    V.lse = lse;
+    V.d_err = d_err;
+    if (!ws_ok(ws, ws_bytes, vocab_loss_ws_bytes(V, 0))) return SPARSE_ERR_WORKSPACE;
+    return from_cuda(vocab_loss(V, ws, stream));
+}
+
+sparse_status_t sparse_vocab_loss_grad(const float* dloss, const void* x, const void* w, sparse_dtype_t type, int64_t n,
+                                       int64_t c, int64_t v, const int64_t* target, const float* lse, void* dx, void* dw,
+                                       void* ws, size_t ws_bytes, int32_t* d_err, cudaStream_t stream)
+{
+    if (!valid_loss(type, n, c, v) || d_err == nullptr) return SPARSE_ERR_INVALID_ARG;
+    if (n == 0)   // no token: no gradient
+        return dw == nullptr ? SPARSE_OK
+                             : from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(v * c) * (is_bf16(type) ? 2 : 4), stream));
+    if (x == nullptr || w == nullptr || target == nullptr || lse == nullptr) return SPARSE_ERR_INVALID_ARG;
+    if (dx == nullptr && dw == nullptr) return SPARSE_OK;
+    VocabLoss V{};
+    V.x = x;
+    V.w = w;
+    V.f32 = !is_bf16(type);
+    V.n = n;
+    V.c = c;
+    V.v = v;
+    V.target = target;
+    V.lse = const_cast<float*>(lse);
+    V.dloss = dloss;
+    V.dx = dx;
+    V.dw = dw;
+    V.d_err = d_err;
+    if (!ws_ok(ws, ws_bytes, vocab_loss_ws_bytes(V, 1))) return SPARSE_ERR_WORKSPACE;
+    return from_cuda(vocab_loss_grad(V, ws, stream));
 }
 
 size_t sparse_muon_workspace_size(int64_t batch, int64_t r, int64_t c, int products)

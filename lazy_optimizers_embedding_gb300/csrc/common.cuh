@@ -393,6 +393,43 @@ cudaError_t expert_combine_grad(const void* dy, const void* ys, int is_bf16, int
                                 const int32_t* pos, const int64_t* end, const float* w, void* dys, float* dw, int vec,
                                 int32_t* d_err, cudaStream_t s);
 
+// Routing (route.cu).
+cudaError_t expert_route(const void* logits, int is_bf16, int64_t n, int64_t experts, int k, int renormalize, int64_t* expert,
+                         float* weights, int32_t* d_err, cudaStream_t s);
+cudaError_t expert_route_grad(const float* dweights, const void* logits, int is_bf16, int64_t n, int64_t experts, int k,
+                              int renormalize, const int64_t* expert, const float* weights, void* dlogits, int32_t* d_err,
+                              cudaStream_t s);
+
+// Products of every expert's rows with its matrix, and their gradient (expert_matmul.cu).
+struct ExpertMatmul {
+    const void *x, *w, *dy;   // rows; matrices (the product) or the rows' gradients (its gradient)
+    int f32, transpose, out_bf16;
+    int64_t n, a, b, experts;
+    const int64_t* offsets;
+    void* out;
+    int32_t* d_err;
+};
+size_t expert_matmul_ws_bytes(int f32, int64_t n, int64_t a, int64_t b, int64_t experts, int is_aligned);
+size_t expert_matmul_ws_bytes(const ExpertMatmul& M);   // of one call
+cudaError_t expert_matmul(const ExpertMatmul& M, void* ws, cudaStream_t s);
+cudaError_t expert_matmul_grad(const ExpertMatmul& M, void* ws, cudaStream_t s);
+
+// Softmax cross entropy over a table's rows and its gradient (vocab_loss.cu).
+struct VocabLoss {
+    const void *x, *w;
+    int f32;
+    int64_t n, c, v;
+    const int64_t* target;
+    float *loss, *lse;        // the gradient reads lse
+    const float* dloss;
+    void *dx, *dw;
+    int32_t* d_err;
+};
+size_t vocab_loss_ws_bytes(int f32, int64_t n, int64_t c, int64_t v, int grad, int is_aligned);
+size_t vocab_loss_ws_bytes(const VocabLoss& V, int grad);
+cudaError_t vocab_loss(const VocabLoss& V, void* ws, cudaStream_t s);
+cudaError_t vocab_loss_grad(const VocabLoss& V, void* ws, cudaStream_t s);
+
 // Newton-Schulz orthogonalisation and the Muon step (muon.cu).
 struct MuonParams {
     const void* g;        // the update itself (buf = nullptr) or the gradient

@@ -793,30 +793,13 @@ __global__ void __launch_bounds__(Shape<kKind, kPair, kSplit, BN, P, G>::kThread
 }
 
 // -------------------------------------------------------------------- host
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder()
-{
-    static const EncodeTiled f = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult how;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &how) != cudaSuccess ||
-            how != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
 // Boxes of 64 rows x 64 values of a batch of rows x cols f16 matrices; zeros beyond.
 bool encode(CUtensorMap* map, const __half* at, int64_t rows, int64_t cols, int64_t ld, int64_t batch)
 {
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
     const cuuint64_t stride[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld * rows) * 2};
     const cuuint32_t box[3] = {kBK, kBox, 1}, step[3] = {1, 1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(at), dim, stride, box, step,
+    return tensor_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(at), dim, stride, box, step,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1009,7 +992,7 @@ size_t muon_ws_bytes(int64_t batch, int64_t r, int64_t c, int products) { return
 
 cudaError_t muon(const MuonParams& M, void* ws, cudaStream_t s)
 {
-    if (encoder() == nullptr) return cudaErrorNotSupported;
+    if (tensor_encoder() == nullptr) return cudaErrorNotSupported;
     const Layout L = muon_layout(M.batch, M.r, M.cols, M.products);
     uint8_t* base = static_cast<uint8_t*>(ws);
     float2* part = reinterpret_cast<float2*>(base + L.part);

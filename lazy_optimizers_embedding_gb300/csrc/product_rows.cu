@@ -1,0 +1,196 @@
+// product_rows.cu -- rows by the matrix of their group, what packs operands for the
+// products, and what joins the sums of a long inner dimension's parts.
+#include "product.cuh"
+
+namespace so {
+
+namespace {
+
+constexpr int kPackBlock = 256;
+
+// Eight values from `from` on, those below `left`.
+template <class T, bool kVec>
+__device__ __forceinline__ void read8(const T* from, int64_t left, float (&x)[8])
+{
+    if (kVec) {
+        Pack<T, 8> q;
+        q.load(from);
+        q.get(x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            Pack<T, 1> q;
+            float one[1];
+            q.zero();
+            if (e < left) q.load(from + e);
+            q.get(one);
+            x[e] = one[0];
+        }
+    }
+}
+
+// A part of v: its bf16, one that stays finite where v is (values above bf16's largest, which would round to
+// infinity, are cut off; what is left goes to the next part).
+__device__ __forceinline__ float part_of(float v)
+{
+    const float h = __bfloat162float(__float2bfloat16_rn(v));
+    return isinf(h) && isfinite(v) ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : h;
+}
+
+template <class T, bool kVec>
+__device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t warps, int lane)
+{
+    constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+    const int64_t groups = A.ld / 8;
+    const int G = groups >= 32 ? 32 : groups > 16 ? 32 : groups > 8 ? 16 : groups > 4 ? 8 : groups > 2 ? 4 : static_cast<int>(groups);
+    const int each = 32 / G;   // rows of a warp at a time
+    const int64_t size = A.rows * A.ld;
+    for (int64_t r = warp * each + lane / G; r < A.rows; r += warps * each)
+        for (int64_t g = lane % G; g * 8 < A.cols; g += G) {
+            float x[8];
+            read8<T, kVec>(static_cast<const T*>(A.from) + r * A.cols + g * 8, A.cols - g * 8, x);
+            bf16* to = A.to + r * A.ld + g * 8;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                float h[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    h[e] = kParts == 1 ? x[e] : part_of(x[e]);
+                    x[e] = isfinite(h[e]) ? x[e] - h[e] : 0.0f;   // an infinity or NaN is all in the first part
+                }
+                Pack<bf16, 8>::put(to + p * size, h);
+            }
+        }
+}
+
+// Rows of one or two arrays as bf16 with aligned rows: fp32 in three parts, hi = bf16(v), mid = bf16(v - hi), lo = what
+// those leave (2^-26 of v at most).  Bound by memory: 4 bytes in, 6 out.
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kPackBlock) k_pack(const Pack1 A, const Pack1 B, int blocks_a)
+{
+    pdl_enter();   // writes the workspace only
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = kPackBlock / 32;
+    if (static_cast<int>(blockIdx.x) < blocks_a)
+        pack_rows<T, kVec>(A, static_cast<int64_t>(blockIdx.x) * per + w, static_cast<int64_t>(blocks_a) * per, lane);
+    else
+        pack_rows<T, kVec>(B, static_cast<int64_t>(blockIdx.x - blocks_a) * per + w,
+                           static_cast<int64_t>(gridDim.x - blocks_a) * per, lane);
+}
+
+// Sums of slabs in order, one value a thread.
+template <class T>
+__global__ void __launch_bounds__(256) k_join_slabs(const float* __restrict__ from, int slabs, int64_t slab, int64_t rows,
+                                                    int64_t cols, const int64_t* __restrict__ end, T* __restrict__ out)
+{
+    pdl_wait();
+    const int64_t count = rows * cols;
+    const int64_t live = end ? min(max(*end, static_cast<int64_t>(0)), rows) * cols : count;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += static_cast<int64_t>(gridDim.x) * 256) {
+        float s = 0.0f;
+        if (i < live)
+            for (int q = 0; q < slabs; ++q) s += from[q * slab + i];
+        out[i] = T(s);
+    }
+}
+
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+// Pairs of blocks take 256 rows of M: not where those would leave much of a tile empty, nor where
+// there are fewer tiles than pairs.
+bool wants_pair(int64_t m, int64_t tiles_of_128)
+{
+    return up(m, 256) * 2 <= up(m, 128) + up(m, 128) / 4 && tiles_of_128 >= num_sms();
+}
+
+// Tiles at most: every group may end in a part of one.
+int64_t row_tiles(int64_t rows, int64_t groups, int64_t width) { return groups == 1 ? up(rows, width) : rows / width + std::min(rows, groups); }
+
+template <class S>
+cudaError_t rows_form(const RowsProduct& R, cudaStream_t s)
+{
+    ProductMaps maps;
+    if (!R.a.map(&maps.a) || !R.b.map(&maps.b)) return cudaErrorInvalidValue;
+    ProductArgs Q{};
+    Q.rows = static_cast<int32_t>(R.rows);
+    Q.m = static_cast<int32_t>(R.m);
+    Q.k = static_cast<int32_t>(R.k);
+    Q.m_tiles = static_cast<int32_t>(up(R.m, S::TM));
+    Q.width = S::BN;
+    const int64_t units = num_sms() / S::kPair;
+    if (R.groups == 1) {   // the width whose rounds over the GPU take least
+        int64_t best = INT64_MAX;
+        for (int w = S::BN; w >= 64; w -= 32) {
+            const int64_t cost = up(up(R.rows, w) * Q.m_tiles * R.splits, units) * w;
+            if (cost < best) best = cost, Q.width = w;
+        }
+    }
+    Q.groups = R.groups;
+    Q.splits = R.splits;
+    Q.offsets = R.offsets;
+    Q.out = R.out;
+    Q.add = R.add ? static_cast<const float*>(R.out) : nullptr;
+    Q.slab = R.rows * R.m;
+    Q.ld = static_cast<int32_t>(R.m);
+    Q.out_bf16 = R.out_bf16;
+    Q.clear = R.clear;
+    Q.release = R.release;
+    Q.d_err = R.d_err;
+    return run_product<S>("rows_product", maps, Q, row_tiles(R.rows, R.groups, Q.width) * Q.m_tiles * R.splits, s);
+}
+
+}  // namespace
+
+cudaError_t pack(const Pack1& a, const Pack1& b, int is_bf16, cudaStream_t s)
+{
+    auto blocks = [](const Pack1& p) { return std::min<int64_t>(8 * num_sms(), up(p.rows * up(p.ld, 8), 8 * kPackBlock)); };
+    const int64_t na = blocks(a), nb = blocks(b);
+    if (na + nb == 0) return cudaSuccess;
+    const int v = is_bf16 ? 8 : 4;
+    auto fits = [&](const Pack1& p) {
+        return p.rows == 0 || (p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.from) % (is_bf16 ? 2 * v : 4 * v) == 0);
+    };
+    const bool vec = fits(a) && fits(b);
+    const dim3 grid(static_cast<unsigned>(na + nb)), block(kPackBlock);
+    SO_PROFILE("pack", s);
+    if (is_bf16)
+        return vec ? launch(k_pack<bf16, true>, grid, block, s, a, b, static_cast<int>(na))
+                   : launch(k_pack<bf16, false>, grid, block, s, a, b, static_cast<int>(na));
+    return vec ? launch(k_pack<float, true>, grid, block, s, a, b, static_cast<int>(na))
+               : launch(k_pack<float, false>, grid, block, s, a, b, static_cast<int>(na));
+}
+
+cudaError_t join_slabs(const float* from, int slabs, int64_t slab, int64_t rows, int64_t cols, const int64_t* end, void* out,
+                       int out_bf16, cudaStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(8 * num_sms(), up(rows * cols, 256))))), block(256);
+    SO_PROFILE("join_slabs", s);
+    return out_bf16 ? launch(k_join_slabs<bf16>, grid, block, s, from, slabs, slab, rows, cols, end, static_cast<bf16*>(out))
+                    : launch(k_join_slabs<float>, grid, block, s, from, slabs, slab, rows, cols, end, static_cast<float*>(out));
+}
+
+int rows_splits(int64_t rows, int64_t m, int64_t k, int64_t groups, int parts)
+{
+    const int64_t width = parts == 3 ? 128 : 256;
+    const int64_t tiles = row_tiles(rows, groups, width) * up(m, 128);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_sms() / std::max<int64_t>(tiles, 1), up(k, kPK) / 4, 64})));
+}
+
+cudaError_t rows_product(const RowsProduct& R, cudaStream_t s)
+{
+    const int64_t width = R.b.parts == 3 ? 128 : 256;
+    const bool pair = R.splits == 1 && wants_pair(R.m, row_tiles(R.rows, R.groups, width) * up(R.m, 128));
+    if (R.b.parts == 3) {
+        if (R.a_mn)
+            return pair ? rows_form<ProductShape<kRows, true, false, 2, 6, false>>(R, s)
+                        : rows_form<ProductShape<kRows, true, false, 1, 6, false>>(R, s);
+        return pair ? rows_form<ProductShape<kRows, false, false, 2, 6, false>>(R, s)
+                    : rows_form<ProductShape<kRows, false, false, 1, 6, false>>(R, s);
+    }
+    if (R.a_mn)
+        return pair ? rows_form<ProductShape<kRows, true, false, 2, 1, false>>(R, s)
+                    : rows_form<ProductShape<kRows, true, false, 1, 1, false>>(R, s);
+    return pair ? rows_form<ProductShape<kRows, false, false, 2, 1, false>>(R, s)
+                : rows_form<ProductShape<kRows, false, false, 1, 1, false>>(R, s);
+}
+
+}  // namespace so

@@ -220,6 +220,95 @@ PyObject* expert_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+PyObject* expert_route(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return run(a, n, 9, [](Args& g) {
+        sparse_dtype_t t;
+        void* logits = g.typed(0, t);
+        return [=, rows = g.number(1), experts = g.number(2), k = g.number(3), again = g.number(4) != 0, expert = g.longs(5),
+                weights = g.floats(6), err = g.ints(7), s = g.stream(8)] {
+            return sparse_expert_route(logits, t, rows, experts, k, again, expert, weights, err, s);
+        };
+    });
+}
+
+PyObject* expert_route_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return run(a, n, 11, [](Args& g) {
+        sparse_dtype_t t;
+        void* dlogits = g.typed(8, t);
+        void* logits = g.typed(1, t, true);
+        return [=, dweights = g.floats(0), rows = g.number(2), experts = g.number(3), k = g.number(4),
+                again = g.number(5) != 0, expert = g.longs(6), weights = g.floats(7), err = g.ints(9), s = g.stream(10)] {
+            return sparse_expert_route_grad(dweights, logits, t, rows, experts, k, again, expert, weights, dlogits, err, s);
+        };
+    });
+}
+
+PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return run(a, n, 12, [](Args& g) {
+        sparse_dtype_t t;
+        size_t bytes;
+        void* x = g.typed(0, t);
+        void* w = g.typed(1, t, true);
+        void* y = g.typed(8, t, true);
+        void* ws = g.workspace(9, bytes);
+        return [=, rows = g.number(2), ca = g.number(3), cb = g.number(4), turned = g.number(5) != 0, offsets = g.longs(6),
+                experts = g.number(7), err = g.ints(10), s = g.stream(11)] {
+            return sparse_expert_matmul(x, w, t, rows, ca, cb, turned, offsets, experts, y, ws, bytes, err, s);
+        };
+    });
+}
+
+PyObject* expert_matmul_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return run(a, n, 11, [](Args& g) {
+        sparse_dtype_t t, wt;
+        size_t bytes;
+        void* x = g.typed(0, t);
+        void* dy = g.typed(1, t, true);
+        void* dw = g.typed(7, wt);
+        void* ws = g.workspace(8, bytes);
+        return [=, rows = g.number(2), ca = g.number(3), cb = g.number(4), offsets = g.longs(5), experts = g.number(6),
+                err = g.ints(9), s = g.stream(10)] {
+            return sparse_expert_matmul_grad(x, dy, t, rows, ca, cb, offsets, experts, dw, wt, ws, bytes, err, s);
+        };
+    });
+}
+
+PyObject* vocab_loss(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return run(a, n, 11, [](Args& g) {
+        sparse_dtype_t t;
+        size_t bytes;
+        void* x = g.typed(0, t);
+        void* w = g.typed(1, t, true);
+        void* ws = g.workspace(8, bytes);
+        return [=, rows = g.number(2), c = g.number(3), v = g.number(4), target = g.longs(5), loss = g.floats(6),
+                lse = g.floats(7), err = g.ints(9), s = g.stream(10)] {
+            return sparse_vocab_loss(x, w, t, rows, c, v, target, loss, lse, ws, bytes, err, s);
+        };
+    });
+}
+
+PyObject* vocab_loss_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return run(a, n, 13, [](Args& g) {
+        sparse_dtype_t t;
+        size_t bytes;
+        void* x = g.typed(1, t);
+        void* w = g.typed(2, t, true);
+        void* dx = g.typed(8, t, true);
+        void* dw = g.typed(9, t, true);
+        void* ws = g.workspace(10, bytes);
+        return [=, dloss = g.floats(0), rows = g.number(3), c = g.number(4), v = g.number(5), target = g.longs(6),
+                lse = g.floats(7), err = g.ints(11), s = g.stream(12)] {
+            return sparse_vocab_loss_grad(dloss, x, w, t, rows, c, v, target, lse, dx, dw, ws, bytes, err, s);
+        };
+    });
+}
+
 PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return run(a, n, 9, [](Args& g) {
@@ -268,6 +357,8 @@ PyObject* configs(PyObject*, PyObject* const* a, Py_ssize_t n)
 #define SO_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SO_METHOD(layer_norm),      SO_METHOD(layer_norm_grad), SO_METHOD(expert_sort),
                          SO_METHOD(expert_dispatch), SO_METHOD(expert_combine),  SO_METHOD(expert_combine_grad),
+                         SO_METHOD(expert_route),    SO_METHOD(expert_route_grad), SO_METHOD(expert_matmul),
+                         SO_METHOD(expert_matmul_grad), SO_METHOD(vocab_loss),   SO_METHOD(vocab_loss_grad),
                          SO_METHOD(orthogonalize),   SO_METHOD(muon_step),       SO_METHOD(configs),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

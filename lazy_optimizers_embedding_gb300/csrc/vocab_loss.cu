@@ -1,0 +1,272 @@
+// vocab_loss.cu -- softmax cross entropy of n tokens against all rows of a table, and
+// its gradient, without the n x v scores.
+//
+//   z = x W^T, lse = log sum exp z, loss = lse - z[target]
+//   G = dloss (exp(z - lse) - [target]), dx = G W, dW = G^T x
+//
+// Forward, a product whose epilogue keeps a running maximum and sum of exponentials for every token (a lane
+// has a token, so nothing is exchanged) over the tiles of an item: some hundred of the table's rows
+// for 256 tokens; a second launch joins the items.  Scores stay in tensor memory and registers.
+// Backward, the scores are made again for a piece of the table at a time, and their slopes G kept as
+// bf16 (fp32 operands: three bf16 parts): G and the piece's rows make the piece's share of dx, which is summed
+// in fp32 over the pieces, G and x the piece's rows of dW, complete.  A piece is as wide as kSlopeBytes allows.
+#include "product.cuh"
+
+namespace so {
+
+namespace {
+
+constexpr size_t kSlopeBytes = size_t(256) << 20;   // G of one piece, all parts
+
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+struct Grid {
+    int width, run, items;   // columns of a tile, tiles of an item, items in a row of them
+    bool pair;
+};
+
+// Tiles of the scores: the width and run whose rounds over the GPU take least (a run costs its item one write of
+// the running sums; with one of 1 to 16 there are enough items to choose from).
+Grid score_grid(int64_t n, int64_t v, int parts, bool runs)
+{
+    Grid g{};
+    g.pair = n > 128;
+    const int most = parts == 3 ? 128 : 256;
+    const int64_t units = num_sms() / (g.pair ? 2 : 1), m_tiles = up(n, g.pair ? 256 : 128);
+    int64_t best = INT64_MAX;
+    for (int w = most; w >= most / 2; w -= 32)
+        for (int run = runs ? 16 : 1; run >= 1; run /= 2) {
+            const int64_t items = up(up(v, w), run);
+            const int64_t cost = up(items * m_tiles, units) * run * (w + 8) + 16;
+            if (cost < best) best = cost, g.width = w, g.run = run, g.items = static_cast<int>(items);
+        }
+    return g;
+}
+
+// The items' sums of 32 tokens a block: each warp some of them, then the warps'.
+__global__ void __launch_bounds__(1024) k_loss_join(const float2* __restrict__ part, int slots, const float* __restrict__ hit,
+                                                    const int64_t* __restrict__ target, int64_t n, float* __restrict__ loss,
+                                                    float* __restrict__ lse)
+{
+    pdl_wait();
+    __shared__ float2 sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    float top = -INFINITY, sum = 0.0f;
+    auto add = [&](float2 q) {
+        const float high = fmaxf(top, q.x), base = high == -INFINITY ? 0.0f : high;
+        sum = sum * exp2_fast((top - base) * kLog2e) + q.y * exp2_fast((q.x - base) * kLog2e);
+        top = high;
+    };
+    if (row < n)
+#pragma unroll 4
+        for (int s = warp; s < slots; s += 32) add(part[static_cast<int64_t>(s) * n + row]);
+    sums[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    // warp w joins token w's 32
+    float2 q = sums[lane][warp];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float t = __shfl_xor_sync(kFull, q.x, d), u = __shfl_xor_sync(kFull, q.y, d);
+        const float high = fmaxf(q.x, t), base = high == -INFINITY ? 0.0f : high;
+        q.y = q.y * exp2_fast((q.x - base) * kLog2e) + u * exp2_fast((t - base) * kLog2e);
+        q.x = high;
+    }
+    const int64_t mine = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && mine < n) {
+        const float l = q.x + logf(q.y);
+        lse[mine] = l;
+        loss[mine] = target[mine] < 0 ? 0.0f : l - hit[mine];
+    }
+}
+
+struct Layout {
+    int parts;
+    bool pack_x, pack_w;
+    int64_t ldx, ldw;        // of the packed arrays, or c
+    Grid score, slope;
+    int64_t piece, pieces, ldg;
+    int dx_splits, dw_splits;
+    bool dx_slabs, dw_slabs;
+    size_t x, w, part, hit, g, dx, dw, total;
+};
+
+Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_aligned, bool w_aligned)
+{
+    Layout L{};
+    L.parts = f32 ? 3 : 1;
+    L.pack_x = f32 || c % 8 != 0 || !x_aligned;
+    L.pack_w = f32 || c % 8 != 0 || !w_aligned;
+    L.ldx = L.pack_x ? packed_ld(c) : c;
+    L.ldw = L.pack_w ? packed_ld(c) : c;
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t p = at;
+        at += (static_cast<size_t>(bytes) + 255) / 256 * 256;
+        return p;
+    };
+    if (L.pack_x) L.x = take(2 * L.parts * n * L.ldx);
+    if (L.pack_w) L.w = take(2 * L.parts * v * L.ldw);
+    if (!grad) {
+        L.score = score_grid(n, v, L.parts, true);
+        const int groups = f32 ? 2 : 4;
+        L.part = take(static_cast<int64_t>(sizeof(float2)) * L.score.items * groups * n);
+        L.hit = take(static_cast<int64_t>(sizeof(float)) * n);
+    } else {
+        const int64_t most = std::max<int64_t>(256, static_cast<int64_t>(kSlopeBytes) / (2 * L.parts * n) / 256 * 256);
+        L.pieces = up(v, most);
+        L.piece = up(up(v, L.pieces), 256) * 256;
+        L.pieces = up(v, L.piece);
+        L.ldg = std::min(L.piece, up(v, 8) * 8);
+        L.slope = score_grid(n, L.piece, L.parts, false);
+        L.g = take(2 * L.parts * n * L.ldg);
+        L.dx_splits = rows_splits(n, c, L.piece, 1, L.parts);
+        L.dx_slabs = L.pieces > 1 || L.dx_splits > 1;
+        if (L.dx_slabs) L.dx = take(4 * L.dx_splits * n * c);
+        L.dw_splits = weights_splits(n, c, L.piece, 1, L.parts);
+        L.dw_slabs = L.dw_splits > 1;
+        if (L.dw_slabs) L.dw = take(4 * L.dw_splits * L.piece * c);
+    }
+    L.total = std::max<size_t>(at, 256);
+    return L;
+}
+
+template <int kForm, int P, bool kDrain>
+cudaError_t run_scores(const char* name, bool pair, const ProductMaps& maps, ProductArgs Q, int64_t across, cudaStream_t s)
+{
+    Q.m_tiles = static_cast<int32_t>(up(Q.rows, pair ? 256 : 128));
+    return pair ? run_product<ProductShape<kForm, false, false, 2, P, kDrain>>(name, maps, Q, across * Q.m_tiles, s)
+                : run_product<ProductShape<kForm, false, false, 1, P, kDrain>>(name, maps, Q, across * Q.m_tiles, s);
+}
+
+// x and w as the products read them.
+cudaError_t prepare(const Layout& L, const VocabLoss& V, uint8_t* ws, const void*& x, const void*& w, cudaStream_t s)
+{
+    x = L.pack_x ? ws + L.x : V.x;
+    w = L.pack_w ? ws + L.w : V.w;
+    if (!L.pack_x && !L.pack_w) return cudaSuccess;
+    return pack(Pack1{V.x, reinterpret_cast<bf16*>(ws + L.x), L.pack_x ? V.n : 0, V.c, L.ldx},
+                Pack1{V.w, reinterpret_cast<bf16*>(ws + L.w), L.pack_w ? V.v : 0, V.c, L.ldw}, !V.f32, s);
+}
+
+bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+
+size_t vocab_loss_ws_bytes(int f32, int64_t n, int64_t c, int64_t v, int grad, int is_aligned)
+{
+    return layout(f32, n, c, v, grad, is_aligned, is_aligned).total;
+}
+
+size_t vocab_loss_ws_bytes(const VocabLoss& V, int grad)
+{
+    return layout(V.f32, V.n, V.c, V.v, grad, aligned(V.x), aligned(V.w)).total;
+}
+
+cudaError_t vocab_loss(const VocabLoss& V, void* workspace, cudaStream_t s)
+{
+    if (tensor_encoder() == nullptr) return cudaErrorNotSupported;
+    const Layout L = layout(V.f32, V.n, V.c, V.v, false, aligned(V.x), aligned(V.w));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const void *x, *w;
+    cudaError_t e = prepare(L, V, ws, x, w, s);
+    if (e != cudaSuccess) return e;
+    ProductMaps maps;
+    if (!Operand{x, V.n, V.c, L.ldx, 1, L.parts}.map(&maps.a) || !Operand{w, V.v, V.c, L.ldw, 1, L.parts}.map(&maps.b))
+        return cudaErrorInvalidValue;
+    ProductArgs Q{};
+    Q.rows = static_cast<int32_t>(V.n);
+    Q.m = Q.rows;
+    Q.n = Q.v = static_cast<int32_t>(V.v);
+    Q.k = static_cast<int32_t>(V.c);
+    Q.width = L.score.width;
+    Q.run = L.score.run;
+    Q.n_tiles = static_cast<int32_t>(up(V.v, Q.width));
+    Q.target = V.target;
+    Q.part = reinterpret_cast<float2*>(ws + L.part);
+    Q.hit = reinterpret_cast<float*>(ws + L.hit);
+    Q.release = 1;
+    Q.d_err = V.d_err;
+    e = V.f32 ? run_scores<kScore, 6, false>("vocab_score", L.score.pair, maps, Q, L.score.items, s)
+              : run_scores<kScore, 1, true>("vocab_score", L.score.pair, maps, Q, L.score.items, s);
+    if (e != cudaSuccess) return e;
+    SO_PROFILE("vocab_join", s);
+    return launch(k_loss_join, dim3(static_cast<unsigned>(up(V.n, 32))), dim3(1024), s, static_cast<const float2*>(Q.part),
+                  L.score.items * (V.f32 ? 2 : 4), static_cast<const float*>(Q.hit), V.target, V.n, V.loss, V.lse);
+}
+
+cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
+{
+    if (tensor_encoder() == nullptr) return cudaErrorNotSupported;
+    const Layout L = layout(V.f32, V.n, V.c, V.v, true, aligned(V.x), aligned(V.w));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const void *x, *w;
+    cudaError_t e = prepare(L, V, ws, x, w, s);
+    const int64_t row = 2 * L.ldw;   // bytes of one part's row
+    for (int64_t p = 0; p < L.pieces && e == cudaSuccess; ++p) {
+        const int64_t v0 = p * L.piece, wide = std::min(L.piece, V.v - v0);
+        ProductMaps maps;
+        const Operand piece{static_cast<const uint8_t*>(w) + v0 * row, wide, V.c, L.ldw, 1, L.parts, V.v * L.ldw};
+        if (!Operand{x, V.n, V.c, L.ldx, 1, L.parts}.map(&maps.a) || !piece.map(&maps.b)) return cudaErrorInvalidValue;
+        ProductArgs Q{};
+        Q.rows = static_cast<int32_t>(V.n);
+        Q.m = Q.rows;
+        Q.n = static_cast<int32_t>(wide);
+        Q.v = static_cast<int32_t>(V.v);
+        Q.v0 = static_cast<int32_t>(v0);
+        Q.k = static_cast<int32_t>(V.c);
+        Q.width = L.slope.width;
+        Q.n_tiles = static_cast<int32_t>(up(wide, Q.width));
+        Q.target = V.target;
+        Q.lse = V.lse;
+        Q.dloss = V.dloss;
+        Q.slope = reinterpret_cast<bf16*>(ws + L.g);
+        Q.slope_part = V.n * L.ldg;
+        Q.ld = static_cast<int32_t>(L.ldg);
+        Q.release = 1;
+        Q.d_err = V.d_err;
+        e = V.f32 ? run_scores<kSlope, 6, false>("vocab_slope", L.slope.pair, maps, Q, Q.n_tiles, s)
+                  : run_scores<kSlope, 1, false>("vocab_slope", L.slope.pair, maps, Q, Q.n_tiles, s);
+        if (e == cudaSuccess && V.dx != nullptr) {
+            RowsProduct R{};
+            R.a = piece;
+            R.b = Operand{ws + L.g, V.n, wide, L.ldg, 1, L.parts};
+            R.a_mn = 1;
+            R.rows = V.n;
+            R.m = V.c;
+            R.k = wide;
+            R.groups = 1;
+            R.splits = L.dx_splits;
+            R.out = L.dx_slabs ? static_cast<void*>(ws + L.dx) : V.dx;
+            R.out_bf16 = !L.dx_slabs && !V.f32;
+            R.add = p > 0;
+            R.release = L.dx_slabs;
+            R.d_err = V.d_err;
+            e = rows_product(R, s);
+        }
+        if (e == cudaSuccess && V.dw != nullptr) {
+            uint8_t* to = static_cast<uint8_t*>(V.dw) + v0 * V.c * (V.f32 ? 4 : 2);
+            WeightsProduct R{};
+            R.a = Operand{x, V.n, V.c, L.ldx, 1, L.parts};
+            R.b = Operand{ws + L.g, V.n, wide, L.ldg, 1, L.parts};
+            R.rows = V.n;
+            R.m = V.c;
+            R.n = wide;
+            R.groups = 1;
+            R.splits = L.dw_splits;
+            R.out = L.dw_slabs ? static_cast<void*>(ws + L.dw) : to;
+            R.out_bf16 = !L.dw_slabs && !V.f32;
+            R.release = L.dw_slabs;
+            R.d_err = V.d_err;
+            e = weights_product(R, s);
+            if (e == cudaSuccess && L.dw_slabs)
+                e = join_slabs(reinterpret_cast<const float*>(ws + L.dw), L.dw_splits, wide * V.c, wide, V.c, nullptr, to,
+                               !V.f32, s);
+        }
+    }
+    if (e == cudaSuccess && V.dx != nullptr && L.dx_slabs)
+        e = join_slabs(reinterpret_cast<const float*>(ws + L.dx), L.dx_splits, V.n * V.c, V.n, V.c, nullptr, V.dx, !V.f32, s);
+    return e;
+}
+
+}  // namespace so

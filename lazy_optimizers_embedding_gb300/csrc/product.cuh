@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                         else if (rank == 0)
                             mbar_expect(full + 8 * s, kPair * bytes);
                         else if (kForm == kWeights)
-                            mbar_arrive_cluster(there);
+                            mbar_arrive_relaxed(there);
                         uint32_t at = data + s * S::kStage;
                         const int kk = kForm == kWeights ? T.k0 + c * kPK : c * kPK;
                         auto load = [&](const CUtensorMap* map, int x, int y, int z) {
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                         for (int part = 0; part < S::kChunk && c < T.c1; ++part, ++c, ++it) {
                             const uint32_t s = it % kStages;
                             if (!(ok = mbar_wait(full + 8 * s, it / kStages & 1, &dead))) break;
-                            if (kForm == kWeights && kPair == 2) fence_cluster();   // the other block's warp 2 cleared rows of its own
+                            if (kForm == kWeights && kPair == 2 && (c + 1) * kPK > T.len) fence_cluster();   // the other block's warp 2 cleared rows
                             tc_fence_after();
                             const uint32_t a = data + s * S::kStage, b = a + S::kParts * S::kA;
                             // 16 K values: 32 bytes along a K-major row, two 8-row groups of an MN-major block
@@ -641,6 +641,14 @@ inline bool encode_bf16(CUtensorMap* map, const void* at, int64_t rows, int64_t 
     return tensor_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), dim, stride, box, each,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What a stage of a tile of w columns takes, in cycles: 128 rows x w x 64 products an SM at 4096 a cycle, or its boxes from L2
+// at about 80 bytes a cycle and SM, whichever is longer.
+template <class S>
+int64_t stage_cycles(int64_t w)
+{
+    return std::max<int64_t>(2 * w * S::P, S::kParts * (kPM + w / S::kPair) * 128 / 80);
 }
 
 // `items` at most, each a block's (a pair's) at a time.

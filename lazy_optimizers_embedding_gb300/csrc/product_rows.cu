@@ -117,10 +117,10 @@ cudaError_t rows_form(const RowsProduct& R, cudaStream_t s)
     Q.m_tiles = static_cast<int32_t>(up(R.m, S::TM));
     Q.width = S::BN;
     const int64_t units = num_sms() / S::kPair;
-    if (R.groups == 1) {   // the width whose rounds over the GPU take least
+    if (R.groups == 1) {   // the width whose rounds over the GPU take least; a stage: see stage_cycles
         int64_t best = INT64_MAX;
         for (int w = S::BN; w >= 64; w -= 32) {
-            const int64_t cost = up(up(R.rows, w) * Q.m_tiles * R.splits, units) * w;
+            const int64_t cost = up(up(R.rows, w) * Q.m_tiles * R.splits, units) * stage_cycles<S>(w);
             if (cost < best) best = cost, Q.width = w;
         }
     }

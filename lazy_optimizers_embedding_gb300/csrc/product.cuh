@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                         for (int part = 0; part < S::kChunk && c < T.c1; ++part, ++c, ++it) {
                             const uint32_t s = it % kStages;
                             if (!(ok = mbar_wait(full + 8 * s, it / kStages & 1, &dead))) break;
-                            if (kForm == kWeights && kPair == 2 && (c + 1) * kPK > T.len) fence_cluster();   // the other block's warp 2 cleared rows
+                            if (kForm == kWeights && kPair == 2 && (c + 1) * kPK > T.len)
+                                mbar_acquire_cluster(full + 8 * s, it / kStages & 1);   // the other block's warp 2 cleared rows
                             tc_fence_after();
                             const uint32_t a = data + s * S::kStage, b = a + S::kParts * S::kA;
                             // 16 K values: 32 bytes along a K-major row, two 8-row groups of an MN-major block
@@ -528,6 +529,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
         }
         uint32_t done = 0;
         bool ok = true;
+        auto leave = [&](uint32_t acc) {   // this warp has read all of the accumulator that it wants
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_near(kPair == 2 ? cluster_addr(tempty + 8 * acc, 0) : tempty + 8 * acc);
+        };
         for (int64_t t = first; ok && t < items; t += step) {
             const int count = tiles_of_item<S>(Q, t);
             float top = -INFINITY, total = 0.0f;      // kScore
@@ -570,9 +576,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                                 }
                             }
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(kPair == 2 ? cluster_addr(tempty + 8 * acc, 0) : tempty + 8 * acc);
+                        leave(acc);
                     }
                     if (!ok) break;
 #pragma unroll
@@ -601,6 +605,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                         else
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                        if (some && col + kWarpGroups * 32 >= T.valid) leave(acc);   // the last piece: the accumulator is free
                         if (kForm == kScore)
                             take_scores(Q, T, row, col, target, top, total, v);
                         else if (kForm == kSlope)
@@ -608,11 +613,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                         else
                             put_columns<S>(Q, T, f, col, v);
                     }
-                    if (some) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(kPair == 2 ? cluster_addr(tempty + 8 * acc, 0) : tempty + 8 * acc);
-                    }
+                    if (some && group * 32 >= T.valid) leave(acc);
                 }
             }
             if (kForm == kScore && ok && row < Q.rows)

@@ -146,7 +146,17 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar)   // orders no
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// The same that orders the thread's accesses within its block alone, and so waits for none of its stores to memory.
+__device__ __forceinline__ void mbar_arrive_near(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Once a phase is over: makes what the other block's threads wrote before their arrivals visible.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity)
+{
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n}" ::"r"(bar), "r"(parity)
+                 : "memory");
+}
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // ------------------------------------------------------------------ tcgen05

@@ -203,6 +203,15 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, u
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
             : "memory");
 }
+// The same for a block alone with A in tensor memory: row i in lane i, two neighbouring K values a column.
+__device__ __forceinline__ void tc_mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
 // Arrives on `bar` (of both blocks of a pair) once every MMA issued before has finished.
 template <int kPair>
 __device__ __forceinline__ void tc_commit(uint32_t bar)
@@ -246,6 +255,15 @@ __device__ __forceinline__ void tmem_load16(uint32_t a, uint32_t b, float (&v)[1
         : "r"(a), "r"(b)
         : "memory");
 }
+
+// 8 columns of the warp's 32 lanes; tmem_store_done: they are written.
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory accesses by address.
 __device__ __forceinline__ uint4 lds128(uint32_t a)

@@ -1,0 +1,445 @@
+// vocab_back.cu -- the gradient of the loss over a table's rows for narrow rows (at
+// most 128 columns), in one launch and without the slopes in memory.
+//
+//   S = own other^T, G = dloss (exp(S - lse) - [target]), D += G other
+//
+// An item has 128 rows of its own, tokens (D is their dx) or rows of the table (their dW, G then
+// transposed), and goes through rows of the other kind, TN at a time.  Scores come from the tensor unit
+// into tensor memory, a warp's lanes have a row each, and their slopes go back to where the scores
+// were, as bf16 parts: the A operand of the second product, whose B operand is the other rows' tile
+// once more, read as it lies but MN-major.  So memory holds the rows and results alone: with the slopes
+// written out (vocab_loss.cu) 2048 x 1M fp32 scores of 64 columns moved 37 GB.
+// Two groups of four warps have every second tile each, so that one's exponentials run beside the
+// other's and both beside the products; a third (and for 128 columns a fourth) empties D into fp32 sums, which
+// round to nearest, every 512 (1024) K values.
+#include "product.cuh"
+#include "vocab_back.cuh"
+
+namespace so {
+
+namespace {
+
+constexpr int kOwn = 128;                 // rows of an item
+
+template <int P_, int C_>
+struct BackShape {
+    static constexpr int P = P_, C = C_, kParts = P == 6 ? 3 : 1;
+    static constexpr int TN = P == 6 ? 64 : 128;                           // rows of the other kind in a tile
+    static constexpr int kBlocks = C / 64;                                 // of 64 columns
+    static constexpr uint32_t kOwnPart = kBlocks * kOwn * 128, kOtherPart = kBlocks * TN * 128;
+    static constexpr uint32_t kOwnBytes = kParts * kOwnPart, kOtherBytes = kParts * kOtherPart;
+    static constexpr uint32_t kStage = kOtherBytes + 2048;                 // and the tokens' numbers, 16 bytes each
+    static constexpr int kOwns = kOwnBytes <= 48 * 1024 ? 2 : 1;
+    static constexpr int kFit = static_cast<int>((224 * 1024 - kOwns * kOwnBytes) / kStage);
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
+    static constexpr uint32_t kSmem = kOwns * kOwnBytes + kStages * kStage + 1024;
+    static constexpr int kSums = C / 64;                                   // groups of warps that empty D, 64 columns each
+    static constexpr int kThreads = 64 + (2 + kSums) * 128;
+    static constexpr int kScoreCols = kParts > 1 ? 2 * TN : TN;            // = 128: hi and lo sums of TN scores, or one
+    static constexpr int kD = 2 * kScoreCols;                              // D's first column: hi, then lo
+    static constexpr int kChunk = 8;                                       // tiles of D between two emptyings
+    static_assert(kStages >= 2 && kD + (kParts > 1 ? 2 : 1) * C <= 512, "shape");
+};
+
+// An item: which rows are its own and which of the other kind it goes through.
+struct Item {
+    bool tokens;
+    int own0, split;
+    int j0, j1;              // tiles of the other kind
+};
+
+template <class S>
+__device__ __forceinline__ Item item_of(const BackArgs& Q, int64_t t)
+{
+    Item I{};
+    I.tokens = t < Q.dx_items;
+    const int64_t u = I.tokens ? t : t - Q.dx_items;
+    const int splits = I.tokens ? Q.dx_splits : Q.dw_splits;
+    I.split = static_cast<int>(u % splits);
+    I.own0 = static_cast<int>(u / splits) * kOwn;
+    const int tiles = ((I.tokens ? Q.v : Q.n) + S::TN - 1) / S::TN;
+    I.j0 = static_cast<int>(static_cast<int64_t>(tiles) * I.split / splits);
+    I.j1 = static_cast<int>(static_cast<int64_t>(tiles) * (I.split + 1) / splits);
+    return I;
+}
+
+struct Maps {
+    CUtensorMap x, w;
+};
+
+// The tokens' numbers: lse log2(e), dloss and target, 0 and -1 for a token that does not count and behind the last.
+__global__ void __launch_bounds__(256) k_loss_tokens(const float* __restrict__ lse, const float* __restrict__ dloss,
+                                                     const int64_t* __restrict__ target, int n, int padded, int v,
+                                                     float4* __restrict__ out, int32_t* d_err)
+{
+    pdl_enter();   // writes the workspace and the error word
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= padded) return;
+    float4 q = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
+    if (i < n) {
+        const int64_t g = target[i];
+        if (g < -1 || g >= v) set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
+        if (g >= 0 && g < v) q = make_float4(lse[i] * kLog2e, dloss ? dloss[i] : 1.0f, __int_as_float(static_cast<int>(g)), 0.0f);
+    }
+    out[i] = q;
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_constant__ Maps maps, const BackArgs Q)
+{
+    constexpr int P = S::P, C = S::C, TN = S::TN, kStages = S::kStages, kParts = S::kParts;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * kStages + 2 * S::kOwns + 2 + 2 + 2 + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int dead;
+    const uint32_t data = (smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t owns = data, stages = data + S::kOwns * S::kOwnBytes;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, own_full = empty + 8 * kStages, own_empty = own_full + 8 * S::kOwns,
+                   scored = own_empty + 8 * S::kOwns, sloped = scored + 16, summed = sloped + 16, emptied = summed + 8, drain = emptied + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = blockIdx.x, step = gridDim.x, items = Q.dx_items + Q.dw_items;
+
+    if (threadIdx.x == 32) {   // while the kernel before ends
+        tma_prefetch(&maps.x);
+        tma_prefetch(&maps.w);
+    }
+    if (threadIdx.x == 0) {
+        dead = 0;
+        for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
+        for (int s = 0; s < S::kOwns; ++s) mbar_init(own_full + 8 * s, 1), mbar_init(own_empty + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) mbar_init(scored + 8 * s, 1), mbar_init(sloped + 8 * s, 4);
+        mbar_init(summed, 1);
+        mbar_init(emptied, 4 * S::kSums);
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<1>(&tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+    fence_async_proxy();   // the kernels before wrote with ordinary stores
+
+    if (warp == 0) {
+        if (elect_one()) {
+            uint32_t it = 0, owned = 0;
+            for (int64_t t = first; t < items; t += step, ++owned) {
+                const Item I = item_of<S>(Q, t);
+                const CUtensorMap *own = I.tokens ? &maps.x : &maps.w, *other = I.tokens ? &maps.w : &maps.x;
+                const uint32_t o = owned % S::kOwns;
+                if (!mbar_wait(own_empty + 8 * o, (owned / S::kOwns & 1) ^ 1, &dead)) goto copied;
+                mbar_expect(own_full + 8 * o, S::kOwnBytes);
+                for (int p = 0; p < kParts; ++p)
+                    for (int b = 0; b < S::kBlocks; ++b)
+                        for (int q = 0; q < kOwn / 64; ++q)
+                            tma_load<1>(owns + o * S::kOwnBytes + p * S::kOwnPart + (b * (kOwn / 64) + q) * kPBoxBytes, own, own_full + 8 * o,
+                                        b * 64, I.own0 + q * 64, p);
+                for (int j = I.j0; j < I.j1; ++j, ++it) {
+                    const uint32_t s = it % kStages, at = stages + s * S::kStage;
+                    if (!mbar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, &dead)) {
+                        ++owned;
+                        goto copied;
+                    }
+                    mbar_expect(full + 8 * s, S::kOtherBytes + (I.tokens ? 0 : TN * 16));
+                    for (int p = 0; p < kParts; ++p)
+                        for (int b = 0; b < S::kBlocks; ++b)
+                            for (int q = 0; q < TN / 64; ++q)
+                                tma_load<1>(at + p * S::kOtherPart + (b * (TN / 64) + q) * kPBoxBytes, other, full + 8 * s, b * 64,
+                                            j * TN + q * 64, p);
+                    if (!I.tokens) bulk_load(at + S::kOtherBytes, Q.tokens + static_cast<int64_t>(j) * TN, TN * 16, full + 8 * s);
+                }
+            }
+        copied:
+            if (dead) {   // copies in flight land before the block leaves
+                volatile int none = 0;
+                for (uint32_t s = 0; s < static_cast<uint32_t>(kStages) && s < it; ++s)
+                    mbar_wait(full + 8 * s, ((it - 1 - s) / kStages) & 1, &none);
+                for (uint32_t o = 0; o < static_cast<uint32_t>(S::kOwns) && o < owned; ++o)
+                    mbar_wait(own_full + 8 * o, ((owned - 1 - o) / S::kOwns) & 1, &none);
+            }
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            constexpr uint32_t score_desc = mma_desc_bf16(kOwn, false, false) | static_cast<uint32_t>(TN >> 3) << 17;
+            constexpr uint32_t sum_desc = mma_desc_bf16(kOwn, false, true) | static_cast<uint32_t>(C >> 3) << 17;
+            uint32_t it = 0, owned = 0, chunks = 0;
+            bool ok = true;
+            // the second product of a tile: its number, its place in its item and whether it is the last there
+            uint32_t back_it = 0, back_at = 0;
+            bool have = false, back_last = false;
+            auto back = [&]() {
+                const uint32_t b = back_it & 1, s = back_it % kStages;
+                if (!(ok = mbar_wait(sloped + 8 * b, back_it >> 1 & 1, &dead))) return;
+                const bool fresh = back_at % S::kChunk == 0;
+                if (fresh) {
+                    if (!(ok = mbar_wait(emptied, (chunks & 1) ^ 1, &dead))) return;
+                }
+                tc_fence_after();
+                const uint32_t g = tmem + b * S::kScoreCols, d = tmem + S::kD, at = stages + s * S::kStage;
+#pragma unroll
+                for (int k = 0; k < TN / 16; ++k) {
+                    auto db = [&](int p) { return smem_desc(at + p * S::kOtherPart + k * 2048, TN * 128, 1024); };
+                    const bool more = !fresh || k > 0;
+                    // parts of G: columns 0, 64 and 32 of the scores' place (see below)
+                    tc_mma_f16_tmem(d, g + k * 8, db(0), sum_desc, more);
+                    if (P == 6) {
+                        tc_mma_f16_tmem(d + C, g + k * 8, db(2), sum_desc, more);
+                        tc_mma_f16_tmem(d + C, g + 32 + k * 8, db(0), sum_desc, true);
+                        tc_mma_f16_tmem(d + C, g + 64 + k * 8, db(1), sum_desc, true);
+                        tc_mma_f16_tmem(d + C, g + k * 8, db(1), sum_desc, true);
+                        tc_mma_f16_tmem(d + C, g + 64 + k * 8, db(0), sum_desc, true);
+                    }
+                }
+                tc_commit<1>(empty + 8 * s);
+                if (back_last || back_at % S::kChunk == S::kChunk - 1) {
+                    tc_commit<1>(summed);
+                    ++chunks;
+                }
+            };
+            for (int64_t t = first; ok && t < items; t += step, ++owned) {
+                const Item I = item_of<S>(Q, t);
+                const uint32_t o = owned % S::kOwns;
+                if (!(ok = mbar_wait(own_full + 8 * o, owned / S::kOwns & 1, &dead))) break;
+                for (int j = I.j0; ok && j < I.j1; ++j, ++it) {
+                    const uint32_t s = it % kStages, b = it & 1;
+                    if (!(ok = mbar_wait(full + 8 * s, it / kStages & 1, &dead))) break;
+                    tc_fence_after();
+                    // (the slopes that were here have been read: products are carried out in the order of their issue)
+                    const uint32_t d = tmem + b * S::kScoreCols;
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k) {
+                        const uint32_t in = (k / 4) * (kOwn * 128) + (k % 4) * 32, out = (k / 4) * (TN * 128) + (k % 4) * 32;
+                        auto da = [&](int p) { return smem_desc(owns + o * S::kOwnBytes + p * S::kOwnPart + in, 16, 1024); };
+                        auto db = [&](int p) { return smem_desc(stages + s * S::kStage + p * S::kOtherPart + out, 16, 1024); };
+                        tc_mma_f16<1>(d, da(0), db(0), score_desc, k > 0);
+                        if (P == 6) {
+                            tc_mma_f16<1>(d + TN, da(0), db(2), score_desc, k > 0);
+                            tc_mma_f16<1>(d + TN, da(2), db(0), score_desc, true);
+                            tc_mma_f16<1>(d + TN, da(1), db(1), score_desc, true);
+                            tc_mma_f16<1>(d + TN, da(0), db(1), score_desc, true);
+                            tc_mma_f16<1>(d + TN, da(1), db(0), score_desc, true);
+                        }
+                    }
+                    tc_commit<1>(scored + 8 * b);
+                    if (j + 1 == I.j1) tc_commit<1>(own_empty + 8 * o);
+                    if (have) back();
+                    have = true;
+                    back_it = it;
+                    back_at = static_cast<uint32_t>(j - I.j0);
+                    back_last = j + 1 == I.j1;
+                }
+            }
+            if (ok && have) back();
+            if (dead) {   // products in flight finish before the block leaves
+                volatile int none = 0;
+                tc_commit<1>(drain);
+                mbar_wait(drain, 0, &none);
+            }
+        }
+    } else if (warp < 10) {
+        const int group = (warp - 2) >> 2, id = 1 + group;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * S::kScoreCols;
+        const int rowl = (warp & 3) * 32 + lane;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < items; t += step) {
+            const Item I = item_of<S>(Q, t);
+            const int row = I.own0 + rowl;
+            float4 mine = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
+            if (I.tokens && row < Q.n) mine = Q.tokens[row];
+            const int target = __float_as_int(mine.z);
+            for (int j = I.j0; ok && j < I.j1; ++j, ++it) {
+                if ((it & 1) != static_cast<uint32_t>(group)) continue;
+                const uint32_t s = it % kStages;
+                if (!(ok = all_of(id, 128, mbar_wait(scored + 8 * group, it >> 1 & 1, &dead)))) break;
+                tc_fence_after();
+                const uint32_t numbers = stages + s * S::kStage + S::kOtherBytes;
+                const int left = I.tokens ? Q.v - j * TN : TN;   // columns that are rows of the table
+                if (!I.tokens && !(ok = all_of(id, 128, mbar_wait(full + 8 * s, it / kStages & 1, &dead)))) break;   // the numbers
+                uint32_t last[kParts > 1 ? TN / 2 : 1];   // the third part, whose place is free last
+#pragma unroll
+                for (int q = 0; q < TN / 16; ++q) {
+                    float z[16], x[16];
+                    tmem_load16(lanes + q * 16, lanes + (P == 6 ? TN : 0) + q * 16, z, x);
+                    if (P == 6)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) z[e] += x[e];
+                    if (I.tokens) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) z[e] = exp2_fast(fmaf(z[e], kLog2e, -mine.x));
+                        const int hit = target - (j * TN + q * 16);
+                        if (static_cast<uint32_t>(hit) < 16u)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (e == hit) z[e] -= 1.0f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) z[e] = target >= 0 ? z[e] * mine.y : 0.0f;
+                        if (q * 16 + 16 > left)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (q * 16 + e >= left) z[e] = 0.0f;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint4 u = lds128(numbers + (q * 16 + e) * 16);
+                            const int other = static_cast<int>(u.z);
+                            float p = exp2_fast(fmaf(z[e], kLog2e, -__uint_as_float(u.x)));
+                            if (other == row) p -= 1.0f;
+                            z[e] = other >= 0 ? p * __uint_as_float(u.y) : 0.0f;
+                        }
+                    }
+                    uint32_t r[8];
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            r[e] = bf16_pair(z[2 * e], z[2 * e + 1]);
+                            if (p + 1 < kParts) {
+                                const float2 h = pair_floats(r[e]);
+                                z[2 * e] -= h.x, z[2 * e + 1] -= h.y;
+                            }
+                            if (p == 2) last[kParts > 1 ? q * 8 + e : 0] = r[e];
+                        }
+                        // columns 8 q of scores 0 to 16 q + 15, all of them read; the second part's of the lo sums likewise
+                        if (p < 2) tmem_store8(lanes + (p == 1 ? TN : 0) + q * 8, r);
+                    }
+                }
+                if (kParts > 1)
+#pragma unroll
+                    for (int q = 0; q < (kParts > 1 ? TN / 16 : 0); ++q) {
+                        uint32_t r[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = last[kParts > 1 ? q * 8 + e : 0];
+                        tmem_store8(lanes + TN / 2 + q * 8, r);
+                    }
+                tmem_store_done();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sloped + 8 * group);
+            }
+        }
+    } else {
+        const int group = (warp - 10) >> 2, id = 3 + group;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kD + group * 64;
+        uint32_t chunks = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < items; t += step) {
+            const Item I = item_of<S>(Q, t);
+            float sum[2][32];
+#pragma unroll
+            for (int q = 0; q < 64; ++q) sum[q / 32][q % 32] = 0.0f;
+#pragma unroll 1
+            for (int j = I.j0; j < I.j1; j += min(S::kChunk, I.j1 - j), ++chunks) {
+                if (!(ok = all_of(id, 128, mbar_wait(summed, chunks & 1, &dead)))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[16], x[16];
+                    tmem_load16(lanes + q * 16, lanes + (P == 6 ? C : 0) + q * 16, v, x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        if (P == 6) v[e] += x[e];
+                        sum[q / 2][q % 2 * 16 + e] += v[e];
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(emptied);
+            }
+            if (!ok) break;
+            const int row = I.own0 + (warp & 3) * 32 + lane;
+            if (row >= (I.tokens ? Q.n : Q.v)) continue;
+            const int64_t rows = I.tokens ? Q.n : Q.v;
+            const bool slabs = (I.tokens ? Q.dx_splits : Q.dw_splits) > 1;
+            void* out = I.tokens ? Q.dx : Q.dw;
+            const int64_t at = ((slabs ? I.split * rows : 0) + row) * Q.c + group * 64;
+            const int left = Q.c - group * 64;
+            const bool narrow = !slabs && Q.out_bf16;
+            if (left >= 64 && (reinterpret_cast<uintptr_t>(out) + at * (narrow ? 2 : 4)) % 16 == 0) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = sum[q / 4][q % 4 * 8 + e];
+                    if (narrow)
+                        Pack<bf16, 8>::put(static_cast<bf16*>(out) + at + q * 8, v);
+                    else
+                        Pack<float, 8>::put(static_cast<float*>(out) + at + q * 8, v);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) {
+                    if (e >= left) break;
+                    if (narrow)
+                        static_cast<bf16*>(out)[at + e] = __float2bfloat16_rn(sum[e / 32][e % 32]);
+                    else
+                        static_cast<float*>(out)[at + e] = sum[e / 32][e % 32];
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (dead && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INTERNAL);
+    if (warp == 1) tmem_free<1>(tmem, 512);
+}
+
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+// Parts that the other rows are cut into: those whose rounds over the GPU take least, of at least 8 tiles each (an item's own rows, its
+// first scores and its sums take about 4 tiles' time).
+int back_splits(int64_t own, int64_t tiles)
+{
+    const int64_t units = num_sms();
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= 64 && (s == 1 || tiles >= 8 * s); ++s) {
+        const int64_t cost = up(own * s, units) * (up(tiles, s) + 4);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
+}
+
+template <class S>
+cudaError_t run_back(const Maps& maps, const BackArgs& Q, cudaStream_t s)
+{
+    auto* kernel = k_loss_back<S>;
+    const cudaError_t ready = allow_smem(kernel, S::kSmem, S::kSmem);
+    if (ready != cudaSuccess) return ready;
+    const int64_t grid = std::min<int64_t>(num_sms(), Q.dx_items + Q.dw_items);
+    SO_PROFILE("vocab_back", s);
+    return launch_smem(kernel, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), S::kSmem, s, maps, Q);
+}
+
+}  // namespace
+
+BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v)
+{
+    BackPlan B{};
+    const int64_t tile = f32 ? 64 : 128;
+    B.dx_splits = back_splits(up(n, kOwn), up(v, tile));
+    B.dw_splits = back_splits(up(v, kOwn), up(n, tile));
+    B.tokens = up(n, 128) * 128;
+    return B;
+}
+
+cudaError_t loss_tokens(const VocabLoss& V, int64_t padded, float4* out, cudaStream_t s)
+{
+    SO_PROFILE("vocab_tokens", s);
+    return launch(k_loss_tokens, dim3(static_cast<unsigned>(up(padded, 256))), dim3(256), s, static_cast<const float*>(V.lse), V.dloss,
+                  V.target, static_cast<int>(V.n), static_cast<int>(padded), static_cast<int>(V.v), out, V.d_err);
+}
+
+cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s)
+{
+    const Maps maps{x, w};
+    Q.dx_items = Q.dx != nullptr ? up(Q.n, kOwn) * Q.dx_splits : 0;
+    Q.dw_items = Q.dw != nullptr ? up(Q.v, kOwn) * Q.dw_splits : 0;
+    if (f32) return Q.c <= 64 ? run_back<BackShape<6, 64>>(maps, Q, s) : run_back<BackShape<6, 128>>(maps, Q, s);
+    return Q.c <= 64 ? run_back<BackShape<1, 64>>(maps, Q, s) : run_back<BackShape<1, 128>>(maps, Q, s);
+}
+
+}  // namespace so

@@ -11,6 +11,7 @@
 // bf16 (fp32 operands: three bf16 parts): G and the piece's rows make the piece's share of dx, which is summed
 // in fp32 over the pieces, G and x the piece's rows of dW, complete.  A piece is as wide as kSlopeBytes allows.
 #include "product.cuh"
+#include "vocab_back.cuh"
 
 namespace so {
 
@@ -88,7 +89,9 @@ struct Layout {
     int64_t piece, pieces, ldg;
     int dx_splits, dw_splits;
     bool dx_slabs, dw_slabs;
-    size_t x, w, part, hit, g, dx, dw, total;
+    bool narrow;             // the gradient in one launch (vocab_back.cu)
+    BackPlan back;
+    size_t x, w, part, hit, g, dx, dw, tokens, total;
 };
 
 Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_aligned, bool w_aligned)
@@ -112,6 +115,16 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         const int groups = f32 ? 2 : 4;
         L.part = take(static_cast<int64_t>(sizeof(float2)) * L.score.items * groups * n);
         L.hit = take(static_cast<int64_t>(sizeof(float)) * n);
+    } else if (c <= kBackCols) {
+        L.narrow = true;
+        L.back = back_plan(f32, n, c, v);
+        L.dx_splits = L.back.dx_splits;
+        L.dw_splits = L.back.dw_splits;
+        L.dx_slabs = L.dx_splits > 1;
+        L.dw_slabs = L.dw_splits > 1;
+        L.tokens = take(static_cast<int64_t>(sizeof(float4)) * L.back.tokens);
+        if (L.dx_slabs) L.dx = take(4 * L.dx_splits * n * c);
+        if (L.dw_slabs) L.dw = take(4 * L.dw_splits * v * c);
     } else {
         const int64_t most = std::max<int64_t>(256, static_cast<int64_t>(kSlopeBytes) / (2 * L.parts * n) / 256 * 256);
         L.pieces = up(v, most);
@@ -195,6 +208,34 @@ cudaError_t vocab_loss(const VocabLoss& V, void* workspace, cudaStream_t s)
                   L.score.items * (V.f32 ? 2 : 4), static_cast<const float*>(Q.hit), V.target, V.n, V.loss, V.lse);
 }
 
+// Rows of at most kBackCols columns.
+static cudaError_t narrow_grad(const VocabLoss& V, const Layout& L, const void* x, const void* w, uint8_t* ws, cudaStream_t s)
+{
+    CUtensorMap mx, mw;
+    if (!Operand{x, V.n, V.c, L.ldx, 1, L.parts}.map(&mx) || !Operand{w, V.v, V.c, L.ldw, 1, L.parts}.map(&mw))
+        return cudaErrorInvalidValue;
+    float4* tokens = reinterpret_cast<float4*>(ws + L.tokens);
+    cudaError_t e = loss_tokens(V, L.back.tokens, tokens, s);
+    if (e != cudaSuccess) return e;
+    BackArgs Q{};
+    Q.n = static_cast<int32_t>(V.n);
+    Q.c = static_cast<int32_t>(V.c);
+    Q.v = static_cast<int32_t>(V.v);
+    Q.tokens = tokens;
+    Q.dx = V.dx == nullptr ? nullptr : L.dx_slabs ? static_cast<void*>(ws + L.dx) : V.dx;
+    Q.dw = V.dw == nullptr ? nullptr : L.dw_slabs ? static_cast<void*>(ws + L.dw) : V.dw;
+    Q.dx_splits = L.dx_splits;
+    Q.dw_splits = L.dw_splits;
+    Q.out_bf16 = !V.f32;
+    Q.d_err = V.d_err;
+    e = loss_back(mx, mw, V.f32, Q, s);
+    if (e == cudaSuccess && V.dx != nullptr && L.dx_slabs)
+        e = join_slabs(reinterpret_cast<const float*>(ws + L.dx), L.dx_splits, V.n * V.c, V.n, V.c, nullptr, V.dx, !V.f32, s);
+    if (e == cudaSuccess && V.dw != nullptr && L.dw_slabs)
+        e = join_slabs(reinterpret_cast<const float*>(ws + L.dw), L.dw_splits, V.v * V.c, V.v, V.c, nullptr, V.dw, !V.f32, s);
+    return e;
+}
+
 cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
 {
     if (tensor_encoder() == nullptr) return cudaErrorNotSupported;
@@ -202,6 +243,7 @@ cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const void *x, *w;
     cudaError_t e = prepare(L, V, ws, x, w, s);
+    if (e == cudaSuccess && L.narrow) return narrow_grad(V, L, x, w, ws, s);
     const int64_t row = 2 * L.ldw;   // bytes of one part's row
     for (int64_t p = 0; p < L.pieces && e == cudaSuccess; ++p) {
         const int64_t v0 = p * L.piece, wide = std::min(L.piece, V.v - v0);

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 E24, BF = 2.0 ** -24, 2.0 ** -8
 SIZES = [(1, 8, 5), (3, 64, 1000), (256, 128, 5000), (130, 515, 777), (1000, 72, 300), (16, 2048, 2000), (300, 33, 4100),
-         (2, 1, 1), (129, 64, 20000)]
+         (2, 1, 1), (129, 64, 20000), (700, 136, 3000), (513, 100, 40001), (1, 128, 70000), (2100, 64, 129)]
 
 
 def _np(t):

@@ -8,17 +8,17 @@ namespace {
 
 constexpr int kPackBlock = 256;
 
-// Eight values from `from` on, those below `left`.
-template <class T, bool kVec>
-__device__ __forceinline__ void read8(const T* from, int64_t left, float (&x)[8])
+// E values from `from` on, those below `left`.
+template <class T, int E, bool kVec>
+__device__ __forceinline__ void read_some(const T* from, int64_t left, float (&x)[E])
 {
     if (kVec) {
-        Pack<T, 8> q;
+        Pack<T, E> q;
         q.load(from);
         q.get(x);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
             Pack<T, 1> q;
             float one[1];
             q.zero();
@@ -41,26 +41,35 @@ template <class T, bool kVec>
 __device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t warps, int lane)
 {
     constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-    const int64_t groups = A.ld / 8;
-    const int G = groups >= 32 ? 32 : groups > 16 ? 32 : groups > 8 ? 16 : groups > 4 ? 8 : groups > 2 ? 4 : static_cast<int>(groups);
-    const int each = 32 / G;   // rows of a warp at a time
+    constexpr int E = kVec ? 8 : 2;                       // values of a lane at a time, 16 or 4 bytes of a part
+    constexpr int R = kVec ? 1 : 4;                       // and how many of these it has on their way
+    const int64_t lanes = (A.cols + E - 1) / E;
+    const int G = lanes > 16 ? 32 : lanes > 8 ? 16 : lanes > 4 ? 8 : lanes > 2 ? 4 : 2;
+    const int each = 32 / G;                              // rows of a warp at a time
     const int64_t size = A.rows * A.ld;
-    for (int64_t r = warp * each + lane / G; r < A.rows; r += warps * each)
-        for (int64_t g = lane % G; g * 8 < A.cols; g += G) {
-            float x[8];
-            read8<T, kVec>(static_cast<const T*>(A.from) + r * A.cols + g * 8, A.cols - g * 8, x);
-            bf16* to = A.to + r * A.ld + g * 8;
+    for (int64_t r = warp * each + lane / G; r < A.rows; r += warps * each) {
+        const T* from = static_cast<const T*>(A.from) + r * A.cols;
+        bf16* row = A.to + r * A.ld;
+        for (int64_t i = lane % G * E; i < A.cols; i += R * G * E) {
+            float x[R][E];
 #pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-                float h[8];
+            for (int q = 0; q < R; ++q) read_some<T, E, kVec>(from + i + q * G * E, A.cols - i - q * G * E, x[q]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[e] = kParts == 1 ? x[e] : part_of(x[e]);
-                    x[e] = isfinite(h[e]) ? x[e] - h[e] : 0.0f;   // an infinity or NaN is all in the first part
+            for (int q = 0; q < R; ++q) {
+                if (i + q * G * E >= A.cols) continue;
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    float h[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        h[e] = kParts == 1 ? x[q][e] : part_of(x[q][e]);
+                        x[q][e] = isfinite(h[e]) ? x[q][e] - h[e] : 0.0f;   // an infinity or NaN is all in the first part
+                    }
+                    Pack<bf16, E>::put(row + i + q * G * E + p * size, h);
                 }
-                Pack<bf16, 8>::put(to + p * size, h);
             }
         }
+    }
 }
 
 // Rows of one or two arrays as bf16 with aligned rows: fp32 in three parts, hi = bf16(v), mid = bf16(v - hi), lo = what

@@ -1,8 +1,11 @@
 // route.cu -- the k experts of every token from its scores, and the scores' gradient.
 //
-// A warp has a token's row in registers, up to 32 scores a lane, as integers of the same order.  A round
-// takes the largest that is left: every lane's own largest, the warp's by one reduction, of equals
-// the lowest index by another; lane j keeps pick j.  Softmax sums are fp32.
+// A warp has a token's row in registers, up to 32 scores a lane.  Most of them never come near: the k-th
+// largest of the lanes' own largest is a bound from below, and the few that reach it (8 of 256: 10 on the
+// average) go to a lane each.  k rounds then take the largest that is left, by one reduction, and of
+// equals the lowest index, by another; lane j keeps pick j.  (Rounds over all scores: 872 issue slots a
+// row of 256, 99 us for 131072 of them; where more than 32 reach the bound, equals all of them, they still are.)
+// Softmax sums are fp32.
 #include <algorithm>
 
 #include "profile.cuh"
@@ -13,15 +16,19 @@ namespace so {
 namespace {
 
 constexpr int kRouteBlock = 256;
-constexpr uint32_t kNone = 0x007fffffu;   // the key of -inf; NaN and +inf are no scores
 
-// Whole numbers in the order of the floats, -0 as 0.
-__device__ __forceinline__ uint32_t key_of(float x)
+__device__ __forceinline__ float warp_max(float x)
 {
-    const uint32_t u = __float_as_uint(x + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
-__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+__device__ __forceinline__ float exp_of(float x)   // of the terms of a sum
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
 
 // Where a lane's value v lies in the row: accesses of W values by neighbouring lanes.
 template <int W>
@@ -54,52 +61,92 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
+template <int V>
+__device__ __forceinline__ float lane_max(const float (&x)[V])
+{
+    float m = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+    return m;
+}
+
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kRouteBlock) k_route(const T* __restrict__ logits, int64_t n, int experts, int k, int renormalize,
                                                        int64_t* __restrict__ expert, float* __restrict__ weights, int32_t* d_err)
 {
     pdl_wait();
+    __shared__ float2 near[kRouteBlock / 32][32];   // a row's scores that may be picked, and their indices
     const int lane = threadIdx.x & 31;
+    float2* mine = near[threadIdx.x >> 5];
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kRouteBlock / 32);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteBlock / 32) + (threadIdx.x >> 5); row < n; row += step) {
         float x[V];
         read_row<T, V, W>(logits + row * experts, experts, lane, x);
         bool odd = false;
-        uint32_t key[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            odd |= !(x[v] < INFINITY);
-            key[v] = key_of(x[v]);
-        }
+        for (int v = 0; v < V; ++v) odd |= !(x[v] < INFINITY);
         odd = __any_sync(kFull, odd);
         if (odd && lane == 0) set_error(d_err, SPARSE_ERR_NON_FINITE);
-        uint32_t first = 0, mine = kNone;   // the first pick's key, and this lane's pick's
-        int at = -1;
-        for (int j = 0; j < k && !odd; ++j) {
-            uint32_t best = kNone;
-            int where = 0;
+        float high = -INFINITY, value = -INFINITY;   // the largest score; this lane's candidate
+        int index = 0, at = -1, count = 0;
+        if (V == 1) {
+            value = x[0];
+            index = lane;
+            count = odd ? 0 : 32;
+        } else if (!odd) {
+            float best = lane_max(x), bound = -INFINITY;
+            for (int j = 0; j < k; ++j) {
+                bound = warp_max(best);
+                if (best == bound) best = -INFINITY;
+            }
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (key[v] > best) best = key[v], where = v;   // of a lane's equals the first
-            const uint32_t top = __reduce_max_sync(kFull, best);
-            if (top == kNone) break;                           // nothing but -inf is left
-            const uint32_t place = best == top ? index_of<W>(where, lane) : 0xffffffffu;
-            const uint32_t pick = __reduce_min_sync(kFull, place);
-            if (place == pick)
+            for (int v = 0; v < V; ++v) {
+                const bool in = x[v] >= bound && x[v] > -INFINITY;
+                const uint32_t votes = __ballot_sync(kFull, in);
+                const int place = count + __popc(votes & ((1u << lane) - 1u));
+                if (in && place < 32) mine[place] = make_float2(x[v], __int_as_float(index_of<W>(v, lane)));
+                count += __popc(votes);
+            }
+            __syncwarp();
+            if (lane < count) value = mine[lane].x, index = __float_as_int(mine[lane].y);
+            __syncwarp();
+        }
+        float pick = -INFINITY;
+        if (count <= 32) {
+            for (int j = 0; j < k && count > 0; ++j) {
+                const float top = warp_max(value);
+                if (top == -INFINITY) break;                 // nothing but -inf is left
+                const uint32_t place = __reduce_min_sync(kFull, value == top ? static_cast<uint32_t>(index) : 0xffffffffu);
+                if (value == top && static_cast<uint32_t>(index) == place) value = -INFINITY;
+                if (j == 0) high = top;
+                if (lane == j) pick = top, at = static_cast<int>(place);
+            }
+        } else {                                             // many equals
+            float y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] = x[v];
+            for (int j = 0; j < k; ++j) {
+                const float top = warp_max(lane_max(y));
+                if (top == -INFINITY) break;
+                uint32_t place = 0xffffffffu;
+#pragma unroll
+                for (int v = V - 1; v >= 0; --v)
+                    if (y[v] == top) place = index_of<W>(v, lane);
+                const uint32_t taken = __reduce_min_sync(kFull, place);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (v == where) key[v] = 0u;
-            if (j == 0) first = top;
-            if (lane == j) mine = top, at = static_cast<int>(pick);
+                    if (static_cast<uint32_t>(index_of<W>(v, lane)) == taken) y[v] = -INFINITY;
+                if (j == 0) high = top;
+                if (lane == j) pick = top, at = static_cast<int>(taken);
+            }
         }
-        const float high = first ? of_key(first) : 0.0f;
-        const float w = at >= 0 ? expf(of_key(mine) - high) : 0.0f;
-        float total = 0.0f;
-        if (renormalize) {
-            total = w;
-        } else if (first) {
+        const float w = at >= 0 ? expf(pick - high) : 0.0f;
+        float total = w;
+        if (!renormalize) {
+            total = 0.0f;
+            if (high > -INFINITY)
 #pragma unroll
-            for (int v = 0; v < V; ++v) total += expf(x[v] - high);
+                for (int v = 0; v < V; ++v) total += exp_of(x[v] - high);
         }
         total = warp_sum(total);
         if (lane < k) {
@@ -109,7 +156,8 @@ __global__ void __launch_bounds__(kRouteBlock) k_route(const T* __restrict__ log
     }
 }
 
-// A row's gradient is written without its picks' share, zeros or -p s, and then the picks over it.
+// A row's picks go to their places by way of shared memory (zeros but for them), so that it leaves in whole
+// accesses.
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kRouteBlock) k_route_grad(const float* __restrict__ dweights, const T* __restrict__ logits,
                                                             int64_t n, int experts, int k, int renormalize,
@@ -117,7 +165,11 @@ __global__ void __launch_bounds__(kRouteBlock) k_route_grad(const float* __restr
                                                             T* __restrict__ dlogits, int32_t* d_err)
 {
     pdl_wait();
+    __shared__ __align__(16) float places[kRouteBlock / 32][32 * V];
     const int lane = threadIdx.x & 31;
+    float* mine = places[threadIdx.x >> 5];
+    for (int i = lane; i < 32 * V; i += 32) mine[i] = 0.0f;
+    __syncwarp();
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kRouteBlock / 32);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteBlock / 32) + (threadIdx.x >> 5); row < n; row += step) {
         int64_t at = -1;
@@ -131,28 +183,24 @@ __global__ void __launch_bounds__(kRouteBlock) k_route_grad(const float* __restr
             if (at >= 0) w = weights[row * k + lane], g = dweights[row * k + lane];   // the others' are not looked at
         }
         const float s = warp_sum(w * g);
-        T* to = dlogits + row * experts;
+        if (at >= 0) mine[at] = renormalize ? w * (g - s) : w * g;
+        __syncwarp();
         float x[V];
         if (renormalize) {
 #pragma unroll
             for (int v = 0; v < V; ++v) x[v] = 0.0f;
         } else {
             read_row<T, V, W>(logits + row * experts, experts, lane, x);
-            float high = -INFINITY;
+            const float high = warp_max(lane_max(x));
             bool odd = false;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                high = fmaxf(high, x[v]);
-                odd |= !(x[v] < INFINITY);
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(kFull, high, d));
+            for (int v = 0; v < V; ++v) odd |= !(x[v] < INFINITY);
             if (__any_sync(kFull, odd) && lane == 0) set_error(d_err, SPARSE_ERR_NON_FINITE);
             const bool some = high > -INFINITY;
             float total = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[v] = some ? expf(x[v] - high) : 0.0f;
+                x[v] = some ? exp_of(x[v] - high) : 0.0f;
                 total += x[v];
             }
             total = warp_sum(total);
@@ -160,19 +208,18 @@ __global__ void __launch_bounds__(kRouteBlock) k_route_grad(const float* __restr
 #pragma unroll
             for (int v = 0; v < V; ++v) x[v] *= scale;
         }
+        T* to = dlogits + row * experts;
 #pragma unroll
         for (int v = 0; v < V; v += W) {
             const int i = index_of<W>(v, lane);
             float y[W];
 #pragma unroll
-            for (int e = 0; e < W; ++e) y[e] = x[v + e];
+            for (int e = 0; e < W; ++e) y[e] = x[v + e] + mine[i + e];
             if (i < experts) Pack<T, W>::put(to + i, y);
         }
         __syncwarp();
-        if (at >= 0) {
-            const float y[1] = {w * (g - s)};
-            Pack<T, 1>::put(to + at, y);
-        }
+        if (at >= 0) mine[at] = 0.0f;
+        __syncwarp();
     }
 }
 

@@ -9,9 +9,10 @@
 // were, as bf16 parts: the A operand of the second product, whose B operand is the other rows' tile
 // once more, read as it lies but MN-major.  So memory holds the rows and results alone: with the slopes
 // written out (vocab_loss.cu) 2048 x 1M fp32 scores of 64 columns moved 37 GB.
-// Two groups of four warps have every second tile each, so that one's exponentials run beside the
-// other's and both beside the products; a third (and for 128 columns a fourth) empties D into fp32 sums, which
-// round to nearest, every 512 (1024) K values.
+// Two pairs of groups of four warps have every second tile each, a group half of its scores, so that one pair's
+// exponentials run beside the other's and both beside the products (one group a tile: 4.9 ms there, the tensor
+// unit 55 % active); a fifth (and for 128 columns a sixth) empties D into fp32 sums, which round to nearest,
+// every 512 (1024) K values.
 #include "product.cuh"
 #include "vocab_back.cuh"
 
@@ -34,7 +35,7 @@ struct BackShape {
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr uint32_t kSmem = kOwns * kOwnBytes + kStages * kStage + 1024;
     static constexpr int kSums = C / 64;                                   // groups of warps that empty D, 64 columns each
-    static constexpr int kThreads = 64 + (2 + kSums) * 128;
+    static constexpr int kThreads = 64 + (4 + kSums) * 128;
     static constexpr int kScoreCols = kParts > 1 ? 2 * TN : TN;            // = 128: hi and lo sums of TN scores, or one
     static constexpr int kD = 2 * kScoreCols;                              // D's first column: hi, then lo
     static constexpr int kChunk = 8;                                       // tiles of D between two emptyings
@@ -49,17 +50,18 @@ struct Item {
 };
 
 template <class S>
-__device__ __forceinline__ Item item_of(const BackArgs& Q, int64_t t)
+__device__ __forceinline__ Item item_of(const BackArgs& Q, int t)
 {
-    Item I{};
+    Item I;
     I.tokens = t < Q.dx_items;
-    const int64_t u = I.tokens ? t : t - Q.dx_items;
+    const int u = I.tokens ? t : t - Q.dx_items;
     const int splits = I.tokens ? Q.dx_splits : Q.dw_splits;
-    I.split = static_cast<int>(u % splits);
-    I.own0 = static_cast<int>(u / splits) * kOwn;
-    const int tiles = ((I.tokens ? Q.v : Q.n) + S::TN - 1) / S::TN;
-    I.j0 = static_cast<int>(static_cast<int64_t>(tiles) * I.split / splits);
-    I.j1 = static_cast<int>(static_cast<int64_t>(tiles) * (I.split + 1) / splits);
+    const int own = u / splits;
+    I.split = u - own * splits;
+    I.own0 = own * kOwn;
+    const int tiles = ((I.tokens ? Q.v : Q.n) + S::TN - 1) / S::TN, each = tiles / splits, more = tiles - each * splits;
+    I.j0 = I.split * each + min(I.split, more);   // the first parts have one more
+    I.j1 = I.j0 + each + (I.split < more ? 1 : 0);
     return I;
 }
 
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
     const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, own_full = empty + 8 * kStages, own_empty = own_full + 8 * S::kOwns,
                    scored = own_empty + 8 * S::kOwns, sloped = scored + 16, summed = sloped + 16, emptied = summed + 8, drain = emptied + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t first = blockIdx.x, step = gridDim.x, items = Q.dx_items + Q.dw_items;
+    const int first = blockIdx.x, step = gridDim.x, items = Q.dx_items + Q.dw_items;
 
     if (threadIdx.x == 32) {   // while the kernel before ends
         tma_prefetch(&maps.x);
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
         dead = 0;
         for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
         for (int s = 0; s < S::kOwns; ++s) mbar_init(own_full + 8 * s, 1), mbar_init(own_empty + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) mbar_init(scored + 8 * s, 1), mbar_init(sloped + 8 * s, 4);
+        for (int s = 0; s < 2; ++s) mbar_init(scored + 8 * s, 1), mbar_init(sloped + 8 * s, 8);
         mbar_init(summed, 1);
         mbar_init(emptied, 4 * S::kSums);
         mbar_init(drain, 1);
@@ -124,17 +126,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
     if (warp == 0) {
         if (elect_one()) {
             uint32_t it = 0, owned = 0;
-            for (int64_t t = first; t < items; t += step, ++owned) {
+            for (int t = first; t < items; t += step, ++owned) {
                 const Item I = item_of<S>(Q, t);
                 const CUtensorMap *own = I.tokens ? &maps.x : &maps.w, *other = I.tokens ? &maps.w : &maps.x;
                 const uint32_t o = owned % S::kOwns;
                 if (!mbar_wait(own_empty + 8 * o, (owned / S::kOwns & 1) ^ 1, &dead)) goto copied;
                 mbar_expect(own_full + 8 * o, S::kOwnBytes);
-                for (int p = 0; p < kParts; ++p)
-                    for (int b = 0; b < S::kBlocks; ++b)
-                        for (int q = 0; q < kOwn / 64; ++q)
-                            tma_load<1>(owns + o * S::kOwnBytes + p * S::kOwnPart + (b * (kOwn / 64) + q) * kPBoxBytes, own, own_full + 8 * o,
-                                        b * 64, I.own0 + q * 64, p);
+#pragma unroll 1
+                for (int q = 0; q < kParts * S::kBlocks * (kOwn / 64); ++q)   // parts, blocks of columns, 64 rows each
+                    tma_load<1>(owns + o * S::kOwnBytes + q * kPBoxBytes, own, own_full + 8 * o, q / (kOwn / 64) % S::kBlocks * 64,
+                                I.own0 + q % (kOwn / 64) * 64, q / (kOwn / 64 * S::kBlocks));
+#pragma unroll 1
                 for (int j = I.j0; j < I.j1; ++j, ++it) {
                     const uint32_t s = it % kStages, at = stages + s * S::kStage;
                     if (!mbar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, &dead)) {
@@ -142,11 +144,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                         goto copied;
                     }
                     mbar_expect(full + 8 * s, S::kOtherBytes + (I.tokens ? 0 : TN * 16));
-                    for (int p = 0; p < kParts; ++p)
-                        for (int b = 0; b < S::kBlocks; ++b)
-                            for (int q = 0; q < TN / 64; ++q)
-                                tma_load<1>(at + p * S::kOtherPart + (b * (TN / 64) + q) * kPBoxBytes, other, full + 8 * s, b * 64,
-                                            j * TN + q * 64, p);
+#pragma unroll 1
+                    for (int q = 0; q < kParts * S::kBlocks * (TN / 64); ++q)
+                        tma_load<1>(at + q * kPBoxBytes, other, full + 8 * s, q / (TN / 64) % S::kBlocks * 64, j * TN + q % (TN / 64) * 64,
+                                    q / (TN / 64 * S::kBlocks));
                     if (!I.tokens) bulk_load(at + S::kOtherBytes, Q.tokens + static_cast<int64_t>(j) * TN, TN * 16, full + 8 * s);
                 }
             }
@@ -177,18 +178,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                 }
                 tc_fence_after();
                 const uint32_t g = tmem + b * S::kScoreCols, d = tmem + S::kD, at = stages + s * S::kStage;
-#pragma unroll
+                const uint64_t rows = smem_desc(at, TN * 128, 1024);   // parts and K steps: so many 16 bytes on
+                constexpr uint64_t kPart = S::kOtherPart / 16;
+#pragma unroll 2
                 for (int k = 0; k < TN / 16; ++k) {
-                    auto db = [&](int p) { return smem_desc(at + p * S::kOtherPart + k * 2048, TN * 128, 1024); };
                     const bool more = !fresh || k > 0;
-                    // parts of G: columns 0, 64 and 32 of the scores' place (see below)
-                    tc_mma_f16_tmem(d, g + k * 8, db(0), sum_desc, more);
+                    const uint32_t a = g + (P == 6 ? k / 2 * 32 + k % 2 * 8 : k / 4 * 64 + k % 4 * 8);   // see the slopes' places below
+                    const uint64_t r = rows + k * (2048 / 16);
+                    tc_mma_f16_tmem(d, a, r, sum_desc, more);
                     if (P == 6) {
-                        tc_mma_f16_tmem(d + C, g + k * 8, db(2), sum_desc, more);
-                        tc_mma_f16_tmem(d + C, g + 32 + k * 8, db(0), sum_desc, true);
-                        tc_mma_f16_tmem(d + C, g + 64 + k * 8, db(1), sum_desc, true);
-                        tc_mma_f16_tmem(d + C, g + k * 8, db(1), sum_desc, true);
-                        tc_mma_f16_tmem(d + C, g + 64 + k * 8, db(0), sum_desc, true);
+                        tc_mma_f16_tmem(d + C, a, r + 2 * kPart, sum_desc, more);
+                        tc_mma_f16_tmem(d + C, a + 16, r, sum_desc, true);
+                        tc_mma_f16_tmem(d + C, a + TN, r + kPart, sum_desc, true);
+                        tc_mma_f16_tmem(d + C, a, r + kPart, sum_desc, true);
+                        tc_mma_f16_tmem(d + C, a + TN, r, sum_desc, true);
                     }
                 }
                 tc_commit<1>(empty + 8 * s);
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                     ++chunks;
                 }
             };
-            for (int64_t t = first; ok && t < items; t += step, ++owned) {
+            for (int t = first; ok && t < items; t += step, ++owned) {
                 const Item I = item_of<S>(Q, t);
                 const uint32_t o = owned % S::kOwns;
                 if (!(ok = mbar_wait(own_full + 8 * o, owned / S::kOwns & 1, &dead))) break;
@@ -207,18 +210,18 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                     tc_fence_after();
                     // (the slopes that were here have been read: products are carried out in the order of their issue)
                     const uint32_t d = tmem + b * S::kScoreCols;
-#pragma unroll
+                    const uint64_t mine = smem_desc(owns + o * S::kOwnBytes, 16, 1024), rows = smem_desc(stages + s * S::kStage, 16, 1024);
+                    constexpr uint64_t kMine = S::kOwnPart / 16, kPart = S::kOtherPart / 16;
+#pragma unroll 2
                     for (int k = 0; k < C / 16; ++k) {
-                        const uint32_t in = (k / 4) * (kOwn * 128) + (k % 4) * 32, out = (k / 4) * (TN * 128) + (k % 4) * 32;
-                        auto da = [&](int p) { return smem_desc(owns + o * S::kOwnBytes + p * S::kOwnPart + in, 16, 1024); };
-                        auto db = [&](int p) { return smem_desc(stages + s * S::kStage + p * S::kOtherPart + out, 16, 1024); };
-                        tc_mma_f16<1>(d, da(0), db(0), score_desc, k > 0);
+                        const uint64_t m = mine + (k / 4) * (kOwn * 128 / 16) + (k % 4) * 2, r = rows + (k / 4) * (TN * 128 / 16) + (k % 4) * 2;
+                        tc_mma_f16<1>(d, m, r, score_desc, k > 0);
                         if (P == 6) {
-                            tc_mma_f16<1>(d + TN, da(0), db(2), score_desc, k > 0);
-                            tc_mma_f16<1>(d + TN, da(2), db(0), score_desc, true);
-                            tc_mma_f16<1>(d + TN, da(1), db(1), score_desc, true);
-                            tc_mma_f16<1>(d + TN, da(0), db(1), score_desc, true);
-                            tc_mma_f16<1>(d + TN, da(1), db(0), score_desc, true);
+                            tc_mma_f16<1>(d + TN, m, r + 2 * kPart, score_desc, k > 0);
+                            tc_mma_f16<1>(d + TN, m + 2 * kMine, r, score_desc, true);
+                            tc_mma_f16<1>(d + TN, m + kMine, r + kPart, score_desc, true);
+                            tc_mma_f16<1>(d + TN, m, r + kPart, score_desc, true);
+                            tc_mma_f16<1>(d + TN, m + kMine, r, score_desc, true);
                         }
                     }
                     tc_commit<1>(scored + 8 * b);
@@ -237,94 +240,105 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                 mbar_wait(drain, 0, &none);
             }
         }
-    } else if (warp < 10) {
-        const int group = (warp - 2) >> 2, id = 1 + group;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * S::kScoreCols;
+    } else if (warp < 18) {
+        const int group = (warp - 2) >> 2, buf = group >> 1, half = group & 1, id = 1 + group;
+        constexpr int kHalf = TN / 2, kOnce = P == 6 ? 16 : 32;   // scores of a group, and those it reads at a time
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * S::kScoreCols + half * kHalf;
         const int rowl = (warp & 3) * 32 + lane;
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t t = first; ok && t < items; t += step) {
+        for (int t = first; ok && t < items; t += step) {
             const Item I = item_of<S>(Q, t);
             const int row = I.own0 + rowl;
             float4 mine = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
             if (I.tokens && row < Q.n) mine = Q.tokens[row];
             const int target = __float_as_int(mine.z);
             for (int j = I.j0; ok && j < I.j1; ++j, ++it) {
-                if ((it & 1) != static_cast<uint32_t>(group)) continue;
+                if ((it & 1) != static_cast<uint32_t>(buf)) continue;
                 const uint32_t s = it % kStages;
-                if (!(ok = all_of(id, 128, mbar_wait(scored + 8 * group, it >> 1 & 1, &dead)))) break;
+                if (!(ok = all_of(id, 128, mbar_wait(scored + 8 * buf, it >> 1 & 1, &dead)))) break;
                 tc_fence_after();
-                const uint32_t numbers = stages + s * S::kStage + S::kOtherBytes;
-                const int left = I.tokens ? Q.v - j * TN : TN;   // columns that are rows of the table
+                const uint32_t numbers = stages + s * S::kStage + S::kOtherBytes + half * kHalf * 16;
+                const int c0 = j * TN + half * kHalf;
+                const int left = I.tokens ? Q.v - c0 : kHalf;   // columns that are rows of the table
                 if (!I.tokens && !(ok = all_of(id, 128, mbar_wait(full + 8 * s, it / kStages & 1, &dead)))) break;   // the numbers
-                uint32_t last[kParts > 1 ? TN / 2 : 1];   // the third part, whose place is free last
+                uint32_t last[kParts > 1 ? kHalf / 2 : 1];   // the third part, whose place is free last
 #pragma unroll
-                for (int q = 0; q < TN / 16; ++q) {
-                    float z[16], x[16];
-                    tmem_load16(lanes + q * 16, lanes + (P == 6 ? TN : 0) + q * 16, z, x);
-                    if (P == 6)
+                for (int q = 0; q < kHalf / kOnce; ++q) {
+                    float z[kOnce];
+                    if constexpr (P == 6) {
+                        float x[kOnce];
+                        tmem_load16(lanes + q * 16, lanes + TN + q * 16, z, x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) z[e] += x[e];
+                        for (int e = 0; e < kOnce; ++e) z[e] += x[e];
+                    } else {
+                        tmem_load32(lanes + q * 32, z);
+                    }
                     if (I.tokens) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) z[e] = exp2_fast(fmaf(z[e], kLog2e, -mine.x));
-                        const int hit = target - (j * TN + q * 16);
-                        if (static_cast<uint32_t>(hit) < 16u)
+                        for (int e = 0; e < kOnce; ++e) z[e] = exp2_fast(fmaf(z[e], kLog2e, -mine.x));
+                        const int hit = target - (c0 + q * kOnce);
+                        if (static_cast<uint32_t>(hit) < static_cast<uint32_t>(kOnce))
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
+                            for (int e = 0; e < kOnce; ++e)
                                 if (e == hit) z[e] -= 1.0f;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) z[e] = target >= 0 ? z[e] * mine.y : 0.0f;
-                        if (q * 16 + 16 > left)
+                        for (int e = 0; e < kOnce; ++e) z[e] = target >= 0 ? z[e] * mine.y : 0.0f;
+                        if (q * kOnce + kOnce > left)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (q * 16 + e >= left) z[e] = 0.0f;
+                            for (int e = 0; e < kOnce; ++e)
+                                if (q * kOnce + e >= left) z[e] = 0.0f;
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint4 u = lds128(numbers + (q * 16 + e) * 16);
+                        for (int e = 0; e < kOnce; ++e) {
+                            const uint4 u = lds128(numbers + (q * kOnce + e) * 16);
                             const int other = static_cast<int>(u.z);
                             float p = exp2_fast(fmaf(z[e], kLog2e, -__uint_as_float(u.x)));
                             if (other == row) p -= 1.0f;
                             z[e] = other >= 0 ? p * __uint_as_float(u.y) : 0.0f;
                         }
                     }
-                    uint32_t r[8];
+                    // A K step's 16 slopes are 8 columns a part, where this group's scores were that it has read: the first part
+                    // from its first score's column on, the second among its lo sums, the third behind the first.
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
+                    for (int h = 0; h < kOnce / 16; ++h) {
+                        uint32_t r[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            r[e] = bf16_pair(z[2 * e], z[2 * e + 1]);
-                            if (p + 1 < kParts) {
-                                const float2 h = pair_floats(r[e]);
-                                z[2 * e] -= h.x, z[2 * e + 1] -= h.y;
+                        for (int p = 0; p < kParts; ++p) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float &a = z[h * 16 + 2 * e], &b = z[h * 16 + 2 * e + 1];
+                                r[e] = bf16_pair(a, b);
+                                if (p + 1 < kParts) {
+                                    const float2 f = pair_floats(r[e]);
+                                    a -= f.x, b -= f.y;
+                                }
+                                if (p == 2) last[kParts > 1 ? q * 8 + e : 0] = r[e];
                             }
-                            if (p == 2) last[kParts > 1 ? q * 8 + e : 0] = r[e];
+                            if (p < 2) tmem_store8(lanes + (p == 1 ? TN : 0) + (q * kOnce / 16 + h) * 8, r);
                         }
-                        // columns 8 q of scores 0 to 16 q + 15, all of them read; the second part's of the lo sums likewise
-                        if (p < 2) tmem_store8(lanes + (p == 1 ? TN : 0) + q * 8, r);
                     }
                 }
                 if (kParts > 1)
 #pragma unroll
-                    for (int q = 0; q < (kParts > 1 ? TN / 16 : 0); ++q) {
+                    for (int q = 0; q < (kParts > 1 ? kHalf / 16 : 0); ++q) {
                         uint32_t r[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) r[e] = last[kParts > 1 ? q * 8 + e : 0];
-                        tmem_store8(lanes + TN / 2 + q * 8, r);
+                        tmem_store8(lanes + 16 + q * 8, r);
                     }
                 tmem_store_done();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sloped + 8 * group);
+                if (lane == 0) mbar_arrive(sloped + 8 * buf);
             }
         }
     } else {
-        const int group = (warp - 10) >> 2, id = 3 + group;
+        const int group = (warp - 18) >> 2, id = 5 + group;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kD + group * 64;
         uint32_t chunks = 0;
         bool ok = true;
-        for (int64_t t = first; ok && t < items; t += step) {
+        for (int t = first; ok && t < items; t += step) {
             const Item I = item_of<S>(Q, t);
             float sum[2][32];
 #pragma unroll
@@ -389,18 +403,23 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
-// Parts that the other rows are cut into: those whose rounds over the GPU take least, of at least 8 tiles each (an item's own rows, its
-// first scores and its sums take about 4 tiles' time).
-int back_splits(int64_t own, int64_t tiles)
+// Parts that the other rows are cut into, for tokens and for the table's rows: those that take least, in 64ths of a tile's time. An item's
+// own rows, its first scores and its sums take about 3 tiles' time, a part's sums are written and read again.
+void back_splits(int64_t n, int64_t v, int64_t tile, int& tokens, int& rows)
 {
-    const int64_t units = num_sms();
-    int best = 1;
+    const int64_t units = num_sms(), own_n = up(n, kOwn), own_v = up(v, kOwn), tiles_v = up(v, tile), tiles_n = up(n, tile);
     int64_t least = INT64_MAX;
-    for (int s = 1; s <= 64 && (s == 1 || tiles >= 8 * s); ++s) {
-        const int64_t cost = up(own * s, units) * (up(tiles, s) + 4);
-        if (cost < least) least = cost, best = s;
-    }
-    return best;
+    tokens = rows = 1;
+    for (int64_t a = 1; a <= 64 && a <= tiles_v; ++a)
+        for (int64_t b = 1; b <= 8 && b <= tiles_n; ++b) {
+            const int64_t la = up(tiles_v, a) + 3, lb = up(tiles_n, b) + 3, items_a = own_n * a, items_b = own_v * b;
+            const int64_t ra = items_a % units, rb = items_b % units;
+            const int64_t whole = items_a / units * la + items_b / units * lb;   // rounds that fill the GPU
+            const int64_t end = ra + rb <= units ? std::max(ra > 0 ? la : 0, rb > 0 ? lb : 0) : la + lb;
+            const int64_t joined = (a > 1 ? a * own_n : 0) + (b > 1 ? b * own_v : 0);
+            const int64_t cost = 64 * (whole + end) + 16 * joined / units;
+            if (cost < least) least = cost, tokens = static_cast<int>(a), rows = static_cast<int>(b);
+        }
 }
 
 template <class S>
@@ -420,8 +439,7 @@ BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v)
 {
     BackPlan B{};
     const int64_t tile = f32 ? 64 : 128;
-    B.dx_splits = back_splits(up(n, kOwn), up(v, tile));
-    B.dw_splits = back_splits(up(v, kOwn), up(n, tile));
+    back_splits(n, v, tile, B.dx_splits, B.dw_splits);
     B.tokens = up(n, 128) * 128;
     return B;
 }
@@ -436,8 +454,8 @@ cudaError_t loss_tokens(const VocabLoss& V, int64_t padded, float4* out, cudaStr
 cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s)
 {
     const Maps maps{x, w};
-    Q.dx_items = Q.dx != nullptr ? up(Q.n, kOwn) * Q.dx_splits : 0;
-    Q.dw_items = Q.dw != nullptr ? up(Q.v, kOwn) * Q.dw_splits : 0;
+    Q.dx_items = Q.dx != nullptr ? static_cast<int32_t>(up(Q.n, kOwn)) * Q.dx_splits : 0;
+    Q.dw_items = Q.dw != nullptr ? static_cast<int32_t>(up(Q.v, kOwn)) * Q.dw_splits : 0;
     if (f32) return Q.c <= 64 ? run_back<BackShape<6, 64>>(maps, Q, s) : run_back<BackShape<6, 128>>(maps, Q, s);
     return Q.c <= 64 ? run_back<BackShape<1, 64>>(maps, Q, s) : run_back<BackShape<1, 128>>(maps, Q, s);
 }

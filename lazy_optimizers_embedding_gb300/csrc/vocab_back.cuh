@@ -14,7 +14,7 @@ struct BackArgs {
     const float4* tokens;    // see loss_tokens
     void *dx, *dw;           // results, or fp32 slabs where there are several parts; nullptr: not wanted
     int32_t dx_splits, dw_splits, out_bf16;
-    int64_t dx_items, dw_items;   // filled in by loss_back
+    int32_t dx_items, dw_items;   // filled in by loss_back
     int32_t* d_err;
 };
 

@@ -27,8 +27,10 @@ struct BackShape {
     static constexpr int P = P_, C = C_, kParts = P == 6 ? 3 : 1;
     static constexpr int TN = P == 6 ? 64 : 128;                           // rows of the other kind in a tile
     static constexpr int kBlocks = C / 64;                                 // of 64 columns
-    static constexpr uint32_t kOwnPart = kBlocks * kOwn * 128, kOtherPart = kBlocks * TN * 128;
-    static constexpr uint32_t kOwnBytes = kParts * kOwnPart, kOtherBytes = kParts * kOtherPart;
+    // In shared memory: blocks of 64 columns, in each its parts, in each all rows.  So the first two parts of the other rows are
+    // one operand of 2 TN rows.
+    static constexpr uint32_t kOwnPart = kOwn * 128, kOtherPart = TN * 128;
+    static constexpr uint32_t kOwnBytes = kBlocks * kParts * kOwnPart, kOtherBytes = kBlocks * kParts * kOtherPart;
     static constexpr uint32_t kStage = kOtherBytes + 2048;                 // and the tokens' numbers, 16 bytes each
     static constexpr int kOwns = kOwnBytes <= 48 * 1024 ? 2 : 1;
     static constexpr int kFit = static_cast<int>((224 * 1024 - kOwns * kOwnBytes) / kStage);
@@ -37,9 +39,11 @@ struct BackShape {
     static constexpr int kSums = C / 64;                                   // groups of warps that empty D, 64 columns each
     static constexpr int kThreads = 64 + (4 + kSums) * 128;
     static constexpr int kScoreCols = kParts > 1 ? 2 * TN : TN;            // = 128: hi and lo sums of TN scores, or one
-    static constexpr int kD = 2 * kScoreCols;                              // D's first column: hi, then lo
+    static constexpr int kSumCols = kParts > 1 ? 2 * C : C;                // D: hi, then lo
+    static constexpr int kBufs = (512 - kSumCols) / kScoreCols;            // tiles whose scores or slopes are there at a time: 2 or 3
+    static constexpr int kD = kBufs * kScoreCols;                          // D's first column
     static constexpr int kChunk = 8;                                       // tiles of D between two emptyings
-    static_assert(kStages >= 2 && kD + (kParts > 1 ? 2 : 1) * C <= 512, "shape");
+    static_assert(kStages >= 2 && kBufs >= 2, "shape");
 };
 
 // An item: which rows are its own and which of the other kind it goes through.
@@ -91,13 +95,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
 {
     constexpr int P = S::P, C = S::C, TN = S::TN, kStages = S::kStages, kParts = S::kParts;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * kStages + 2 * S::kOwns + 2 + 2 + 2 + 1];
+    __shared__ uint64_t bars[2 * kStages + 2 * S::kOwns + 2 * S::kBufs + 3];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     const uint32_t data = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t owns = data, stages = data + S::kOwns * S::kOwnBytes;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, own_full = empty + 8 * kStages, own_empty = own_full + 8 * S::kOwns,
-                   scored = own_empty + 8 * S::kOwns, sloped = scored + 16, summed = sloped + 16, emptied = summed + 8, drain = emptied + 8;
+                   scored = own_empty + 8 * S::kOwns, sloped = scored + 8 * S::kBufs, summed = sloped + 8 * S::kBufs, emptied = summed + 8, drain = emptied + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = blockIdx.x, step = gridDim.x, items = Q.dx_items + Q.dw_items;
 
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
         dead = 0;
         for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
         for (int s = 0; s < S::kOwns; ++s) mbar_init(own_full + 8 * s, 1), mbar_init(own_empty + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) mbar_init(scored + 8 * s, 1), mbar_init(sloped + 8 * s, 8);
+        for (int s = 0; s < S::kBufs; ++s) mbar_init(scored + 8 * s, 1), mbar_init(sloped + 8 * s, 8);
         mbar_init(summed, 1);
         mbar_init(emptied, 4 * S::kSums);
         mbar_init(drain, 1);
@@ -133,9 +137,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                 if (!mbar_wait(own_empty + 8 * o, (owned / S::kOwns & 1) ^ 1, &dead)) goto copied;
                 mbar_expect(own_full + 8 * o, S::kOwnBytes);
 #pragma unroll 1
-                for (int q = 0; q < kParts * S::kBlocks * (kOwn / 64); ++q)   // parts, blocks of columns, 64 rows each
-                    tma_load<1>(owns + o * S::kOwnBytes + q * kPBoxBytes, own, own_full + 8 * o, q / (kOwn / 64) % S::kBlocks * 64,
-                                I.own0 + q % (kOwn / 64) * 64, q / (kOwn / 64 * S::kBlocks));
+                for (int q = 0; q < kParts * S::kBlocks * (kOwn / 64); ++q)
+                    tma_load<1>(owns + o * S::kOwnBytes + q * kPBoxBytes, own, own_full + 8 * o, q / (kOwn / 64 * kParts) * 64,
+                                I.own0 + q % (kOwn / 64) * 64, q / (kOwn / 64) % kParts);
 #pragma unroll 1
                 for (int j = I.j0; j < I.j1; ++j, ++it) {
                     const uint32_t s = it % kStages, at = stages + s * S::kStage;
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                     mbar_expect(full + 8 * s, S::kOtherBytes + (I.tokens ? 0 : TN * 16));
 #pragma unroll 1
                     for (int q = 0; q < kParts * S::kBlocks * (TN / 64); ++q)
-                        tma_load<1>(at + q * kPBoxBytes, other, full + 8 * s, q / (TN / 64) % S::kBlocks * 64, j * TN + q % (TN / 64) * 64,
-                                    q / (TN / 64 * S::kBlocks));
+                        tma_load<1>(at + q * kPBoxBytes, other, full + 8 * s, q / (TN / 64 * kParts) * 64, j * TN + q % (TN / 64) * 64,
+                                    q / (TN / 64) % kParts);
                     if (!I.tokens) bulk_load(at + S::kOtherBytes, Q.tokens + static_cast<int64_t>(j) * TN, TN * 16, full + 8 * s);
                 }
             }
@@ -163,77 +167,110 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
     } else if (warp == 1) {
         if (elect_one()) {
             constexpr uint32_t score_desc = mma_desc_bf16(kOwn, false, false) | static_cast<uint32_t>(TN >> 3) << 17;
+            constexpr uint32_t score_desc2 = mma_desc_bf16(kOwn, false, false) | static_cast<uint32_t>(2 * TN >> 3) << 17;
             constexpr uint32_t sum_desc = mma_desc_bf16(kOwn, false, true) | static_cast<uint32_t>(C >> 3) << 17;
-            uint32_t it = 0, owned = 0, chunks = 0;
-            bool ok = true;
-            // the second product of a tile: its number, its place in its item and whether it is the last there
-            uint32_t back_it = 0, back_at = 0;
-            bool have = false, back_last = false;
-            auto back = [&]() {
-                const uint32_t b = back_it & 1, s = back_it % kStages;
-                if (!(ok = mbar_wait(sloped + 8 * b, back_it >> 1 & 1, &dead))) return;
-                const bool fresh = back_at % S::kChunk == 0;
-                if (fresh) {
-                    if (!(ok = mbar_wait(emptied, (chunks & 1) ^ 1, &dead))) return;
-                }
-                tc_fence_after();
-                const uint32_t g = tmem + b * S::kScoreCols, d = tmem + S::kD, at = stages + s * S::kStage;
-                const uint64_t rows = smem_desc(at, TN * 128, 1024);   // parts and K steps: so many 16 bytes on
-                constexpr uint64_t kPart = S::kOtherPart / 16;
-#pragma unroll 2
-                for (int k = 0; k < TN / 16; ++k) {
-                    const bool more = !fresh || k > 0;
-                    const uint32_t a = g + (P == 6 ? k / 2 * 32 + k % 2 * 8 : k / 4 * 64 + k % 4 * 8);   // see the slopes' places below
-                    const uint64_t r = rows + k * (2048 / 16);
-                    tc_mma_f16_tmem(d, a, r, sum_desc, more);
-                    if (P == 6) {
-                        tc_mma_f16_tmem(d + C, a, r + 2 * kPart, sum_desc, more);
-                        tc_mma_f16_tmem(d + C, a + 16, r, sum_desc, true);
-                        tc_mma_f16_tmem(d + C, a + TN, r + kPart, sum_desc, true);
-                        tc_mma_f16_tmem(d + C, a, r + kPart, sum_desc, true);
-                        tc_mma_f16_tmem(d + C, a + TN, r, sum_desc, true);
+            constexpr uint32_t sum_desc2 = mma_desc_bf16(kOwn, false, true) | static_cast<uint32_t>(2 * C >> 3) << 17;
+            // Scores of tile it, the next, are asked for as soon as its rows are there and the slopes of tile it - kBufs have been used, the
+            // second product of tile back_it when its slopes are there, whichever is first: with two stages the
+            // rows of the next tile come only after a second product (128 fp32 columns in fixed order: 6350 cycles a tile of 3840 of products).
+            uint32_t it = 0, back_it = 0, owned = 0, chunks = 0;
+            uint32_t place = 0, ends = 0;            // of the next second product: its place in its item; tiles (by buffer) that end theirs
+            int t = first, j = 0;
+            Item I{};
+            bool fresh_item = true;
+            uint64_t since = 0;
+            uint32_t spins = 0;
+            while (t < items || back_it < it) {
+                bool done_something = false;
+                if (t < items && it - back_it < S::kBufs) {
+                    if (fresh_item) {
+                        I = item_of<S>(Q, t);
+                        j = I.j0;
+                        fresh_item = false;
                     }
-                }
-                tc_commit<1>(empty + 8 * s);
-                if (back_last || back_at % S::kChunk == S::kChunk - 1) {
-                    tc_commit<1>(summed);
-                    ++chunks;
-                }
-            };
-            for (int t = first; ok && t < items; t += step, ++owned) {
-                const Item I = item_of<S>(Q, t);
-                const uint32_t o = owned % S::kOwns;
-                if (!(ok = mbar_wait(own_full + 8 * o, owned / S::kOwns & 1, &dead))) break;
-                for (int j = I.j0; ok && j < I.j1; ++j, ++it) {
-                    const uint32_t s = it % kStages, b = it & 1;
-                    if (!(ok = mbar_wait(full + 8 * s, it / kStages & 1, &dead))) break;
-                    tc_fence_after();
-                    // (the slopes that were here have been read: products are carried out in the order of their issue)
-                    const uint32_t d = tmem + b * S::kScoreCols;
-                    const uint64_t mine = smem_desc(owns + o * S::kOwnBytes, 16, 1024), rows = smem_desc(stages + s * S::kStage, 16, 1024);
-                    constexpr uint64_t kMine = S::kOwnPart / 16, kPart = S::kOtherPart / 16;
-#pragma unroll 2
-                    for (int k = 0; k < C / 16; ++k) {
-                        const uint64_t m = mine + (k / 4) * (kOwn * 128 / 16) + (k % 4) * 2, r = rows + (k / 4) * (TN * 128 / 16) + (k % 4) * 2;
-                        tc_mma_f16<1>(d, m, r, score_desc, k > 0);
-                        if (P == 6) {
-                            tc_mma_f16<1>(d + TN, m, r + 2 * kPart, score_desc, k > 0);
-                            tc_mma_f16<1>(d + TN, m + 2 * kMine, r, score_desc, true);
-                            tc_mma_f16<1>(d + TN, m + kMine, r + kPart, score_desc, true);
-                            tc_mma_f16<1>(d + TN, m, r + kPart, score_desc, true);
-                            tc_mma_f16<1>(d + TN, m + kMine, r, score_desc, true);
+                    const uint32_t o = owned % S::kOwns, s = it % kStages, b = it % S::kBufs;
+                    if (mbar_test(full + 8 * s, it / kStages & 1) && (j > I.j0 || mbar_test(own_full + 8 * o, owned / S::kOwns & 1))) {
+                        tc_fence_after();
+                        // (the slopes that were here have been read: products are carried out in the order of their issue)
+                        const uint32_t d = tmem + b * S::kScoreCols;
+                        const uint64_t mine = smem_desc(owns + o * S::kOwnBytes, 16, 1024), rows = smem_desc(stages + s * S::kStage, 16, 1024);
+                        constexpr uint64_t kMine = S::kOwnPart / 16, kPart = S::kOtherPart / 16;   // so many 16 bytes on
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k) {
+                            const uint64_t m = mine + (k / 4) * (kParts * kMine) + (k % 4) * 2, r = rows + (k / 4) * (kParts * kPart) + (k % 4) * 2;
+                            if (P == 6) {
+                                tc_mma_f16<1>(d, m, r, score_desc2, k > 0);   // hi hi, and hi mid among the lo sums behind them
+                                tc_mma_f16<1>(d + TN, m, r + 2 * kPart, score_desc, true);
+                                tc_mma_f16<1>(d + TN, m + 2 * kMine, r, score_desc, true);
+                                tc_mma_f16<1>(d + TN, m + kMine, r + kPart, score_desc, true);
+                                tc_mma_f16<1>(d + TN, m + kMine, r, score_desc, true);
+                            } else {
+                                tc_mma_f16<1>(d, m, r, score_desc, k > 0);
+                            }
                         }
+                        tc_commit<1>(scored + 8 * b);
+                        const bool end = j + 1 == I.j1;
+                        ends = (ends & ~(1u << b)) | static_cast<uint32_t>(end) << b;
+                        ++it;
+                        ++j;
+                        if (end) {
+                            tc_commit<1>(own_empty + 8 * o);
+                            ++owned;
+                            t += step;
+                            fresh_item = true;
+                        }
+                        done_something = true;
                     }
-                    tc_commit<1>(scored + 8 * b);
-                    if (j + 1 == I.j1) tc_commit<1>(own_empty + 8 * o);
-                    if (have) back();
-                    have = true;
-                    back_it = it;
-                    back_at = static_cast<uint32_t>(j - I.j0);
-                    back_last = j + 1 == I.j1;
+                }
+                if (back_it < it && (it - back_it == S::kBufs || t >= items || !done_something)) {
+                    const uint32_t b = back_it % S::kBufs, s = back_it % kStages;
+                    const bool fresh = place % S::kChunk == 0;
+                    if (mbar_test(sloped + 8 * b, back_it / S::kBufs & 1) && (!fresh || mbar_test(emptied, (chunks & 1) ^ 1))) {
+                        tc_fence_after();
+                        const uint32_t g = tmem + b * S::kScoreCols, d = tmem + S::kD;
+                        const uint64_t rows = smem_desc(stages + s * S::kStage, C == 64 ? TN * 128 : kParts * TN * 128, 1024);
+                        constexpr uint64_t kPart = S::kOtherPart / 16;
+#pragma unroll
+                        for (int k = 0; k < TN / 16; ++k) {
+                            const bool more = !fresh || k > 0;
+                            const uint32_t a = g + (P == 6 ? k / 2 * 32 + k % 2 * 8 : k / 4 * 64 + k % 4 * 8);   // see the slopes' places below
+                            const uint64_t r = rows + k * (2048 / 16);
+                            if (P == 6 && C == 64) {   // the first two parts lie side by side as D's hi and lo sums do
+                                tc_mma_f16_tmem(d, a, r, sum_desc2, more);
+                            } else {
+                                tc_mma_f16_tmem(d, a, r, sum_desc, more);
+                                if (P == 6) tc_mma_f16_tmem(d + C, a, r + kPart, sum_desc, more);
+                            }
+                            if (P == 6) {
+                                tc_mma_f16_tmem(d + C, a, r + 2 * kPart, sum_desc, true);
+                                tc_mma_f16_tmem(d + C, a + 16, r, sum_desc, true);
+                                tc_mma_f16_tmem(d + C, a + TN, r + kPart, sum_desc, true);
+                                tc_mma_f16_tmem(d + C, a + TN, r, sum_desc, true);
+                            }
+                        }
+                        tc_commit<1>(empty + 8 * s);
+                        const bool end = ends >> b & 1;
+                        if (end || place % S::kChunk == S::kChunk - 1) {
+                            tc_commit<1>(summed);
+                            ++chunks;
+                        }
+                        place = end ? 0 : place + 1;
+                        ++back_it;
+                        done_something = true;
+                    }
+                }
+                if (done_something) {
+                    spins = 0;
+                } else if ((++spins & 63) == 0) {   // bounded as mbar_wait is
+                    if (dead) break;
+                    if (spins == 64)
+                        since = now_ns();
+                    else if (now_ns() - since > 2000000000ull) {
+                        dead = 1;
+                        break;
+                    }
                 }
             }
-            if (ok && have) back();
             if (dead) {   // products in flight finish before the block leaves
                 volatile int none = 0;
                 tc_commit<1>(drain);
@@ -241,9 +278,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
             }
         }
     } else if (warp < 18) {
-        const int group = (warp - 2) >> 2, buf = group >> 1, half = group & 1, id = 1 + group;
+        const int group = (warp - 2) >> 2, pair = group >> 1, half = group & 1, id = 1 + group;
         constexpr int kHalf = TN / 2, kOnce = P == 6 ? 16 : 32;   // scores of a group, and those it reads at a time
-        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * S::kScoreCols + half * kHalf;
         const int rowl = (warp & 3) * 32 + lane;
         uint32_t it = 0;
         bool ok = true;
@@ -254,9 +290,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
             if (I.tokens && row < Q.n) mine = Q.tokens[row];
             const int target = __float_as_int(mine.z);
             for (int j = I.j0; ok && j < I.j1; ++j, ++it) {
-                if ((it & 1) != static_cast<uint32_t>(buf)) continue;
-                const uint32_t s = it % kStages;
-                if (!(ok = all_of(id, 128, mbar_wait(scored + 8 * buf, it >> 1 & 1, &dead)))) break;
+                if ((it & 1) != static_cast<uint32_t>(pair)) continue;
+                const uint32_t s = it % kStages, buf = it % S::kBufs;
+                const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * S::kScoreCols + half * kHalf;
+                if (!(ok = all_of(id, 128, mbar_wait(scored + 8 * buf, it / S::kBufs & 1, &dead)))) break;
                 tc_fence_after();
                 const uint32_t numbers = stages + s * S::kStage + S::kOtherBytes + half * kHalf * 16;
                 const int c0 = j * TN + half * kHalf;

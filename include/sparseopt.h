@@ -531,7 +531,7 @@ size_t sparse_vocab_loss_workspace_size(sparse_dtype_t type, int64_t n, int64_t 
  *   target[n]           a row of w, or -1 for a token that does not count: its loss is 0.
  *                       Others set SPARSE_ERR_INDEX_OUT_OF_RANGE
  *   loss[n], lse[n]     out, fp32; lse is kept for the backward pass
- * Limits: n, v <= 2^30, c <= 2^20, n c and v c <= 2^37.
+ * Limits: n, v <= 2^30, c <= 2^20, n c and v c <= 2^37, n v <= 2^43.
  */
 sparse_status_t sparse_vocab_loss(const void* x, const void* w, sparse_dtype_t type, int64_t n, int64_t c, int64_t v,
                                   const int64_t* target, float* loss, float* lse, void* ws, size_t ws_bytes,

@@ -65,8 +65,8 @@ bool valid_route(sparse_dtype_t type, int64_t n, int64_t experts, int64_t k, con
            valid_rows(n, experts) && d_err != nullptr;
 }
 
-// Sizes that the tensor copies can address.
-constexpr int64_t kMaxCols = int64_t(1) << 20, kMaxValues = int64_t(1) << 37;
+// Sizes that the tensor copies can address, and whose tiles (64 x 128 scores at least) are fewer than 2^31.
+constexpr int64_t kMaxCols = int64_t(1) << 20, kMaxValues = int64_t(1) << 37, kMaxScores = int64_t(1) << 43;
 
 bool valid_matmul(sparse_dtype_t type, int64_t n, int64_t a, int64_t b, int64_t experts)
 {
@@ -77,7 +77,7 @@ bool valid_matmul(sparse_dtype_t type, int64_t n, int64_t a, int64_t b, int64_t 
 bool valid_loss(sparse_dtype_t type, int64_t n, int64_t c, int64_t v)
 {
     return valid_type(type) && n >= 0 && n <= (1 << 30) && c >= 1 && c <= kMaxCols && v >= 1 && v <= (1 << 30) &&
-           n <= kMaxValues / c && v <= kMaxValues / c;
+           n <= kMaxValues / c && v <= kMaxValues / c && n <= kMaxScores / v;
 }
 
 // Newton-Schulz keeps X, A = X X^T and B = b A + c A^2, with and without a on its

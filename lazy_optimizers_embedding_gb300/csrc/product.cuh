@@ -76,8 +76,9 @@ struct ProductShape {
     static constexpr uint32_t kA = kPM / kPBox * kPBoxBytes, kB = BN / kPair / kPBox * kPBoxBytes;
     static constexpr uint32_t kStage = kParts * (kA + kB);
     static constexpr bool kSum = P == 6 || kDrain_;
-    // groups of four warps that finish tiles: 64 columns each where sums are in registers, else pieces of 32 in turn
-    static constexpr int kWarpGroups = kSum ? BN / 64 : kForm == kSlope ? 4 : 2;
+    // groups of four warps that finish tiles: some columns each where sums are in registers, else pieces of 32 in turn
+    static constexpr int kCols = 64;
+    static constexpr int kWarpGroups = kSum ? BN / kCols : kForm == kSlope ? 4 : 2;
     static constexpr int kThreads = 96 + kWarpGroups * 128;               // copy warp, product warp, clearing warp
     static constexpr int kStages = static_cast<int>((kGrouped ? 220 * 1024 : 225 * 1024) / kStage);
     static constexpr uint32_t kSmem = kStages * kStage + 1024;            // + alignment
@@ -87,7 +88,7 @@ struct ProductShape {
 };
 
 struct Tile {
-    int e, split;
+    int e, split;            // group (kScore: item of its row of items) and part of K
     int m0, n0;              // first row of M (of the pair's) and column of N (kRows: row of the result)
     int valid, N;            // columns that count, and that the product has
     int k0, len;             // kWeights: the group's first row and rows
@@ -96,30 +97,29 @@ struct Tile {
 
 __device__ __forceinline__ int up32(int x) { return (x + 31) & ~31; }
 
-// Items of a launch (kRows: known once the groups' rows are).
+// Items of a launch (kRows: known once the groups' rows are).  All counts of items stay below 2^31 (see the entry points' limits).
 template <class S>
-__device__ __forceinline__ int64_t items_of(const ProductArgs& Q, const uint32_t* start)
+__device__ __forceinline__ int items_of(const ProductArgs& Q, const uint32_t* start)
 {
-    if (S::kForm == kRows) return static_cast<int64_t>(start[Q.groups]) * Q.splits;
-    if (S::kForm == kWeights) return static_cast<int64_t>(Q.groups) * Q.m_tiles * Q.n_tiles * Q.splits;
-    if (S::kForm == kScore) return static_cast<int64_t>((Q.n_tiles + Q.run - 1) / Q.run) * Q.m_tiles;
-    return static_cast<int64_t>(Q.n_tiles) * Q.m_tiles;
-}
-template <class S>
-__device__ __forceinline__ int tiles_of_item(const ProductArgs& Q, int64_t t)
-{
-    return S::kForm == kScore ? min(Q.run, Q.n_tiles - static_cast<int>(t / Q.m_tiles) * Q.run) : 1;
+    if (S::kForm == kRows) return static_cast<int>(start[Q.groups]) * Q.splits;
+    if (S::kForm == kWeights) return Q.groups * Q.m_tiles * Q.n_tiles * Q.splits;
+    if (S::kForm == kScore) return (Q.n_tiles + Q.run - 1) / Q.run * Q.m_tiles;
+    return Q.n_tiles * Q.m_tiles;
 }
 
-// Tile j of item t.  The experts' tiles of a column of M follow one another (they share A), the score's token blocks
-// of some columns do (they share the table's rows).
+// Item t, at its first tile; `count` tiles.  The experts' tiles of a column of M follow one another (they share A), the
+// score's token blocks of some columns do (they share the table's rows).
 template <class S>
-__device__ __forceinline__ Tile tile_of(const ProductArgs& Q, const int* begin, const uint32_t* start, int64_t t, int j)
+__device__ __forceinline__ Tile item_of(const ProductArgs& Q, const int* begin, const uint32_t* start, int t, int& count)
 {
     Tile T{};
+    count = 1;
     if (S::kForm == kRows) {
-        T.split = static_cast<int>(t % Q.splits);
-        const uint32_t u = static_cast<uint32_t>(t / Q.splits);
+        uint32_t u = t;
+        if (Q.splits > 1) {
+            u /= Q.splits;
+            T.split = t - static_cast<int>(u) * Q.splits;
+        }
         int lo = 0, hi = Q.groups;             // start[lo] <= u < start[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -132,35 +132,52 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& Q, const int* begin, 
         const int rows = begin[lo + 1] - begin[lo], r = static_cast<int>(u - start[lo]);
         const int tiles = (rows + Q.width - 1) / Q.width;
         const int w = up32((rows + tiles - 1) / tiles);        // equal tiles; the last has a row at least
-        const int i = r % tiles;
-        T.m0 = r / tiles * S::TM;
+        const int across = r / tiles, i = r - across * tiles;
+        T.m0 = across * S::TM;
         T.n0 = begin[lo] + i * w;
         T.valid = min(w, rows - i * w);
-        const int chunks = (Q.k + kPK - 1) / kPK;
-        T.c0 = static_cast<int>(static_cast<int64_t>(chunks) * T.split / Q.splits);
-        T.c1 = static_cast<int>(static_cast<int64_t>(chunks) * (T.split + 1) / Q.splits);
+        T.c1 = (Q.k + kPK - 1) / kPK;
     } else if (S::kForm == kWeights) {
-        T.split = static_cast<int>(t % Q.splits);
-        int64_t u = t / Q.splits;
-        T.m0 = static_cast<int>(u % Q.m_tiles) * S::TM;
-        u /= Q.m_tiles;
-        T.n0 = static_cast<int>(u % Q.n_tiles) * Q.width;
-        T.e = static_cast<int>(u / Q.n_tiles);
+        uint32_t u = t;
+        if (Q.splits > 1) {
+            u /= Q.splits;
+            T.split = t - static_cast<int>(u) * Q.splits;
+        }
+        const uint32_t v = u / Q.m_tiles;
+        T.m0 = static_cast<int>(u - v * Q.m_tiles) * S::TM;
+        T.e = static_cast<int>(v / Q.n_tiles);
+        T.n0 = static_cast<int>(v - T.e * Q.n_tiles) * Q.width;
         T.valid = min(Q.width, Q.n - T.n0);
         T.k0 = begin[T.e];
         T.len = begin[T.e + 1] - T.k0;
-        const int chunks = (T.len + kPK - 1) / kPK;
-        T.c0 = static_cast<int>(static_cast<int64_t>(chunks) * T.split / Q.splits);
-        T.c1 = static_cast<int>(static_cast<int64_t>(chunks) * (T.split + 1) / Q.splits);
+        T.c1 = (T.len + kPK - 1) / kPK;
     } else {
-        const int across = static_cast<int>(t / Q.m_tiles);
-        T.m0 = static_cast<int>(t % Q.m_tiles) * S::TM;
-        T.n0 = (S::kForm == kScore ? across * Q.run + j : across) * Q.width;
+        const uint32_t across = static_cast<uint32_t>(t) / Q.m_tiles;
+        T.m0 = (t - static_cast<int>(across) * Q.m_tiles) * S::TM;
+        if (S::kForm == kScore) {
+            T.n0 = static_cast<int>(across) * Q.run * Q.width;
+            count = min(Q.run, Q.n_tiles - static_cast<int>(across) * Q.run);
+            T.e = static_cast<int>(across);
+        } else {
+            T.n0 = static_cast<int>(across) * Q.width;
+        }
         T.valid = min(Q.width, Q.n - T.n0);
         T.c1 = (Q.k + kPK - 1) / kPK;
     }
+    if (S::kGrouped && Q.splits > 1) {   // chunks shared out, the first parts one more
+        const int each = T.c1 / Q.splits, more = T.c1 - each * Q.splits;
+        T.c0 = T.split * each + min(T.split, more);
+        T.c1 = T.c0 + each + (T.split < more ? 1 : 0);
+    }
     T.N = up32(T.valid);
     return T;
+}
+// The item's next tile (kScore: the next columns).
+__device__ __forceinline__ void next_tile(const ProductArgs& Q, Tile& T)
+{
+    T.n0 += Q.width;
+    T.valid = min(Q.width, Q.n - T.n0);
+    T.N = up32(T.valid);
 }
 
 __device__ __forceinline__ float exp2_fast(float x)   // 2 ulp
@@ -311,7 +328,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                    tempty = tfull + 8 * S::kAccs, drain = tempty + 8 * S::kAccs, fix = drain + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = kPair == 2 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t first = blockIdx.x / kPair, step = gridDim.x / kPair;
+    const int first = blockIdx.x / kPair, step = gridDim.x / kPair;
 
     if (threadIdx.x == 32) {   // while the kernel before ends
         tma_prefetch(&maps.a);
@@ -368,15 +385,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             __syncthreads();
         }
     }
-    const int64_t items = sound ? items_of<S>(Q, start) : 0;
+    const int items = sound ? items_of<S>(Q, start) : 0;
 
     if (warp == 0) {
         if (elect_one()) {
             uint32_t it = 0, fixed = 0, turn = 0;   // stages; those that warp 2 has had at all, and (parity) how often
-            for (int64_t t = first; t < items; t += step) {
-                const int count = tiles_of_item<S>(Q, t);
-                for (int j = 0; j < count; ++j) {
-                    const Tile T = tile_of<S>(Q, begin, start, t, j);
+            for (int t = first; t < items; t += step) {
+                int count;
+                Tile T = item_of<S>(Q, begin, start, t, count);
+                for (int j = 0; j < count; ++j, next_tile(Q, T)) {
                     const int boxes = (T.N / kPair + kPBox - 1) / kPBox;
                     const uint32_t bytes = S::kParts * (S::kA + boxes * kPBoxBytes);
                     const int m0 = T.m0 + rank * kPM, n0 = T.n0 + rank * (T.N / kPair);
@@ -440,10 +457,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             constexpr uint32_t idesc = mma_desc_bf16(S::TM, kAmn, kBmn);
             uint32_t it = 0, done = 0;   // stages, accumulators used
             bool ok = true;
-            for (int64_t t = first; ok && t < items; t += step) {
-                const int count = tiles_of_item<S>(Q, t);
-                for (int j = 0; ok && j < count; ++j) {
-                    const Tile T = tile_of<S>(Q, begin, start, t, j);
+            for (int t = first; ok && t < items; t += step) {
+                int count;
+                Tile T = item_of<S>(Q, begin, start, t, count);
+                for (int j = 0; ok && j < count; ++j, next_tile(Q, T)) {
                     const uint32_t what = idesc | static_cast<uint32_t>(T.N >> 3) << 17;
                     for (int c = T.c0; ok && c < T.c1; ++done) {
                         const uint32_t acc = done % S::kAccs;
@@ -491,8 +508,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
         if (kForm == kWeights) {
             uint32_t it = 0, turn = 0;
             bool ok = true;
-            for (int64_t t = first; ok && t < items; t += step) {
-                const Tile T = tile_of<S>(Q, begin, start, t, 0);
+            for (int t = first; ok && t < items; t += step) {
+                int count;
+                const Tile T = item_of<S>(Q, begin, start, t, count);
                 it += T.c1 - T.c0;
                 if (T.c1 == T.c0 || T.c1 * kPK <= T.len) continue;   // no last stage, or a whole one
                 const uint32_t s = (it - 1) % kStages;
@@ -534,14 +552,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive_near(kPair == 2 ? cluster_addr(tempty + 8 * acc, 0) : tempty + 8 * acc);
         };
-        for (int64_t t = first; ok && t < items; t += step) {
-            const int count = tiles_of_item<S>(Q, t);
+        for (int t = first; ok && t < items; t += step) {
+            int count;
+            Tile T = item_of<S>(Q, begin, start, t, count);
+            const int f = T.m0 + rank * kPM + rowl;
             float top = -INFINITY, total = 0.0f;      // kScore
             float lse2 = 0.0f, scale = 0.0f;          // kSlope
             int target = -1, row = 0;
-            for (int j = 0; ok && j < count; ++j) {
-                const Tile T = tile_of<S>(Q, begin, start, t, j);
-                const int f = T.m0 + rank * kPM + rowl;
+            for (int j = 0; ok && j < count; ++j, next_tile(Q, T)) {
                 if (!S::kGrouped && j == 0) {
                     row = f;
                     if (row < Q.rows) {
@@ -555,24 +573,33 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                     }
                 }
                 if (S::kSum) {
-                    float sum[2][32];
+                    constexpr int kCols = S::kCols;
+                    float sum[kCols / 32][32];
+                    if (P == 1 || T.c0 == T.c1)   // (with one product first values in their place cost 500 bytes of spills)
 #pragma unroll
-                    for (int q = 0; q < 64; ++q) sum[q / 32][q % 32] = 0.0f;
+                        for (int q = 0; q < kCols; ++q) sum[q / 32][q % 32] = 0.0f;
 #pragma unroll 1
                     for (int c = T.c0; c < T.c1; c += min(S::kChunk, T.c1 - c), ++done) {
                         const uint32_t acc = done % S::kAccs;
                         if (!(ok = all_of(id, 128, mbar_wait(tfull + 8 * acc, done / S::kAccs & 1, &dead)))) break;
                         tc_fence_after();
-                        if (group * 64 < T.N) {
+                        if (group * kCols < T.N) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const uint32_t from = lanes + acc * S::kAccCols + group * 64 + q * 16;
-                                float v[16], x[16];
-                                tmem_load16(from, P == 6 ? from + S::BN : from, v, x);
+                            for (int q = 0; q < kCols / 16; ++q) {
+                                const uint32_t from = lanes + acc * S::kAccCols + group * kCols + q * 16;
+                                float v[16];
+                                if constexpr (P == 6) {
+                                    float x[16];
+                                    tmem_load16(from, from + S::BN, v, x);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) v[e] += x[e];
+                                } else {
+                                    tmem_load16(from, v);
+                                }
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
-                                    if (P == 6) v[e] += x[e];
-                                    sum[q / 2][q % 2 * 16 + e] += v[e];
+                                    float& to = sum[q / 2][q % 2 * 16 + e];
+                                    to = P == 6 && c == T.c0 ? v[e] : to + v[e];
                                 }
                             }
                         }
@@ -580,8 +607,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                     }
                     if (!ok) break;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int col = group * 64 + q * 32;
+                    for (int q = 0; q < kCols / 32; ++q) {
+                        const int col = group * kCols + q * 32;
                         if (col >= T.valid) break;
                         if (kForm == kScore)
                             take_scores(Q, T, row, col, target, top, total, sum[q]);
@@ -617,7 +644,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                 }
             }
             if (kForm == kScore && ok && row < Q.rows)
-                Q.part[(t / Q.m_tiles * kWarpGroups + group) * Q.rows + row] = make_float2(top, total);
+                Q.part[static_cast<int64_t>(T.e * kWarpGroups + group) * Q.rows + row] = make_float2(top, total);
         }
     }
     __syncwarp();

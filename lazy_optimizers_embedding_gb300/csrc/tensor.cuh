@@ -267,6 +267,18 @@ __device__ __forceinline__ void tmem_load16(uint32_t a, uint32_t b, float (&v)[1
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t a, float (&v)[16])
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        " tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
+        : "memory");
+}
+
 // 8 columns of the warp's 32 lanes; tmem_store_done: they are written.
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8])
 {

@@ -386,13 +386,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                 tc_fence_after();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float v[16], x[16];
-                    tmem_load16(lanes + q * 16, lanes + (P == 6 ? C : 0) + q * 16, v, x);
+                    float v[16];
+                    if constexpr (P == 6) {
+                        float x[16];
+                        tmem_load16(lanes + q * 16, lanes + C + q * 16, v, x);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if (P == 6) v[e] += x[e];
-                        sum[q / 2][q % 2 * 16 + e] += v[e];
+                        for (int e = 0; e < 16; ++e) v[e] += x[e];
+                    } else {
+                        tmem_load16(lanes + q * 16, v);
                     }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[q / 2][q % 2 * 16 + e] += v[e];
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -17,6 +17,11 @@ namespace so {
 
 namespace {
 
+// Groups of warps of a score's tile, each with running sums of its own.
+constexpr int score_groups(bool f32)
+{
+    return f32 ? ProductShape<kScore, false, false, 2, 6, false>::kWarpGroups : ProductShape<kScore, false, false, 2, 1, true>::kWarpGroups;
+}
 constexpr size_t kSlopeBytes = size_t(256) << 20;   // G of one piece, all parts
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
@@ -112,7 +117,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
     if (L.pack_w) L.w = take(2 * L.parts * v * L.ldw);
     if (!grad) {
         L.score = score_grid(n, v, L.parts, true);
-        const int groups = f32 ? 2 : 4;
+        const int groups = score_groups(f32);
         L.part = take(static_cast<int64_t>(sizeof(float2)) * L.score.items * groups * n);
         L.hit = take(static_cast<int64_t>(sizeof(float)) * n);
     } else if (c <= kBackCols) {
@@ -205,7 +210,7 @@ cudaError_t vocab_loss(const VocabLoss& V, void* workspace, cudaStream_t s)
     if (e != cudaSuccess) return e;
     SO_PROFILE("vocab_join", s);
     return launch(k_loss_join, dim3(static_cast<unsigned>(up(V.n, 32))), dim3(1024), s, static_cast<const float2*>(Q.part),
-                  L.score.items * (V.f32 ? 2 : 4), static_cast<const float*>(Q.hit), V.target, V.n, V.loss, V.lse);
+                  L.score.items * score_groups(V.f32), static_cast<const float*>(Q.hit), V.target, V.n, V.loss, V.lse);
 }
 
 // Rows of at most kBackCols columns.

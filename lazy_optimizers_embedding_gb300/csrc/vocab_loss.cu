@@ -31,21 +31,25 @@ struct Grid {
     bool pair;
 };
 
-// Tiles of the scores: the width and run whose rounds over the GPU take least (a run costs its item one write of
-// the running sums; with one of 1 to 16 there are enough items to choose from).
-Grid score_grid(int64_t n, int64_t v, int parts, bool runs)
+// Tiles of the scores: the width and run whose rounds over the GPU take least, in cycles.  A tile takes its stages (2 cycles a column and
+// product, or the boxes' way from L2), 1500 at least, which is the epilogue's; an item 2000 more, for its tokens' numbers and its running sums, which the
+// second launch reads at 3400 bytes a cycle.  (A run of one tile: 1.44 against 1.03 ms at 2048 x 64 x 1M fp32, and 94 us of that launch.)
+Grid score_grid(int64_t n, int64_t c, int64_t v, int parts, bool runs)
 {
     Grid g{};
     g.pair = n > 128;
-    const int most = parts == 3 ? 128 : 256;
-    const int64_t units = num_sms() / (g.pair ? 2 : 1), m_tiles = up(n, g.pair ? 256 : 128);
+    const int most = parts == 3 ? 128 : 256, products = parts == 3 ? 6 : 1;
+    const int64_t units = num_sms() / (g.pair ? 2 : 1), m_tiles = up(n, g.pair ? 256 : 128), chunks = up(c, kPK);
     int64_t best = INT64_MAX;
-    for (int w = most; w >= most / 2; w -= 32)
-        for (int run = runs ? 16 : 1; run >= 1; run /= 2) {
+    for (int w = most; w >= most / 2; w -= 32) {
+        const int64_t stage = std::max<int64_t>(2 * w * products, parts * (kPM + w / (g.pair ? 2 : 1)) * 128 / 80);
+        const int64_t tile = std::max<int64_t>(chunks * stage, 1500);
+        for (int run = runs ? 32 : 1; run >= 1; run /= 2) {
             const int64_t items = up(up(v, w), run);
-            const int64_t cost = up(items * m_tiles, units) * run * (w + 8) + 16;
+            const int64_t cost = up(items * m_tiles, units) * (run * tile + 2000) + (runs ? items * n * 32 / 3400 : 0);
             if (cost < best) best = cost, g.width = w, g.run = run, g.items = static_cast<int>(items);
         }
+    }
     return g;
 }
 
@@ -116,7 +120,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
     if (L.pack_x) L.x = take(2 * L.parts * n * L.ldx);
     if (L.pack_w) L.w = take(2 * L.parts * v * L.ldw);
     if (!grad) {
-        L.score = score_grid(n, v, L.parts, true);
+        L.score = score_grid(n, c, v, L.parts, true);
         const int groups = score_groups(f32);
         L.part = take(static_cast<int64_t>(sizeof(float2)) * L.score.items * groups * n);
         L.hit = take(static_cast<int64_t>(sizeof(float)) * n);
@@ -136,7 +140,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         L.piece = up(up(v, L.pieces), 256) * 256;
         L.pieces = up(v, L.piece);
         L.ldg = std::min(L.piece, up(v, 8) * 8);
-        L.slope = score_grid(n, L.piece, L.parts, false);
+        L.slope = score_grid(n, c, L.piece, L.parts, false);
         L.g = take(2 * L.parts * n * L.ldg);
         L.dx_splits = rows_splits(n, c, L.piece, 1, L.parts);
         L.dx_slabs = L.pieces > 1 || L.dx_splits > 1;

@@ -245,19 +245,18 @@ __device__ __forceinline__ void put_slopes(const ProductArgs& Q, const Tile& T, 
 #pragma unroll
     for (int p = 0; p < S::kParts; ++p) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint4 w;
-            uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+        for (int q = 0; q < 2; ++q) {
+            uint32_t u[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float &a = x[q * 8 + 2 * e], &b = x[q * 8 + 2 * e + 1];
+            for (int e = 0; e < 8; ++e) {
+                float &a = x[q * 16 + 2 * e], &b = x[q * 16 + 2 * e + 1];
                 u[e] = bf16_pair(a, b);
                 if (p + 1 < S::kParts) {
                     const float2 h = pair_floats(u[e]);
                     a -= h.x, b -= h.y;
                 }
             }
-            if (q * 8 < left) *reinterpret_cast<uint4*>(to + p * Q.slope_part + q * 8) = w;   // rows are padded to eight
+            if (q * 16 < left) stg256(to + p * Q.slope_part + q * 16, u);   // rows are padded to 16
         }
     }
 }

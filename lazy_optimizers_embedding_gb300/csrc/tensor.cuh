@@ -288,6 +288,14 @@ __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8
 }
 __device__ __forceinline__ void tmem_store_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes to global memory, a whole sector of L2.
+__device__ __forceinline__ void stg256(void* p, const uint32_t (&r)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+                 "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Shared-memory accesses by address.
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {

@@ -33,7 +33,7 @@ struct Grid {
 
 // Tiles of the scores: the width and run whose rounds over the GPU take least, in cycles.  A tile takes its stages (2 cycles a column and
 // product, or the boxes' way from L2), 1500 at least, which is the epilogue's; an item 2000 more, for its tokens' numbers and its running sums, which the
-// second launch reads at 3400 bytes a cycle.  (A run of one tile: 1.44 against 1.03 ms at 2048 x 64 x 1M fp32, and 94 us of that launch.)
+// second launch reads at 3400 bytes a cycle.  (A run of one tile: 1.44 against 1.10 ms at 2048 x 64 x 1M fp32, and 94 us of that launch.)
 Grid score_grid(int64_t n, int64_t c, int64_t v, int parts, bool runs)
 {
     Grid g{};
@@ -139,7 +139,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         L.pieces = up(v, most);
         L.piece = up(up(v, L.pieces), 256) * 256;
         L.pieces = up(v, L.piece);
-        L.ldg = std::min(L.piece, up(v, 8) * 8);
+        L.ldg = std::min(L.piece, up(v, 16) * 16);   // rows of whole 32-byte accesses
         L.slope = score_grid(n, c, L.piece, L.parts, false);
         L.g = take(2 * L.parts * n * L.ldg);
         L.dx_splits = rows_splits(n, c, L.piece, 1, L.parts);

@@ -106,7 +106,7 @@ cudaError_t expert_matmul(const ExpertMatmul& M, void* workspace, cudaStream_t s
     R.d_err = M.d_err;
     e = rows_product(R, s);
     if (e != cudaSuccess || !slabs) return e;
-    return join_slabs(reinterpret_cast<const float*>(ws + L.slabs), L.splits, M.n * m, M.n, m, M.offsets + M.experts, M.out,
+    return join_slabs(Join{reinterpret_cast<const float*>(ws + L.slabs), L.splits, M.n * m, M.n, m, M.offsets + M.experts}, M.out,
                       !M.f32, s);
 }
 
@@ -136,7 +136,7 @@ cudaError_t expert_matmul_grad(const ExpertMatmul& M, void* workspace, cudaStrea
     e = weights_product(R, s);
     if (e != cudaSuccess || !slabs) return e;
     const int64_t rows = M.experts * M.a;
-    return join_slabs(reinterpret_cast<const float*>(ws + L.slabs), L.splits, rows * M.b, rows, M.b, nullptr, M.out, M.out_bf16, s);
+    return join_slabs(Join{reinterpret_cast<const float*>(ws + L.slabs), L.splits, rows * M.b, rows, M.b}, M.out, M.out_bf16, s);
 }
 
 }  // namespace so

@@ -52,6 +52,7 @@ struct ProductArgs {
     const float* add;        // fp32, laid out as the result: added to it (nullptr: nothing)
     int64_t slab;
     int32_t ld;              // values of a row of the result
+    float* unit;             // kSlope with one part: written, see common_unit; else, where given, what results are multiplied by
     int32_t out_bf16, clear; // clear: zeros in the rows behind the last group
     // kScore, kSlope
     const int64_t* target;
@@ -205,8 +206,9 @@ __device__ __forceinline__ void put_columns(const ProductArgs& Q, const Tile& T,
     const int64_t row = S::kForm == kRows ? T.n0 + col : static_cast<int64_t>(T.e) * Q.n + T.n0 + col;
     const int64_t at = row * Q.ld + f + T.split * Q.slab;
     float x[32];
+    const float unit = Q.unit != nullptr ? *Q.unit : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = v[e];
+    for (int e = 0; e < 32; ++e) x[e] = v[e] * unit;
     if (Q.add != nullptr)
 #pragma unroll
         for (int e = 0; e < 32; ++e)
@@ -222,6 +224,26 @@ __device__ __forceinline__ void put_columns(const ProductArgs& Q, const Tile& T,
         for (int e = 0; e < 32; ++e, to += Q.ld)
             if (e < have) *to = x[e];
     }
+}
+
+// Slopes that leave as bf16 are first divided by this, the significand (1 to 2) of the first dloss of a token that counts (among 1024), and the products
+// with them multiplied by it.  Where all tokens have one dloss, as under a mean, a token's largest slope is then a
+// power of two less a probability; as dloss itself it would be rounded the same way for every token, by up to 2^-8 of all results.
+// By a warp.
+__device__ __forceinline__ float common_unit(const float* dloss, const int64_t* target, int n, int lane)
+{
+    if (dloss == nullptr) return 1.0f;
+    for (int i0 = 0; i0 < min(n, 1024); i0 += 32) {
+        const int i = i0 + lane;
+        float d = 0.0f;
+        if (i < n && target[i] >= 0) d = dloss[i];
+        const uint32_t votes = __ballot_sync(kFull, d != 0.0f && isfinite(d));
+        if (votes != 0) {
+            d = __shfl_sync(kFull, d, __ffs(votes) - 1);
+            return __uint_as_float((__float_as_uint(d) & 0x007fffffu) | 0x3f800000u);
+        }
+    }
+    return 1.0f;
 }
 
 // The slopes of a lane's token in 32 of the table's rows: dloss (softmax - [target]).
@@ -544,6 +566,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             else
                 clear_values(static_cast<float*>(Q.out) + from, count, mine, all);
         }
+        float unit = 1.0f;
+        if (kForm == kSlope && S::kParts == 1) {
+            unit = common_unit(Q.dloss, Q.target, Q.rows, lane);
+            if (blockIdx.x == 0 && threadIdx.x == 96) *Q.unit = unit;
+        }
         uint32_t done = 0;
         bool ok = true;
         auto leave = [&](uint32_t acc) {   // this warp has read all of the accumulator that it wants
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                         target = g < 0 || g >= Q.v ? -1 : static_cast<int>(g);
                         if (kForm == kSlope) {
                             lse2 = Q.lse[row] * kLog2e;
-                            scale = Q.dloss ? Q.dloss[row] : 1.0f;
+                            scale = Q.dloss ? __fdiv_rn(Q.dloss[row], unit) : 1.0f;
                         }
                     }
                 }
@@ -726,8 +753,13 @@ struct Pack1 {
 cudaError_t pack(const Pack1& a, const Pack1& b, int is_bf16, cudaStream_t s);
 
 // rows x cols fp32 sums of `slabs` arrays, in order; rows from *end on (end given) are zeros.
-cudaError_t join_slabs(const float* from, int slabs, int64_t slab, int64_t rows, int64_t cols, const int64_t* end, void* out,
-                       int out_bf16, cudaStream_t s);
+struct Join {
+    const float* from;
+    int slabs;
+    int64_t slab, rows, cols;
+    const int64_t* end;
+};
+cudaError_t join_slabs(const Join& J, void* out, int out_bf16, cudaStream_t s);
 
 // The product of rows with their group's matrix, and of two arrays of rows (product_rows.cu, product_weights.cu): fills in the rest of Q
 // (extents, tiles); `pieces`: sums are added to what `out` (fp32 slabs) holds.
@@ -740,6 +772,7 @@ struct RowsProduct {
     int splits;
     void* out;
     int out_bf16, add, clear, release;
+    float* unit;
     int32_t* d_err;
 };
 int rows_splits(int64_t rows, int64_t m, int64_t k, int64_t groups, int parts);
@@ -753,6 +786,7 @@ struct WeightsProduct {
     int splits;
     void* out;               // [groups, n, m]
     int out_bf16, release;
+    float* unit;
     int32_t* d_err;
 };
 int weights_splits(int64_t rows, int64_t m, int64_t n, int64_t groups, int parts);

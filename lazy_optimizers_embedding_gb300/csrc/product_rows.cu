@@ -86,19 +86,46 @@ __global__ void __launch_bounds__(kPackBlock) k_pack(const Pack1 A, const Pack1 
                            static_cast<int64_t>(gridDim.x - blocks_a) * per, lane);
 }
 
-// Sums of slabs in order, one value a thread.
-template <class T>
-__global__ void __launch_bounds__(256) k_join_slabs(const float* __restrict__ from, int slabs, int64_t slab, int64_t rows,
-                                                    int64_t cols, const int64_t* __restrict__ end, T* __restrict__ out)
+// Sums of slabs in order, four neighbours a thread.
+template <class T, bool kVec>
+__global__ void __launch_bounds__(256) k_join_slabs(const Join J, T* __restrict__ out)
 {
     pdl_wait();
-    const int64_t count = rows * cols;
-    const int64_t live = end ? min(max(*end, static_cast<int64_t>(0)), rows) * cols : count;
+    const int64_t groups = (J.cols + 3) / 4, count = J.rows * groups;
+    const int64_t live = J.end ? min(max(*J.end, static_cast<int64_t>(0)), J.rows) : J.rows;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += static_cast<int64_t>(gridDim.x) * 256) {
-        float s = 0.0f;
-        if (i < live)
-            for (int q = 0; q < slabs; ++q) s += from[q * slab + i];
-        out[i] = T(s);
+        const int64_t row = (count >> 32) == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(groups) : i / groups;
+        const int col = static_cast<int>(i - row * groups) * 4, left = static_cast<int>(min(J.cols - col, static_cast<int64_t>(4)));
+        const int64_t at = row * J.cols + col;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (row < live) {
+            for (int q = 0; q < J.slabs; ++q) {
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (kVec) {
+                    Pack<float, 4> k;
+                    k.load(J.from + q * J.slab + at);
+                    k.get(v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) v[e] = J.from[q * J.slab + at + e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += v[e];
+            }
+        }
+        if (kVec && sizeof(T) == 4) {
+            Pack<float, 4>::put(reinterpret_cast<float*>(out) + at, s);
+        } else if (kVec) {
+            uint2 w;
+            w.x = bf16_pair(s[0], s[1]);
+            w.y = bf16_pair(s[2], s[3]);
+            *reinterpret_cast<uint2*>(out + at) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) out[at + e] = T(s[e]);
+        }
     }
 }
 
@@ -143,6 +170,7 @@ cudaError_t rows_form(const RowsProduct& R, cudaStream_t s)
     Q.out_bf16 = R.out_bf16;
     Q.clear = R.clear;
     Q.release = R.release;
+    Q.unit = R.unit;
     Q.d_err = R.d_err;
     return run_product<S>("rows_product", maps, Q, row_tiles(R.rows, R.groups, Q.width) * Q.m_tiles * R.splits, s);
 }
@@ -168,13 +196,14 @@ cudaError_t pack(const Pack1& a, const Pack1& b, int is_bf16, cudaStream_t s)
                : launch(k_pack<float, false>, grid, block, s, a, b, static_cast<int>(na));
 }
 
-cudaError_t join_slabs(const float* from, int slabs, int64_t slab, int64_t rows, int64_t cols, const int64_t* end, void* out,
-                       int out_bf16, cudaStream_t s)
+cudaError_t join_slabs(const Join& J, void* out, int out_bf16, cudaStream_t s)
 {
-    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(8 * num_sms(), up(rows * cols, 256))))), block(256);
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(8 * num_sms(), up(J.rows * up(J.cols, 4), 256))))), block(256);
+    const bool vec = J.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;   // the slabs lie in the workspace
     SO_PROFILE("join_slabs", s);
-    return out_bf16 ? launch(k_join_slabs<bf16>, grid, block, s, from, slabs, slab, rows, cols, end, static_cast<bf16*>(out))
-                    : launch(k_join_slabs<float>, grid, block, s, from, slabs, slab, rows, cols, end, static_cast<float*>(out));
+    if (out_bf16)
+        return launch(vec ? k_join_slabs<bf16, true> : k_join_slabs<bf16, false>, grid, block, s, J, static_cast<bf16*>(out));
+    return launch(vec ? k_join_slabs<float, true> : k_join_slabs<float, false>, grid, block, s, J, static_cast<float*>(out));
 }
 
 int rows_splits(int64_t rows, int64_t m, int64_t k, int64_t groups, int parts)

@@ -28,6 +28,7 @@ cudaError_t weights_form(const WeightsProduct& R, cudaStream_t s)
     Q.ld = static_cast<int32_t>(R.m);
     Q.out_bf16 = R.out_bf16;
     Q.release = R.release;
+    Q.unit = R.unit;
     Q.d_err = R.d_err;
     return run_product<S>("weights_product", maps, Q, static_cast<int64_t>(Q.m_tiles) * Q.n_tiles * R.groups * R.splits, s);
 }

@@ -73,19 +73,21 @@ struct Maps {
     CUtensorMap x, w;
 };
 
-// The tokens' numbers: lse log2(e), dloss and target, 0 and -1 for a token that does not count and behind the last.
+// The tokens' numbers: lse log2(e), dloss (over the unit, where one is asked for) and target, 0 and -1 for a token that does not count and behind the last.
 __global__ void __launch_bounds__(256) k_loss_tokens(const float* __restrict__ lse, const float* __restrict__ dloss,
                                                      const int64_t* __restrict__ target, int n, int padded, int v,
-                                                     float4* __restrict__ out, int32_t* d_err)
+                                                     float4* __restrict__ out, float* unit, int32_t* d_err)
 {
     pdl_enter();   // writes the workspace and the error word
+    const float u = unit != nullptr ? common_unit(dloss, target, n, threadIdx.x & 31) : 1.0f;
+    if (unit != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *unit = u;
     const int i = blockIdx.x * 256 + threadIdx.x;
     if (i >= padded) return;
     float4 q = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
     if (i < n) {
         const int64_t g = target[i];
         if (g < -1 || g >= v) set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
-        if (g >= 0 && g < v) q = make_float4(lse[i] * kLog2e, dloss ? dloss[i] : 1.0f, __int_as_float(static_cast<int>(g)), 0.0f);
+        if (g >= 0 && g < v) q = make_float4(lse[i] * kLog2e, dloss ? __fdiv_rn(dloss[i], u) : 1.0f, __int_as_float(static_cast<int>(g)), 0.0f);
     }
     out[i] = q;
 }
@@ -407,6 +409,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
             if (row >= (I.tokens ? Q.n : Q.v)) continue;
             const int64_t rows = I.tokens ? Q.n : Q.v;
             const bool slabs = (I.tokens ? Q.dx_splits : Q.dw_splits) > 1;
+            if (kParts == 1) {
+                const float unit = *Q.unit;
+#pragma unroll
+                for (int q = 0; q < 64; ++q) sum[q / 32][q % 32] *= unit;
+            }
             void* out = I.tokens ? Q.dx : Q.dw;
             const int64_t at = ((slabs ? I.split * rows : 0) + row) * Q.c + group * 64;
             const int left = Q.c - group * 64;
@@ -485,11 +492,11 @@ BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v)
     return B;
 }
 
-cudaError_t loss_tokens(const VocabLoss& V, int64_t padded, float4* out, cudaStream_t s)
+cudaError_t loss_tokens(const VocabLoss& V, int64_t padded, float4* out, float* unit, cudaStream_t s)
 {
     SO_PROFILE("vocab_tokens", s);
     return launch(k_loss_tokens, dim3(static_cast<unsigned>(up(padded, 256))), dim3(256), s, static_cast<const float*>(V.lse), V.dloss,
-                  V.target, static_cast<int>(V.n), static_cast<int>(padded), static_cast<int>(V.v), out, V.d_err);
+                  V.target, static_cast<int>(V.n), static_cast<int>(padded), static_cast<int>(V.v), out, unit, V.d_err);
 }
 
 cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s)

@@ -100,7 +100,7 @@ struct Layout {
     bool dx_slabs, dw_slabs;
     bool narrow;             // the gradient in one launch (vocab_back.cu)
     BackPlan back;
-    size_t x, w, part, hit, g, dx, dw, tokens, total;
+    size_t x, w, part, hit, g, dx, dw, tokens, unit, total;
 };
 
 Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_aligned, bool w_aligned)
@@ -131,6 +131,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         L.dw_splits = L.back.dw_splits;
         L.dx_slabs = L.dx_splits > 1;
         L.dw_slabs = L.dw_splits > 1;
+        if (!f32) L.unit = take(4);
         L.tokens = take(static_cast<int64_t>(sizeof(float4)) * L.back.tokens);
         if (L.dx_slabs) L.dx = take(4 * L.dx_splits * n * c);
         if (L.dw_slabs) L.dw = take(4 * L.dw_splits * v * c);
@@ -144,6 +145,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         L.g = take(2 * L.parts * n * L.ldg);
         L.dx_splits = rows_splits(n, c, L.piece, 1, L.parts);
         L.dx_slabs = L.pieces > 1 || L.dx_splits > 1;
+        if (!f32) L.unit = take(4);
         if (L.dx_slabs) L.dx = take(4 * L.dx_splits * n * c);
         L.dw_splits = weights_splits(n, c, L.piece, 1, L.parts);
         L.dw_slabs = L.dw_splits > 1;
@@ -224,7 +226,8 @@ static cudaError_t narrow_grad(const VocabLoss& V, const Layout& L, const void* 
     if (!Operand{x, V.n, V.c, L.ldx, 1, L.parts}.map(&mx) || !Operand{w, V.v, V.c, L.ldw, 1, L.parts}.map(&mw))
         return cudaErrorInvalidValue;
     float4* tokens = reinterpret_cast<float4*>(ws + L.tokens);
-    cudaError_t e = loss_tokens(V, L.back.tokens, tokens, s);
+    float* unit = V.f32 ? nullptr : reinterpret_cast<float*>(ws + L.unit);
+    cudaError_t e = loss_tokens(V, L.back.tokens, tokens, unit, s);
     if (e != cudaSuccess) return e;
     BackArgs Q{};
     Q.n = static_cast<int32_t>(V.n);
@@ -236,12 +239,13 @@ static cudaError_t narrow_grad(const VocabLoss& V, const Layout& L, const void* 
     Q.dx_splits = L.dx_splits;
     Q.dw_splits = L.dw_splits;
     Q.out_bf16 = !V.f32;
+    Q.unit = unit;
     Q.d_err = V.d_err;
     e = loss_back(mx, mw, V.f32, Q, s);
     if (e == cudaSuccess && V.dx != nullptr && L.dx_slabs)
-        e = join_slabs(reinterpret_cast<const float*>(ws + L.dx), L.dx_splits, V.n * V.c, V.n, V.c, nullptr, V.dx, !V.f32, s);
+        e = join_slabs(Join{reinterpret_cast<const float*>(ws + L.dx), L.dx_splits, V.n * V.c, V.n, V.c}, V.dx, !V.f32, s);
     if (e == cudaSuccess && V.dw != nullptr && L.dw_slabs)
-        e = join_slabs(reinterpret_cast<const float*>(ws + L.dw), L.dw_splits, V.v * V.c, V.v, V.c, nullptr, V.dw, !V.f32, s);
+        e = join_slabs(Join{reinterpret_cast<const float*>(ws + L.dw), L.dw_splits, V.v * V.c, V.v, V.c}, V.dw, !V.f32, s);
     return e;
 }
 
@@ -273,6 +277,7 @@ cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
         Q.dloss = V.dloss;
         Q.slope = reinterpret_cast<bf16*>(ws + L.g);
         Q.slope_part = V.n * L.ldg;
+        Q.unit = V.f32 ? nullptr : reinterpret_cast<float*>(ws + L.unit);
         Q.ld = static_cast<int32_t>(L.ldg);
         Q.release = 1;
         Q.d_err = V.d_err;
@@ -292,6 +297,7 @@ cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
             R.out_bf16 = !L.dx_slabs && !V.f32;
             R.add = p > 0;
             R.release = L.dx_slabs;
+            R.unit = Q.unit;
             R.d_err = V.d_err;
             e = rows_product(R, s);
         }
@@ -308,15 +314,15 @@ cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
             R.out = L.dw_slabs ? static_cast<void*>(ws + L.dw) : to;
             R.out_bf16 = !L.dw_slabs && !V.f32;
             R.release = L.dw_slabs;
+            R.unit = Q.unit;
             R.d_err = V.d_err;
             e = weights_product(R, s);
             if (e == cudaSuccess && L.dw_slabs)
-                e = join_slabs(reinterpret_cast<const float*>(ws + L.dw), L.dw_splits, wide * V.c, wide, V.c, nullptr, to,
-                               !V.f32, s);
+                e = join_slabs(Join{reinterpret_cast<const float*>(ws + L.dw), L.dw_splits, wide * V.c, wide, V.c}, to, !V.f32, s);
         }
     }
     if (e == cudaSuccess && V.dx != nullptr && L.dx_slabs)
-        e = join_slabs(reinterpret_cast<const float*>(ws + L.dx), L.dx_splits, V.n * V.c, V.n, V.c, nullptr, V.dx, !V.f32, s);
+        e = join_slabs(Join{reinterpret_cast<const float*>(ws + L.dx), L.dx_splits, V.n * V.c, V.n, V.c}, V.dx, !V.f32, s);
     return e;
 }
 

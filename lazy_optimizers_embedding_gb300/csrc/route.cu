@@ -1,12 +1,14 @@
 // route.cu -- the k experts of every token from its scores, and the scores' gradient.
 //
 // A warp has a token's row in registers, up to 32 scores a lane.  Most of them never come near: the k-th
-// largest of the lanes' own largest is a bound from below, and the few that reach it (8 of 256: 10 on the
-// average) go to a lane each.  k rounds then take the largest that is left, by one reduction, and of
-// equals the lowest index, by another; lane j keeps pick j.  (Rounds over all scores: 872 issue slots a
-// row of 256, 99 us for 131072 of them; where more than 32 reach the bound, equals all of them, they still are.)
-// Softmax sums are fp32.
+// largest of the lanes' own largest (different ones) is a bound from below, and the few that reach it (8 of
+// 256: 10 on the average) go to a lane each by way of shared memory, which counts those that stand before its
+// own: larger ones, and equals of a lower index.  (131072 rows of 256, 8 picks, are bound by instructions: k rounds of a
+// maximum over all scores 99 us; bitonic sorts of the lanes' largest and of the candidates 64 us; the least of 8 groups of lanes
+// as the bound, which 19 reach, 66 us.)  Where more than 32 reach the bound, equals most of them, k rounds over all
+// scores remain.  Softmax sums are fp32.
 #include <algorithm>
+#include <cfloat>
 
 #include "profile.cuh"
 #include "rowio.cuh"
@@ -61,12 +63,20 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
+// A score and its index as one whole number: larger scores above smaller ones, -0 as 0, of equals the lower index above.
+__device__ __forceinline__ uint64_t key_of(float x, int index)
+{
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return static_cast<uint64_t>(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | ~static_cast<uint32_t>(index);
+}
+
+// A lane's largest score, NaN where there is one.
 template <int V>
 __device__ __forceinline__ float lane_max(const float (&x)[V])
 {
     float m = x[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+    for (int v = 1; v < V; ++v) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(x[v]));
     return m;
 }
 
@@ -75,71 +85,78 @@ __global__ void __launch_bounds__(kRouteBlock) k_route(const T* __restrict__ log
                                                        int64_t* __restrict__ expert, float* __restrict__ weights, int32_t* d_err)
 {
     pdl_wait();
-    __shared__ float2 near[kRouteBlock / 32][32];   // a row's scores that may be picked, and their indices
+    __shared__ uint64_t near[kRouteBlock / 32][32];   // a row's candidates
     const int lane = threadIdx.x & 31;
-    float2* mine = near[threadIdx.x >> 5];
+    uint64_t* mine = near[threadIdx.x >> 5];
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kRouteBlock / 32);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteBlock / 32) + (threadIdx.x >> 5); row < n; row += step) {
         float x[V];
         read_row<T, V, W>(logits + row * experts, experts, lane, x);
-        bool odd = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) odd |= !(x[v] < INFINITY);
-        odd = __any_sync(kFull, odd);
+        const float best = lane_max(x);
+        const bool odd = __any_sync(kFull, !(best < INFINITY));
         if (odd && lane == 0) set_error(d_err, SPARSE_ERR_NON_FINITE);
-        float high = -INFINITY, value = -INFINITY;   // the largest score; this lane's candidate
-        int index = 0, at = -1, count = 0;
-        if (V == 1) {
-            value = x[0];
-            index = lane;
-            count = odd ? 0 : 32;
-        } else if (!odd) {
-            float best = lane_max(x), bound = -INFINITY;
+        int count = 0, place = 32, at = -1;   // candidates; which pick this lane's is, and its index
+        float high = -INFINITY, pick = -INFINITY;
+        if (!odd) {
+            float bound = best, left = best;
             for (int j = 0; j < k; ++j) {
-                bound = warp_max(best);
-                if (best == bound) best = -INFINITY;
+                bound = warp_max(left);
+                if (j == 0) high = bound;
+                if (left == bound) left = -INFINITY;
             }
+            bound = fmaxf(bound, -FLT_MAX);   // -inf is no candidate
+            int own = 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const bool in = x[v] >= bound && x[v] > -INFINITY;
-                const uint32_t votes = __ballot_sync(kFull, in);
-                const int place = count + __popc(votes & ((1u << lane) - 1u));
-                if (in && place < 32) mine[place] = make_float2(x[v], __int_as_float(index_of<W>(v, lane)));
-                count += __popc(votes);
+            for (int v = 0; v < V; ++v) own += x[v] >= bound ? 1 : 0;
+            int to = own;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int y = __shfl_up_sync(kFull, to, s);
+                if (lane >= s) to += y;
             }
-            __syncwarp();
-            if (lane < count) value = mine[lane].x, index = __float_as_int(mine[lane].y);
-            __syncwarp();
+            count = __shfl_sync(kFull, to, 31);
+            to -= own;
+            if (count <= 32) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (x[v] >= bound) mine[to++] = static_cast<uint64_t>(__float_as_uint(x[v])) << 32 | static_cast<uint32_t>(index_of<W>(v, lane));
+                __syncwarp();
+                const uint64_t raw = lane < count ? mine[lane] : 0u;
+                const uint64_t key = key_of(__uint_as_float(static_cast<uint32_t>(raw >> 32)), static_cast<int>(raw));
+                mine[lane] = key;
+                __syncwarp();
+                int before = 0;
+#pragma unroll 4
+                for (int c = 0; c < count; ++c) before += mine[c] > key ? 1 : 0;
+                if (lane < count && before < k) {
+                    pick = __uint_as_float(static_cast<uint32_t>(raw >> 32));
+                    at = static_cast<int>(raw);
+                    place = before;
+                }
+                __syncwarp();
+            }
         }
-        float pick = -INFINITY;
-        if (count <= 32) {
-            for (int j = 0; j < k && count > 0; ++j) {
-                const float top = warp_max(value);
-                if (top == -INFINITY) break;                 // nothing but -inf is left
-                const uint32_t place = __reduce_min_sync(kFull, value == top ? static_cast<uint32_t>(index) : 0xffffffffu);
-                if (value == top && static_cast<uint32_t>(index) == place) value = -INFINITY;
-                if (j == 0) high = top;
-                if (lane == j) pick = top, at = static_cast<int>(place);
-            }
-        } else {                                             // many equals
+        if (count > 32) {                                     // many equals
             float y[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) y[v] = x[v];
+            count = 0;
             for (int j = 0; j < k; ++j) {
                 const float top = warp_max(lane_max(y));
                 if (top == -INFINITY) break;
-                uint32_t place = 0xffffffffu;
+                uint32_t first = 0xffffffffu;
 #pragma unroll
                 for (int v = V - 1; v >= 0; --v)
-                    if (y[v] == top) place = index_of<W>(v, lane);
-                const uint32_t taken = __reduce_min_sync(kFull, place);
+                    if (y[v] == top) first = index_of<W>(v, lane);
+                const uint32_t taken = __reduce_min_sync(kFull, first);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (static_cast<uint32_t>(index_of<W>(v, lane)) == taken) y[v] = -INFINITY;
-                if (j == 0) high = top;
-                if (lane == j) pick = top, at = static_cast<int>(taken);
+                if (lane == j) pick = top, at = static_cast<int>(taken), place = j;
+                ++count;
             }
         }
+        if (lane >= count) place = lane;                      // picks that there are none for
         const float w = at >= 0 ? expf(pick - high) : 0.0f;
         float total = w;
         if (!renormalize) {
@@ -149,9 +166,9 @@ __global__ void __launch_bounds__(kRouteBlock) k_route(const T* __restrict__ log
                 for (int v = 0; v < V; ++v) total += exp_of(x[v] - high);
         }
         total = warp_sum(total);
-        if (lane < k) {
-            expert[row * k + lane] = at;
-            weights[row * k + lane] = at >= 0 ? w / total : 0.0f;
+        if (place < k) {
+            expert[row * k + place] = at;
+            weights[row * k + place] = at >= 0 ? __fdividef(w, total) : 0.0f;
         }
     }
 }

@@ -188,17 +188,24 @@ __global__ void __launch_bounds__(kRouteBlock) k_route_grad(const float* __restr
     for (int i = lane; i < 32 * V; i += 32) mine[i] = 0.0f;
     __syncwarp();
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kRouteBlock / 32);
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteBlock / 32) + (threadIdx.x >> 5); row < n; row += step) {
-        int64_t at = -1;
-        float w = 0.0f, g = 0.0f;
-        if (lane < k) {
-            at = expert[row * k + lane];
-            if (at < -1 || at >= experts) {
-                set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
-                at = -1;
-            }
-            if (at >= 0) w = weights[row * k + lane], g = dweights[row * k + lane];   // the others' are not looked at
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRouteBlock / 32) + (threadIdx.x >> 5);
+    int64_t at = -1, next_at = -1;
+    float w = 0.0f, g = 0.0f, next_w = 0.0f, next_g = 0.0f;
+    auto fetch = [&](int64_t row) {   // a row ahead
+        if (lane >= k || row >= n) return;
+        next_at = expert[row * k + lane];
+        next_w = weights[row * k + lane];
+        next_g = dweights[row * k + lane];
+    };
+    fetch(first);
+    for (int64_t row = first; row < n; row += step) {
+        at = next_at, w = next_w, g = next_g;
+        fetch(row + step);
+        if (at < -1 || at >= experts) {
+            set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
+            at = -1;
         }
+        if (at < 0) w = g = 0.0f;   // whatever stands there
         const float s = warp_sum(w * g);
         if (at >= 0) mine[at] = renormalize ? w * (g - s) : w * g;
         __syncwarp();

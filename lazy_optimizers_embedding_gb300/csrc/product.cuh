@@ -34,6 +34,7 @@ constexpr int kPM = 128, kPK = 64;                    // rows of a block's tile;
 constexpr int kPBox = 64;                             // rows of one copied box: 64 x 128 bytes
 constexpr uint32_t kPBoxBytes = kPBox * kPK * 2;
 constexpr int kMaxGroups = 1024;
+constexpr int64_t kSms = 152;                         // what tiles and parts, and so workspaces, are planned for, whatever the device of a size query
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct ProductMaps {

@@ -126,7 +126,7 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
 // there are fewer tiles than pairs.
 bool wants_pair(int64_t m, int64_t tiles_of_128)
 {
-    return up(m, 256) * 2 <= up(m, 128) + up(m, 128) / 4 && tiles_of_128 >= num_sms();
+    return up(m, 256) * 2 <= up(m, 128) + up(m, 128) / 4 && tiles_of_128 >= kSms;
 }
 
 // Tiles at most: every group may end in a part of one.
@@ -143,7 +143,7 @@ cudaError_t rows_form(const RowsProduct& R, cudaStream_t s)
     Q.k = static_cast<int32_t>(R.k);
     Q.m_tiles = static_cast<int32_t>(up(R.m, S::TM));
     Q.width = S::BN;
-    const int64_t units = num_sms() / S::kPair;
+    const int64_t units = kSms / S::kPair;
     if (R.groups == 1) {   // the width whose rounds over the GPU take least; a stage: see stage_cycles
         int64_t best = INT64_MAX;
         for (int w = S::BN; w >= 64; w -= 32) {
@@ -201,7 +201,7 @@ int rows_splits(int64_t rows, int64_t m, int64_t k, int64_t groups, int parts)
 {
     const int64_t width = parts == 3 ? 128 : 256;
     const int64_t tiles = row_tiles(rows, groups, width) * up(m, 128);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_sms() / std::max<int64_t>(tiles, 1), up(k, kPK) / 4, 64})));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kSms / std::max<int64_t>(tiles, 1), up(k, kPK) / 4, 64})));
 }
 
 cudaError_t rows_product(const RowsProduct& R, cudaStream_t s)

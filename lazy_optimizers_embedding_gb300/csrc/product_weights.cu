@@ -38,14 +38,14 @@ cudaError_t weights_form(const WeightsProduct& R, cudaStream_t s)
 int weights_splits(int64_t rows, int64_t m, int64_t n, int64_t groups, int parts)
 {
     const int64_t tiles = groups * up(m, 128) * up(n, parts == 3 ? 128 : 256);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_sms() / tiles, rows / groups / (4 * kPK), 64})));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kSms / tiles, rows / groups / (4 * kPK), 64})));
 }
 
 cudaError_t weights_product(const WeightsProduct& R, cudaStream_t s)
 {
     // pairs of blocks: see rows_product
     const int64_t tiles = R.groups * up(R.m, 128) * up(R.n, R.b.parts == 3 ? 128 : 256);
-    const bool pair = R.splits == 1 && up(R.m, 256) * 2 <= up(R.m, 128) + up(R.m, 128) / 4 && tiles >= num_sms();
+    const bool pair = R.splits == 1 && up(R.m, 256) * 2 <= up(R.m, 128) + up(R.m, 128) / 4 && tiles >= kSms;
     if (R.b.parts == 3)
         return pair ? weights_form<ProductShape<kWeights, true, true, 2, 6, false>>(R, s)
                     : weights_form<ProductShape<kWeights, true, true, 1, 6, false>>(R, s);

@@ -455,7 +455,7 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
 // own rows, its first scores and its sums take about 3 tiles' time, a part's sums are written and read again.
 void back_splits(int64_t n, int64_t v, int64_t tile, int& tokens, int& rows)
 {
-    const int64_t units = num_sms(), own_n = up(n, kOwn), own_v = up(v, kOwn), tiles_v = up(v, tile), tiles_n = up(n, tile);
+    const int64_t units = kSms, own_n = up(n, kOwn), own_v = up(v, kOwn), tiles_v = up(v, tile), tiles_n = up(n, tile);
     int64_t least = INT64_MAX;
     tokens = rows = 1;
     for (int64_t a = 1; a <= 64 && a <= tiles_v; ++a)

@@ -39,7 +39,7 @@ Grid score_grid(int64_t n, int64_t c, int64_t v, int parts, bool runs)
     Grid g{};
     g.pair = n > 128;
     const int most = parts == 3 ? 128 : 256, products = parts == 3 ? 6 : 1;
-    const int64_t units = num_sms() / (g.pair ? 2 : 1), m_tiles = up(n, g.pair ? 256 : 128), chunks = up(c, kPK);
+    const int64_t units = kSms / (g.pair ? 2 : 1), m_tiles = up(n, g.pair ? 256 : 128), chunks = up(c, kPK);
     int64_t best = INT64_MAX;
     for (int w = most; w >= most / 2; w -= 32) {
         const int64_t stage = std::max<int64_t>(2 * w * products, parts * (kPM + w / (g.pair ? 2 : 1)) * 128 / 80);

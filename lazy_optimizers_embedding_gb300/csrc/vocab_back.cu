@@ -39,7 +39,8 @@ struct BackShape {
     static constexpr int kSums = C / 64;                                   // groups of warps that empty D, 64 columns each
     static constexpr int kThreads = 64 + (4 + kSums) * 128;
     static constexpr int kScoreCols = kParts > 1 ? 2 * TN : TN;            // = 128: hi and lo sums of TN scores, or one
-    static constexpr int kSumCols = kParts > 1 ? 2 * C : C;                // D: hi, then lo
+    static constexpr bool kWide = kParts > 1 && C == 64;                   // three accumulators of D, by the order of their products
+    static constexpr int kSumCols = kWide ? 3 * C : kParts > 1 ? 2 * C : C;
     static constexpr int kBufs = (512 - kSumCols) / kScoreCols;            // tiles whose scores or slopes are there at a time: 2 or 3
     static constexpr int kD = kBufs * kScoreCols;                          // D's first column
     static constexpr int kChunk = 8;                                       // tiles of D between two emptyings
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
             constexpr uint32_t score_desc2 = mma_desc_bf16(kOwn, false, false) | static_cast<uint32_t>(2 * TN >> 3) << 17;
             constexpr uint32_t sum_desc = mma_desc_bf16(kOwn, false, true) | static_cast<uint32_t>(C >> 3) << 17;
             constexpr uint32_t sum_desc2 = mma_desc_bf16(kOwn, false, true) | static_cast<uint32_t>(2 * C >> 3) << 17;
+            constexpr uint32_t sum_desc3 = mma_desc_bf16(kOwn, false, true) | static_cast<uint32_t>(3 * C >> 3) << 17;
             // Scores of tile it, the next, are asked for as soon as its rows are there and the slopes of tile it - kBufs have been used, the
             // second product of tile back_it when its slopes are there, whichever is first: with two stages the
             // rows of the next tile come only after a second product (128 fp32 columns in fixed order: 6350 cycles a tile of 3840 of products).
@@ -237,13 +239,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                             const bool more = !fresh || k > 0;
                             const uint32_t a = g + (P == 6 ? k / 2 * 32 + k % 2 * 8 : k / 4 * 64 + k % 4 * 8);   // see the slopes' places below
                             const uint64_t r = rows + k * (2048 / 16);
-                            if (P == 6 && C == 64) {   // the first two parts lie side by side as D's hi and lo sums do
-                                tc_mma_f16_tmem(d, a, r, sum_desc2, more);
-                            } else {
-                                tc_mma_f16_tmem(d, a, r, sum_desc, more);
-                                if (P == 6) tc_mma_f16_tmem(d + C, a, r + kPart, sum_desc, more);
+                            if (S::kWide) {   // the parts lie side by side as D's sums do; a product of 64 columns takes as long as one of 128
+                                tc_mma_f16_tmem(d, a, r, sum_desc3, more);
+                                tc_mma_f16_tmem(d + C, a + TN, r, sum_desc2, true);
+                                tc_mma_f16_tmem(d + 2 * C, a + 16, r, sum_desc, true);
+                                continue;
                             }
+                            tc_mma_f16_tmem(d, a, r, sum_desc, more);
                             if (P == 6) {
+                                tc_mma_f16_tmem(d + C, a, r + kPart, sum_desc, more);
                                 tc_mma_f16_tmem(d + C, a, r + 2 * kPart, sum_desc, true);
                                 tc_mma_f16_tmem(d + C, a + 16, r, sum_desc, true);
                                 tc_mma_f16_tmem(d + C, a + TN, r + kPart, sum_desc, true);
@@ -394,6 +398,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                         tmem_load16(lanes + q * 16, lanes + C + q * 16, v, x);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] += x[e];
+                        if constexpr (S::kWide) {
+                            tmem_load16(lanes + 2 * C + q * 16, x);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] += x[e];
+                        }
                     } else {
                         tmem_load16(lanes + q * 16, v);
                     }

@@ -60,7 +60,7 @@ cudaError_t prepare(const Layout& L, bool f32, const void*& p, int64_t p_rows, i
     const Pack1 second{q, reinterpret_cast<bf16*>(ws + L.q_at), L.q.packed ? q_rows : 0, q_cols, L.q.ld};
     if (L.p.packed) p = first.to;
     if (L.q.packed) q = second.to;
-    return L.p.packed || L.q.packed ? pack(first, second, !f32, s) : cudaSuccess;
+    return L.p.packed || L.q.packed ? pack(first, second, TokenRows{}, !f32, s) : cudaSuccess;
 }
 
 }  // namespace

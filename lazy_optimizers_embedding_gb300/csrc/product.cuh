@@ -750,8 +750,31 @@ struct Pack1 {
     bf16* to;
     int64_t rows, cols, ld;
 };
-// Up to two arrays in one launch (the second's rows may be 0).
-cudaError_t pack(const Pack1& a, const Pack1& b, int is_bf16, cudaStream_t s);
+// The tokens' numbers for the loss's gradient: lse log2(e), dloss (over the unit, where one is asked for) and target, 0 and -1 for
+// a token that does not count and behind the last (vocab_back.cu).
+struct TokenRows {
+    const float *lse, *dloss;
+    const int64_t* target;
+    int n, padded, v;
+    float4* out;
+    float* unit;
+    int32_t* d_err;
+};
+__device__ __forceinline__ void put_token(const TokenRows& R, int i, float unit)
+{
+    if (i >= R.padded) return;
+    float4 q = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
+    if (i < R.n) {
+        const int64_t g = R.target[i];
+        if (g < -1 || g >= R.v) set_error(R.d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
+        if (g >= 0 && g < R.v)
+            q = make_float4(R.lse[i] * kLog2e, R.dloss ? __fdiv_rn(R.dloss[i], unit) : 1.0f, __int_as_float(static_cast<int>(g)), 0.0f);
+    }
+    R.out[i] = q;
+}
+
+// Up to two arrays in one launch (the second's rows may be 0), and the tokens' numbers (no unit; padded may be 0).
+cudaError_t pack(const Pack1& a, const Pack1& b, const TokenRows& tokens, int is_bf16, cudaStream_t s);
 
 // rows x cols fp32 sums of `slabs` arrays, in order; rows from *end on (end given) are zeros.
 struct Join {
@@ -761,6 +784,7 @@ struct Join {
     const int64_t* end;
 };
 cudaError_t join_slabs(const Join& J, void* out, int out_bf16, cudaStream_t s);
+cudaError_t join_two(const Join& a, void* out_a, const Join& b, void* out_b, int out_bf16, cudaStream_t s);
 
 // The product of rows with their group's matrix, and of two arrays of rows (product_rows.cu, product_weights.cu): fills in the rest of Q
 // (extents, tiles); `pieces`: sums are added to what `out` (fp32 slabs) holds.

@@ -66,25 +66,25 @@ __device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t 
 // Rows of one or two arrays as bf16 with aligned rows: fp32 in three parts, hi = bf16(v), mid = bf16(v - hi), lo = what
 // those leave (2^-26 of v at most).  Bound by memory: 4 bytes in, 6 out.
 template <class T, bool kVec>
-__global__ void __launch_bounds__(kPackBlock) k_pack(const Pack1 A, const Pack1 B, int blocks_a)
+__global__ void __launch_bounds__(kPackBlock) k_pack(const Pack1 A, const Pack1 B, const TokenRows R, int blocks_a, int blocks_b)
 {
-    pdl_enter();   // writes the workspace only
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = kPackBlock / 32;
-    if (static_cast<int>(blockIdx.x) < blocks_a)
-        pack_rows<T, kVec>(A, static_cast<int64_t>(blockIdx.x) * per + w, static_cast<int64_t>(blocks_a) * per, lane);
+    pdl_enter();   // writes the workspace and the error word
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = kPackBlock / 32, block = blockIdx.x;
+    if (block < blocks_a)
+        pack_rows<T, kVec>(A, static_cast<int64_t>(block) * per + w, static_cast<int64_t>(blocks_a) * per, lane);
+    else if (block < blocks_a + blocks_b)
+        pack_rows<T, kVec>(B, static_cast<int64_t>(block - blocks_a) * per + w, static_cast<int64_t>(blocks_b) * per, lane);
     else
-        pack_rows<T, kVec>(B, static_cast<int64_t>(blockIdx.x - blocks_a) * per + w,
-                           static_cast<int64_t>(gridDim.x - blocks_a) * per, lane);
+        put_token(R, (block - blocks_a - blocks_b) * kPackBlock + static_cast<int>(threadIdx.x), 1.0f);
 }
 
 // Sums of slabs in order, four neighbours a thread.
 template <class T, bool kVec>
-__global__ void __launch_bounds__(256) k_join_slabs(const Join J, T* __restrict__ out)
+__device__ __forceinline__ void join_rows(const Join& J, T* __restrict__ out, int block, int blocks)
 {
-    pdl_wait();
     const int64_t groups = (J.cols + 3) / 4, count = J.rows * groups;
     const int64_t live = J.end ? min(max(*J.end, static_cast<int64_t>(0)), J.rows) : J.rows;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += static_cast<int64_t>(gridDim.x) * 256) {
+    for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < count; i += static_cast<int64_t>(blocks) * 256) {
         const int64_t row = (count >> 32) == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(groups) : i / groups;
         const int col = static_cast<int>(i - row * groups) * 4, left = static_cast<int>(min(J.cols - col, static_cast<int64_t>(4)));
         const int64_t at = row * J.cols + col;
@@ -118,6 +118,17 @@ __global__ void __launch_bounds__(256) k_join_slabs(const Join J, T* __restrict_
                 if (e < left) out[at + e] = T(s[e]);
         }
     }
+}
+
+// Of one or two arrays in one launch.
+template <class T, bool kVec>
+__global__ void __launch_bounds__(256) k_join_slabs(const Join A, T* a, const Join B, T* b, int blocks_a)
+{
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) < blocks_a)
+        join_rows<T, kVec>(A, a, blockIdx.x, blocks_a);
+    else
+        join_rows<T, kVec>(B, b, static_cast<int>(blockIdx.x) - blocks_a, static_cast<int>(gridDim.x) - blocks_a);
 }
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a; }
@@ -168,34 +179,40 @@ cudaError_t rows_form(const RowsProduct& R, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t pack(const Pack1& a, const Pack1& b, int is_bf16, cudaStream_t s)
+cudaError_t pack(const Pack1& a, const Pack1& b, const TokenRows& tokens, int is_bf16, cudaStream_t s)
 {
     auto blocks = [](const Pack1& p) { return std::min<int64_t>(8 * num_sms(), up(p.rows * up(p.ld, 8), 8 * kPackBlock)); };
-    const int64_t na = blocks(a), nb = blocks(b);
-    if (na + nb == 0) return cudaSuccess;
+    const int64_t na = blocks(a), nb = blocks(b), nt = up(tokens.padded, kPackBlock);
+    if (na + nb + nt == 0) return cudaSuccess;
     const int v = is_bf16 ? 8 : 4;
     auto fits = [&](const Pack1& p) {
         return p.rows == 0 || (p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.from) % (is_bf16 ? 2 * v : 4 * v) == 0);
     };
     const bool vec = fits(a) && fits(b);
-    const dim3 grid(static_cast<unsigned>(na + nb)), block(kPackBlock);
+    auto go = [&](auto* kernel) {
+        return launch(kernel, dim3(static_cast<unsigned>(na + nb + nt)), dim3(kPackBlock), s, a, b, tokens, static_cast<int>(na),
+                      static_cast<int>(nb));
+    };
     SO_PROFILE("pack", s);
-    if (is_bf16)
-        return vec ? launch(k_pack<bf16, true>, grid, block, s, a, b, static_cast<int>(na))
-                   : launch(k_pack<bf16, false>, grid, block, s, a, b, static_cast<int>(na));
-    return vec ? launch(k_pack<float, true>, grid, block, s, a, b, static_cast<int>(na))
-               : launch(k_pack<float, false>, grid, block, s, a, b, static_cast<int>(na));
+    if (is_bf16) return vec ? go(k_pack<bf16, true>) : go(k_pack<bf16, false>);
+    return vec ? go(k_pack<float, true>) : go(k_pack<float, false>);
 }
 
-cudaError_t join_slabs(const Join& J, void* out, int out_bf16, cudaStream_t s)
+cudaError_t join_two(const Join& a, void* out_a, const Join& b, void* out_b, int out_bf16, cudaStream_t s)
 {
-    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(8 * num_sms(), up(J.rows * up(J.cols, 4), 256))))), block(256);
-    const bool vec = J.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;   // the slabs lie in the workspace
+    auto blocks = [](const Join& J) { return J.rows > 0 ? std::max<int64_t>(1, std::min<int64_t>(8 * num_sms(), up(J.rows * up(J.cols, 4), 256))) : 0; };
+    const int64_t na = blocks(a), nb = blocks(b);
+    // the slabs lie in the workspace
+    const bool vec = a.cols % 4 == 0 && b.cols % 4 == 0 && ((reinterpret_cast<uintptr_t>(out_a) | reinterpret_cast<uintptr_t>(out_b)) & 15) == 0;
     SO_PROFILE("join_slabs", s);
-    if (out_bf16)
-        return launch(vec ? k_join_slabs<bf16, true> : k_join_slabs<bf16, false>, grid, block, s, J, static_cast<bf16*>(out));
-    return launch(vec ? k_join_slabs<float, true> : k_join_slabs<float, false>, grid, block, s, J, static_cast<float*>(out));
+    auto go = [&](auto* kernel, auto* one, auto* two) {
+        return launch(kernel, dim3(static_cast<unsigned>(na + nb)), dim3(256), s, a, one, b, two, static_cast<int>(na));
+    };
+    if (out_bf16) return go(vec ? k_join_slabs<bf16, true> : k_join_slabs<bf16, false>, static_cast<bf16*>(out_a), static_cast<bf16*>(out_b));
+    return go(vec ? k_join_slabs<float, true> : k_join_slabs<float, false>, static_cast<float*>(out_a), static_cast<float*>(out_b));
 }
+
+cudaError_t join_slabs(const Join& J, void* out, int out_bf16, cudaStream_t s) { return join_two(J, out, Join{}, nullptr, out_bf16, s); }
 
 int rows_splits(int64_t rows, int64_t m, int64_t k, int64_t groups, int parts)
 {

@@ -74,23 +74,12 @@ struct Maps {
     CUtensorMap x, w;
 };
 
-// The tokens' numbers: lse log2(e), dloss (over the unit, where one is asked for) and target, 0 and -1 for a token that does not count and behind the last.
-__global__ void __launch_bounds__(256) k_loss_tokens(const float* __restrict__ lse, const float* __restrict__ dloss,
-                                                     const int64_t* __restrict__ target, int n, int padded, int v,
-                                                     float4* __restrict__ out, float* unit, int32_t* d_err)
+__global__ void __launch_bounds__(256) k_loss_tokens(const TokenRows R)
 {
     pdl_enter();   // writes the workspace and the error word
-    const float u = unit != nullptr ? common_unit(dloss, target, n, threadIdx.x & 31) : 1.0f;
-    if (unit != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *unit = u;
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= padded) return;
-    float4 q = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
-    if (i < n) {
-        const int64_t g = target[i];
-        if (g < -1 || g >= v) set_error(d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
-        if (g >= 0 && g < v) q = make_float4(lse[i] * kLog2e, dloss ? __fdiv_rn(dloss[i], u) : 1.0f, __int_as_float(static_cast<int>(g)), 0.0f);
-    }
-    out[i] = q;
+    const float u = R.unit != nullptr ? common_unit(R.dloss, R.target, R.n, threadIdx.x & 31) : 1.0f;
+    if (R.unit != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *R.unit = u;
+    put_token(R, blockIdx.x * 256 + threadIdx.x, u);
 }
 
 template <class S>
@@ -128,6 +117,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();
+    if (Q.release) pdl_release();   // after this block's allocation, so that no later block can hold what it waits for
     fence_async_proxy();   // the kernels before wrote with ordinary stores
 
     if (warp == 0) {
@@ -501,11 +491,10 @@ BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v)
     return B;
 }
 
-cudaError_t loss_tokens(const VocabLoss& V, int64_t padded, float4* out, float* unit, cudaStream_t s)
+cudaError_t loss_tokens(const TokenRows& R, cudaStream_t s)
 {
     SO_PROFILE("vocab_tokens", s);
-    return launch(k_loss_tokens, dim3(static_cast<unsigned>(up(padded, 256))), dim3(256), s, static_cast<const float*>(V.lse), V.dloss,
-                  V.target, static_cast<int>(V.n), static_cast<int>(padded), static_cast<int>(V.v), out, unit, V.d_err);
+    return launch(k_loss_tokens, dim3(static_cast<unsigned>(up(R.padded, 256))), dim3(256), s, R);
 }
 
 cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s)

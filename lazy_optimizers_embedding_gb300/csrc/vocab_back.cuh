@@ -1,9 +1,7 @@
 // vocab_back.cuh -- the interface of the loss's gradient for narrow rows.
 #pragma once
 
-#include <cuda.h>
-
-#include "common.cuh"
+#include "product.cuh"
 
 namespace so {
 
@@ -14,6 +12,7 @@ struct BackArgs {
     const float4* tokens;    // see loss_tokens
     void *dx, *dw;           // results, or fp32 slabs where there are several parts; nullptr: not wanted
     int32_t dx_splits, dw_splits, out_bf16;
+    int32_t release;         // writes slabs only
     const float* unit;       // bf16: what results are multiplied by (see common_unit)
     int32_t dx_items, dw_items;   // filled in by loss_back
     int32_t* d_err;
@@ -25,7 +24,7 @@ struct BackPlan {
 };
 
 BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v);
-cudaError_t loss_tokens(const VocabLoss& V, int64_t padded, float4* out, float* unit, cudaStream_t s);
+cudaError_t loss_tokens(const TokenRows& R, cudaStream_t s);
 cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s);
 
 }  // namespace so

@@ -50,15 +50,38 @@ __device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t 
         for (int64_t i = lane % G * 8; i < A.cols; i += G * 8) {
             float x[8];
             read8<T, kVec>(static_cast<const T*>(A.from) + r * A.cols + i, A.cols - i, x);
+            bf16* to = A.to + r * A.ld + i;
+            if (kParts == 1) {
+                Pack<bf16, 8>::put(to, x);
+                continue;
+            }
+            bool plain = true;   // nothing that is not finite, or not as bf16
+#pragma unroll
+            for (int e = 0; e < 8; ++e) plain = plain && fabsf(x[e]) <= 3.38e38f;
+            if (plain) {         // (with every value looked at for itself: 42 us and not 34 at 7200 x 515 and 19055 x 771)
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    uint4 w;
+                    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = bf16_pair(x[2 * e], x[2 * e + 1]);
+                        const float2 h = pair_floats(u[e]);
+                        x[2 * e] -= h.x, x[2 * e + 1] -= h.y;
+                    }
+                    *reinterpret_cast<uint4*>(to + p * size) = w;
+                }
+                continue;
+            }
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 float h[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    h[e] = kParts == 1 ? x[e] : part_of(x[e]);
+                    h[e] = part_of(x[e]);
                     x[e] = isfinite(h[e]) ? x[e] - h[e] : 0.0f;   // an infinity or NaN is all in the first part
                 }
-                Pack<bf16, 8>::put(A.to + r * A.ld + i + p * size, h);
+                Pack<bf16, 8>::put(to + p * size, h);
             }
         }
 }
@@ -90,6 +113,7 @@ __device__ __forceinline__ void join_rows(const Join& J, T* __restrict__ out, in
         const int64_t at = row * J.cols + col;
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (row < live) {
+#pragma unroll 4
             for (int q = 0; q < J.slabs; ++q) {
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (kVec) {

@@ -34,6 +34,7 @@ constexpr int kPM = 128, kPK = 64;                    // rows of a block's tile;
 constexpr int kPBox = 64;                             // rows of one copied box: 64 x 128 bytes
 constexpr uint32_t kPBoxBytes = kPBox * kPK * 2;
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxSorted = 256;                       // groups that kWeights takes the longest first (each block ranks them: 0.5 us)
 constexpr int64_t kSms = 152;                         // what tiles and parts, and so workspaces, are planned for, whatever the device of a size query
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -149,6 +150,7 @@ __device__ __forceinline__ Tile item_of(const ProductArgs& Q, const int* begin, 
         T.m0 = static_cast<int>(u - v * Q.m_tiles) * S::TM;
         T.e = static_cast<int>(v / Q.n_tiles);
         T.n0 = static_cast<int>(v - T.e * Q.n_tiles) * Q.width;
+        if (Q.groups > 1 && Q.groups <= kMaxSorted) T.e = static_cast<int>(start[T.e]);
         T.valid = min(Q.width, Q.n - T.n0);
         T.k0 = begin[T.e];
         T.len = begin[T.e + 1] - T.k0;
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     __shared__ int begin[S::kGrouped ? kMaxGroups + 1 : 1];
-    __shared__ uint32_t start[kForm == kRows ? kMaxGroups + 1 : 1];
+    __shared__ uint32_t start[kForm == kRows ? kMaxGroups + 1 : kForm == kWeights ? kMaxSorted : 1];   // (kWeights: the groups by length)
     const uint32_t data = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages,
                    tempty = tfull + 8 * S::kAccs, drain = tempty + 8 * S::kAccs, fix = drain + 8;
@@ -390,6 +392,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             if (!sound && blockIdx.x == 0 && threadIdx.x == 0) set_error(Q.d_err, SPARSE_ERR_INDEX_OUT_OF_RANGE);
         } else {
             if (threadIdx.x == 0) begin[0] = 0, begin[1] = Q.rows;
+            __syncthreads();
+        }
+        // Items go to the blocks in turn: with the longest groups first, neighbours are alike and the blocks' sums even out
+        // (16384 x 8 rows among 128 experts of uneven favour: 448 against 402 us).
+        if (kForm == kWeights && sound && Q.groups > 1 && Q.groups <= kMaxSorted) {
+            for (int e = threadIdx.x; e < Q.groups; e += S::kThreads) {
+                const int mine = begin[e + 1] - begin[e];
+                int rank = 0;
+                for (int f = 0; f < Q.groups; ++f) {
+                    const int rows = begin[f + 1] - begin[f];
+                    rank += rows > mine || (rows == mine && f < e) ? 1 : 0;
+                }
+                start[rank] = e;
+            }
             __syncthreads();
         }
         if (kForm == kRows && sound) {

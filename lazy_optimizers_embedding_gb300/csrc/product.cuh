@@ -34,7 +34,7 @@ constexpr int kPM = 128, kPK = 64;                    // rows of a block's tile;
 constexpr int kPBox = 64;                             // rows of one copied box: 64 x 128 bytes
 constexpr uint32_t kPBoxBytes = kPBox * kPK * 2;
 constexpr int kMaxGroups = 1024;
-constexpr int kMaxSorted = 256;                       // groups that kWeights takes the longest first (each block ranks them: 0.5 us)
+constexpr int kMaxSorted = 256;                       // groups that kWeights takes by their length (each block ranks them: 0.5 us)
 constexpr int64_t kSms = 152;                         // what tiles and parts, and so workspaces, are planned for, whatever the device of a size query
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -100,6 +100,8 @@ struct Tile {
 
 __device__ __forceinline__ int up32(int x) { return (x + 31) & ~31; }
 
+__device__ __forceinline__ bool sorted_groups(const ProductArgs& Q) { return Q.groups > 1 && Q.groups <= kMaxSorted; }
+
 // Items of a launch (kRows: known once the groups' rows are).  All counts of items stay below 2^31 (see the entry points' limits).
 template <class S>
 __device__ __forceinline__ int items_of(const ProductArgs& Q, const uint32_t* start)
@@ -113,7 +115,7 @@ __device__ __forceinline__ int items_of(const ProductArgs& Q, const uint32_t* st
 // Item t, at its first tile; `count` tiles.  The experts' tiles of a column of M follow one another (they share A), the
 // score's token blocks of some columns do (they share the table's rows).
 template <class S>
-__device__ __forceinline__ Tile item_of(const ProductArgs& Q, const int* begin, const uint32_t* start, int t, int& count)
+__device__ __forceinline__ Tile item_of(const ProductArgs& Q, const int* begin, const uint32_t* start, const uint16_t* order, int t, int& count)
 {
     Tile T{};
     count = 1;
@@ -132,12 +134,12 @@ __device__ __forceinline__ Tile item_of(const ProductArgs& Q, const int* begin, 
                 hi = mid;
         }
         T.e = lo;
-        const int rows = begin[lo + 1] - begin[lo], r = static_cast<int>(u - start[lo]);
+        const int rows = begin[T.e + 1] - begin[T.e], r = static_cast<int>(u - start[lo]);
         const int tiles = (rows + Q.width - 1) / Q.width;
         const int w = up32((rows + tiles - 1) / tiles);        // equal tiles; the last has a row at least
         const int across = r / tiles, i = r - across * tiles;
         T.m0 = across * S::TM;
-        T.n0 = begin[lo] + i * w;
+        T.n0 = begin[T.e] + i * w;
         T.valid = min(w, rows - i * w);
         T.c1 = (Q.k + kPK - 1) / kPK;
     } else if (S::kForm == kWeights) {
@@ -150,7 +152,7 @@ __device__ __forceinline__ Tile item_of(const ProductArgs& Q, const int* begin, 
         T.m0 = static_cast<int>(u - v * Q.m_tiles) * S::TM;
         T.e = static_cast<int>(v / Q.n_tiles);
         T.n0 = static_cast<int>(v - T.e * Q.n_tiles) * Q.width;
-        if (Q.groups > 1 && Q.groups <= kMaxSorted) T.e = static_cast<int>(start[T.e]);
+        if (sorted_groups(Q)) T.e = order[T.e];
         T.valid = min(Q.width, Q.n - T.n0);
         T.k0 = begin[T.e];
         T.len = begin[T.e + 1] - T.k0;
@@ -346,7 +348,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int dead;
     __shared__ int begin[S::kGrouped ? kMaxGroups + 1 : 1];
-    __shared__ uint32_t start[kForm == kRows ? kMaxGroups + 1 : kForm == kWeights ? kMaxSorted : 1];   // (kWeights: the groups by length)
+    __shared__ uint32_t start[kForm == kRows ? kMaxGroups + 1 : 1];   // first item of the groups
+    __shared__ uint16_t order[kForm == kWeights ? kMaxSorted : 1];    // the groups by length
     const uint32_t data = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages,
                    tempty = tfull + 8 * S::kAccs, drain = tempty + 8 * S::kAccs, fix = drain + 8;
@@ -394,9 +397,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             if (threadIdx.x == 0) begin[0] = 0, begin[1] = Q.rows;
             __syncthreads();
         }
-        // Items go to the blocks in turn: with the longest groups first, neighbours are alike and the blocks' sums even out
-        // (16384 x 8 rows among 128 experts of uneven favour: 448 against 402 us).
-        if (kForm == kWeights && sound && Q.groups > 1 && Q.groups <= kMaxSorted) {
+        // Items go to the blocks in turn: with the longest groups first neighbours are alike and the blocks' sums even out (16384 x 8 rows
+        // among 128 experts of uneven favour: 448 against 402 us).  kRows' tiles differ by their width alone, and took longer that way (304
+        // against 285 us there).
+        if (kForm == kWeights && sound && sorted_groups(Q)) {
             for (int e = threadIdx.x; e < Q.groups; e += S::kThreads) {
                 const int mine = begin[e + 1] - begin[e];
                 int rank = 0;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
                     const int rows = begin[f + 1] - begin[f];
                     rank += rows > mine || (rows == mine && f < e) ? 1 : 0;
                 }
-                start[rank] = e;
+                order[rank] = static_cast<uint16_t>(e);
             }
             __syncthreads();
         }
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             uint32_t it = 0, fixed = 0, turn = 0;   // stages; those that warp 2 has had at all, and (parity) how often
             for (int t = first; t < items; t += step) {
                 int count;
-                Tile T = item_of<S>(Q, begin, start, t, count);
+                Tile T = item_of<S>(Q, begin, start, order, t, count);
                 for (int j = 0; j < count; ++j, next_tile(Q, T)) {
                     const int boxes = (T.N / kPair + kPBox - 1) / kPBox;
                     const uint32_t bytes = S::kParts * (S::kA + boxes * kPBoxBytes);
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             bool ok = true;
             for (int t = first; ok && t < items; t += step) {
                 int count;
-                Tile T = item_of<S>(Q, begin, start, t, count);
+                Tile T = item_of<S>(Q, begin, start, order, t, count);
                 for (int j = 0; ok && j < count; ++j, next_tile(Q, T)) {
                     const uint32_t what = idesc | static_cast<uint32_t>(T.N >> 3) << 17;
                     for (int c = T.c0; ok && c < T.c1; ++done) {
@@ -548,7 +552,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
             bool ok = true;
             for (int t = first; ok && t < items; t += step) {
                 int count;
-                const Tile T = item_of<S>(Q, begin, start, t, count);
+                const Tile T = item_of<S>(Q, begin, start, order, t, count);
                 it += T.c1 - T.c0;
                 if (T.c1 == T.c0 || T.c1 * kPK <= T.len) continue;   // no last stage, or a whole one
                 const uint32_t s = (it - 1) % kStages;
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_product(const __grid_constan
         };
         for (int t = first; ok && t < items; t += step) {
             int count;
-            Tile T = item_of<S>(Q, begin, start, t, count);
+            Tile T = item_of<S>(Q, begin, start, order, t, count);
             const int f = T.m0 + rank * kPM + rowl;
             float top = -INFINITY, total = 0.0f;      // kScore
             float lse2 = 0.0f, scale = 0.0f;          // kSlope

@@ -52,12 +52,12 @@ Layout grad_layout(bool f32, int64_t n, int64_t a, int64_t b, int64_t experts, b
     return L;
 }
 
-// Packs what has to be; p and q as the product reads them.
+// Packs what has to be (of q, matrices of `each` rows, those of groups with rows); p and q as the product reads them.
 cudaError_t prepare(const Layout& L, bool f32, const void*& p, int64_t p_rows, int64_t p_cols, const void*& q, int64_t q_rows,
-                    int64_t q_cols, uint8_t* ws, cudaStream_t s)
+                    int64_t q_cols, const int64_t* offsets, int64_t each, uint8_t* ws, cudaStream_t s)
 {
     const Pack1 first{p, reinterpret_cast<bf16*>(ws), L.p.packed ? p_rows : 0, p_cols, L.p.ld};
-    const Pack1 second{q, reinterpret_cast<bf16*>(ws + L.q_at), L.q.packed ? q_rows : 0, q_cols, L.q.ld};
+    const Pack1 second{q, reinterpret_cast<bf16*>(ws + L.q_at), L.q.packed ? q_rows : 0, q_cols, L.q.ld, offsets, each};
     if (L.p.packed) p = first.to;
     if (L.q.packed) q = second.to;
     return L.p.packed || L.q.packed ? pack(first, second, TokenRows{}, !f32, s) : cudaSuccess;
@@ -86,7 +86,7 @@ cudaError_t expert_matmul(const ExpertMatmul& M, void* workspace, cudaStream_t s
     const int64_t k = M.transpose ? M.b : M.a, m = M.transpose ? M.a : M.b;
     const int parts = M.f32 ? 3 : 1;
     const void *x = M.x, *w = M.w;
-    cudaError_t e = prepare(L, M.f32, x, M.n, k, w, M.experts * M.a, M.b, ws, s);
+    cudaError_t e = prepare(L, M.f32, x, M.n, k, w, M.experts * M.a, M.b, M.offsets, M.a, ws, s);
     if (e != cudaSuccess) return e;
     RowsProduct R{};
     R.a = Operand{w, M.a, M.b, L.q.ld, M.experts, parts};
@@ -117,7 +117,7 @@ cudaError_t expert_matmul_grad(const ExpertMatmul& M, void* workspace, cudaStrea
     const Layout L = grad_layout(M.f32, M.n, M.a, M.b, M.experts, aligned(M.x), aligned(M.dy));
     const int parts = M.f32 ? 3 : 1;
     const void *x = M.x, *dy = M.dy;
-    cudaError_t e = prepare(L, M.f32, x, M.n, M.a, dy, M.n, M.b, ws, s);
+    cudaError_t e = prepare(L, M.f32, x, M.n, M.a, dy, M.n, M.b, nullptr, 1, ws, s);
     if (e != cudaSuccess) return e;
     WeightsProduct R{};
     R.a = Operand{dy, M.n, M.b, L.q.ld, 1, parts};

@@ -765,10 +765,13 @@ struct Operand {
 inline int64_t packed_ld(int64_t cols) { return cols >= 256 ? (cols + 63) / 64 * 64 : (cols + 7) / 8 * 8; }
 
 // One array to be packed: rows x cols values, fp32 into three parts or bf16 into one with aligned rows.
+// With offsets the rows are those of matrices of `each` rows, and a matrix whose group has no rows is left out.
 struct Pack1 {
     const void* from;
     bf16* to;
     int64_t rows, cols, ld;
+    const int64_t* offsets = nullptr;
+    int64_t each = 1;
 };
 // The tokens' numbers for the loss's gradient: lse log2(e), dloss (over the unit, where one is asked for) and target, 0 and -1 for
 // a token that does not count and behind the last (vocab_back.cu).

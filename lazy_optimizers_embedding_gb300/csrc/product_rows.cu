@@ -46,7 +46,11 @@ __device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t 
     const int G = lanes > 16 ? 32 : lanes > 8 ? 16 : lanes > 4 ? 8 : lanes > 2 ? 4 : static_cast<int>(lanes);
     const int each = 32 / G;                              // rows of a warp at a time
     const int64_t size = A.rows * A.ld;
-    for (int64_t r = warp * each + lane / G; r < A.rows; r += warps * each)
+    for (int64_t r = warp * each + lane / G; r < A.rows; r += warps * each) {
+        if (A.offsets != nullptr) {     // 10 bytes a value for nothing
+            const int64_t g = r / A.each;
+            if (A.offsets[g] == A.offsets[g + 1]) continue;
+        }
         for (int64_t i = lane % G * 8; i < A.cols; i += G * 8) {
             float x[8];
             read8<T, kVec>(static_cast<const T*>(A.from) + r * A.cols + i, A.cols - i, x);
@@ -84,6 +88,7 @@ __device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t 
                 Pack<bf16, 8>::put(to + p * size, h);
             }
         }
+    }
 }
 
 // Rows of one or two arrays as bf16 with aligned rows: fp32 in three parts, hi = bf16(v), mid = bf16(v - hi), lo = what

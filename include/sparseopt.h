@@ -501,7 +501,7 @@ size_t sparse_expert_matmul_workspace_size(sparse_dtype_t type, int64_t n, int64
  * an infinite value gives NaN where fp32 arithmetic would give an infinity.  A row that is not
  * finite spoils its own results only, a matrix its own expert's.
  * Offsets that do not ascend from 0 to at most n set SPARSE_ERR_INDEX_OUT_OF_RANGE.
- * Limits: experts <= 1024, n < 2^31, a, b <= 2^20, n max(a, b) and experts a b <= 2^37.
+ * Limits: experts <= 1024, n < 2^31 - 1024, a, b <= 2^20, n max(a, b) and experts a b <= 2^37.
  *   ws          sparse_expert_matmul_workspace_size() bytes, 256-byte aligned
  */
 sparse_status_t sparse_expert_matmul(const void* x, const void* w, sparse_dtype_t type, int64_t n, int64_t a, int64_t b,

@@ -66,11 +66,12 @@ bool valid_route(sparse_dtype_t type, int64_t n, int64_t experts, int64_t k, con
 }
 
 // Sizes that the tensor copies can address, and whose tiles (64 x 128 scores at least) are fewer than 2^31.
+constexpr int64_t kMaxRows = INT32_MAX - 1024;   // 32-bit rows, a tile past the last included
 constexpr int64_t kMaxCols = int64_t(1) << 20, kMaxValues = int64_t(1) << 37, kMaxScores = int64_t(1) << 43;
 
 bool valid_matmul(sparse_dtype_t type, int64_t n, int64_t a, int64_t b, int64_t experts)
 {
-    return valid_type(type) && n >= 0 && n <= INT32_MAX && a >= 1 && a <= kMaxCols && b >= 1 && b <= kMaxCols &&
+    return valid_type(type) && n >= 0 && n <= kMaxRows && a >= 1 && a <= kMaxCols && b >= 1 && b <= kMaxCols &&
            experts >= 1 && experts <= kMaxExperts && n <= kMaxValues / std::max(a, b) && experts * a <= kMaxValues / b;
 }
 

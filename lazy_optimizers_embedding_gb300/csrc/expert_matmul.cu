@@ -1,6 +1,6 @@
 // expert_matmul.cu -- the products of every expert's rows with its matrix, and the
 // gradient of the matrices: which arrays are packed, where the workspace's parts lie.
-#include "product.cuh"
+#include "few_rows.cuh"
 
 namespace so {
 
@@ -23,6 +23,7 @@ Placed place(bool f32, int64_t rows, int64_t cols, bool is_aligned)
 
 struct Layout {
     Placed p, q;             // rows and matrices; rows and their gradients
+    bool few;                // few fp32 rows: see few_rows.cuh
     int splits;
     size_t q_at, slabs, total;
 };
@@ -33,6 +34,12 @@ Layout product_layout(bool f32, int64_t n, int64_t a, int64_t b, int64_t experts
     const int64_t k = transpose ? b : a, m = transpose ? a : b;
     L.p = place(f32, n, k, x_aligned);
     L.q = place(f32, experts * a, b, w_aligned);
+    if (f32 && few_rows(n, experts)) {
+        L.few = true;
+        L.splits = transpose ? 0 : few_sums_splits(n, m, k, experts);
+        L.total = std::max<size_t>(256, sizeof(float) * L.splits * n * m);
+        return L;
+    }
     L.splits = rows_splits(n, m, k, experts, f32 ? 3 : 1);
     L.q_at = L.p.bytes;
     L.slabs = L.q_at + L.q.bytes;
@@ -45,6 +52,11 @@ Layout grad_layout(bool f32, int64_t n, int64_t a, int64_t b, int64_t experts, b
     Layout L{};
     L.p = place(f32, n, a, x_aligned);
     L.q = place(f32, n, b, dy_aligned);
+    if (f32 && few_rows(n, experts)) {
+        L.few = true;
+        L.total = 256;
+        return L;
+    }
     L.splits = weights_splits(n, b, a, experts, f32 ? 3 : 1);
     L.q_at = L.p.bytes;
     L.slabs = L.q_at + L.q.bytes;
@@ -85,6 +97,26 @@ cudaError_t expert_matmul(const ExpertMatmul& M, void* workspace, cudaStream_t s
     const Layout L = product_layout(M.f32, M.n, M.a, M.b, M.experts, M.transpose, aligned(M.x), aligned(M.w));
     const int64_t k = M.transpose ? M.b : M.a, m = M.transpose ? M.a : M.b;
     const int parts = M.f32 ? 3 : 1;
+    if (L.few && M.transpose) {
+        FewDots D{};
+        D.x = static_cast<const float*>(M.x);
+        D.w = static_cast<const float*>(M.w);
+        D.n = M.n;
+        D.m = m;
+        D.k = k;
+        D.groups = static_cast<int>(M.experts);
+        D.offsets = M.offsets;
+        D.out = static_cast<float*>(M.out);
+        D.d_err = M.d_err;
+        return few_dots(D, s);
+    }
+    if (L.few) {
+        float* slabs = reinterpret_cast<float*>(ws);
+        const cudaError_t e = few_sums(FewSums{static_cast<const float*>(M.x), static_cast<const float*>(M.w), M.n, m, k,
+                                               static_cast<int>(M.experts), M.offsets, L.splits, slabs, M.d_err}, s);
+        if (e != cudaSuccess) return e;
+        return join_slabs(Join{slabs, L.splits, M.n * m, M.n, m, M.offsets + M.experts}, M.out, !M.f32, s);
+    }
     const void *x = M.x, *w = M.w;
     cudaError_t e = prepare(L, M.f32, x, M.n, k, w, M.experts * M.a, M.b, M.offsets, M.a, ws, s);
     if (e != cudaSuccess) return e;
@@ -116,6 +148,9 @@ cudaError_t expert_matmul_grad(const ExpertMatmul& M, void* workspace, cudaStrea
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Layout L = grad_layout(M.f32, M.n, M.a, M.b, M.experts, aligned(M.x), aligned(M.dy));
     const int parts = M.f32 ? 3 : 1;
+    if (L.few)
+        return few_outer(FewOuter{static_cast<const float*>(M.x), static_cast<const float*>(M.dy), M.n, M.a, M.b,
+                                  static_cast<int>(M.experts), M.offsets, static_cast<float*>(M.out), M.d_err}, s);
     const void *x = M.x, *dy = M.dy;
     cudaError_t e = prepare(L, M.f32, x, M.n, M.a, dy, M.n, M.b, nullptr, 1, ws, s);
     if (e != cudaSuccess) return e;

@@ -11,6 +11,7 @@
 // bf16 (fp32 operands: three bf16 parts): G and the piece's rows make the piece's share of dx, which is summed
 // in fp32 over the pieces, G and x the piece's rows of dW, complete.  A piece is as wide as kSlopeBytes allows.
 #include "product.cuh"
+#include "few_rows.cuh"
 #include "vocab_back.cuh"
 
 namespace so {
@@ -106,6 +107,8 @@ struct Layout {
     int dx_splits, dw_splits;
     bool dx_slabs, dw_slabs;
     bool narrow;             // the gradient in one launch (vocab_back.cu)
+    bool few;                // scores of few fp32 tokens: see few_rows.cuh
+    int slots;               // running sums of a token
     BackPlan back;
     size_t x, w, part, hit, g, dx, dw, tokens, unit, total;
 };
@@ -124,12 +127,20 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         at += (static_cast<size_t>(bytes) + 255) / 256 * 256;
         return p;
     };
+    if (f32 && !grad && n <= kFewTokens) {
+        L.few = true;
+        L.slots = few_dot_slots(v);
+        L.part = take(static_cast<int64_t>(sizeof(float2)) * L.slots * n);
+        L.hit = take(4 * n);
+        L.total = std::max<size_t>(at, 256);
+        return L;
+    }
     if (L.pack_x) L.x = take(2 * L.parts * n * L.ldx);
     if (L.pack_w) L.w = take(2 * L.parts * v * L.ldw);
     if (!grad) {
         L.score = score_grid(n, c, v, L.parts, true);
-        const int groups = score_groups(f32);
-        L.part = take(static_cast<int64_t>(sizeof(float2)) * L.score.items * groups * n);
+        L.slots = L.score.items * score_groups(f32);
+        L.part = take(static_cast<int64_t>(sizeof(float2)) * L.slots * n);
         L.hit = take(static_cast<int64_t>(sizeof(float)) * n);
     } else if (c <= kBackCols) {
         L.narrow = true;
@@ -194,11 +205,35 @@ size_t vocab_loss_ws_bytes(const VocabLoss& V, int grad)
     return layout(V.f32, V.n, V.c, V.v, grad, aligned(V.x), aligned(V.w)).total;
 }
 
+static cudaError_t join_scores(const VocabLoss& V, const Layout& L, const float2* part, const float* hit, cudaStream_t s)
+{
+    SO_PROFILE("vocab_join", s);
+    auto join = [&](auto* kernel, int rows) {
+        return launch(kernel, dim3(static_cast<unsigned>(up(V.n, rows))), dim3(1024), s, part, L.slots, hit, V.target, V.n, V.loss, V.lse);
+    };
+    return V.n <= 4 * kSms ? join(k_loss_join<4>, 4) : join(k_loss_join<32>, 32);
+}
+
 cudaError_t vocab_loss(const VocabLoss& V, void* workspace, cudaStream_t s)
 {
     if (tensor_encoder() == nullptr) return cudaErrorNotSupported;
     const Layout L = layout(V.f32, V.n, V.c, V.v, false, aligned(V.x), aligned(V.w));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (L.few) {
+        FewDots D{};
+        D.x = static_cast<const float*>(V.x);
+        D.w = static_cast<const float*>(V.w);
+        D.n = V.n;
+        D.m = V.v;
+        D.k = V.c;
+        D.groups = 1;
+        D.target = V.target;
+        D.d_err = V.d_err;
+        D.part = reinterpret_cast<float2*>(ws + L.part);
+        D.hit = reinterpret_cast<float*>(ws + L.hit);
+        const cudaError_t e = few_dots(D, s);
+        return e != cudaSuccess ? e : join_scores(V, L, D.part, D.hit, s);
+    }
     const void *x, *w;
     cudaError_t e = prepare(L, V, ws, x, w, TokenRows{}, s);
     if (e != cudaSuccess) return e;
@@ -221,13 +256,7 @@ cudaError_t vocab_loss(const VocabLoss& V, void* workspace, cudaStream_t s)
     e = V.f32 ? run_scores<kScore, 6, false>("vocab_score", L.score.pair, maps, Q, L.score.items, s)
               : run_scores<kScore, 1, true>("vocab_score", L.score.pair, maps, Q, L.score.items, s);
     if (e != cudaSuccess) return e;
-    SO_PROFILE("vocab_join", s);
-    const int slots = L.score.items * score_groups(V.f32);
-    auto join = [&](auto* kernel, int rows) {
-        return launch(kernel, dim3(static_cast<unsigned>(up(V.n, rows))), dim3(1024), s, static_cast<const float2*>(Q.part), slots,
-                      static_cast<const float*>(Q.hit), V.target, V.n, V.loss, V.lse);
-    };
-    return V.n <= 4 * kSms ? join(k_loss_join<4>, 4) : join(k_loss_join<32>, 32);
+    return join_scores(V, L, Q.part, Q.hit, s);
 }
 
 // Rows of at most kBackCols columns.

@@ -229,7 +229,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_const
                             const bool more = !fresh || k > 0;
                             const uint32_t a = g + (P == 6 ? k / 2 * 32 + k % 2 * 8 : k / 4 * 64 + k % 4 * 8);   // see the slopes' places below
                             const uint64_t r = rows + k * (2048 / 16);
-                            if (S::kWide) {   // the parts lie side by side as D's sums do; a product of 64 columns takes as long as one of 128
+                            // The parts lie side by side as D's sums do.  Fetching A bounds a product of few columns: 64 take about as long as
+                            // 128, 57 cycles with A in shared memory. (Three accumulators of scores and two of D, 12 and 20 products a tile of
+                            // 64 and not 20 and 12: 555 against 477 us for dx at 2048 x 64 x 200000; three of both do not fit.)
+                            if (S::kWide) {
                                 tc_mma_f16_tmem(d, a, r, sum_desc3, more);
                                 tc_mma_f16_tmem(d + C, a + TN, r, sum_desc2, true);
                                 tc_mma_f16_tmem(d + 2 * C, a + 16, r, sum_desc, true);

@@ -544,7 +544,7 @@ sparse_status_t sparse_vocab_loss(const void* x, const void* w, sparse_dtype_t t
  *   dloss[n]            fp32 (NULL: ones); dx [n, c], dw [v, c]: of x's type (each may be NULL);
  *                       dw is the whole table's gradient, zeros where v has none
  * With bf16, G is rounded to bf16 (an operand of the two products: 2^-9 of each of its values).
- * A token that does not count has part in the products all the same, times zero: its x must be finite.
+ * The x of a token that does not count is not looked at.
  * Sums are in a fixed order: equal inputs give equal bits.
  */
 sparse_status_t sparse_vocab_loss_grad(const float* dloss, const void* x, const void* w, sparse_dtype_t type, int64_t n,

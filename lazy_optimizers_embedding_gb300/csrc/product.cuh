@@ -765,13 +765,16 @@ struct Operand {
 inline int64_t packed_ld(int64_t cols) { return cols >= 256 ? (cols + 63) / 64 * 64 : (cols + 7) / 8 * 8; }
 
 // One array to be packed: rows x cols values, fp32 into three parts or bf16 into one with aligned rows.
-// With offsets the rows are those of matrices of `each` rows, and a matrix whose group has no rows is left out.
+// With offsets the rows are those of matrices of `each` rows, and a matrix whose group has no rows is left out.  With targets a
+// row whose target is none of v rows is zeros, whatever lies there.
 struct Pack1 {
     const void* from;
     bf16* to;
     int64_t rows, cols, ld;
     const int64_t* offsets = nullptr;
     int64_t each = 1;
+    const int64_t* target = nullptr;
+    int64_t v = 0;
 };
 // The tokens' numbers for the loss's gradient: lse log2(e), dloss (over the unit, where one is asked for) and target, 0 and -1 for
 // a token that does not count and behind the last (vocab_back.cu).
@@ -796,7 +799,7 @@ __device__ __forceinline__ void put_token(const TokenRows& R, int i, float unit)
     R.out[i] = q;
 }
 
-// Up to two arrays in one launch (the second's rows may be 0), and the tokens' numbers (no unit; padded may be 0).
+// Up to two arrays in one launch (either's rows may be 0), and the tokens' numbers and their unit (padded may be 0).
 cudaError_t pack(const Pack1& a, const Pack1& b, const TokenRows& tokens, int is_bf16, cudaStream_t s);
 
 // rows x cols fp32 sums of `slabs` arrays, in order; rows from *end on (end given) are zeros.

@@ -51,9 +51,17 @@ __device__ __forceinline__ void pack_rows(const Pack1& A, int64_t warp, int64_t 
             const int64_t g = r / A.each;
             if (A.offsets[g] == A.offsets[g + 1]) continue;
         }
+        bool none = false;
+        if (A.target != nullptr) {
+            const int64_t g = A.target[r];
+            none = g < 0 || g >= A.v;
+        }
         for (int64_t i = lane % G * 8; i < A.cols; i += G * 8) {
             float x[8];
             read8<T, kVec>(static_cast<const T*>(A.from) + r * A.cols + i, A.cols - i, x);
+            if (none)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.0f;
             bf16* to = A.to + r * A.ld + i;
             if (kParts == 1) {
                 Pack<bf16, 8>::put(to, x);
@@ -102,8 +110,11 @@ __global__ void __launch_bounds__(kPackBlock) k_pack(const Pack1 A, const Pack1 
         pack_rows<T, kVec>(A, static_cast<int64_t>(block) * per + w, static_cast<int64_t>(blocks_a) * per, lane);
     else if (block < blocks_a + blocks_b)
         pack_rows<T, kVec>(B, static_cast<int64_t>(block - blocks_a) * per + w, static_cast<int64_t>(blocks_b) * per, lane);
-    else
-        put_token(R, (block - blocks_a - blocks_b) * kPackBlock + static_cast<int>(threadIdx.x), 1.0f);
+    else {
+        const float unit = R.unit != nullptr ? common_unit(R.dloss, R.target, R.n, lane) : 1.0f;
+        if (R.unit != nullptr && block == blocks_a + blocks_b && threadIdx.x == 0) *R.unit = unit;
+        put_token(R, (block - blocks_a - blocks_b) * kPackBlock + static_cast<int>(threadIdx.x), unit);
+    }
 }
 
 // Sums of slabs in order, four neighbours a thread.

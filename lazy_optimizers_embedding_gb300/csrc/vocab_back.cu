@@ -74,14 +74,6 @@ struct Maps {
     CUtensorMap x, w;
 };
 
-__global__ void __launch_bounds__(256) k_loss_tokens(const TokenRows R)
-{
-    pdl_enter();   // writes the workspace and the error word
-    const float u = R.unit != nullptr ? common_unit(R.dloss, R.target, R.n, threadIdx.x & 31) : 1.0f;
-    if (R.unit != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *R.unit = u;
-    put_token(R, blockIdx.x * 256 + threadIdx.x, u);
-}
-
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, 1) k_loss_back(const __grid_constant__ Maps maps, const BackArgs Q)
 {
@@ -492,12 +484,6 @@ BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v)
     back_splits(n, v, tile, B.dx_splits, B.dw_splits);
     B.tokens = up(n, 128) * 128;
     return B;
-}
-
-cudaError_t loss_tokens(const TokenRows& R, cudaStream_t s)
-{
-    SO_PROFILE("vocab_tokens", s);
-    return launch(k_loss_tokens, dim3(static_cast<unsigned>(up(R.padded, 256))), dim3(256), s, R);
 }
 
 cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s)

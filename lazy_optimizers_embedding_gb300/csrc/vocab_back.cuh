@@ -9,7 +9,7 @@ constexpr int64_t kBackCols = 128;   // columns at most
 
 struct BackArgs {
     int32_t n, c, v;
-    const float4* tokens;    // see loss_tokens
+    const float4* tokens;    // see TokenRows
     void *dx, *dw;           // results, or fp32 slabs where there are several parts; nullptr: not wanted
     int32_t dx_splits, dw_splits, out_bf16;
     int32_t release;         // writes slabs only
@@ -24,7 +24,6 @@ struct BackPlan {
 };
 
 BackPlan back_plan(bool f32, int64_t n, int64_t c, int64_t v);
-cudaError_t loss_tokens(const TokenRows& R, cudaStream_t s);
 cudaError_t loss_back(const CUtensorMap& x, const CUtensorMap& w, bool f32, BackArgs Q, cudaStream_t s);
 
 }  // namespace so

@@ -117,7 +117,7 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
 {
     Layout L{};
     L.parts = f32 ? 3 : 1;
-    L.pack_x = f32 || c % 8 != 0 || !x_aligned;
+    L.pack_x = f32 || c % 8 != 0 || !x_aligned || grad;   // the gradient reads zeros for a token that does not count: 0 times NaN is NaN
     L.pack_w = f32 || c % 8 != 0 || !w_aligned;
     L.ldx = L.pack_x ? packed_ld(c) : c;
     L.ldw = L.pack_w ? packed_ld(c) : c;
@@ -181,13 +181,14 @@ cudaError_t run_scores(const char* name, bool pair, const ProductMaps& maps, Pro
                 : run_product<ProductShape<kForm, false, false, 1, P, kDrain>>(name, maps, Q, across * Q.m_tiles, s);
 }
 
-// x and w as the products read them.
-cudaError_t prepare(const Layout& L, const VocabLoss& V, uint8_t* ws, const void*& x, const void*& w, const TokenRows& tokens, cudaStream_t s)
+// x and w as the products read them, for the gradient with the tokens' numbers.
+cudaError_t prepare(const Layout& L, const VocabLoss& V, bool grad, uint8_t* ws, const void*& x, const void*& w, const TokenRows& tokens,
+                    cudaStream_t s)
 {
     x = L.pack_x ? ws + L.x : V.x;
     w = L.pack_w ? ws + L.w : V.w;
     if (!L.pack_x && !L.pack_w) return cudaSuccess;
-    return pack(Pack1{V.x, reinterpret_cast<bf16*>(ws + L.x), L.pack_x ? V.n : 0, V.c, L.ldx},
+    return pack(Pack1{V.x, reinterpret_cast<bf16*>(ws + L.x), L.pack_x ? V.n : 0, V.c, L.ldx, nullptr, 1, grad ? V.target : nullptr, V.v},
                 Pack1{V.w, reinterpret_cast<bf16*>(ws + L.w), L.pack_w ? V.v : 0, V.c, L.ldw}, tokens, !V.f32, s);
 }
 
@@ -235,7 +236,7 @@ cudaError_t vocab_loss(const VocabLoss& V, void* workspace, cudaStream_t s)
         return e != cudaSuccess ? e : join_scores(V, L, D.part, D.hit, s);
     }
     const void *x, *w;
-    cudaError_t e = prepare(L, V, ws, x, w, TokenRows{}, s);
+    cudaError_t e = prepare(L, V, false, ws, x, w, TokenRows{}, s);
     if (e != cudaSuccess) return e;
     ProductMaps maps;
     if (!Operand{x, V.n, V.c, L.ldx, 1, L.parts}.map(&maps.a) || !Operand{w, V.v, V.c, L.ldw, 1, L.parts}.map(&maps.b))
@@ -297,8 +298,7 @@ cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
         tokens = TokenRows{V.lse, V.dloss, V.target, static_cast<int>(V.n), static_cast<int>(L.back.tokens), static_cast<int>(V.v),
                            reinterpret_cast<float4*>(ws + L.tokens), V.f32 ? nullptr : reinterpret_cast<float*>(ws + L.unit), V.d_err};
     }
-    cudaError_t e = prepare(L, V, ws, x, w, V.f32 ? tokens : TokenRows{}, s);   // fp32 rows are packed, and the tokens' numbers with them
-    if (e == cudaSuccess && L.narrow && !V.f32) e = loss_tokens(tokens, s);
+    cudaError_t e = prepare(L, V, true, ws, x, w, tokens, s);
     if (e == cudaSuccess && L.narrow) return narrow_grad(V, L, x, w, ws, s);
     const int64_t row = 2 * L.ldw;   // bytes of one part's row
     for (int64_t p = 0; p < L.pieces && e == cudaSuccess; ++p) {

@@ -228,3 +228,27 @@ def test_gradient_by_differences(cuda_lib):
     slope, mine = (up.double() - down.double()) / (2 * h), (dx.double() * d.double()).sum(1)
     # a third derivative of a few units times h^2 / 6, and the losses' own errors (2^-19 of 7 each) over h
     assert float((slope - mine).abs().max()) <= 2.0 ** -12 * 20 / 6 + 7 * 2.0 ** -19 / h
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [40, 64, 128, 131, 200, 264])
+def test_rows_of_tokens_that_do_not_count_are_not_looked_at(cuda_lib, c, kind):
+    """A padded batch's rows hold anything: results are those of zeros there, bit for bit, whatever else they were."""
+    import torch
+    so = cuda_lib
+    x, w, target, dloss = _case(torch, 333, c, 905, kind)
+    target[300:] = -1                                         # a batch's padding
+    none = target < 0
+    for size in (333, 1):                                     # and a single token
+        for d in (dloss, None):
+            d = d if d is None else d[-size:].contiguous()
+            clean, t = x[-size:].clone(), target[-size:].contiguous()
+            clean[none[-size:]] = 0.0
+            want = _run(torch, so, clean, w, t, d)
+            for what in (float("nan"), float("inf"), -float("inf")):
+                dirty = clean.clone()
+                dirty[none[-size:]] = what
+                got = _run(torch, so, dirty, w, t, d)
+                assert int(got[4].item()) == 0
+                assert all(torch.equal(p, q) for p, q in zip((got[0], got[2], got[3]), (want[0], want[2], want[3])))
+                assert torch.equal(got[1][t >= 0], want[1][t >= 0])

@@ -150,7 +150,7 @@ cudaError_t expert_matmul_grad(const ExpertMatmul& M, void* workspace, cudaStrea
     const int parts = M.f32 ? 3 : 1;
     if (L.few)
         return few_outer(FewOuter{static_cast<const float*>(M.x), static_cast<const float*>(M.dy), M.n, M.a, M.b,
-                                  static_cast<int>(M.experts), M.offsets, static_cast<float*>(M.out), M.d_err}, s);
+                                  static_cast<int>(M.experts), M.offsets, static_cast<float*>(M.out), nullptr, M.d_err}, s);
     const void *x = M.x, *dy = M.dy;
     cudaError_t e = prepare(L, M.f32, x, M.n, M.a, dy, M.n, M.b, nullptr, 1, ws, s);
     if (e != cudaSuccess) return e;

@@ -107,7 +107,7 @@ struct Layout {
     int dx_splits, dw_splits;
     bool dx_slabs, dw_slabs;
     bool narrow;             // the gradient in one launch (vocab_back.cu)
-    bool few;                // scores of few fp32 tokens: see few_rows.cuh
+    bool few;                // few fp32 tokens: see few_rows.cuh
     int slots;               // running sums of a token
     BackPlan back;
     size_t x, w, part, hit, g, dx, dw, tokens, unit, total;
@@ -133,6 +133,14 @@ Layout layout(bool f32, int64_t n, int64_t c, int64_t v, bool grad, bool x_align
         L.part = take(static_cast<int64_t>(sizeof(float2)) * L.slots * n);
         L.hit = take(4 * n);
         L.total = std::max<size_t>(at, 256);
+        return L;
+    }
+    if (f32 && grad && n <= kFewGrad) {
+        L.few = true;
+        L.g = take(4 * n * v);
+        L.dx_splits = few_sums_splits(n, c, v, 1);
+        L.dx = take(4 * L.dx_splits * n * c);
+        L.total = at;
         return L;
     }
     if (L.pack_x) L.x = take(2 * L.parts * n * L.ldx);
@@ -287,11 +295,38 @@ static cudaError_t narrow_grad(const VocabLoss& V, const Layout& L, const void* 
     return dx.rows > 0 ? join_two(dx, V.dx, dw, V.dw, !V.f32, s) : join_slabs(dw, V.dw, !V.f32, s);
 }
 
+// Few fp32 tokens: the slopes in fp32, then the sums of the table's rows and the outer products, each a pass over the table.
+static cudaError_t few_loss_grad(const VocabLoss& V, const Layout& L, uint8_t* ws, cudaStream_t s)
+{
+    float *g = reinterpret_cast<float*>(ws + L.g), *slabs = reinterpret_cast<float*>(ws + L.dx);
+    FewDots D{};
+    D.x = static_cast<const float*>(V.x);
+    D.w = static_cast<const float*>(V.w);
+    D.n = V.n;
+    D.m = V.v;
+    D.k = V.c;
+    D.groups = 1;
+    D.out = g;
+    D.target = V.target;
+    D.lse = V.lse;
+    D.dloss = V.dloss;
+    D.d_err = V.d_err;
+    cudaError_t e = few_dots(D, s);
+    if (e == cudaSuccess && V.dw != nullptr)
+        e = few_outer(FewOuter{g, D.x, V.n, V.v, V.c, 1, nullptr, static_cast<float*>(V.dw), V.target, V.d_err}, s);
+    if (e == cudaSuccess && V.dx != nullptr) {
+        e = few_sums(FewSums{g, D.w, V.n, V.c, V.v, 1, nullptr, L.dx_splits, slabs, V.d_err}, s);
+        if (e == cudaSuccess) e = join_slabs(Join{slabs, L.dx_splits, V.n * V.c, V.n, V.c}, V.dx, 0, s);
+    }
+    return e;
+}
+
 cudaError_t vocab_loss_grad(const VocabLoss& V, void* workspace, cudaStream_t s)
 {
     if (tensor_encoder() == nullptr) return cudaErrorNotSupported;
     const Layout L = layout(V.f32, V.n, V.c, V.v, true, aligned(V.x), aligned(V.w));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (L.few) return few_loss_grad(V, L, ws, s);
     const void *x, *w;
     TokenRows tokens{};
     if (L.narrow) {

@@ -85,3 +85,74 @@ def test_targets_that_are_no_rows(cuda_lib):
                 so.check(so.sparse_vocab_loss_grad(t.dloss, t.x, t.w, 9, 20, 50, t.target, t.lse, t.dx, t.dw, t.ws, t.err))
             t.G.check("bad target")
             assert int(t.err.item()) == so.ERR_INDEX_OUT_OF_RANGE
+
+
+# both sides of every count of tokens that changes the kernels of the loss or of its gradient
+@pytest.mark.parametrize("n", [2, 3, 4, 8, 9, 12])
+@pytest.mark.parametrize("c,v", [(1, 1), (33, 4097), (64, 70001), (515, 20000), (1100, 640), (4100, 257)])
+def test_few_tokens_there_and_back(cuda_lib, n, c, v):
+    import torch
+    for shift in (0, 1):
+        t = Loss(torch, cuda_lib, n, c, v, "f32", shift=shift)
+        t.run()
+        t.check()
+        if v > 1:
+            t.compare()
+            continue
+        # A table of one row: every result is 0, and no share of its norm a bound.  The gradient's score may be added up in another order
+        # than lse's, so p = exp(z - lse) is off by the errors of both, twice the first term, and by the exponential's own, the second.
+        x, w, lse, d = _np(t.x), _np(t.w), _np(t.lse), _np(t.dloss)
+        near = 2 * 560 * E24 * np.abs(x @ w.T) + (16 + np.abs(lse[:, None])) * 4 * E24
+        far = d[:, None] * near
+        assert (np.abs(_np(t.dx)) <= far @ np.abs(w)).all() and (np.abs(_np(t.dw)) <= far.T @ np.abs(x)).all()
+        assert (np.abs(_np(t.loss)) <= near[:, 0]).all()      # lse less the score, off by as much
+
+
+@pytest.mark.parametrize("n", [1, 3, 7])
+@pytest.mark.parametrize("c,v", [(40, 905), (515, 3001)])
+def test_few_tokens_results_one_by_one_masked_and_captured(cuda_lib, n, c, v):
+    """dx and dw alone are those of both together; a token that does not count leaves nothing, whatever its row holds; two graphs share a
+    workspace; equal inputs give equal bits."""
+    import torch
+    so = cuda_lib
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, w = torch.randn(n, c, device="cuda", generator=g), torch.randn(v, c, device="cuda", generator=g) * c ** -0.5
+    target, dloss = torch.randint(0, v, (n,), device="cuda", generator=g), torch.rand(n, device="cuda", generator=g) + 0.5
+    target[n // 2] = -1
+    x[n // 2], dloss[n // 2] = 0.0, float("nan")
+    ws = torch.empty(so.sparse_vocab_loss_workspace_size(x.dtype, n, c, v, True), dtype=torch.uint8, device="cuda")
+    err = so.error_word()
+
+    def run(x, dx, dw):
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        so.check(so.sparse_vocab_loss(x, w, n, c, v, target, loss, lse, ws, err))
+        so.check(so.sparse_vocab_loss_grad(dloss, x, w, n, c, v, target, lse, dx, dw, ws, err))
+
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    run(x, dx, dw)
+    z = x.double() @ w.double().T
+    p = torch.exp(z - torch.logsumexp(z, 1, keepdim=True))
+    live = target >= 0
+    p[torch.arange(n, device="cuda")[live], target[live]] -= 1.0
+    p = torch.where(live[:, None], p * dloss.double()[:, None], 0.0)
+    # slopes: 2^-19 of their scores' exponentials at the most; sums of v and of n terms
+    for got, ref, terms in ((dx, p @ w.double(), p.abs() @ w.double().abs()), (dw, p.T @ x.double(), p.abs().T @ x.double().abs())):
+        assert bool(((got.double() - ref).abs() <= (v / 8 + 60) * E24 * terms + 2.0 ** -19 * terms).all())
+    dirty = x.clone()
+    dirty[n // 2] = float("nan")
+    one, two = torch.full_like(dx, 3.0), torch.full_like(dw, 3.0)
+    run(dirty, one, None)
+    run(dirty, None, two)
+    assert torch.equal(one, dx) and torch.equal(two, dw) and not one[n // 2].any()
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        outs.append((torch.empty_like(dx), torch.empty_like(dw)))
+        with torch.cuda.graph(graphs[-1]):
+            run(dirty, *outs[-1])
+    for _ in range(3):
+        for q in graphs:
+            q.replay()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, (dx, dw)))

@@ -197,21 +197,23 @@ __global__ void __launch_bounds__(kFewBlock, 2) k_few_dots(const FewDots D, int 
 
 // ---------------------------------------------------------------- weighted sums
 // A warp has every eighth four of the matrix's rows, a lane four of 128 columns and 16 tokens' sums of them; x comes from shared
-// memory by broadcasts of four tokens.  The warps' sums are added up in order.
-template <bool kVec>
+// memory by broadcasts of four tokens.  The warps' sums are added up in order.  Where there are at most 64 columns half a warp is a team with rows
+// of its own (1M x 64 and a token, dx with the slopes: 173 us, by whole warps 217).
+template <bool kVec, bool kNarrow>
 __global__ void __launch_bounds__(kFewBlock, 2) k_few_sums(const FewSums D, int tiles)
 {
     pdl_enter();   // writes the workspace and the error word
-    extern __shared__ float smem[];          // [256][kR] of x, then the warps' sums [8][kR][kCols]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int L = kNarrow ? 16 : 32, kTeams = kFewBlock / L, kWide = 4 * L;
+    extern __shared__ float smem[];          // [256][kR] of x, then the teams' sums [kTeams][kR][kWide]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = threadIdx.x / L, l = threadIdx.x % L;
     const int64_t all = static_cast<int64_t>(D.groups) * tiles * D.splits;
     for (int64_t item = blockIdx.x; item < all; item += gridDim.x) {
         const int split = static_cast<int>(item % D.splits);
         const int64_t u = item / D.splits;
         const int e = static_cast<int>(u / tiles);
-        const int64_t c0 = (u - static_cast<int64_t>(e) * tiles) * kCols;
+        const int64_t c0 = (u - static_cast<int64_t>(e) * tiles) * kWide;
         const int64_t ka = D.k * split / D.splits, kb = D.k * (split + 1) / D.splits;
-        const int64_t col = c0 + (kVec ? 4 * lane : lane);
+        const int64_t col = c0 + (kVec ? 4 * l : l);
         int64_t t0, t1;
         rows_of(D.offsets, e, D.n, D.d_err, t0, t1);
         auto pass = [&](auto size, int64_t t) {
@@ -227,13 +229,14 @@ __global__ void __launch_bounds__(kFewBlock, 2) k_few_sums(const FewSums D, int 
                     for (int i = lane; i < 256; i += 32)
                         smem[i * R + r] = t + r < t1 && kc + i < kb ? D.x[(t + r) * D.k + kc + i] : 0.0f;
                 __syncthreads();
-                for (int i0 = warp * 4; i0 < 256 && kc + i0 < kb; i0 += 4 * kFewWarps) {
+#pragma unroll (R <= 8 ? 2 : 1)
+                for (int i0 = team * 4; i0 < 256 && kc + i0 < kb; i0 += 4 * kTeams) {
                     float v[4][4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int64_t k = kc + i0 + j;
                         if (k < kb)
-                            four<kVec, 32>(D.w + (e * D.k + k) * D.m, col, D.m, v[j]);
+                            four<kVec, L>(D.w + (e * D.k + k) * D.m, col, D.m, v[j]);
                         else
                             v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.0f;
                     }
@@ -254,13 +257,13 @@ __global__ void __launch_bounds__(kFewBlock, 2) k_few_sums(const FewSums D, int 
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) smem[(warp * R + r) * kCols + (kVec ? 4 * lane + q : lane + 32 * q)] = acc[r][q];
+                for (int q = 0; q < 4; ++q) smem[(team * R + r) * kWide + (kVec ? 4 * l + q : l + L * q)] = acc[r][q];
             __syncthreads();
-            for (int i = threadIdx.x; i < R * kCols; i += kFewBlock) {
-                const int r = i / kCols, c = i % kCols;
+            for (int i = threadIdx.x; i < R * kWide; i += kFewBlock) {
+                const int r = i / kWide, c = i % kWide;
                 float s = 0.0f;
 #pragma unroll
-                for (int p = 0; p < kFewWarps; ++p) s += smem[(p * R + r) * kCols + c];
+                for (int p = 0; p < kTeams; ++p) s += smem[(p * R + r) * kWide + c];
                 if (t + r < t1 && c0 + c < D.m) D.slabs[(split * D.n + t + r) * D.m + c0 + c] = s;
             }
         };
@@ -357,6 +360,7 @@ int few_sums_splits(int64_t n, int64_t m, int64_t k, int64_t groups)
 
 cudaError_t few_sums(const FewSums& D, cudaStream_t s)
 {
+    const bool narrow = D.m <= kCols / 2;
     const int tiles = static_cast<int>(up(D.m, kCols));
     const size_t smem = sizeof(float) * kFewWarps * kR * kCols;
     const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(D.groups) * tiles * D.splits, 64 * kSms);
@@ -365,7 +369,8 @@ cudaError_t few_sums(const FewSums& D, cudaStream_t s)
         const cudaError_t e = allow_smem(kernel, smem, smem);
         return e != cudaSuccess ? e : launch_smem(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFewBlock), smem, s, D, tiles);
     };
-    return whole(D.w, D.m) ? go(k_few_sums<true>) : go(k_few_sums<false>);
+    if (narrow) return whole(D.w, D.m) ? go(k_few_sums<true, true>) : go(k_few_sums<false, true>);
+    return whole(D.w, D.m) ? go(k_few_sums<true, false>) : go(k_few_sums<false, false>);
 }
 
 cudaError_t few_outer(const FewOuter& D, cudaStream_t s)

@@ -10,8 +10,8 @@ namespace so {
 // experts' products go this way with at most 64 rows and 16 for an expert on the average (there and back, us, this way and packed: 64 rows
 // among 37 experts of 515 x 771 91 and 150, 16 among 100 of 1000 x 1000 147 and 197, 64 among 8 of 2048 x 1024 87 and 134; but 64
 // rows of one expert 37 and 16 forward), and a table's scores with at most 16 tokens (1M x 64: 16 tokens 126 and 215, 32 tokens 240 and
-// 205).  Their gradient does with at most 8 (this way and by the tensor unit, 1M x 64: 1 token 273 and 617, 8 451 and 619, 16 684 and 617;
-// 124271 x 515: 224 and 499, 325 and 427, 474 and 433), bf16 rows of odd sizes, whose packing costs half, do not (8 tokens against
+// 205).  Their gradient does with at most 8 (this way and by the tensor unit, 1M x 64: 1 token 230 and 617, 8 397 and 619, 16 609 and 617;
+// 124271 x 515: 223 and 499, 324 and 427, 480 and 433), bf16 rows of odd sizes, whose packing costs half, do not (8 tokens against
 // 100000 x 515 94 and 70).
 constexpr int64_t kFewRows = 64, kFewTokens = 16, kFewGrad = 8;
 inline bool few_rows(int64_t n, int64_t groups) { return n <= kFewRows && n <= 16 * groups; }
